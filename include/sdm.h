@@ -67,7 +67,9 @@ typedef enum {
     SDM_ERR_TIMEOUT = 7        /* a bounded device wait ran out (from sdm_status_of_device) */
 } sdm_status;
 
-typedef enum { SDM_BF16 = 0, SDM_FP32 = 1 } sdm_dtype;
+/* SDM_E4M3 (8-bit floating point: sign, 4 exponent and 3 mantissa bits,
+ * finite up to 448, one NaN) only as the element type of a paged cache. */
+typedef enum { SDM_BF16 = 0, SDM_FP32 = 1, SDM_E4M3 = 2 } sdm_dtype;
 typedef enum { SDM_GREEDY = 0, SDM_SAMPLE = 1 } sdm_decode;
 typedef enum { SDM_STATIC = 0, SDM_COMPACT = 1, SDM_CAP_ACCEPT = 2 } sdm_vmode;
 
@@ -79,7 +81,8 @@ enum {
     SDM_DEV_BAD_WINDOW = 8,       /* budget or cu_seqlens window outside [0, gamma] */
     SDM_DEV_CAPACITY = 16,        /* packed rows would exceed the given capacity */
     SDM_DEV_BAD_CLASS = 32,       /* a request class id outside [0, n_class) */
-    SDM_DEV_TIER_OVERFLOW = 64    /* strict pack: packed total above every tier */
+    SDM_DEV_TIER_OVERFLOW = 64,   /* strict pack: packed total above every tier */
+    SDM_DEV_BAD_PAGE = 128        /* paged cache: a page id outside the pool, or a token past the page table */
 };
 
 /* The status a caller reports for the device bits it read back after
@@ -104,7 +107,8 @@ enum {
     SDM_OP_VERIFY = 4,
     SDM_OP_VERIFY_TREE = 5,
     SDM_OP_TV_LABEL = 6,
-    SDM_OP_DRAFT_CHAIN_RNN = 7
+    SDM_OP_DRAFT_CHAIN_RNN = 7,
+    SDM_OP_ATTEND = 8
 };
 
 /* Bytes of scratch the operation needs for these sizes (0 if none).  Pass the
@@ -572,6 +576,122 @@ sdm_status sdm_observe(const float* conf, const int32_t* cu_seqlens, const int32
                        int gamma, int n_class, int n_bins, int32_t* hist, int32_t* reached, int32_t* hits,
                        int32_t* bin_n, int32_t* bin_hit, double* bin_conf, double* ece, int32_t* dev_status,
                        void* stream);
+
+/*
+ * Paged key/value cache of one attention layer: the state that the target
+ * forward between pack and verify reads and extends ([SGLang] "ragged verify"
+ * packs the rows; the cache itself is the serving engine's and has no
+ * counterpart on the pages).
+ *
+ * Token t of request i lives in slot t % page of page table[i, t / page].
+ * Pools are [n_pages, kv_heads, page, head_dim], K and V apart, in bf16 or
+ * e4m3.  An e4m3 cache holds one scale per token and kv head, a power of two:
+ * k_exp / v_exp [n_pages, kv_heads, page] hold its exponent + 127, and the
+ * value that a code stands for is code * 2^(exp - 127), exact in bf16.
+ * Constraints: head_dim 64 or 128; page 16, 32, 64 or 128; n_pages * kv_heads
+ * * page < 2^31; pools and exponents 16-byte aligned.  Else
+ * SDM_ERR_UNSUPPORTED.
+ *
+ * The operations below take each request's committed length ctx_len[i] and
+ * its window of new tokens: rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 of the
+ * packed arrays (sdm_pack_ragged's layout; a tree's window is its N + 1 slots)
+ * sit at tokens ctx_len[i], ctx_len[i] + 1, ....  `rows` is the packed arrays'
+ * row count, an upper bound on cu_seqlens[R]; rows past cu_seqlens[R] are
+ * neither read nor written.  Device checks (OR-ed into *dev_status): a window
+ * that is not within [0, rows] or not monotone counts as empty, a negative
+ * ctx_len as 0 (SDM_DEV_BAD_WINDOW); tokens past max_pages * page are left
+ * out, and a token whose page id is outside [0, n_pages) is skipped when
+ * written and moved, read back as zeros, and as page 0 by sdm_attend
+ * (SDM_DEV_BAD_PAGE).
+ */
+typedef struct {
+    void* k;              /* device pool */
+    void* v;
+    uint8_t* k_exp;       /* e4m3 only, else NULL */
+    uint8_t* v_exp;
+    const int32_t* table; /* device [R, max_pages] page ids */
+    int32_t dtype;        /* SDM_BF16 or SDM_E4M3 */
+    int32_t n_pages;
+    int32_t kv_heads;
+    int32_t page;         /* tokens per page */
+    int32_t head_dim;
+    int32_t max_pages;    /* columns of table */
+} sdm_cache;
+
+/*
+ * cache_write: the window's keys and values into their slots.  e4m3: per
+ * token and kv head x[head_dim], e = the least integer in [-110, 119] with
+ * max |x| <= 448 * 2^e over the finite elements; code = x * 2^-e rounded to
+ * the nearest e4m3 value, ties to even, cut at +-448; a NaN or infinity is
+ * stored as NaN.
+ * In:  cache (host struct; its pools are written), k, v [rows, kv_heads,
+ *      head_dim] bf16 with k_stride / v_stride elements from row to row (a
+ *      multiple of 8, at least kv_heads * head_dim; bases 16-byte aligned: a
+ *      slice of a fused projection's output will do), cu_seqlens [R+1],
+ *      ctx_len [R].
+ * Slots of different tokens must differ (they do when no two requests share
+ * a page they write).
+ */
+sdm_status sdm_cache_write(const sdm_cache* cache, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                           int64_t v_stride, const int32_t* cu_seqlens, const int32_t* ctx_len, int R, int rows,
+                           int32_t* dev_status, void* stream);
+
+/*
+ * cache_read: tokens back as bf16 rows (exactly the values held).  Request
+ * i's tokens first[i], first[i] + 1, ... fill rows cu_rows[i] .. cu_rows[i+1]
+ * - 1 of k_out, v_out [rows, kv_heads, head_dim] (first NULL: from token 0).
+ */
+sdm_status sdm_cache_read(const sdm_cache* cache, const int32_t* cu_rows, const int32_t* first, int R, int rows,
+                          uint16_t* k_out, uint16_t* v_out, int32_t* dev_status, void* stream);
+
+/*
+ * cache_commit: after sdm_verify_tree, the accepted path's keys, values and
+ * scales move from their tree slots to follow the committed tokens, so that
+ * the next window can start there.  path[i, 0] = 0 (the root) and path[i, j]
+ * = the lowest slot c > path[i, j-1] whose parent is path[i, j-1] and whose
+ * token is out_tok[i, j-1], j = 1..accept[i]; token ctx_len[i] + path[i, j]
+ * moves to ctx_len[i] + j.  (A chain's accepted drafts are a prefix of its
+ * window and need no move.)
+ * In:  tok, parent [R, N+1], n_nodes [R] (sdm_draft_tree), out_tok [R, B+1],
+ *      accept [R] (sdm_verify_tree), ctx_len [R].  N < 16384.
+ * Out: path [R, B+1] int32 (-1 past the path); length [R] = ctx_len +
+ *      accepted + 1, the next ctx_len (may be NULL; may be ctx_len itself).
+ * A path that breaks off (no such slot) is cut there: SDM_DEV_BAD_TOKEN.
+ */
+sdm_status sdm_cache_commit(const sdm_cache* cache, const int32_t* tok, const int32_t* parent,
+                            const int32_t* n_nodes, const int32_t* out_tok, const int32_t* accept,
+                            const int32_t* ctx_len, int R, int N, int B, int32_t* path, int32_t* length,
+                            int32_t* dev_status, void* stream);
+
+/*
+ * attend: attention of every window row over its request's cached tokens,
+ * the window's own among them (write them first).  For row p of request i,
+ * query head h, kv head h / (H / kv_heads):
+ *     s_j = scale * q . k_j over the tokens j that the row sees
+ *     out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
+ * The row's position is t = ctx_len[i] + p.  It sees the tokens j <= t with
+ * t - j < window or j < sinks (window <= 0: all j <= t).  With tree_mask (the
+ * mask of sdm_draft_tree, [R, tree_nodes, words], words = ceil(tree_nodes /
+ * 32): bit c of node p set if c is p or an ancestor) the window's tokens are
+ * seen as the row's bits say, whatever their distance, and t = ctx_len[i] +
+ * depth, depth = max(0, bits set - 1).  A row that sees nothing gives out 0,
+ * lse -inf.  What a row does not see does not touch its result, NaN and
+ * infinities included.
+ * In:  cache; q [rows, H, head_dim] bf16, q_stride elements from row to row
+ *      (a multiple of 8, at least H * head_dim, base 16-byte aligned); H a
+ *      multiple of kv_heads; cu_seqlens [R+1], ctx_len [R]; max_window: the
+ *      longest window (a longer one is cut: SDM_DEV_BAD_WINDOW; with
+ *      tree_mask at most tree_nodes); scale > 0; sinks >= 0; R <= 16384.
+ * Out: out [rows, H, head_dim] bf16; lse [rows, H] fp32 (may be NULL).
+ * Scores, statistics and sums are fp32; the weights exp(s - m) are rounded to
+ * bf16 for the second product (the tensor cores' operand type).
+ * ws:  sdm_workspace_size(SDM_OP_ATTEND, R, max_window, H, head_dim, rows,
+ *      kv_heads, 0).
+ */
+sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_stride, const int32_t* cu_seqlens,
+                      const int32_t* ctx_len, int R, int rows, int max_window, int H, float scale, int window,
+                      int sinks, const int32_t* tree_mask, int tree_nodes, uint16_t* out, float* lse, void* ws,
+                      size_t ws_bytes, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,18 +17,20 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsdm.so")
 
-BF16, FP32 = 0, 1
+BF16, FP32, E4M3 = 0, 1, 2
 GREEDY, SAMPLE = 0, 1
 STATIC, COMPACT, CAP_ACCEPT = 0, 1, 2
 OP_DRAFT_CHAIN, OP_DRAFT_TREE, OP_SCHEDULE, OP_PACK, OP_VERIFY, OP_VERIFY_TREE, OP_TV_LABEL, OP_DRAFT_CHAIN_RNN = range(8)
+OP_ATTEND = 8
 DEV_BAD_TOKEN, DEV_TIER_UNCAPTURED, DEV_TIMEOUT, DEV_BAD_WINDOW, DEV_CAPACITY, DEV_BAD_CLASS = 1, 2, 4, 8, 16, 32
-DEV_TIER_OVERFLOW = 64
+DEV_TIER_OVERFLOW, DEV_BAD_PAGE = 64, 128
 
 EXPORTS = ("sdm_workspace_size", "sdm_markov_prepared_size", "sdm_markov_prepare", "sdm_draft_chain",
            "sdm_draft_tree", "sdm_schedule_budget", "sdm_pack_ragged", "sdm_verify", "sdm_verify_tree",
            "sdm_verify_greedy_static", "sdm_schedule_dynamic", "sdm_tv_label", "sdm_observe", "sdm_schedule_threshold",
            "sdm_threshold_sweep", "sdm_draft_chain_rnn", "sdm_status_str", "sdm_status_of_device", "sdm_check_timeout_path",
            "sdm_draft_chain_packed", "sdm_draft_chain_front",
+           "sdm_cache_write", "sdm_cache_read", "sdm_cache_commit", "sdm_attend",
            "sdm_version")
 
 
@@ -36,8 +38,16 @@ class SdmRng(ctypes.Structure):
     _fields_ = [("seed", ctypes.c_uint64), ("cycle", ctypes.c_uint64)]
 
 
+class SdmCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("table", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 _lib = None
 _VP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_I64 = ctypes.c_int64
 
 
 def _declare(lib):
@@ -90,6 +100,16 @@ def _declare(lib):
                                  _SZ, _VP, _VP]
     lib.sdm_observe.restype = _I
     lib.sdm_observe.argtypes = [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]
+    cache = ctypes.POINTER(SdmCache)
+    lib.sdm_cache_write.restype = _I
+    lib.sdm_cache_write.argtypes = [cache, _VP, _VP, _I64, _I64, _VP, _VP, _I, _I, _VP, _VP]
+    lib.sdm_cache_read.restype = _I
+    lib.sdm_cache_read.argtypes = [cache, _VP, _VP, _I, _I, _VP, _VP, _VP, _VP]
+    lib.sdm_cache_commit.restype = _I
+    lib.sdm_cache_commit.argtypes = [cache, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP, _VP, _VP, _VP]
+    lib.sdm_attend.restype = _I
+    lib.sdm_attend.argtypes = [cache, _VP, _I64, _VP, _VP, _I, _I, _I, _I, _F, _I, _I, _VP, _I, _VP, _VP, _VP, _SZ,
+                               _VP, _VP]
     lib.sdm_verify_tree.restype = _I
     lib.sdm_verify_tree.argtypes = [_VP, _I, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _SZ, _VP, _VP]
 
@@ -509,4 +529,162 @@ def verify_tree(target, tok, parent, n_nodes, B, out=None, ws=None, dev_status=N
                                _ptr(dev_status), _stream())
     _check(st, "sdm_verify_tree")
     out["dev_status"] = dev_status
+    return out
+
+
+# ---------------------------------------------------------------------------
+class PagedCache:
+    """One layer's paged key/value cache over the caller's tensors: pools k, v
+    [pages, kv heads, page, head dim] (bf16, or float8_e4m3fn with the scale
+    exponents k_exp, v_exp [pages, kv heads, page] uint8) and the page table
+    [requests, columns] int32.  Holds the tensors and their C description."""
+
+    def __init__(self, k, v, table, k_exp=None, v_exp=None):
+        _need_cuda(k, v, table, k_exp, v_exp)
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must be [pages, kv heads, page, head dim] alike")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if not e4m3 and k.dtype != torch.bfloat16:
+            raise TypeError(f"unsupported cache dtype {k.dtype}")
+        if e4m3:
+            for e in (k_exp, v_exp):
+                if e is None or e.dtype != torch.uint8 or e.shape != k.shape[:3]:
+                    raise ValueError("an e4m3 cache needs k_exp and v_exp [pages, kv heads, page] uint8")
+        elif k_exp is not None or v_exp is not None:
+            raise ValueError("only an e4m3 cache has scale exponents")
+        if table.dim() != 2 or table.dtype != torch.int32:
+            raise ValueError("table must be [requests, columns] int32")
+        self.k, self.v, self.table, self.k_exp, self.v_exp = k, v, table, k_exp, v_exp
+        self.requests = table.shape[0]
+        self.kv_heads, self.page, self.head_dim = k.shape[1:]
+        self.c = SdmCache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
+                          v_exp.data_ptr() if e4m3 else None, table.data_ptr(), E4M3 if e4m3 else BF16, k.shape[0],
+                          self.kv_heads, self.page, self.head_dim, table.shape[1])
+        self.ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def empty(pages, kv_heads, page, head_dim, table, dtype=torch.bfloat16):
+        """A cache with pools of its own (dtype bfloat16 or float8_e4m3fn)."""
+        dev = table.device
+        pool = [torch.zeros((pages, kv_heads, page, head_dim), dtype=torch.uint8 if dtype != torch.bfloat16 else dtype,
+                            device=dev) for _ in range(2)]
+        if dtype == torch.bfloat16:
+            return PagedCache(*pool, table)
+        exps = [torch.full((pages, kv_heads, page), 127, dtype=torch.uint8, device=dev) for _ in range(2)]
+        return PagedCache(*(x.view(dtype) for x in pool), table, *exps)
+
+
+def _need_rows(what, x, heads, head_dim):
+    """Packed rows [rows, heads, head dim] bf16, contiguous within a row (a
+    slice of a fused projection's output will do); returns the row stride."""
+    if x.dtype != torch.bfloat16 or not x.is_cuda:
+        raise TypeError(f"{what} must be a bf16 CUDA tensor")
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+        raise ValueError(f"{what} must be [rows, {heads}, {head_dim}]")
+    if st[2] != 1 or (heads > 1 and st[1] != head_dim):
+        raise ValueError(f"{what} must be contiguous within a row")
+    return st[0] if shape[0] > 1 else max(st[0], heads * head_dim)
+
+
+def _need_i32(what, x, n):
+    if x.dtype != torch.int32 or x.numel() < n or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 CUDA tensor of at least {n} entries")
+    return x.data_ptr()
+
+
+def cache_write(cache, k, v, cu_seqlens, ctx_len, dev_status=None):
+    """The windows' keys and values [rows, kv heads, head dim] into their slots
+    (tokens ctx_len[i], ctx_len[i] + 1, ...), quantised if the cache is e4m3."""
+    R = cache.requests
+    ks = _need_rows("k", k, cache.kv_heads, cache.head_dim)
+    vs = _need_rows("v", v, cache.kv_heads, cache.head_dim)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    dev_status = new_status(k.device) if dev_status is None else dev_status
+    st = lib().sdm_cache_write(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, _need_i32("cu_seqlens", cu_seqlens, R + 1),
+                               _need_i32("ctx_len", ctx_len, R), R, k.shape[0], dev_status.data_ptr(),
+                               torch.cuda.current_stream().cuda_stream)
+    _check(st, "sdm_cache_write")
+    return dev_status
+
+
+def cache_read(cache, cu_rows, rows, first=None, out=None, dev_status=None):
+    """Tokens first[i], first[i] + 1, ... (first None: from 0) of every request
+    back as bf16 rows cu_rows[i] .. cu_rows[i+1] - 1 of out["k"], out["v"]."""
+    R = cache.requests
+    if out is None:
+        out = {n: torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.k.device)
+               for n in ("k", "v")}
+    for n in ("k", "v"):
+        if out[n].shape != (rows, cache.kv_heads, cache.head_dim) or not out[n].is_contiguous() \
+                or out[n].dtype != torch.bfloat16:
+            raise ValueError("out must hold contiguous bf16 [rows, kv heads, head dim] tensors")
+    dev_status = new_status(cache.k.device) if dev_status is None else dev_status
+    st = lib().sdm_cache_read(cache.ref, _need_i32("cu_rows", cu_rows, R + 1),
+                              None if first is None else _need_i32("first", first, R), R, rows, out["k"].data_ptr(),
+                              out["v"].data_ptr(), dev_status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    _check(st, "sdm_cache_read")
+    return out
+
+
+def cache_commit(cache, tok, parent, n_nodes, out_tok, accept, ctx_len, out=None, dev_status=None):
+    """Moves a verified tree's accepted path (verify_tree's out_tok, accept) to
+    follow the committed tokens; returns the path's slots and the new lengths."""
+    R, S = tok.shape
+    B = out_tok.shape[1] - 1
+    if R != cache.requests:
+        raise ValueError("tok must have one row per request of the cache")
+    if out is None:
+        out = dict(path=torch.empty((R, B + 1), dtype=torch.int32, device=tok.device),
+                   length=torch.empty((R,), dtype=torch.int32, device=tok.device))
+    dev_status = new_status(tok.device) if dev_status is None else dev_status
+    st = lib().sdm_cache_commit(cache.ref, _need_i32("tok", tok, R * S), _need_i32("parent", parent, R * S),
+                                _need_i32("n_nodes", n_nodes, R), _need_i32("out_tok", out_tok, R * (B + 1)),
+                                _need_i32("accept", accept, R), _need_i32("ctx_len", ctx_len, R), R, S - 1, B,
+                                _need_i32("path", out["path"], R * (B + 1)), _need_i32("length", out["length"], R),
+                                dev_status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    _check(st, "sdm_cache_commit")
+    return out
+
+
+def attend_workspace(cache, rows, max_window, H):
+    return workspace(OP_ATTEND, cache.requests, max_window, H, cache.head_dim, rows, cache.kv_heads,
+                     device=cache.k.device)
+
+
+def attend(cache, q, cu_seqlens, ctx_len, max_window, scale=None, window=0, sinks=0, tree_mask=None, lse=False,
+           out=None, ws=None, dev_status=None):
+    """Attention of every window row q [rows, H, head dim] over its request's
+    cached tokens: causal, or by a draft tree's ancestor mask (draft_tree's
+    mask); window > 0 limits it to that many last tokens and the first
+    `sinks`.  Returns out (and the log-sum-exp if lse)."""
+    R, D = cache.requests, cache.head_dim
+    rows, H = q.shape[0], q.shape[1]
+    qs = _need_rows("q", q, H, D)
+    if H % cache.kv_heads:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    if out is None:
+        out = dict(out=torch.empty((rows, H, D), dtype=torch.bfloat16, device=q.device))
+        if lse:
+            out["lse"] = torch.empty((rows, H), dtype=torch.float32, device=q.device)
+    o, z = out["out"], out.get("lse")
+    if o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous():
+        raise ValueError("out must be contiguous bf16 of q's shape")
+    if z is not None and (z.shape != (rows, H) or z.dtype != torch.float32 or not z.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [rows, H]")
+    nodes, mask = 0, None
+    if tree_mask is not None:
+        nodes = tree_mask.shape[1]
+        mask = _need_i32("tree_mask", tree_mask, R * nodes * ((nodes + 31) // 32))
+        if tree_mask.shape != (R, nodes, (nodes + 31) // 32):
+            raise ValueError("tree_mask must be [requests, nodes, ceil(nodes / 32)]")
+    ws = attend_workspace(cache, rows, max_window, H) if ws is None else ws
+    dev_status = new_status(q.device) if dev_status is None else dev_status
+    st = lib().sdm_attend(cache.ref, q.data_ptr(), qs, _need_i32("cu_seqlens", cu_seqlens, R + 1),
+                          _need_i32("ctx_len", ctx_len, R), R, rows, max_window, H,
+                          D ** -0.5 if scale is None else scale, window, sinks, mask, nodes, o.data_ptr(),
+                          None if z is None else z.data_ptr(), ws.data_ptr(), ws.numel(), dev_status.data_ptr(),
+                          torch.cuda.current_stream().cuda_stream)
+    _check(st, "sdm_attend")
     return out

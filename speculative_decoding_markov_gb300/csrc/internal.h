@@ -455,4 +455,70 @@ cudaError_t launch_schedule_threshold(const float* conf, int R, int gamma, float
 cudaError_t launch_threshold_sweep(const float* conf, const int32_t* ceiling, int R, int gamma, const float* taus,
                                    int K, int32_t* drafts, int32_t* accepted, double* expected, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Paged key/value cache (cache.cu) and attention over it (attend.cu)
+// ---------------------------------------------------------------------------
+struct CacheView {
+    uint8_t* k;            // [n_pages, heads, page, D] bf16 or e4m3
+    uint8_t* v;
+    uint8_t* k_exp;        // [n_pages, heads, page] exponent + 127 (e4m3)
+    uint8_t* v_exp;
+    const int32_t* table;  // [R, max_pages]
+    int e4m3, n_pages, heads, page_shift, D, max_pages;
+};
+
+struct CacheWriteParams {
+    CacheView c;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t k_stride, v_stride;   // elements
+    const int32_t* cu;
+    const int32_t* ctx;
+    int R, rows;
+    int32_t* dev_status;
+};
+struct CacheReadParams {
+    CacheView c;
+    const int32_t* cu;
+    const int32_t* first;   // or NULL
+    uint16_t* k_out;
+    uint16_t* v_out;
+    int R, rows;
+    int32_t* dev_status;
+};
+struct CacheCommitParams {
+    CacheView c;
+    const int32_t* tok;
+    const int32_t* parent;
+    const int32_t* n_nodes;
+    const int32_t* out_tok;
+    const int32_t* accept;
+    const int32_t* ctx;
+    int32_t* path;
+    int32_t* length;   // or NULL
+    int R, N, B;
+    int32_t* dev_status;
+};
+cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheReadParams& p, cudaStream_t s);
+cudaError_t launch_cache_commit(const CacheCommitParams& p, cudaStream_t s);
+
+struct AttendParams {
+    CacheView c;
+    const uint16_t* q;
+    int64_t q_stride;     // elements
+    const int32_t* cu;
+    const int32_t* ctx;
+    int R, rows, max_window, H, group;   // group = query heads per kv head
+    float scale;
+    int window, sinks;
+    const uint32_t* tree;   // [R, nodes, words] or NULL
+    int nodes, words;
+    uint16_t* out;
+    float* lse;             // or NULL
+    int32_t* dev_status;
+};
+size_t attend_workspace(int R, int max_window, int H, int D, int rows, int kv_heads);
+cudaError_t launch_attend(const AttendParams& p, void* ws, cudaStream_t s);
+
 }  // namespace sdm
