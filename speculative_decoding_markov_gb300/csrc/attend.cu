@@ -1,231 +1,1231 @@
-// attend.cu - attention of packed windows over a paged key/value cache.
+// attend.cu - attention of packed windows over a paged key/value cache on the
+// tcgen05 tensor cores.
 //
-// One CTA per (request, kv head, 64 rows), a row being one query head of one
-// window token (the query heads that share a kv head stand side by side, so
-// a tile of keys serves them all).  Tiles of 64 keys pass through shared
-// memory as fp32 with the running maximum and sum of the softmax per row:
-//     m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
-//     o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j,   out = o / l.
+// Mathematics.  A row is one query head of one window token; the rows of a
+// request that share a kv head (its query heads side by side, token by token)
+// share their keys, so they are packed into the 128 lanes of one tile.  Per
+// tile of 128 keys, with s = q k^T and x = s * scale * log2 e:
+//     m' = max(m, max_j x_j)           l' = l 2^(m - m') + sum_j 2^(x_j - m')
+//     o' = o 2^(m - m') + sum_j bf16(2^(x_j - m')) v_j     out = o / l
+// m is only moved when a tile exceeds it by more than 2^8 (kLazy): any m near
+// the maximum serves, and o, which lives in tensor memory, is then rescaled
+// in the first tiles of a row and hardly ever after.
+//
+// Work.  A block is up to 256 rows (two 128-row sub-tiles) of one request and
+// kv head.  A block of more than 128 rows runs in `pair` form: both softmax
+// warpgroups see every key tile, each for its own 128 rows.  A smaller one
+// runs in `stream` form: the warpgroups take alternate key tiles of the same
+// rows and their (m, l, o) are joined at its end.  The key tiles of all blocks
+// laid end to end are cut into equal shares, one per CTA (one CTA per SM,
+// persistent): a long context is split over as many SMs as it fills, many
+// short ones share an SM, and no schedule is kept between calls.  Blocks that
+// a cut splits leave (m, l, o) in the workspace and attend_merge_kernel joins
+// them in the order of the keys, so results do not depend on timing.
+//
+// Pipeline of a CTA: a producer warp brings K and V tiles page by page with
+// TMA into a ring; (e4m3: four warps turn codes into bf16, exactly, the scale
+// included, in a second ring); one warp issues S = Q K^T and O += P V; eight
+// warps do the softmax, S from tensor memory to registers and P back over S;
+// two warps gather Q.  Each warpgroup's S, P and O are its own, so one's
+// softmax runs beside the other's products.
+//
+// What a row does not see does not reach it: scores are replaced, not added
+// to; values of a tile that some row sees only in part are cleared of NaN and
+// infinities in shared memory, and the rows that do see one get its product
+// from add_nonfinite() at the end.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace sdm {
 namespace {
 
-constexpr int kRows = 64;
-constexpr int kKeys = 64;
-constexpr int kThreads = 256;
+constexpr int kTile = 128;            // keys per tile, rows per sub-tile
+constexpr int kBlockRows = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;
+// The weights enter the second product as bf16.  Where a row sees few keys,
+// nothing averages that rounding out, so the remainder p - bf16(p) is
+// multiplied too: as rows of the same product where the block leaves half of
+// the 128 lanes free (row r in lane r of its 16, the remainder 16 lanes on),
+// by a second product in blocks of at most kFineTiles key tiles.
+constexpr int kStackRows = 64;
+constexpr int kFineTiles = 9;
+constexpr int kTmemCols = 512;        // S0, S1, O0, O1 at columns 0, 128, 256, 384; P over S
 
-template <int D>
-struct Smem {
-    float q[kRows][D + 4];
-    float kv[kKeys][D + 4];
-    float p[kRows][kKeys + 4];
-    float m[kRows], l[kRows], corr[kRows];
-    int page[kKeys];
+template <int D, bool E4M3>
+struct Cfg {
+    static constexpr int kThreads = E4M3 ? 512 : 384;
+    static constexpr int kHalves = D / 64;                   // 128-byte column blocks of a bf16 tile
+    static constexpr int kQBytes = kTile * D * 2;            // one 128-row sub-tile
+    static constexpr int kTileBytes = kTile * D * 2;         // one bf16 K or V tile
+    static constexpr int kSlots = (E4M3 ? 96 : 160) * 1024 / kTileBytes;
+    static constexpr int kRawBytes = kTile * D;              // e4m3 codes of a tile
+    static constexpr int kRawSlots = E4M3 ? 64 * 1024 / kRawBytes : 0;
+    static constexpr int kRing = 2 * kQBytes;
+    static constexpr int kRaw = kRing + kSlots * kTileBytes;
+    static constexpr int kExps = kRaw + kRawSlots * kRawBytes;
+    static constexpr int kXch = kExps + kRawSlots * kTile;   // (m, l) of both warpgroups' rows
+    static constexpr int kBars = kXch + 2 * kTile * 8;
+    static constexpr int kNumBars = 4 * kSlots + 2 * kRawSlots + 2 + 6 + 3;
+    static constexpr int kMisc = kBars + kNumBars * 8;
+    static constexpr int kTotal = kMisc + 96;
+    // registers of a thread: the softmax warpgroups', the others' (together
+    // the launch's own: 3 x 168 and 4 x 128)
+    static constexpr int kRegsSoft = E4M3 ? 184 : 208;
+    static constexpr int kRegsRest = E4M3 ? 72 : 88;
+    static_assert(kTotal <= 232448, "shared memory");
+    static_assert(E4M3 ? 2 * kRegsSoft + 2 * kRegsRest == 4 * 128 : 2 * kRegsSoft + kRegsRest == 3 * 168, "registers");
 };
 
-// Whether the row at window position w (position pos) sees token j.
-__device__ __forceinline__ bool sees(const AttendParams& p, const Window& w, const uint32_t* bits, int pos, int j) {
-    if (p.tree && j >= w.ctx) {
-        const int c = j - w.ctx;
-        return c < w.n && ((__ldg(bits + (c >> 5)) >> (c & 31)) & 1u);
-    }
-    return j <= pos && (p.window <= 0 || pos - j < p.window || j < p.sinks);
+struct Share {             // per CTA, for the merge: the block its last segment starts, and how its first goes on
+    int rows;              // rows of the block that its last segment starts and does not finish; 0: none
+    int row0, m0, hk;      // that block: first packed row of its window, first row, kv head
+    int head;              // its first segment continues a block: 0 no, 1 and finishes it, 2 and does not; 3: no work
+    int pad[3];
+};
+
+struct Scratch {
+    Share* share;          // [grid]
+    float2* ml;            // [2 grid][cap]: (m, l) of split blocks' rows
+    float* o;              // [2 grid][cap][D]
+    int cap;               // rows per slot
+};
+
+// ---------------------------------------------------------------------------
+// Geometry: a request's blocks, a block's key tiles, a CTA's share of them
+// ---------------------------------------------------------------------------
+struct Geom {
+    int m0, M;             // first row and rows of the block
+    int p0, p1;            // window positions of its first and last row
+    int ns, lo, n;         // tiles 0 .. ns - 1 hold the sinks, tiles ns .. n - 1 are key tiles lo, lo + 1, ...
+    int weight;            // cost of a tile: the sub-tiles it is multiplied with
+    // how the weights' rounding to bf16 is made up for (kFineTiles)
+    bool stacked;          // M <= 64: their remainders are 64 more rows of the same product
+    bool twice;            // few keys: their remainders are multiplied in a second product
+};
+
+__device__ __forceinline__ int blocks_of(const AttendParams& p, const Window& w) {
+    return (w.n * p.group + kBlockRows - 1) / kBlockRows;
 }
 
-template <int D, bool E4M3>
-__device__ __forceinline__ void load_rows(const AttendParams& p, float (*dst)[D + 4], const int* page, bool v, int h,
-                                          int j0, int end) {
-    for (int t = threadIdx.x; t < kKeys * (D / 8); t += kThreads) {
-        const int r = t / (D / 8), c = t % (D / 8);
-        float f[8] = {};
-        if (j0 + r < end) {
-            const size_t row = pool_row(p.c, page[r], j0 + r) + (static_cast<size_t>(h) << p.c.page_shift);
-            if constexpr (E4M3) {
-                const float s = pow2f(static_cast<int>((v ? p.c.v_exp : p.c.k_exp)[row]) - 127);
-                const uint2 x = reinterpret_cast<const uint2*>((v ? p.c.v : p.c.k) + row * D)[c];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 y = f16x2_to_f32x2(
-                        e4m3x2_to_f16x2(static_cast<uint16_t>((k < 2 ? x.x : x.y) >> (16 * (k & 1)))));
-                    f[2 * k] = y.x * s;
-                    f[2 * k + 1] = y.y * s;
-                }
-            } else {
-                const uint4 x = reinterpret_cast<const uint4*>((v ? p.c.v : p.c.k) + row * D * 2)[c];
-                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    f[2 * k] = bf16_bits_to_float(u[k] & 0xffffu);
-                    f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) dst[r][c * 8 + k] = f[k];
+__device__ __forceinline__ Geom geom_of(const AttendParams& p, const Window& w, int b) {
+    Geom g;
+    g.m0 = b * kBlockRows;
+    g.M = min(kBlockRows, w.n * p.group - g.m0);
+    g.p0 = g.m0 / p.group;
+    g.p1 = (g.m0 + g.M - 1) / p.group;
+    const int end = p.tree ? w.ctx + w.n : w.ctx + g.p1 + 1;
+    g.ns = g.lo = 0;
+    if (p.window > 0) {
+        g.lo = max(0, w.ctx + (p.tree ? 0 : g.p0) + 1 - p.window) / kTile;
+        g.ns = min((p.sinks + kTile - 1) / kTile, g.lo);
     }
+    g.n = g.ns + (end + kTile - 1) / kTile - g.lo;
+    g.weight = g.M > kTile ? 2 : 1;
+    g.stacked = g.M <= kStackRows;
+    g.twice = !g.stacked && g.n <= kFineTiles;
+    return g;
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    Smem<D>& s = *reinterpret_cast<Smem<D>*>(raw);
-    pdl_wait();
-    pdl_trigger();
-    const int i = blockIdx.z, h = blockIdx.y;
-    const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, table_tokens(p.c));
-    if (w.bad && threadIdx.x == 0) set_status(p.dev_status, w.bad);
-    const int M = w.n * p.group, m0 = blockIdx.x * kRows;
-    if (m0 >= M) return;
-    const int m1 = min(M, m0 + kRows);
-    for (int t = threadIdx.x; t < kRows * D; t += kThreads) {
-        const int r = t / D, d = t % D, m = m0 + r;
-        float x = 0.f;
-        if (m < M) {
-            const int wp = m / p.group, g = m % p.group;
-            x = bf16_bits_to_float(p.q[(w.row0 + wp) * p.q_stride + static_cast<size_t>(h * p.group + g) * D + d]);
-        }
-        s.q[r][d] = x;
+__device__ __forceinline__ int tile_key(const Geom& g, int t) { return (t < g.ns ? t : g.lo + t - g.ns) * kTile; }
+
+// Whether some row at window positions p0 .. p1 does not see all of the tile's keys.
+__device__ __forceinline__ bool tile_mixed(const AttendParams& p, const Window& w, int p0, int p1, int key0) {
+    const int last = key0 + kTile - 1;
+    if (last > (p.tree ? w.ctx - 1 : w.ctx + p0)) return true;
+    if (p.window <= 0 || last < p.sinks) return false;
+    return key0 <= w.ctx + (p.tree ? w.n - 1 : p1) - p.window;
+}
+
+// Whether the tile's values are cleared of NaN and infinities: a row may not
+// see them, or a remainder (of either sign) may meet an infinity.
+__device__ __forceinline__ bool tile_cleaned(const AttendParams& p, const Window& w, const Geom& g, int key0) {
+    return g.twice || tile_mixed(p, w, g.p0, g.p1, key0);
+}
+
+struct Start {
+    unsigned long long us, u0, u1;   // unit at which the first block begins, the CTA's units [u0, u1)
+    int i, b, hk;
+};
+
+// Walks the blocks of a CTA's share.
+struct Walk {
+    unsigned long long us, u0, u1;
+    int i, b, hk;
+    int have;              // request whose window (and block whose geometry) is loaded
+    int have_b;
+    Window w;
+    Geom g;
+    int t0, t1;            // the share's key tiles of the current block
+
+    __device__ __forceinline__ void init(const Start& s) {
+        us = s.us;
+        u0 = s.u0;
+        u1 = s.u1;
+        i = s.i;
+        b = s.b;
+        hk = s.hk - 1;
+        have = have_b = -1;
     }
-    if (threadIdx.x < kRows) {
-        s.m[threadIdx.x] = -INFINITY;
-        s.l[threadIdx.x] = 0.f;
+
+    __device__ __forceinline__ bool next(const AttendParams& p) {
+        if (have >= 0) us += static_cast<unsigned long long>(g.n) * g.weight;
+        for (;;) {
+            if (us >= u1) return false;
+            if (++hk >= p.c.heads) {
+                hk = 0;
+                ++b;
+            }
+            for (;;) {
+                if (i >= p.R) return false;
+                if (have != i) {
+                    w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, table_tokens(p.c));
+                    have = i;
+                    have_b = -1;
+                }
+                if (b < blocks_of(p, w)) break;
+                ++i;
+                b = hk = 0;
+            }
+            if (have_b != b) {
+                g = geom_of(p, w, b);
+                have_b = b;
+            }
+            const unsigned wt = g.weight;
+            t0 = us < u0 ? static_cast<int>((u0 - us + wt - 1) / wt) : 0;
+            const unsigned long long left = (u1 - us + wt - 1) / wt;
+            t1 = left < static_cast<unsigned long long>(g.n) ? static_cast<int>(left) : g.n;
+            if (t0 < t1) return true;
+            us += static_cast<unsigned long long>(g.n) * wt;
+        }
     }
-    // thread (ty, tx): rows ty * 4 .. + 3; keys tx + 16 c of the scores; dims tx * (D / 16) .. of the output
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float o[4][D / 16] = {};
-    const int last = (m1 - 1) / p.group, first = m0 / p.group;
-    const int end = p.tree ? w.ctx + w.n : w.ctx + last + 1;
-    const int lo = p.window > 0 ? max(0, w.ctx + (p.tree ? 0 : first) - p.window + 1) : 0;
-    const float sl = p.scale * kLog2e;
-    for (int j0 = 0; j0 < end; j0 += kKeys) {
-        if (j0 + kKeys <= lo && j0 >= p.sinks) continue;
-        __syncthreads();
-        if (threadIdx.x < kKeys) {
-            int pg = j0 + threadIdx.x < end ? page_of(p.c, i, j0 + threadIdx.x) : 0;
-            if (pg < 0) {
-                set_status(p.dev_status, SDM_DEV_BAD_PAGE);
-                pg = 0;
+};
+
+__device__ __forceinline__ unsigned long long shfl_up64(unsigned long long v, int d) {
+    return __shfl_up_sync(0xffffffffu, v, d);
+}
+
+// This CTA's share of the units (key tiles times their weight) of all blocks,
+// and where it starts.  cost: shared memory for R entries.
+template <int THREADS>
+__device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* cost, Start* start,
+                                     unsigned long long* wsum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = THREADS / 32;
+    const long long tokens = table_tokens(p.c);
+    const int most = (p.max_window * p.group + kBlockRows - 1) / kBlockRows;
+    if (most <= 4) {
+        for (int i = tid; i < p.R; i += THREADS) {
+            const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
+            if (w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
+            unsigned long long c = 0;
+            for (int b = 0; b < blocks_of(p, w); ++b) {
+                const Geom g = geom_of(p, w, b);
+                c += static_cast<unsigned long long>(g.n) * g.weight;
             }
-            s.page[threadIdx.x] = pg;
+            cost[i] = c * p.c.heads;
         }
-        __syncthreads();
-        load_rows<D, E4M3>(p, s.kv, s.page, false, h, j0, end);
-        __syncthreads();
-        float x[4][4] = {};
-        for (int d = 0; d < D; ++d) {
-            float a[4], b[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) a[r] = s.q[ty * 4 + r][d];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) b[c] = s.kv[tx + 16 * c][d];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) x[r][c] = fmaf(a[r], b[c], x[r][c]);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int m = m0 + ty * 4 + r;
-            const int wp = m / p.group;
-            const uint32_t* bits = p.tree ? p.tree + (static_cast<size_t>(i) * p.nodes + min(wp, w.n - 1)) * p.words : nullptr;
-            int pos = w.ctx + wp;
-            if (p.tree) {
-                int n = 0;
-                for (int k = 0; k < p.words; ++k) n += __popc(__ldg(bits + k));
-                pos = w.ctx + max(0, n - 1);
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int j = j0 + tx + 16 * c;
-                x[r][c] = (m < M && j < end && sees(p, w, bits, pos, j)) ? x[r][c] * sl : -INFINITY;
-                top = fmaxf(top, x[r][c]);
+    } else {
+        for (int i = warp; i < p.R; i += kWarps) {
+            const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
+            if (w.bad && blockIdx.x == 0 && lane == 0) set_status(p.dev_status, w.bad);
+            unsigned long long c = 0;
+            for (int b = lane; b < blocks_of(p, w); b += 32) {
+                const Geom g = geom_of(p, w, b);
+                c += static_cast<unsigned long long>(g.n) * g.weight;
             }
 #pragma unroll
-            for (int k = 8; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-            const float m_old = s.m[ty * 4 + r];
-            const float m_new = fmaxf(m_old, top);
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
-            float sum = 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float e = exp2f(x[r][c] - ref);
-                s.p[ty * 4 + r][tx + 16 * c] = e;
-                sum += e;
-            }
-#pragma unroll
-            for (int k = 8; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-            __syncwarp();
-            const float corr = exp2f(m_old - ref);
-            if (tx == 0) {
-                s.m[ty * 4 + r] = m_new;
-                s.l[ty * 4 + r] = s.l[ty * 4 + r] * corr + sum;
-                s.corr[ty * 4 + r] = corr;
-            }
-        }
-        __syncthreads();
-        load_rows<D, E4M3>(p, s.kv, s.page, true, h, j0, end);
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float corr = s.corr[ty * 4 + r];
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d) o[r][d] *= corr;
-        }
-        for (int j = 0; j < kKeys; ++j) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float e = s.p[ty * 4 + r][j];
-                if (e == 0.f) continue;   // unseen: its value may be anything
-#pragma unroll
-                for (int d = 0; d < D / 16; ++d) o[r][d] = fmaf(e, s.kv[j][tx + 16 * d], o[r][d]);
-            }
+            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            if (lane == 0) cost[i] = c * p.c.heads;
         }
     }
     __syncthreads();
+    const int per = (p.R + THREADS - 1) / THREADS;
+    const int a = min(p.R, tid * per), e = min(p.R, a + per);
+    unsigned long long mine = 0;
+    for (int i = a; i < e; ++i) mine += cost[i];
+    unsigned long long incl = mine;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int m = m0 + ty * 4 + r;
-        if (m >= M) continue;
-        const int wp = m / p.group, g = m % p.group;
-        const size_t at = static_cast<size_t>(w.row0 + wp) * p.H + h * p.group + g;
-        const float l = s.l[ty * 4 + r];
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-            p.out[at * D + tx + 16 * d] =
-                static_cast<uint16_t>(f32x2_to_bf16x2(l == 0.f ? 0.f : o[r][d] / l, 0.f) & 0xffffu);
-        if (tx == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : s.m[ty * 4 + r] * kLn2 + logf(l);
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = shfl_up64(incl, o);
+        if (lane >= o) incl += v;
     }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    unsigned long long base = incl - mine, total = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+        const unsigned long long v = wsum[k];
+        if (k < warp) base += v;
+        total += v;
+    }
+    const unsigned long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (tid == 0) {
+        start->u0 = u0;
+        start->u1 = u1;
+    }
+    if (u0 < u1 && base <= u0 && u0 < base + mine) {
+        int i = a;
+        for (; i < e - 1 && u0 >= base + cost[i]; ++i) base += cost[i];
+        start->i = i;
+        start->us = base;
+    }
+    __syncthreads();
+    if (warp == 0 && u0 < u1) {
+        const int i = start->i;
+        unsigned long long us = start->us;
+        const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
+        const int nb = blocks_of(p, w);
+        int found = -1;
+        unsigned long long step = 1;
+        for (int b0 = 0; b0 < nb && found < 0; b0 += 32) {
+            const int b = b0 + lane;
+            unsigned long long one = 0;
+            if (b < nb) {
+                const Geom g = geom_of(p, w, b);
+                one = static_cast<unsigned long long>(g.n) * g.weight;
+            }
+            unsigned long long sum = one * p.c.heads;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long v = shfl_up64(sum, o);
+                if (lane >= o) sum += v;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, us + sum > u0);
+            const int at = hit ? __ffs(hit) - 1 : 31;
+            const unsigned long long before = __shfl_sync(0xffffffffu, sum - one * p.c.heads, at);
+            const unsigned long long all = __shfl_sync(0xffffffffu, sum, 31);
+            step = __shfl_sync(0xffffffffu, one, at);
+            if (hit) {
+                found = b0 + at;
+                us += before;
+            } else {
+                us += all;
+            }
+        }
+        const unsigned long long k = step > 0 ? (u0 - us) / step : 0;
+        if (lane == 0) {
+            start->b = max(found, 0);
+            start->hk = static_cast<int>(k);
+            start->us = us + k * step;
+        }
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// Barriers: every wait is bounded; a wait that runs out records
+// SDM_DEV_TIMEOUT and the role winds down.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool wait_or_fail(const AttendParams& p, uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_wait(bar, parity))) return true;   // one answer for the whole warp
+    set_status(p.dev_status, SDM_DEV_TIMEOUT);
+    return false;
+}
+
+template <int SLOTS, int RAW>
+struct Bars {
+    // a tile arrives at full, one to be cleaned at dirty and then, cleaned, at
+    // clean: whoever waits on one of them waits for all its phases
+    uint64_t full[SLOTS], empty[SLOTS], dirty[SLOTS], clean[SLOTS];
+    uint64_t raw_full[RAW > 0 ? RAW : 1], raw_empty[RAW > 0 ? RAW : 1];
+    uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], xch, xdone, drain;
+};
+
+// Nonzero if one of the two bf16 in x is an infinity or NaN (the exponent
+// field 0xff plus one carries into the sign's place).
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// 32 bits: which of the keys base .. base + 31 a row sees.
+struct RowView {
+    int pos, lo;            // keys <= pos (tree: < ctx) and >= lo or < sinks
+    int sinks;
+    const uint32_t* bits;   // tree: the row's mask words
+    int ctx, n, words;
+};
+
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+__device__ __forceinline__ uint32_t seen32(const RowView& r, int base) {
+    uint32_t m = below(r.pos + 1 - base) & (~below(r.lo - base) | below(r.sinks - base));
+    if (r.bits) {
+        const int o = base - r.ctx;
+        if (o > -32 && o < r.n) {
+            const int k = o >> 5, sh = o & 31;
+            const uint32_t a = k >= 0 && k < r.words ? __ldg(r.bits + k) : 0u;
+            const uint32_t b = k + 1 < r.words ? __ldg(r.bits + k + 1) : 0u;
+            m |= __funnelshift_r(a, b, sh) & below(r.n - o);
+        }
+    }
+    return m;
+}
+
+__device__ __forceinline__ RowView row_view(const AttendParams& p, const Window& w, int i, int wp) {
+    RowView r;
+    r.ctx = w.ctx;
+    r.n = w.n;
+    r.words = p.words;
+    r.sinks = p.window > 0 ? p.sinks : 0;
+    r.bits = nullptr;
+    int pos = w.ctx + wp;
+    r.pos = pos;
+    if (p.tree) {
+        r.bits = p.tree + (static_cast<size_t>(i) * p.nodes + wp) * p.words;
+        int n = 0;
+        for (int k = 0; k < p.words; ++k) n += __popc(__ldg(r.bits + k));
+        pos = w.ctx + max(0, n - 1);
+        r.pos = w.ctx - 1;
+    }
+    r.lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    return r;
+}
+
+// Adds weight * value for the infinite and NaN values that a row sees in its
+// block's partly seen tiles (where shared memory holds zeros for them), to 32
+// of its output columns.  Rare: one thread per row, straight from the cache.
+template <int D, bool E4M3>
+__device__ __noinline__ void add_nonfinite(const AttendParams& p, const Window& w, const Geom& g, int i, int hk,
+                                           int t0, int t1, int m, float m_ref, int col0, float* o) {
+    const int wp = m / p.group;
+    const RowView r = row_view(p, w, i, wp);
+    const uint16_t* q = p.q + (w.row0 + wp) * p.q_stride + static_cast<size_t>(hk * p.group + m % p.group) * D;
+    for (int t = t0; t < t1; ++t) {
+        const int key0 = tile_key(g, t);
+        if (!tile_cleaned(p, w, g, key0)) continue;
+        for (int j = key0; j < min(key0 + kTile, w.ctx + w.n); ++j) {
+            if (!((seen32(r, j & ~31) >> (j & 31)) & 1u)) continue;
+            const int pg = max(page_of(p.c, i, j), 0);
+            const size_t row = pool_row(p.c, pg, j) + (static_cast<size_t>(hk) << p.c.page_shift);
+            float weight = -1.0f;
+            for (int c = 0; c < 32; ++c) {
+                float v;
+                if constexpr (E4M3) {
+                    v = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.v[row * D + col0 + c])).x;
+                } else {
+                    v = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p.c.v)[row * D + col0 + c]);
+                }
+                if (fabsf(v) < INFINITY) continue;
+                if (weight < 0.f) {
+                    float s = 0.f;
+                    for (int d = 0; d < D; ++d) {
+                        float k;
+                        if constexpr (E4M3) {
+                            k = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.k[row * D + d])).x *
+                                pow2f(static_cast<int>(p.c.k_exp[row]) - 127);
+                        } else {
+                            k = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p.c.k)[row * D + d]);
+                        }
+                        s = fmaf(bf16_bits_to_float(q[d]), k, s);
+                    }
+                    weight = fast_exp2(s * p.scale * kLog2e - m_ref);
+                }
+                o[c] += weight * v;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void ffma2(float& x, float& y, float a, float b) {   // (x, y) = (x, y) * a + b
+    asm("{\n\t.reg .b64 v, s, t;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %3};\n\t"
+        "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
+__device__ __forceinline__ void fadd2(float& x, float& y, float a, float b) {   // (x, y) += (a, b)
+    asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tadd.rn.f32x2 v, v, s;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ AttendParams p, const __grid_constant__ Scratch ws) {
+    using C = Cfg<D, E4M3>;
+    using B = Bars<C::kSlots, C::kRawSlots>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    static_assert(sizeof(B) <= (C::kNumBars + 2) * 8, "barriers");
+    B& bar = *reinterpret_cast<B*>(smem + C::kBars);
+    float2* xch = reinterpret_cast<float2*>(smem + C::kXch);
+    Start* start = reinterpret_cast<Start*>(smem + C::kXch);               // only until the roles begin
+    unsigned long long* wsum = reinterpret_cast<unsigned long long*>(smem + C::kXch + 64);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc + 16);
+    // [16]: count + 1 of the last block (16 apart) in whose partly seen tiles a value was not finite
+    volatile int* nonfin = reinterpret_cast<volatile int*>(smem + C::kMisc + 24);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int k = 0; k < C::kSlots; ++k) {
+            mbar_init(&bar.full[k], E4M3 ? 4 : 1);
+            mbar_init(&bar.empty[k], 1);
+            mbar_init(&bar.dirty[k], 1);
+            mbar_init(&bar.clean[k], 2);
+        }
+        for (int k = 0; k < C::kRawSlots; ++k) {
+            mbar_init(&bar.raw_full[k], 1);
+            mbar_init(&bar.raw_empty[k], 4);
+        }
+        mbar_init(&bar.q_full, 2);
+        mbar_init(&bar.q_empty, 1);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&bar.s_full[k], 1);
+            mbar_init(&bar.p_ready[k], 4);
+            mbar_init(&bar.o_full[k], 1);
+        }
+        mbar_init(&bar.xch, 8);
+        mbar_init(&bar.xdone, 8);
+        mbar_init(&bar.drain, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        for (int k = 0; k < 16; ++k) nonfin[k] = 0;
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    plan<C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
+    const Start st = *start;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const bool work = st.u0 < st.u1;
+    if (!work && tid == 0) {
+        Share s = {};
+        s.head = 3;
+        ws.share[blockIdx.x] = s;
+    }
+
+    if (warp < 8) {
+        // ------------------------------------------------------------------
+        // softmax warpgroups
+        // ------------------------------------------------------------------
+        set_regs_up<C::kRegsSoft>();
+        const int wg = warp >> 2, row = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + wg * 128;
+        const uint32_t tO0 = tmem + lanes + 256, tO1 = tO0 + 128;
+        const uint32_t tO = wg ? tO1 : tO0;
+        const float sl = p.scale * kLog2e;
+        Walk k;
+        k.init(st);
+        uint32_t n_s = 0, n_o[2] = {0, 0}, n_x = 0;   // phases of s_full, o_full, xch / xdone
+        bool ok = true, x_open = false;
+        Share share = {};
+        share.head = 3;
+        int blk = 0;
+        while (ok && work && k.next(p)) {
+            const bool pair = k.g.weight == 2;
+            const int n_tiles = k.t1 - k.t0;
+            const int mine = pair ? n_tiles : (n_tiles + 1 - wg) >> 1;
+            const bool stacked = k.g.stacked, twice = k.g.twice;
+            const bool rest = stacked && (lane & 16);             // this lane holds the weights' remainders
+            const int r = stacked ? (row >> 5) * 16 + (row & 15) : pair ? wg * kTile + row : row;   // row of the block
+            const bool valid = r < k.g.M && !rest;
+            const int m = k.g.m0 + r;
+            const int wp = min(m / p.group, k.w.n - 1);
+            const int first_m = k.g.m0 + (pair ? wg * kTile : 0);
+            const int last_m = min(first_m + kTile, k.g.m0 + k.g.M) - 1;
+            const int p0 = first_m / p.group, p1 = last_m / p.group;
+            const bool busy = (stacked ? r & ~15 : r & ~31) < k.g.M;   // the warp has rows
+            const RowView view = row_view(p, k.w, k.i, wp);
+            float m_ref = -INFINITY, l = 0.f;
+            for (int it = 0; it < mine && ok; ++it) {
+                const int key0 = tile_key(k.g, k.t0 + (pair ? it : 2 * it + wg));
+                const bool mixed = tile_mixed(p, k.w, p0, p1, key0);
+                ok = wait_or_fail(p, &bar.s_full[wg], n_s & 1);
+                ++n_s;
+                if (!ok) break;
+                tc_fence_after();
+                if (busy) {
+                    float x[128];
+                    {
+                        uint32_t(*xs)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, xs[c]);
+                        tmem_ld_wait();
+                    }
+                    if (mixed) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t see = seen32(view, key0 + 32 * c);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!((see >> j) & 1u)) x[32 * c + j] = -INFINITY;
+                        }
+                    }
+                    float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
+#pragma unroll
+                    for (int j = 4; j < 128; j += 4) {
+                        t0 = fmaxf(t0, x[j]);
+                        t1 = fmaxf(t1, x[j + 1]);
+                        t2 = fmaxf(t2, x[j + 2]);
+                        t3 = fmaxf(t3, x[j + 3]);
+                    }
+                    const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sl;
+                    if (__any_sync(0xffffffffu, top > m_ref + kLazy || (m_ref == -INFINITY && top > -INFINITY))) {
+                        const float to = fmaxf(m_ref, top);
+                        const float corr = to == -INFINITY ? 1.f : fast_exp2(m_ref - to);
+                        m_ref = to;
+                        l *= corr;
+                        if (it > 0) {
+                            // the tile before has been added: S of this one was
+                            // issued after that product and has completed
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + c * 32, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                                tmem_st32(tO + c * 32, o);
+                            }
+                        }
+                    }
+                    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            float* y = x + 32 * c + j;
+                            ffma2(y[0], y[1], sl, neg);
+                            ffma2(y[2], y[3], sl, neg);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e] = fast_exp2(y[e]);
+                            fadd2(l0, l1, y[0], y[1]);
+                            fadd2(l2, l3, y[2], y[3]);
+                            w[j / 2] = f32x2_to_bf16x2(y[0], y[1]);
+                            w[j / 2 + 1] = f32x2_to_bf16x2(y[2], y[3]);
+                        }
+                        if (stacked || twice) {
+                            uint32_t u[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float* y = x + 32 * c + 2 * j;
+                                u[j] = f32x2_to_bf16x2(y[0] - __uint_as_float(w[j] << 16),
+                                                       y[1] - __uint_as_float(w[j] & 0xffff0000u));
+                            }
+                            if (twice) {
+                                tmem_st16(tS + 64 + c * 16, u);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) w[j] = rest ? u[j] : w[j];
+                            }
+                        }
+                        tmem_st16(tS + c * 16, w);
+                    }
+                    l += (l0 + l1) + (l2 + l3);
+                    tmem_st_wait();
+                }
+                if (x_open && it == 0) {
+                    // the other warpgroup has read this one's O of the block before
+                    ok = wait_or_fail(p, &bar.xdone, (n_x - 1) & 1);
+                    x_open = false;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_ready[wg]);
+            }
+            if (!ok) break;
+            // ---- the block's end -------------------------------------------
+            const bool whole = k.t0 == 0 && k.t1 == k.g.n;
+            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (k.t0 > 0 ? 0 : 1);
+            if (blk == 0) share.head = k.t0 == 0 ? 0 : k.t1 == k.g.n ? 1 : 2;
+            if (k.t0 == 0 && !whole) {
+                share.rows = k.g.M;
+                share.row0 = k.w.row0;
+                share.m0 = k.g.m0;
+                share.hk = k.hk;
+            }
+            float a0 = 1.f, a1 = 0.f;      // weights of this warpgroup's o and the other's
+            const bool joined = !pair;
+            if (joined) {
+                if (x_open) {              // only a block in which this warpgroup had no tile leaves it open
+                    ok = wait_or_fail(p, &bar.xdone, (n_x - 1) & 1);
+                    x_open = false;
+                    if (!ok) break;
+                }
+                xch[wg * kTile + row] = make_float2(m_ref, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.xch);
+                ok = wait_or_fail(p, &bar.xch, n_x & 1);
+                if (!ok) break;
+                const float2 other = xch[(wg ^ 1) * kTile + row];
+                const float mm = fmaxf(m_ref, other.x);
+                const float ref = mm == -INFINITY ? 0.f : mm;
+                a0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref);
+                a1 = other.x == -INFINITY ? 0.f : fast_exp2(other.x - ref);
+                l = l * a0 + other.y * a1;
+                m_ref = mm;
+                const int n0 = (n_tiles + 1) >> 1, n1 = n_tiles >> 1;
+                ok = wait_or_fail(p, &bar.o_full[0], n_o[0] & 1);
+                if (ok && n1 > 0) ok = wait_or_fail(p, &bar.o_full[1], n_o[1] & 1);
+                n_o[0] += n0 > 0;
+                n_o[1] += n1 > 0;
+            } else {
+                ok = wait_or_fail(p, &bar.o_full[wg], n_o[wg] & 1);
+                ++n_o[0];
+                ++n_o[1];
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const bool odd = nonfin[blk & 15] == blk + 1;
+            const int none = joined && n_tiles < 2;    // the second warpgroup's o was never written
+            const int c0 = joined ? wg * (D / 64) : 0, c1 = joined ? c0 + D / 64 : D / 32;
+            if (busy) {
+                const int h = k.hk * p.group + m % p.group;
+                const size_t at = (static_cast<size_t>(k.w.row0) + m / p.group) * p.H + h;
+                const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+                for (int c = c0; c < c1; ++c) {
+                    uint32_t o[32];
+                    float f[32];
+                    tmem_ld32((joined ? tO0 : tO) + c * 32, o);
+                    tmem_ld_wait();
+                    if (joined) {
+                        const float w0 = wg ? a1 : a0, w1 = wg ? a0 : a1;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = w0 == 0.f ? 0.f : __uint_as_float(o[j]) * w0;
+                        if (!none) {
+                            tmem_ld32(tO1 + c * 32, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                f[j] = w1 == 0.f ? f[j] : fmaf(__uint_as_float(o[j]), w1, f[j]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]);
+                    }
+                    if (stacked) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float y = __shfl_down_sync(0xffffffffu, f[j], 16);
+                            if (fabsf(f[j]) < INFINITY) f[j] += y;   // a remainder has either sign: not on infinities
+                        }
+                    }
+                    if (odd && valid) {
+                        float g[32];
+                        const Window w2 = k.w;
+                        const Geom g2 = k.g;
+                        for (int j = 0; j < 32; ++j) g[j] = f[j];
+                        add_nonfinite<D, E4M3>(p, w2, g2, k.i, k.hk, k.t0, k.t1, m, m_ref, c * 32, g);
+                        for (int j = 0; j < 32; ++j) f[j] = g[j];
+                    }
+                    if (whole && valid) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + c * 32);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float* y = f + 8 * j;
+                            dst[j] = make_uint4(f32x2_to_bf16x2(y[0] * inv, y[1] * inv),
+                                                f32x2_to_bf16x2(y[2] * inv, y[3] * inv),
+                                                f32x2_to_bf16x2(y[4] * inv, y[5] * inv),
+                                                f32x2_to_bf16x2(y[6] * inv, y[7] * inv));
+                        }
+                    } else if (valid) {
+                        float4* dst = reinterpret_cast<float4*>(ws.o + (slot * ws.cap + r) * D + c * 32);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (valid && (!joined || wg == 0)) {
+                    if (!whole) ws.ml[slot * ws.cap + r] = make_float2(m_ref, l);
+                    else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : m_ref * kLn2 + logf(l);
+                }
+            }
+            tc_fence_before();   // O has been read before the next block's products are let go
+            if (joined) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.xdone);
+                ++n_x;
+                x_open = true;
+            }
+            ++blk;
+        }
+        if (tid == 0 && work) ws.share[blockIdx.x] = share;
+    } else if (warp < 12) {
+        set_regs_down<C::kRegsRest>();
+        Walk k;
+        k.init(st);
+        if (warp == 8) {
+            // ----------------------------------------------------------------
+            // producer: K and V tiles in turn, a lane per page
+            // ----------------------------------------------------------------
+            const int pages = kTile >> p.c.page_shift, page = 1 << p.c.page_shift;
+            constexpr int kN = E4M3 ? C::kRawSlots : C::kSlots;
+            constexpr int kRow = E4M3 ? D : 128;          // bytes of a shared-memory row
+            uint64_t* full = E4M3 ? bar.raw_full : bar.full;
+            uint64_t* empty = E4M3 ? bar.raw_empty : bar.empty;
+            uint32_t n = 0, dirty = 0, odd_full = 0, odd_dirty = 0;   // per slot: the barrier armed last, phases mod 2
+            bool ok = true;
+            while (ok && work && k.next(p)) {
+                const int len = k.w.ctx + k.w.n;
+                for (int t = k.t0; t < k.t1 && ok; ++t) {
+                    const int key0 = tile_key(k.g, t);
+                    const bool cleaned = !E4M3 && tile_cleaned(p, k.w, k.g, key0);
+                    const int live = min(pages, (len - key0 + page - 1) >> p.c.page_shift);
+                    int pg = 0;
+                    if (lane < live) {
+                        pg = page_of(p.c, k.i, key0 + lane * page);
+                        if (pg < 0) {
+                            set_status(p.dev_status, SDM_DEV_BAD_PAGE);
+                            pg = 0;
+                        }
+                    }
+                    const int y = (pg * p.c.heads + k.hk) << p.c.page_shift;
+                    const uint32_t bytes = static_cast<uint32_t>(live) * page * (E4M3 ? D + 1 : 2 * D);
+                    for (int v = 0; v < 2 && ok; ++v, ++n) {
+                        const int s = n % kN;
+                        if (n >= kN) ok = wait_or_fail(p, &empty[s], ((n / kN) - 1) & 1);
+                        if (!ok) break;
+                        const bool to_dirty = cleaned && v == 1;
+                        uint64_t* arrive = to_dirty ? &bar.dirty[s] : &full[s];
+                        const uint32_t bit = 1u << s;
+                        dirty = to_dirty ? dirty | bit : dirty & ~bit;
+                        if (to_dirty) odd_dirty ^= bit;
+                        else odd_full ^= bit;
+                        if (lane == 0) mbar_arrive_expect_tx(arrive, bytes);
+                        __syncwarp();
+                        if (lane < live) {
+                            if constexpr (E4M3) {
+                                tma_load_2d(smem + C::kRaw + s * C::kRawBytes + lane * page * kRow, v ? &tmV : &tmK,
+                                            arrive, 0, y);
+                                bulk_load(smem + C::kExps + s * kTile + lane * page, (v ? p.c.v_exp : p.c.k_exp) + y,
+                                          page, arrive);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < C::kHalves; ++h)
+                                    tma_load_2d(smem + C::kRing + s * C::kTileBytes + h * (kTile * 128) +
+                                                    lane * page * kRow,
+                                                v ? &tmV : &tmK, arrive, h * 64, y);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (!ok) {
+                // copies in flight land before the CTA may exit
+                for (uint32_t s = 0; s < kN && s < n; ++s) {
+                    if ((dirty >> s) & 1u) mbar_wait(&bar.dirty[s], ((odd_dirty >> s) & 1u) ^ 1u);
+                    else mbar_wait(&full[s], ((odd_full >> s) & 1u) ^ 1u);
+                }
+            }
+        } else if (warp == 9) {
+            // ----------------------------------------------------------------
+            // products
+            // ----------------------------------------------------------------
+            constexpr uint32_t kIdQK = idesc_bf16_f32(kTile, kTile, false);
+            constexpr uint32_t kIdPV = idesc_bf16_f32(kTile, D, true);
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+            const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::kRing), 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kRing), kTile * 128, 1024);
+            uint32_t n_t = 0, n_q = 0, n_p[2] = {0, 0}, full_phase = 0, clean_phase = 0;
+            bool ok = true;
+            // tile t of the current block, counted over the CTA's share
+            auto slot_of = [&](uint32_t t, int v) { return (2 * t + v) % C::kSlots; };
+            auto wait_full = [&](int s) {
+                const bool r = wait_or_fail(p, &bar.full[s], (full_phase >> s) & 1);
+                full_phase ^= 1u << s;
+                return r;
+            };
+            auto wait_k = [&](uint32_t t) { return wait_full(slot_of(t, 0)); };
+            auto wait_v = [&](uint32_t t, int tile) {
+                const int s = slot_of(t, 1);
+                if (E4M3 || !tile_cleaned(p, k.w, k.g, tile_key(k.g, tile))) return wait_full(s);
+                const bool r = wait_or_fail(p, &bar.clean[s], (clean_phase >> s) & 1);
+                clean_phase ^= 1u << s;
+                return r;
+            };
+            auto qk = [&](int wg, int q, uint32_t t) {
+                const uint64_t a = q_desc + static_cast<uint64_t>(q * (C::kQBytes >> 4));
+                const uint64_t b = k_desc + static_cast<uint64_t>(slot_of(t, 0) * (C::kTileBytes >> 4));
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint64_t off = static_cast<uint64_t>((ks >> 2) * ((kTile * 128) >> 4) + (ks & 3) * 2);
+                    mma_bf16_warp(tmem + wg * 128, a + off, b + off, kIdQK, ks > 0);
+                }
+                mma_commit_warp(&bar.s_full[wg]);
+            };
+            auto pv = [&](int wg, uint32_t t, bool add) {
+                const uint64_t b = v_desc + static_cast<uint64_t>(slot_of(t, 1) * (C::kTileBytes >> 4));
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    mma_bf16_ts_warp(tmem + 256 + wg * 128, tmem + wg * 128 + ks * 8,
+                                     b + static_cast<uint64_t>(ks * (2048 >> 4)), kIdPV, add || ks > 0);
+                if (k.g.twice) {
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        mma_bf16_ts_warp(tmem + 256 + wg * 128, tmem + wg * 128 + 64 + ks * 8,
+                                         b + static_cast<uint64_t>(ks * (2048 >> 4)), kIdPV, 1);
+                }
+            };
+            auto wait_p = [&](int wg) {
+                const bool r = wait_or_fail(p, &bar.p_ready[wg], n_p[wg] & 1);
+                ++n_p[wg];
+                tc_fence_after();
+                return r;
+            };
+            while (ok && work && k.next(p)) {
+                const int n = k.t1 - k.t0;
+                const uint32_t base = n_t;
+                n_t += n;
+                ok = wait_or_fail(p, &bar.q_full, n_q & 1);
+                ++n_q;
+                if (!ok) break;
+                if (k.g.weight == 2) {
+                    for (int t = 0; t <= n && ok; ++t) {
+                        if (t < n) ok = wait_k(base + t);
+                        for (int wg = 0; wg < 2 && ok; ++wg) {
+                            if (t > 0) {
+                                if (wg == 0) ok = wait_v(base + t - 1, k.t0 + t - 1);
+                                ok = ok && wait_p(wg);
+                                if (!ok) break;
+                                pv(wg, base + t - 1, t > 1);
+                                if (t == n) mma_commit_warp(&bar.o_full[wg]);
+                            }
+                            if (t < n) {
+                                tc_fence_after();
+                                qk(wg, wg, base + t);
+                            }
+                        }
+                        if (!ok) break;
+                        if (t < n) mma_commit_warp(&bar.empty[slot_of(base + t, 0)]);
+                        if (t > 0) mma_commit_warp(&bar.empty[slot_of(base + t - 1, 1)]);
+                        if (t == n - 1) mma_commit_warp(&bar.q_empty);
+                    }
+                } else {
+                    for (int t = 0; t < n + 2 && ok; ++t) {
+                        const int wg = t & 1;
+                        if (t >= 2) {
+                            ok = wait_v(base + t - 2, k.t0 + t - 2) && wait_p(wg);
+                            if (!ok) break;
+                            pv(wg, base + t - 2, t >= 4);
+                            if (t >= n) mma_commit_warp(&bar.o_full[wg]);
+                            mma_commit_warp(&bar.empty[slot_of(base + t - 2, 1)]);
+                        }
+                        if (t < n) {
+                            ok = wait_k(base + t);
+                            if (!ok) break;
+                            tc_fence_after();
+                            qk(wg, 0, base + t);
+                            mma_commit_warp(&bar.empty[slot_of(base + t, 0)]);
+                            if (t == n - 1) mma_commit_warp(&bar.q_empty);
+                        }
+                    }
+                }
+            }
+            if (!ok) {   // this warp's own tensor-core work ends before tensor memory is freed
+                mma_commit_warp(&bar.drain);
+                mbar_wait(&bar.drain, 0);
+            }
+        } else {
+            // ----------------------------------------------------------------
+            // Q rows of each block; bf16: then the values of its partly seen tiles
+            // ----------------------------------------------------------------
+            constexpr int kChunks = D / 8;                // 16-byte pieces of a row
+            constexpr int kStep = 64 / kChunks;           // rows per pass of the two warps
+            const int t64 = tid & 63;
+            uint32_t n_q = 0, n_t = 0, dirty_phase = 0;
+            bool ok = true;
+            int blk = 0;
+            while (ok && work && k.next(p)) {
+                if (n_q > 0) ok = wait_or_fail(p, &bar.q_empty, (n_q - 1) & 1);
+                ++n_q;
+                if (!ok) break;
+                const int c = t64 % kChunks;
+                int r = t64 / kChunks;
+                int wp = (k.g.m0 + r) / p.group, h = (k.g.m0 + r) % p.group;
+                for (; r < k.g.M; r += kStep) {
+                    const uint16_t* src = p.q + (k.w.row0 + wp) * p.q_stride +
+                                          static_cast<size_t>(k.hk * p.group + h) * D + c * 8;
+                    const int to = k.g.stacked ? (r >> 4) * 32 + (r & 15) : r;   // 16 rows keep r mod 8 and the swizzle
+                    uint8_t* dst = smem + (to >> 7) * C::kQBytes + (c >> 3) * (kTile * 128) + (to & 127) * 128 +
+                                   (((c & 7) ^ (to & 7)) << 4);
+                    cp_async_16(dst, src, 16u);
+                    if (k.g.stacked) cp_async_16(dst + 16 * 128, src, 16u);
+                    h += kStep;
+                    while (h >= p.group) {
+                        h -= p.group;
+                        ++wp;
+                    }
+                }
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.q_full);
+                if constexpr (!E4M3) {
+                    const int len = k.w.ctx + k.w.n;
+                    for (int t = k.t0; t < k.t1 && ok; ++t) {
+                        const int key0 = tile_key(k.g, t);
+                        if (!tile_cleaned(p, k.w, k.g, key0)) continue;
+                        const uint32_t idx = 2 * (n_t + (t - k.t0)) + 1;
+                        const int s = idx % C::kSlots;
+                        ok = wait_or_fail(p, &bar.dirty[s], (dirty_phase >> s) & 1);
+                        dirty_phase ^= 1u << s;
+                        if (!ok) break;
+                        uint4* v = reinterpret_cast<uint4*>(smem + C::kRing + s * C::kTileBytes);
+                        bool found = false;
+#pragma unroll 4
+                        for (int e = t64; e < C::kTileBytes / 16; e += 64) {
+                            uint4 x = v[e];
+                            if (nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) {
+                                uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t bad = nonfinite2(u[j]);
+                                    if (bad & 0x8000u) u[j] &= 0xffff0000u;
+                                    if (bad & 0x80000000u) u[j] &= 0xffffu;
+                                }
+                                v[e] = x;
+                                found |= key0 + ((e >> 3) & (kTile - 1)) < len;
+                            }
+                        }
+                        if (found) nonfin[blk & 15] = blk + 1;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.clean[s]);
+                    }
+                    n_t += k.t1 - k.t0;
+                }
+                ++blk;
+            }
+        }
+    } else {
+        // --------------------------------------------------------------------
+        // e4m3 codes -> bf16 values, one key's row per thread
+        // --------------------------------------------------------------------
+        if constexpr (E4M3) {
+            set_regs_down<C::kRegsRest>();
+            Walk k;
+            k.init(st);
+            const int row = tid & 127;
+            uint32_t n = 0;
+            bool ok = true;
+            int blk = 0;
+            while (ok && work && k.next(p)) {
+                const int len = k.w.ctx + k.w.n;
+                for (int t = k.t0; t < k.t1 && ok; ++t) {
+                    const int key0 = tile_key(k.g, t);
+                    const bool cleaned = tile_cleaned(p, k.w, k.g, key0);
+                    for (int v = 0; v < 2; ++v, ++n) {
+                        const int s = n % C::kSlots, rs = n % C::kRawSlots;
+                        if (n >= C::kSlots) ok = wait_or_fail(p, &bar.empty[s], ((n / C::kSlots) - 1) & 1);
+                        ok = ok && wait_or_fail(p, &bar.raw_full[rs], (n / C::kRawSlots) & 1);
+                        if (!ok) break;
+                        const uint8_t* src = smem + C::kRaw + rs * C::kRawBytes + row * D;
+                        uint8_t* dst = smem + C::kRing + s * C::kTileBytes + row * 128;
+                        const uint32_t e = smem[C::kExps + rs * kTile + row];
+                        // 2^(e - 127) as bf16, twice: every e a write leaves is in bf16's range
+                        const uint32_t sc = e << 7;
+                        const uint32_t scale2 = sc | (sc << 16);
+                        const bool clear = cleaned && v == 1;
+                        bool found = false;
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
+                            // bytes at c ^ (r / 2 mod 4)
+                            const int at = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+                            const uint4 x = *reinterpret_cast<const uint4*>(src + at * 16);
+                            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 f = f16x2_to_f32x2(
+                                    e4m3x2_to_f16x2(static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1)))));
+                                uint32_t b = f32x2_to_bf16x2(f.x, f.y);
+                                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(scale2));
+                                o[j] = b;
+                            }
+                            if (clear) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const uint32_t bad = nonfinite2(o[j]);
+                                    if (bad & 0x8000u) o[j] &= 0xffff0000u;
+                                    if (bad & 0x80000000u) o[j] &= 0xffffu;
+                                    found |= bad != 0;
+                                }
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int oc = 2 * c + h;
+                                *reinterpret_cast<uint4*>(dst + (oc >> 3) * (kTile * 128) +
+                                                          (((oc & 7) ^ (row & 7)) << 4)) =
+                                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+                            }
+                        }
+                        if (found && key0 + row < len) nonfin[blk & 15] = blk + 1;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bar.raw_empty[rs]);
+                            mbar_arrive(&bar.full[s]);
+                        }
+                    }
+                }
+                ++blk;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the segments of split blocks, in key order: the CTA whose share
+// starts a block and the next ones that continue it.  One warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p, const Scratch ws, int grid) {
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const Share s = ws.share[c];
+    if (s.rows == 0) return;
+    // slots of the block: 2c + 1, then slot 0 of the CTAs after c up to the one that finishes it
+    int end = c + 1;
+    for (;;) {
+        const int at = end + lane;
+        const int head = at < grid ? ws.share[at].head : 1;
+        const unsigned stop = __ballot_sync(0xffffffffu, head == 1 || head == 0);
+        if (stop) {
+            end += __ffs(stop);
+            break;
+        }
+        end += 32;
+    }
+    end = min(end, grid);
+    constexpr int kV = D / 32;
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < s.rows; r += gridDim.y * 8) {
+        float m = -INFINITY, l = 0.f, o[kV] = {};
+        for (int k = c; k < end; ++k) {
+            if (k > c && ws.share[k].head == 3) continue;
+            const size_t slot = k == c ? 2 * static_cast<size_t>(c) + 1 : 2 * static_cast<size_t>(k);
+            const float2 ml = ws.ml[slot * ws.cap + r];
+            const float* src = ws.o + (slot * ws.cap + r) * D + lane * kV;
+            float x[kV];
+            if constexpr (kV == 4) {
+                const float4 t = *reinterpret_cast<const float4*>(src);
+                x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+            } else {
+                const float2 t = *reinterpret_cast<const float2*>(src);
+                x[0] = t.x, x[1] = t.y;
+            }
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;
+            const float to = fmaxf(m, ml.x);
+            const float a = m == -INFINITY ? 0.f : fast_exp2(m - to), b = fast_exp2(ml.x - to);
+            m = to;
+            l = l * a + ml.y * b;
+#pragma unroll
+            for (int j = 0; j < kV; ++j) o[j] = o[j] * a + x[j] * b;
+        }
+        const int mm = s.m0 + r;
+        const size_t at = (static_cast<size_t>(s.row0) + mm / p.group) * p.H + s.hk * p.group + mm % p.group;
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * kV);
+        if constexpr (kV == 4)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(f32x2_to_bf16x2(o[0] * inv, o[1] * inv), f32x2_to_bf16x2(o[2] * inv, o[3] * inv));
+        else
+            *dst = f32x2_to_bf16x2(o[0] * inv, o[1] * inv);
+        if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+    }
+}
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int slot_rows(int max_window, int group) {
+    const long long m = static_cast<long long>(max_window) * group;
+    return m >= kBlockRows ? kBlockRows : static_cast<int>((m + 7) & ~7ll);
+}
+
+bool encode(CUtensorMap* map, const CacheView& c, void* pool) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }
+    if (!fn) return false;
+    // rows = (page, head, slot); a box is one page of one head, 128 bytes (e4m3 with 64-wide heads: 64) across
+    const int es = c.e4m3 ? 1 : 2;
+    const int cols = c.e4m3 ? c.D : 64;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.D),
+                          static_cast<cuuint64_t>(c.n_pages) * c.heads << c.page_shift};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.D) * es};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(cols), 1u << c.page_shift};
+    cuuint32_t el[2] = {1, 1};
+    return fn(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides,
+              box, el, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              cols * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
+    using C = Cfg<D, E4M3>;
+    static bool configured = false;
+    if (!configured) {
+        const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   C::kTotal);
+        if (e != cudaSuccess) return e;
+        configured = true;
+    }
+    CUtensorMap tmK, tmV;
+    if (!encode(&tmK, p.c, p.c.k) || !encode(&tmV, p.c, p.c.v)) return cudaErrorInvalidValue;
+    const int grid = num_sms();
+    Scratch ws;
+    uint8_t* at = static_cast<uint8_t*>(work);
+    ws.cap = slot_rows(p.max_window, p.group);
+    ws.share = reinterpret_cast<Share*>(at);
+    at += align256(sizeof(Share) * grid);
+    ws.ml = reinterpret_cast<float2*>(at);
+    at += align256(2 * static_cast<size_t>(grid) * ws.cap * sizeof(float2));
+    ws.o = reinterpret_cast<float*>(at);
+    cudaError_t e = launch_pdl(attend_kernel<D, E4M3>, dim3(grid), dim3(C::kThreads), C::kTotal, s, tmK, tmV, p, ws);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attend_merge_kernel<D>, dim3(grid, std::min(4, (ws.cap + 7) / 8)), dim3(256), 0, s, p, ws, grid);
 }
 
 }  // namespace
 
 size_t attend_workspace(int R, int max_window, int H, int D, int rows, int kv_heads) {
     (void)R;
-    (void)max_window;
-    (void)H;
-    (void)D;
     (void)rows;
-    (void)kv_heads;
-    return 256;
+    if (max_window <= 0 || H <= 0 || D <= 0 || kv_heads <= 0) return 0;
+    const size_t grid = num_sms(), cap = slot_rows(max_window, (H + kv_heads - 1) / kv_heads);
+    return align256(sizeof(Share) * grid) + align256(2 * grid * cap * sizeof(float2)) + 2 * grid * cap * D * 4;
 }
 
-template <int D, bool E4M3>
-static cudaError_t launch_one(const AttendParams& p, cudaStream_t s) {
-    const int smem = static_cast<int>(sizeof(Smem<D>));
-    const cudaError_t e =
-        cudaFuncSetAttribute(attend_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const int blocks = static_cast<int>((static_cast<long long>(p.max_window) * p.group + kRows - 1) / kRows);
-    return launch_pdl(attend_kernel<D, E4M3>, dim3(blocks, p.c.heads, p.R), dim3(kThreads), smem, s, p);
-}
-
-cudaError_t launch_attend(const AttendParams& p, void*, cudaStream_t s) {
-    if (p.c.D == 64) return p.c.e4m3 ? launch_one<64, true>(p, s) : launch_one<64, false>(p, s);
-    return p.c.e4m3 ? launch_one<128, true>(p, s) : launch_one<128, false>(p, s);
+cudaError_t launch_attend(const AttendParams& p, void* ws, cudaStream_t s) {
+    if (p.c.D == 64) return p.c.e4m3 ? launch_one<64, true>(p, ws, s) : launch_one<64, false>(p, ws, s);
+    return p.c.e4m3 ? launch_one<128, true>(p, ws, s) : launch_one<128, false>(p, ws, s);
 }
 
 }  // namespace sdm
