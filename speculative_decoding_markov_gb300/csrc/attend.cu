@@ -22,12 +22,13 @@
 // a cut splits leave (m, l, o) in the workspace and attend_merge_kernel joins
 // them in the order of the keys, so results do not depend on timing.
 //
-// Pipeline of a CTA: a producer warp brings K and V tiles page by page with
-// TMA into a ring; (e4m3: four warps turn codes into bf16, exactly, the scale
-// included, in a second ring); one warp issues S = Q K^T and O += P V; eight
-// warps do the softmax, S from tensor memory to registers and P back over S;
-// two warps gather Q.  Each warpgroup's S, P and O are its own, so one's
-// softmax runs beside the other's products.
+// Pipeline of a CTA (sixteen warps): one walks the share and hands each block
+// to the others; a producer brings K and V tiles page by page with TMA into a
+// ring; one gathers Q; one issues S = Q K^T and O += P V; eight do the
+// softmax, S from tensor memory to registers and P back over S; four clear
+// (bf16) or convert (e4m3: codes to bf16, exactly, the scale included, into a
+// second ring) the tiles.  Each softmax warpgroup's S, P and O are its own, so
+// one's softmax runs beside the other's products.
 //
 // What a row does not see does not reach it: scores are replaced, not added
 // to; values of a tile that some row sees only in part are cleared of NaN and
@@ -56,29 +57,43 @@ constexpr int kStackRows = 64;
 constexpr int kFineTiles = 9;
 constexpr int kTmemCols = 512;        // S0, S1, O0, O1 at columns 0, 128, 256, 384; P over S
 
-template <int D, bool E4M3>
+constexpr int kThreads = 512;
+// registers of a thread: the softmax warpgroups', the others' (together the
+// launch's own 4 x 128)
+constexpr int kRegsSoft = 184, kRegsRest = 72;
+static_assert(2 * kRegsSoft + 2 * kRegsRest == 4 * 128, "registers");
+
+// One block, as the walking warp hands it to the others.
+struct Blk {
+    int i, hk, row0, n;               // request, kv head, first packed row and rows of its window
+    int ctx, m0, M, p1;               // committed tokens; first row and rows of the block, its last window position
+    int ns, lo, tiles, t0;            // Geom's; the share's key tiles of the block are t0 .. t1 - 1
+    int t1, flags, p0, nonfinite;     // t1 = 0: no more blocks; set if a cleared value was not finite
+};
+enum { BLK_PAIR = 1, BLK_STACKED = 2, BLK_TWICE = 4 };
+
+template <int D, bool E4M3, bool SMALL>
 struct Cfg {
-    static constexpr int kThreads = E4M3 ? 512 : 384;
-    static constexpr int kHalves = D / 64;                   // 128-byte column blocks of a bf16 tile
     static constexpr int kQBytes = kTile * D * 2;            // one 128-row sub-tile
     static constexpr int kTileBytes = kTile * D * 2;         // one bf16 K or V tile
-    static constexpr int kSlots = (E4M3 ? 96 : 160) * 1024 / kTileBytes;
+    static constexpr int kQs = SMALL ? 1 : 2;                // sub-tiles of Q
+    static constexpr int kRawSlots = E4M3 ? (D == 128 ? 4 : 6) : 0;
+    static constexpr int kFit = (224 * 1024 - kQs * kQBytes - kRawSlots * kTile * D) / kTileBytes;
+    static constexpr int kSlots = kFit < 8 ? kFit : 8;
+    static constexpr int kRingBlocks = E4M3 && D == 128 && !SMALL ? 3 : 8;   // blocks handed out ahead
+    static constexpr int kXchRows = SMALL ? kStackRows : kTile;
     static constexpr int kRawBytes = kTile * D;              // e4m3 codes of a tile
-    static constexpr int kRawSlots = E4M3 ? 64 * 1024 / kRawBytes : 0;
-    static constexpr int kRing = 2 * kQBytes;
+    static constexpr int kRing = kQs * kQBytes;
     static constexpr int kRaw = kRing + kSlots * kTileBytes;
     static constexpr int kExps = kRaw + kRawSlots * kRawBytes;
     static constexpr int kXch = kExps + kRawSlots * kTile;   // (m, l) of both warpgroups' rows
-    static constexpr int kBars = kXch + 2 * kTile * 8;
-    static constexpr int kNumBars = 4 * kSlots + 2 * kRawSlots + 2 + 6 + 3;
+    static constexpr int kBlks = kXch + 2 * kXchRows * 8;
+    static constexpr int kBars = kBlks + kRingBlocks * static_cast<int>(sizeof(Blk));
+    static constexpr int kNumBars = 4 * kSlots + 2 * (kRawSlots > 0 ? kRawSlots : 1) + 2 * kRingBlocks + 11;
     static constexpr int kMisc = kBars + kNumBars * 8;
-    static constexpr int kTotal = kMisc + 96;
-    // registers of a thread: the softmax warpgroups', the others' (together
-    // the launch's own: 3 x 168 and 4 x 128)
-    static constexpr int kRegsSoft = E4M3 ? 184 : 208;
-    static constexpr int kRegsRest = E4M3 ? 72 : 88;
+    static constexpr int kTotal = kMisc + 16;
     static_assert(kTotal <= 232448, "shared memory");
-    static_assert(E4M3 ? 2 * kRegsSoft + 2 * kRegsRest == 4 * 128 : 2 * kRegsSoft + kRegsRest == 3 * 168, "registers");
+    static_assert(kSlots >= 3, "a K tile, the V tile before it and the next");
 };
 
 struct Share {             // per CTA, for the merge: the block its last segment starts, and how its first goes on
@@ -131,20 +146,20 @@ __device__ __forceinline__ Geom geom_of(const AttendParams& p, const Window& w, 
     return g;
 }
 
-__device__ __forceinline__ int tile_key(const Geom& g, int t) { return (t < g.ns ? t : g.lo + t - g.ns) * kTile; }
+__device__ __forceinline__ int tile_key(const Blk& b, int t) { return (t < b.ns ? t : b.lo + t - b.ns) * kTile; }
 
 // Whether some row at window positions p0 .. p1 does not see all of the tile's keys.
-__device__ __forceinline__ bool tile_mixed(const AttendParams& p, const Window& w, int p0, int p1, int key0) {
+__device__ __forceinline__ bool tile_mixed(const AttendParams& p, int ctx, int n, int p0, int p1, int key0) {
     const int last = key0 + kTile - 1;
-    if (last > (p.tree ? w.ctx - 1 : w.ctx + p0)) return true;
+    if (last > (p.tree ? ctx - 1 : ctx + p0)) return true;
     if (p.window <= 0 || last < p.sinks) return false;
-    return key0 <= w.ctx + (p.tree ? w.n - 1 : p1) - p.window;
+    return key0 <= ctx + (p.tree ? n - 1 : p1) - p.window;
 }
 
 // Whether the tile's values are cleared of NaN and infinities: a row may not
 // see them, or a remainder (of either sign) may meet an infinity.
-__device__ __forceinline__ bool tile_cleaned(const AttendParams& p, const Window& w, const Geom& g, int key0) {
-    return g.twice || tile_mixed(p, w, g.p0, g.p1, key0);
+__device__ __forceinline__ bool tile_cleaned(const AttendParams& p, const Blk& b, int key0) {
+    return (b.flags & BLK_TWICE) || tile_mixed(p, b.ctx, b.n, b.p0, b.p1, key0);
 }
 
 struct Start {
@@ -195,9 +210,9 @@ struct Walk {
                 g = geom_of(p, w, b);
                 have_b = b;
             }
-            const unsigned wt = g.weight;
-            t0 = us < u0 ? static_cast<int>((u0 - us + wt - 1) / wt) : 0;
-            const unsigned long long left = (u1 - us + wt - 1) / wt;
+            const unsigned wt = g.weight;   // 1 or 2
+            t0 = us < u0 ? static_cast<int>((u0 - us + wt - 1) >> (wt - 1)) : 0;
+            const unsigned long long left = (u1 - us + wt - 1) >> (wt - 1);
             t1 = left < static_cast<unsigned long long>(g.n) ? static_cast<int>(left) : g.n;
             if (t0 < t1) return true;
             us += static_cast<unsigned long long>(g.n) * wt;
@@ -211,15 +226,14 @@ __device__ __forceinline__ unsigned long long shfl_up64(unsigned long long v, in
 
 // This CTA's share of the units (key tiles times their weight) of all blocks,
 // and where it starts.  cost: shared memory for R entries.
-template <int THREADS>
 __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* cost, Start* start,
                                      unsigned long long* wsum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kWarps = THREADS / 32;
+    constexpr int kWarps = kThreads / 32;
     const long long tokens = table_tokens(p.c);
     const int most = (p.max_window * p.group + kBlockRows - 1) / kBlockRows;
     if (most <= 4) {
-        for (int i = tid; i < p.R; i += THREADS) {
+        for (int i = tid; i < p.R; i += kThreads) {
             const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
             if (w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
             unsigned long long c = 0;
@@ -244,7 +258,7 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
         }
     }
     __syncthreads();
-    const int per = (p.R + THREADS - 1) / THREADS;
+    const int per = (p.R + kThreads - 1) / kThreads;
     const int a = min(p.R, tid * per), e = min(p.R, a + per);
     unsigned long long mine = 0;
     for (int i = a; i < e; ++i) mine += cost[i];
@@ -263,7 +277,11 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
         if (k < warp) base += v;
         total += v;
     }
-    const unsigned long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    // the first (total mod grid) shares are one unit longer
+    const unsigned long long each = total >> 32 ? total / gridDim.x : static_cast<unsigned>(total) / gridDim.x;
+    const unsigned more = static_cast<unsigned>(total - each * gridDim.x);
+    const unsigned long long u0 = each * blockIdx.x + min(blockIdx.x, more);
+    const unsigned long long u1 = u0 + each + (blockIdx.x < more ? 1 : 0);
     if (tid == 0) {
         start->u0 = u0;
         start->u1 = u1;
@@ -307,7 +325,10 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
                 us += all;
             }
         }
-        const unsigned long long k = step > 0 ? (u0 - us) / step : 0;
+        const unsigned long long into = u0 - us;
+        const unsigned long long k = step == 0 ? 0
+                                     : (into | step) >> 32 ? into / step
+                                                           : static_cast<unsigned>(into) / static_cast<unsigned>(step);
         if (lane == 0) {
             start->b = max(found, 0);
             start->hk = static_cast<int>(k);
@@ -321,20 +342,28 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
 // Barriers: every wait is bounded; a wait that runs out records
 // SDM_DEV_TIMEOUT and the role winds down.
 // ---------------------------------------------------------------------------
+// One short loop (the callers' loops have to fit the instruction cache).
 __device__ __forceinline__ bool wait_or_fail(const AttendParams& p, uint64_t* bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_wait(bar, parity))) return true;   // one answer for the whole warp
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;   // one answer for the whole warp
+    const uint64_t t0 = globaltimer();
+#pragma unroll 1
+    do {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    } while (__all_sync(0xffffffffu, globaltimer() - t0 < kWaitLimitNs));
     set_status(p.dev_status, SDM_DEV_TIMEOUT);
     return false;
 }
 
-template <int SLOTS, int RAW>
+template <int SLOTS, int RAW, int BLOCKS>
 struct Bars {
     // a tile arrives at full, one to be cleaned at dirty and then, cleaned, at
     // clean: whoever waits on one of them waits for all its phases
     uint64_t full[SLOTS], empty[SLOTS], dirty[SLOTS], clean[SLOTS];
     uint64_t raw_full[RAW > 0 ? RAW : 1], raw_empty[RAW > 0 ? RAW : 1];
+    uint64_t blk_full[BLOCKS], blk_empty[BLOCKS];
     uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], xch, xdone, drain;
 };
+constexpr int kBlkReaders = 8 + 3 + 4;   // warps that read a handed-out block
 
 // Nonzero if one of the two bf16 in x is an infinity or NaN (the exponent
 // field 0xff plus one carries into the sign's place).
@@ -364,21 +393,21 @@ __device__ __forceinline__ uint32_t seen32(const RowView& r, int base) {
     return m;
 }
 
-__device__ __forceinline__ RowView row_view(const AttendParams& p, const Window& w, int i, int wp) {
+__device__ __forceinline__ RowView row_view(const AttendParams& p, int i, int ctx, int n_rows, int wp) {
     RowView r;
-    r.ctx = w.ctx;
-    r.n = w.n;
+    r.ctx = ctx;
+    r.n = n_rows;
     r.words = p.words;
     r.sinks = p.window > 0 ? p.sinks : 0;
     r.bits = nullptr;
-    int pos = w.ctx + wp;
+    int pos = ctx + wp;
     r.pos = pos;
     if (p.tree) {
         r.bits = p.tree + (static_cast<size_t>(i) * p.nodes + wp) * p.words;
         int n = 0;
         for (int k = 0; k < p.words; ++k) n += __popc(__ldg(r.bits + k));
-        pos = w.ctx + max(0, n - 1);
-        r.pos = w.ctx - 1;
+        pos = ctx + max(0, n - 1);
+        r.pos = ctx - 1;
     }
     r.lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
     return r;
@@ -388,18 +417,18 @@ __device__ __forceinline__ RowView row_view(const AttendParams& p, const Window&
 // block's partly seen tiles (where shared memory holds zeros for them), to 32
 // of its output columns.  Rare: one thread per row, straight from the cache.
 template <int D, bool E4M3>
-__device__ __noinline__ void add_nonfinite(const AttendParams& p, const Window& w, const Geom& g, int i, int hk,
-                                           int t0, int t1, int m, float m_ref, int col0, float* o) {
+__device__ __noinline__ void add_nonfinite(const AttendParams& p, const Blk& blk, int m, float m_ref, int col0,
+                                           float* o) {
     const int wp = m / p.group;
-    const RowView r = row_view(p, w, i, wp);
-    const uint16_t* q = p.q + (w.row0 + wp) * p.q_stride + static_cast<size_t>(hk * p.group + m % p.group) * D;
-    for (int t = t0; t < t1; ++t) {
-        const int key0 = tile_key(g, t);
-        if (!tile_cleaned(p, w, g, key0)) continue;
-        for (int j = key0; j < min(key0 + kTile, w.ctx + w.n); ++j) {
+    const RowView r = row_view(p, blk.i, blk.ctx, blk.n, wp);
+    const uint16_t* q = p.q + (blk.row0 + wp) * p.q_stride + static_cast<size_t>(blk.hk * p.group + m % p.group) * D;
+    for (int t = blk.t0; t < blk.t1; ++t) {
+        const int key0 = tile_key(blk, t);
+        if (!tile_cleaned(p, blk, key0)) continue;
+        for (int j = key0; j < min(key0 + kTile, blk.ctx + blk.n); ++j) {
             if (!((seen32(r, j & ~31) >> (j & 31)) & 1u)) continue;
-            const int pg = max(page_of(p.c, i, j), 0);
-            const size_t row = pool_row(p.c, pg, j) + (static_cast<size_t>(hk) << p.c.page_shift);
+            const int pg = max(page_of(p.c, blk.i, j), 0);
+            const size_t row = pool_row(p.c, pg, j) + (static_cast<size_t>(blk.hk) << p.c.page_shift);
             float weight = -1.0f;
             for (int c = 0; c < 32; ++c) {
                 float v;
@@ -451,212 +480,312 @@ __device__ __forceinline__ void set_regs_up() { asm volatile("setmaxnreg.inc.syn
 template <int N>
 __device__ __forceinline__ void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
+// S[wg] = Q K^T over D / 16 steps, O[wg] (+)= P V over kTile / 16: one asm
+// statement each, the lane elect.sync picks issuing, so that nothing but the
+// descriptors' constant steps stands between two products.
+__device__ __forceinline__ void issue_qk4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+__device__ __forceinline__ void issue_pv4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+        "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+        "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+__device__ __forceinline__ void store_v8(void* to, const uint32_t (&x)[8]) {   // 32 bytes, 32-byte aligned
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
+// Reads the handed-out blocks in turn.
+template <int BLOCKS>
+struct Reader {
+    uint32_t n = 0;
+    __device__ __forceinline__ int at() const { return n % BLOCKS; }
+    __device__ __forceinline__ uint32_t phase() const { return (n / BLOCKS) & 1; }
+};
+
+template <int D, bool E4M3, bool SMALL>
+__global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ AttendParams p, const __grid_constant__ Scratch ws) {
-    using C = Cfg<D, E4M3>;
-    using B = Bars<C::kSlots, C::kRawSlots>;
+    using C = Cfg<D, E4M3, SMALL>;
+    using B = Bars<C::kSlots, C::kRawSlots, C::kRingBlocks>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    static_assert(sizeof(B) <= (C::kNumBars + 2) * 8, "barriers");
+    static_assert(sizeof(B) == C::kNumBars * 8, "barriers");
     B& bar = *reinterpret_cast<B*>(smem + C::kBars);
+    Blk* blks = reinterpret_cast<Blk*>(smem + C::kBlks);
     float2* xch = reinterpret_cast<float2*>(smem + C::kXch);
     Start* start = reinterpret_cast<Start*>(smem + C::kXch);               // only until the roles begin
     unsigned long long* wsum = reinterpret_cast<unsigned long long*>(smem + C::kXch + 64);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc + 16);
-    // [16]: count + 1 of the last block (16 apart) in whose partly seen tiles a value was not finite
-    volatile int* nonfin = reinterpret_cast<volatile int*>(smem + C::kMisc + 24);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int k = 0; k < C::kSlots; ++k) {
+    if (warp == 8) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+    } else if (warp == 9) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    } else if (warp == 10) {
+        for (int k = lane; k < C::kSlots; k += 32) {
             mbar_init(&bar.full[k], E4M3 ? 4 : 1);
             mbar_init(&bar.empty[k], 1);
             mbar_init(&bar.dirty[k], 1);
-            mbar_init(&bar.clean[k], 2);
+            mbar_init(&bar.clean[k], 4);
         }
-        for (int k = 0; k < C::kRawSlots; ++k) {
+        for (int k = lane; k < C::kRawSlots; k += 32) {
             mbar_init(&bar.raw_full[k], 1);
             mbar_init(&bar.raw_empty[k], 4);
         }
-        mbar_init(&bar.q_full, 2);
-        mbar_init(&bar.q_empty, 1);
-        for (int k = 0; k < 2; ++k) {
-            mbar_init(&bar.s_full[k], 1);
-            mbar_init(&bar.p_ready[k], 4);
-            mbar_init(&bar.o_full[k], 1);
+        for (int k = lane; k < C::kRingBlocks; k += 32) {
+            mbar_init(&bar.blk_full[k], 1);
+            mbar_init(&bar.blk_empty[k], kBlkReaders);
         }
-        mbar_init(&bar.xch, 8);
-        mbar_init(&bar.xdone, 8);
-        mbar_init(&bar.drain, 1);
+        if (lane < 2) {
+            mbar_init(&bar.s_full[lane], 1);
+            mbar_init(&bar.p_ready[lane], 4);
+            mbar_init(&bar.o_full[lane], 1);
+        }
+        if (lane == 0) {
+            mbar_init(&bar.q_full, 1);
+            mbar_init(&bar.q_empty, 1);
+            mbar_init(&bar.xch, 8);
+            mbar_init(&bar.xdone, 8);
+            mbar_init(&bar.drain, 1);
+        }
         fence_mbar_init();
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-        for (int k = 0; k < 16; ++k) nonfin[k] = 0;
-    }
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, kTmemCols);
-        tmem_relinquish();
     }
     pdl_wait();
     pdl_trigger();
-    plan<C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
+    plan(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
     const Start st = *start;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const bool work = st.u0 < st.u1;
-    if (!work && tid == 0) {
-        Share s = {};
-        s.head = 3;
-        ws.share[blockIdx.x] = s;
-    }
+
+    Reader<C::kRingBlocks> rd;
+    // waits for the next block; its entry stays valid until release()
+    auto take = [&](bool& ok) -> const volatile Blk* {
+        ok = wait_or_fail(p, &bar.blk_full[rd.at()], rd.phase());
+        if (!ok) return nullptr;
+        const volatile Blk* b = blks + rd.at();
+        return b->t1 > 0 ? b : nullptr;
+    };
+    auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.blk_empty[rd.at()]);
+        ++rd.n;
+    };
+    auto copy = [](const volatile Blk* b) {
+        Blk r;
+        const int4* src = reinterpret_cast<const int4*>(const_cast<const Blk*>(b));
+        int4* dst = reinterpret_cast<int4*>(&r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dst[k] = src[k];
+        return r;
+    };
 
     if (warp < 8) {
         // ------------------------------------------------------------------
         // softmax warpgroups
         // ------------------------------------------------------------------
-        set_regs_up<C::kRegsSoft>();
+        set_regs_up<kRegsSoft>();
         const int wg = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + wg * 128;
         const uint32_t tO0 = tmem + lanes + 256, tO1 = tO0 + 128;
         const uint32_t tO = wg ? tO1 : tO0;
         const float sl = p.scale * kLog2e;
-        Walk k;
-        k.init(st);
-        uint32_t n_s = 0, n_o[2] = {0, 0}, n_x = 0;   // phases of s_full, o_full, xch / xdone
-        bool ok = true, x_open = false;
+        uint32_t n_s = 0, n_o0 = 0, n_o1 = 0, n_x = 0;   // phases of s_full, o_full, xch and xdone
+        bool ok, x_open = false;
         Share share = {};
         share.head = 3;
-        int blk = 0;
-        while (ok && work && k.next(p)) {
-            const bool pair = k.g.weight == 2;
-            const int n_tiles = k.t1 - k.t0;
-            const int mine = pair ? n_tiles : (n_tiles + 1 - wg) >> 1;
-            const bool stacked = k.g.stacked, twice = k.g.twice;
+        for (;;) {
+            const volatile Blk* vb = take(ok);
+            if (!vb) break;
+            const int flags = vb->flags, M = vb->M, m0 = vb->m0, t0 = vb->t0;
+            const bool pair = !SMALL && (flags & BLK_PAIR);
+            const bool stacked = SMALL || (flags & BLK_STACKED), twice = !SMALL && (flags & BLK_TWICE);
+            const int n_tiles = vb->t1 - t0;
             const bool rest = stacked && (lane & 16);             // this lane holds the weights' remainders
             const int r = stacked ? (row >> 5) * 16 + (row & 15) : pair ? wg * kTile + row : row;   // row of the block
-            const bool valid = r < k.g.M && !rest;
-            const int m = k.g.m0 + r;
-            const int wp = min(m / p.group, k.w.n - 1);
-            const int first_m = k.g.m0 + (pair ? wg * kTile : 0);
-            const int last_m = min(first_m + kTile, k.g.m0 + k.g.M) - 1;
-            const int p0 = first_m / p.group, p1 = last_m / p.group;
-            const bool busy = (stacked ? r & ~15 : r & ~31) < k.g.M;   // the warp has rows
-            const RowView view = row_view(p, k.w, k.i, wp);
+            const bool busy = (stacked ? r & ~15 : r & ~31) < M;  // the warp has rows
             float m_ref = -INFINITY, l = 0.f;
-            for (int it = 0; it < mine && ok; ++it) {
-                const int key0 = tile_key(k.g, k.t0 + (pair ? it : 2 * it + wg));
-                const bool mixed = tile_mixed(p, k.w, p0, p1, key0);
-                ok = wait_or_fail(p, &bar.s_full[wg], n_s & 1);
-                ++n_s;
-                if (!ok) break;
-                tc_fence_after();
-                if (busy) {
-                    float x[128];
-                    {
-                        uint32_t(*xs)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, xs[c]);
-                        tmem_ld_wait();
-                    }
-                    if (mixed) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t see = seen32(view, key0 + 32 * c);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!((see >> j) & 1u)) x[32 * c + j] = -INFINITY;
-                        }
-                    }
-                    float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
-#pragma unroll
-                    for (int j = 4; j < 128; j += 4) {
-                        t0 = fmaxf(t0, x[j]);
-                        t1 = fmaxf(t1, x[j + 1]);
-                        t2 = fmaxf(t2, x[j + 2]);
-                        t3 = fmaxf(t3, x[j + 3]);
-                    }
-                    const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sl;
-                    if (__any_sync(0xffffffffu, top > m_ref + kLazy || (m_ref == -INFINITY && top > -INFINITY))) {
-                        const float to = fmaxf(m_ref, top);
-                        const float corr = to == -INFINITY ? 1.f : fast_exp2(m_ref - to);
-                        m_ref = to;
-                        l *= corr;
-                        if (it > 0) {
-                            // the tile before has been added: S of this one was
-                            // issued after that product and has completed
-#pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + c * 32, o);
+            {
+                const int ctx = vb->ctx, n_rows = vb->n, ns = vb->ns, lo = vb->lo;
+                const int first_m = m0 + (pair ? wg * kTile : 0);
+                const int p0 = pair ? first_m / p.group : vb->p0;
+                const int p1 = pair ? (min(first_m + kTile, m0 + M) - 1) / p.group : vb->p1;
+                const RowView view = row_view(p, vb->i, ctx, n_rows, min((m0 + r) / p.group, n_rows - 1));
+                const int mine = pair ? n_tiles : (n_tiles + 1 - wg) >> 1;
+                for (int it = 0; it < mine; ++it) {
+                    const int t = t0 + (pair ? it : 2 * it + wg);
+                    const int key0 = (t < ns ? t : lo + t - ns) * kTile;
+                    const bool mixed = tile_mixed(p, ctx, n_rows, p0, p1, key0);
+                    ok = wait_or_fail(p, &bar.s_full[wg], n_s & 1);
+                    ++n_s;
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (busy) {
+                        if (mixed) {
+                            // few tiles: their scores are masked where they stand
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t see = seen32(view, key0 + 32 * c);
+                                uint32_t y[32];
+                                tmem_ld32(tS + c * 32, y);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-                                tmem_st32(tO + c * 32, o);
+                                for (int j = 0; j < 32; ++j)
+                                    if (!((see >> j) & 1u)) y[j] = 0xff800000u;
+                                tmem_st32(tS + c * 32, y);
+                            }
+                            tmem_st_wait();
+                        }
+                        // pass 1: the maximum.  The scores are read again for
+                        // pass 2, 32 at a time, the next 32 on their way: held
+                        // between the passes they would leave no registers to
+                        // overlap the exponentials with
+                        float top;
+                        {
+                            uint32_t x[4][32];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, x[c]);
+                            tmem_ld_wait();
+                            float y[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                y[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+#pragma unroll
+                                for (int j = 2; j < 32; j += 2)
+                                    y[c] = fmaxf(fmaxf(y[c], __uint_as_float(x[c][j])), __uint_as_float(x[c][j + 1]));
+                            }
+                            top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * sl;
+                        }
+                        uint32_t xs[2][32];
+                        tmem_ld32(tS, xs[0]);
+                        if (__any_sync(0xffffffffu, top > m_ref + kLazy)) {
+                            const float to = fmaxf(m_ref, top);
+                            const float corr = to == -INFINITY ? 1.f : fast_exp2(m_ref - to);
+                            m_ref = to;
+                            l *= corr;
+                            if (it > 0) {
+                                // the tile before has been added: S of this one was
+                                // issued after that product and has completed
+#pragma unroll 1
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t o[32];
+                                    tmem_ld32(tO + c * 32, o);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                                    tmem_st32(tO + c * 32, o);
+                                }
                             }
                         }
+                        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+                        uint32_t held[2][16];   // twice: remainders that wait for their columns
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_ld_wait();
+                            if (c < 3) tmem_ld32(tS + (c + 1) * 32, xs[(c + 1) & 1]);
+                            float y[32];
+                            uint32_t w[16];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(xs[c & 1][j]);
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) ffma2(y[j], y[j + 1], sl, neg);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = fast_exp2(y[j]);
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                fadd2(l0, l1, y[j], y[j + 1]);
+                                fadd2(l2, l3, y[j + 2], y[j + 3]);
+                                w[j / 2] = f32x2_to_bf16x2(y[j], y[j + 1]);
+                                w[j / 2 + 1] = f32x2_to_bf16x2(y[j + 2], y[j + 3]);
+                            }
+                            if (stacked || twice) {
+                                uint32_t u[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    u[j] = f32x2_to_bf16x2(y[2 * j] - __uint_as_float(w[j] << 16),
+                                                           y[2 * j + 1] - __uint_as_float(w[j] & 0xffff0000u));
+                                if (twice) {
+                                    // beside P, columns 64 .. 127: a piece waits until the scores there
+                                    // have been read
+                                    if (c >= 2) {
+#pragma unroll
+                                        for (int h = 0; h < (c == 2 ? 2 : 1); ++h)
+                                            tmem_st16(tS + 64 + (c == 2 ? h : 2) * 16, held[h]);
+                                    }
+                                    if (c == 3) tmem_st16(tS + 64 + 48, u);
+                                    else {
+#pragma unroll
+                                        for (int j = 0; j < 16; ++j) held[c & 1][j] = u[j];
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) w[j] = rest ? u[j] : w[j];
+                                }
+                            }
+                            tmem_st16(tS + c * 16, w);
+                        }
+                        l += (l0 + l1) + (l2 + l3);
+                        tmem_st_wait();
                     }
-                    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-                    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            float* y = x + 32 * c + j;
-                            ffma2(y[0], y[1], sl, neg);
-                            ffma2(y[2], y[3], sl, neg);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) y[e] = fast_exp2(y[e]);
-                            fadd2(l0, l1, y[0], y[1]);
-                            fadd2(l2, l3, y[2], y[3]);
-                            w[j / 2] = f32x2_to_bf16x2(y[0], y[1]);
-                            w[j / 2 + 1] = f32x2_to_bf16x2(y[2], y[3]);
-                        }
-                        if (stacked || twice) {
-                            uint32_t u[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float* y = x + 32 * c + 2 * j;
-                                u[j] = f32x2_to_bf16x2(y[0] - __uint_as_float(w[j] << 16),
-                                                       y[1] - __uint_as_float(w[j] & 0xffff0000u));
-                            }
-                            if (twice) {
-                                tmem_st16(tS + 64 + c * 16, u);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) w[j] = rest ? u[j] : w[j];
-                            }
-                        }
-                        tmem_st16(tS + c * 16, w);
+                    if (x_open) {
+                        // the other warpgroup has read this one's O of the block before
+                        ok = wait_or_fail(p, &bar.xdone, (n_x - 1) & 1);
+                        x_open = false;
+                        if (!ok) break;
                     }
-                    l += (l0 + l1) + (l2 + l3);
-                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.p_ready[wg]);
                 }
-                if (x_open && it == 0) {
-                    // the other warpgroup has read this one's O of the block before
-                    ok = wait_or_fail(p, &bar.xdone, (n_x - 1) & 1);
-                    x_open = false;
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_ready[wg]);
             }
             if (!ok) break;
             // ---- the block's end -------------------------------------------
-            const bool whole = k.t0 == 0 && k.t1 == k.g.n;
-            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (k.t0 > 0 ? 0 : 1);
-            if (blk == 0) share.head = k.t0 == 0 ? 0 : k.t1 == k.g.n ? 1 : 2;
-            if (k.t0 == 0 && !whole) {
-                share.rows = k.g.M;
-                share.row0 = k.w.row0;
-                share.m0 = k.g.m0;
-                share.hk = k.hk;
+            const int all = vb->tiles;
+            const bool whole = t0 == 0 && n_tiles == all;
+            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (t0 > 0 ? 0 : 1);
+            if (tid == 0) {
+                if (rd.n == 0) share.head = t0 == 0 ? 0 : t0 + n_tiles == all ? 1 : 2;
+                if (t0 == 0 && !whole) {
+                    share.rows = M;
+                    share.row0 = vb->row0;
+                    share.m0 = m0;
+                    share.hk = vb->hk;
+                }
             }
-            float a0 = 1.f, a1 = 0.f;      // weights of this warpgroup's o and the other's
+            float a0 = 1.f, a1 = 0.f;      // weights of the first and the second warpgroup's o
             const bool joined = !pair;
             if (joined) {
                 if (x_open) {              // only a block in which this warpgroup had no tile leaves it open
@@ -664,56 +793,57 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     x_open = false;
                     if (!ok) break;
                 }
-                xch[wg * kTile + row] = make_float2(m_ref, l);
+                if (!SMALL || !rest) xch[wg * C::kXchRows + (SMALL ? r : row)] = make_float2(m_ref, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.xch);
                 ok = wait_or_fail(p, &bar.xch, n_x & 1);
                 if (!ok) break;
-                const float2 other = xch[(wg ^ 1) * kTile + row];
+                const float2 other = xch[(wg ^ 1) * C::kXchRows + (SMALL ? r : row)];
                 const float mm = fmaxf(m_ref, other.x);
                 const float ref = mm == -INFINITY ? 0.f : mm;
-                a0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref);
-                a1 = other.x == -INFINITY ? 0.f : fast_exp2(other.x - ref);
-                l = l * a0 + other.y * a1;
+                const float b0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref);
+                const float b1 = other.x == -INFINITY ? 0.f : fast_exp2(other.x - ref);
+                l = l * b0 + other.y * b1;
                 m_ref = mm;
-                const int n0 = (n_tiles + 1) >> 1, n1 = n_tiles >> 1;
-                ok = wait_or_fail(p, &bar.o_full[0], n_o[0] & 1);
-                if (ok && n1 > 0) ok = wait_or_fail(p, &bar.o_full[1], n_o[1] & 1);
-                n_o[0] += n0 > 0;
-                n_o[1] += n1 > 0;
+                a0 = wg ? b1 : b0;
+                a1 = wg ? b0 : b1;
+                ok = wait_or_fail(p, &bar.o_full[0], n_o0 & 1);
+                if (ok && n_tiles > 1) ok = wait_or_fail(p, &bar.o_full[1], n_o1 & 1);
+                ++n_o0;
+                n_o1 += n_tiles > 1;
             } else {
-                ok = wait_or_fail(p, &bar.o_full[wg], n_o[wg] & 1);
-                ++n_o[0];
-                ++n_o[1];
+                ok = wait_or_fail(p, &bar.o_full[wg], (wg ? n_o1 : n_o0) & 1);
+                ++n_o0;
+                ++n_o1;
             }
             if (!ok) break;
             tc_fence_after();
-            const bool odd = nonfin[blk & 15] == blk + 1;
-            const int none = joined && n_tiles < 2;    // the second warpgroup's o was never written
-            const int c0 = joined ? wg * (D / 64) : 0, c1 = joined ? c0 + D / 64 : D / 32;
             if (busy) {
-                const int h = k.hk * p.group + m % p.group;
-                const size_t at = (static_cast<size_t>(k.w.row0) + m / p.group) * p.H + h;
+                const int m = m0 + r, hk = vb->hk;
+                const bool valid = r < M && !rest;
+                const int wp = m / p.group;
+                const size_t at = (static_cast<size_t>(vb->row0) + wp) * p.H + hk * p.group + (m - wp * p.group);
+                const bool odd = vb->nonfinite != 0;
                 const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+                const bool other_o = joined && n_tiles > 1;   // else the second warpgroup's o was never written
+                const int c0 = joined ? wg * (D / 64) : 0, c1 = joined ? c0 + D / 64 : D / 32;
+#pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
-                    uint32_t o[32];
+                    uint32_t o[32], q[32];
                     float f[32];
                     tmem_ld32((joined ? tO0 : tO) + c * 32, o);
+                    if (other_o) tmem_ld32(tO1 + c * 32, q);
                     tmem_ld_wait();
-                    if (joined) {
-                        const float w0 = wg ? a1 : a0, w1 = wg ? a0 : a1;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) f[j] = w0 == 0.f ? 0.f : __uint_as_float(o[j]) * w0;
-                        if (!none) {
-                            tmem_ld32(tO1 + c * 32, o);
-                            tmem_ld_wait();
+                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]);
+                    if (joined) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = a0 == 0.f ? 0.f : f[j] * a0;
+                        if (other_o) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                f[j] = w1 == 0.f ? f[j] : fmaf(__uint_as_float(o[j]), w1, f[j]);
+                                f[j] = a1 == 0.f ? f[j] : fmaf(__uint_as_float(q[j]), a1, f[j]);
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]);
                     }
                     if (stacked) {
 #pragma unroll
@@ -724,27 +854,36 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     }
                     if (odd && valid) {
                         float g[32];
-                        const Window w2 = k.w;
-                        const Geom g2 = k.g;
+                        const Blk blk = copy(vb);
                         for (int j = 0; j < 32; ++j) g[j] = f[j];
-                        add_nonfinite<D, E4M3>(p, w2, g2, k.i, k.hk, k.t0, k.t1, m, m_ref, c * 32, g);
+                        add_nonfinite<D, E4M3>(p, blk, m, m_ref, c * 32, g);
                         for (int j = 0; j < 32; ++j) f[j] = g[j];
                     }
-                    if (whole && valid) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + c * 32);
+                    if (valid && whole) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float* y = f + 8 * j;
-                            dst[j] = make_uint4(f32x2_to_bf16x2(y[0] * inv, y[1] * inv),
-                                                f32x2_to_bf16x2(y[2] * inv, y[3] * inv),
-                                                f32x2_to_bf16x2(y[4] * inv, y[5] * inv),
-                                                f32x2_to_bf16x2(y[6] * inv, y[7] * inv));
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                y[j] = f32x2_to_bf16x2(f[16 * h + 2 * j] * inv, f[16 * h + 2 * j + 1] * inv);
+                            // out is 16-byte aligned: 32-byte stores where it is more
+                            uint16_t* dst = p.out + at * D + c * 32 + h * 16;
+                            if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
+                                store_v8(dst, y);
+                            } else {
+                                reinterpret_cast<uint4*>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                                reinterpret_cast<uint4*>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                            }
                         }
                     } else if (valid) {
-                        float4* dst = reinterpret_cast<float4*>(ws.o + (slot * ws.cap + r) * D + c * 32);
+                        float* dst = ws.o + (slot * ws.cap + r) * D + c * 32;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) y[j] = __float_as_uint(f[8 * h + j]);
+                            store_v8(dst + 8 * h, y);
+                        }
                     }
                     __syncwarp();
                 }
@@ -760,13 +899,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                 ++n_x;
                 x_open = true;
             }
-            ++blk;
+            release();
         }
-        if (tid == 0 && work) ws.share[blockIdx.x] = share;
+        if (tid == 0) ws.share[blockIdx.x] = share;
     } else if (warp < 12) {
-        set_regs_down<C::kRegsRest>();
-        Walk k;
-        k.init(st);
+        set_regs_down<kRegsRest>();
+        bool ok = true;
         if (warp == 8) {
             // ----------------------------------------------------------------
             // producer: K and V tiles in turn, a lane per page
@@ -777,26 +915,30 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             uint64_t* full = E4M3 ? bar.raw_full : bar.full;
             uint64_t* empty = E4M3 ? bar.raw_empty : bar.empty;
             uint32_t n = 0, dirty = 0, odd_full = 0, odd_dirty = 0;   // per slot: the barrier armed last, phases mod 2
-            bool ok = true;
-            while (ok && work && k.next(p)) {
-                const int len = k.w.ctx + k.w.n;
-                for (int t = k.t0; t < k.t1 && ok; ++t) {
-                    const int key0 = tile_key(k.g, t);
-                    const bool cleaned = !E4M3 && tile_cleaned(p, k.w, k.g, key0);
+            int s = 0;
+            uint32_t turn = 0;
+            for (;;) {
+                const volatile Blk* vb = take(ok);
+                if (!vb) break;
+                const Blk b = copy(vb);
+                release();
+                const int len = b.ctx + b.n;
+                for (int t = b.t0; t < b.t1 && ok; ++t) {
+                    const int key0 = tile_key(b, t);
+                    const bool cleaned = !E4M3 && tile_cleaned(p, b, key0);
                     const int live = min(pages, (len - key0 + page - 1) >> p.c.page_shift);
                     int pg = 0;
                     if (lane < live) {
-                        pg = page_of(p.c, k.i, key0 + lane * page);
+                        pg = page_of(p.c, b.i, key0 + lane * page);
                         if (pg < 0) {
                             set_status(p.dev_status, SDM_DEV_BAD_PAGE);
                             pg = 0;
                         }
                     }
-                    const int y = (pg * p.c.heads + k.hk) << p.c.page_shift;
+                    const int y = (pg * p.c.heads + b.hk) << p.c.page_shift;
                     const uint32_t bytes = static_cast<uint32_t>(live) * page * (E4M3 ? D + 1 : 2 * D);
-                    for (int v = 0; v < 2 && ok; ++v, ++n) {
-                        const int s = n % kN;
-                        if (n >= kN) ok = wait_or_fail(p, &empty[s], ((n / kN) - 1) & 1);
+                    for (int v = 0; v < 2; ++v) {
+                        if (turn > 0) ok = wait_or_fail(p, &empty[s], (turn - 1) & 1);
                         if (!ok) break;
                         const bool to_dirty = cleaned && v == 1;
                         uint64_t* arrive = to_dirty ? &bar.dirty[s] : &full[s];
@@ -814,21 +956,27 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                                           page, arrive);
                             } else {
 #pragma unroll
-                                for (int h = 0; h < C::kHalves; ++h)
+                                for (int h = 0; h < D / 64; ++h)
                                     tma_load_2d(smem + C::kRing + s * C::kTileBytes + h * (kTile * 128) +
                                                     lane * page * kRow,
                                                 v ? &tmV : &tmK, arrive, h * 64, y);
                             }
                         }
                         __syncwarp();
+                        ++n;
+                        if (++s == kN) {
+                            s = 0;
+                            ++turn;
+                        }
                     }
                 }
+                if (!ok) break;
             }
             if (!ok) {
                 // copies in flight land before the CTA may exit
-                for (uint32_t s = 0; s < kN && s < n; ++s) {
-                    if ((dirty >> s) & 1u) mbar_wait(&bar.dirty[s], ((odd_dirty >> s) & 1u) ^ 1u);
-                    else mbar_wait(&full[s], ((odd_full >> s) & 1u) ^ 1u);
+                for (uint32_t k = 0; k < kN && k < n; ++k) {
+                    if ((dirty >> k) & 1u) mbar_wait(&bar.dirty[k], ((odd_dirty >> k) & 1u) ^ 1u);
+                    else mbar_wait(&full[k], ((odd_full >> k) & 1u) ^ 1u);
                 }
             }
         } else if (warp == 9) {
@@ -840,198 +988,236 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::kRing), 16, 1024);
             const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kRing), kTile * 128, 1024);
-            uint32_t n_t = 0, n_q = 0, n_p[2] = {0, 0}, full_phase = 0, clean_phase = 0;
-            bool ok = true;
-            // tile t of the current block, counted over the CTA's share
-            auto slot_of = [&](uint32_t t, int v) { return (2 * t + v) % C::kSlots; };
+            uint32_t n_q = 0, n_p0 = 0, n_p1 = 0, full_phase = 0, clean_phase = 0;
+            int sk = 0, sv = 1;    // slots of the next K tile and the next V tile to be multiplied
             auto wait_full = [&](int s) {
                 const bool r = wait_or_fail(p, &bar.full[s], (full_phase >> s) & 1);
                 full_phase ^= 1u << s;
                 return r;
             };
-            auto wait_k = [&](uint32_t t) { return wait_full(slot_of(t, 0)); };
-            auto wait_v = [&](uint32_t t, int tile) {
-                const int s = slot_of(t, 1);
-                if (E4M3 || !tile_cleaned(p, k.w, k.g, tile_key(k.g, tile))) return wait_full(s);
-                const bool r = wait_or_fail(p, &bar.clean[s], (clean_phase >> s) & 1);
-                clean_phase ^= 1u << s;
+            auto wait_v = [&](bool cleaned) {
+                if (E4M3 || !cleaned) return wait_full(sv);
+                const bool r = wait_or_fail(p, &bar.clean[sv], (clean_phase >> sv) & 1);
+                clean_phase ^= 1u << sv;
                 return r;
             };
-            auto qk = [&](int wg, int q, uint32_t t) {
+            auto next = [&](int s) { return s + 2 >= C::kSlots ? s + 2 - C::kSlots : s + 2; };
+            auto qk = [&](int wg, int q) {
                 const uint64_t a = q_desc + static_cast<uint64_t>(q * (C::kQBytes >> 4));
-                const uint64_t b = k_desc + static_cast<uint64_t>(slot_of(t, 0) * (C::kTileBytes >> 4));
+                const uint64_t b = k_desc + static_cast<uint64_t>(sk * (C::kTileBytes >> 4));
+                tc_fence_after();
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint64_t off = static_cast<uint64_t>((ks >> 2) * ((kTile * 128) >> 4) + (ks & 3) * 2);
-                    mma_bf16_warp(tmem + wg * 128, a + off, b + off, kIdQK, ks > 0);
-                }
+                for (int h = 0; h < D / 64; ++h)
+                    issue_qk4(tmem + wg * 128, a + h * ((kTile * 128) >> 4), b + h * ((kTile * 128) >> 4), kIdQK, h > 0);
                 mma_commit_warp(&bar.s_full[wg]);
             };
-            auto pv = [&](int wg, uint32_t t, bool add) {
-                const uint64_t b = v_desc + static_cast<uint64_t>(slot_of(t, 1) * (C::kTileBytes >> 4));
-#pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
-                    mma_bf16_ts_warp(tmem + 256 + wg * 128, tmem + wg * 128 + ks * 8,
-                                     b + static_cast<uint64_t>(ks * (2048 >> 4)), kIdPV, add || ks > 0);
-                if (k.g.twice) {
-#pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        mma_bf16_ts_warp(tmem + 256 + wg * 128, tmem + wg * 128 + 64 + ks * 8,
-                                         b + static_cast<uint64_t>(ks * (2048 >> 4)), kIdPV, 1);
+            auto pv = [&](int wg, bool add, bool twice) {
+                const uint64_t b = v_desc + static_cast<uint64_t>(sv * (C::kTileBytes >> 4));
+                const uint32_t o = tmem + 256 + wg * 128, a = tmem + wg * 128;
+                issue_pv4(o, a, b, kIdPV, add);
+                issue_pv4(o, a + 32, b + 512, kIdPV, 1);
+                if (twice) {
+                    issue_pv4(o, a + 64, b, kIdPV, 1);
+                    issue_pv4(o, a + 96, b + 512, kIdPV, 1);
                 }
             };
             auto wait_p = [&](int wg) {
-                const bool r = wait_or_fail(p, &bar.p_ready[wg], n_p[wg] & 1);
-                ++n_p[wg];
+                const bool r = wait_or_fail(p, &bar.p_ready[wg], (wg ? n_p1 : n_p0) & 1);
+                if (wg) ++n_p1;
+                else ++n_p0;
                 tc_fence_after();
                 return r;
             };
-            while (ok && work && k.next(p)) {
-                const int n = k.t1 - k.t0;
-                const uint32_t base = n_t;
-                n_t += n;
+            for (;;) {
+                const volatile Blk* vb = take(ok);
+                if (!vb) break;
+                const Blk b = copy(vb);
+                release();
+                const int n = b.t1 - b.t0;
+                const bool twice = !SMALL && (b.flags & BLK_TWICE);
                 ok = wait_or_fail(p, &bar.q_full, n_q & 1);
                 ++n_q;
                 if (!ok) break;
-                if (k.g.weight == 2) {
-                    for (int t = 0; t <= n && ok; ++t) {
-                        if (t < n) ok = wait_k(base + t);
-                        for (int wg = 0; wg < 2 && ok; ++wg) {
+                if (!SMALL && (b.flags & BLK_PAIR)) {
+                    for (int t = 0; t <= n; ++t) {
+                        if (t < n) ok = wait_full(sk);
+                        if (ok && t > 0) ok = wait_v(tile_cleaned(p, b, tile_key(b, b.t0 + t - 1)));
+                        if (!ok) break;
+#pragma unroll
+                        for (int wg = 0; wg < 2; ++wg) {
                             if (t > 0) {
-                                if (wg == 0) ok = wait_v(base + t - 1, k.t0 + t - 1);
-                                ok = ok && wait_p(wg);
+                                ok = wait_p(wg);
                                 if (!ok) break;
-                                pv(wg, base + t - 1, t > 1);
+                                pv(wg, t > 1, twice);
                                 if (t == n) mma_commit_warp(&bar.o_full[wg]);
                             }
-                            if (t < n) {
-                                tc_fence_after();
-                                qk(wg, wg, base + t);
-                            }
+                            if (t < n) qk(wg, wg);
                         }
                         if (!ok) break;
-                        if (t < n) mma_commit_warp(&bar.empty[slot_of(base + t, 0)]);
-                        if (t > 0) mma_commit_warp(&bar.empty[slot_of(base + t - 1, 1)]);
+                        if (t < n) {
+                            mma_commit_warp(&bar.empty[sk]);
+                            sk = next(sk);
+                        }
+                        if (t > 0) {
+                            mma_commit_warp(&bar.empty[sv]);
+                            sv = next(sv);
+                        }
                         if (t == n - 1) mma_commit_warp(&bar.q_empty);
                     }
                 } else {
-                    for (int t = 0; t < n + 2 && ok; ++t) {
+                    for (int t = 0; t < n + 2; ++t) {
                         const int wg = t & 1;
                         if (t >= 2) {
-                            ok = wait_v(base + t - 2, k.t0 + t - 2) && wait_p(wg);
+                            ok = wait_v(tile_cleaned(p, b, tile_key(b, b.t0 + t - 2))) && wait_p(wg);
                             if (!ok) break;
-                            pv(wg, base + t - 2, t >= 4);
+                            pv(wg, t >= 4, twice);
                             if (t >= n) mma_commit_warp(&bar.o_full[wg]);
-                            mma_commit_warp(&bar.empty[slot_of(base + t - 2, 1)]);
+                            mma_commit_warp(&bar.empty[sv]);
+                            sv = next(sv);
                         }
                         if (t < n) {
-                            ok = wait_k(base + t);
+                            ok = wait_full(sk);
                             if (!ok) break;
-                            tc_fence_after();
-                            qk(wg, 0, base + t);
-                            mma_commit_warp(&bar.empty[slot_of(base + t, 0)]);
+                            qk(wg, 0);
+                            mma_commit_warp(&bar.empty[sk]);
+                            sk = next(sk);
                             if (t == n - 1) mma_commit_warp(&bar.q_empty);
                         }
                     }
                 }
+                if (!ok) break;
             }
             if (!ok) {   // this warp's own tensor-core work ends before tensor memory is freed
                 mma_commit_warp(&bar.drain);
                 mbar_wait(&bar.drain, 0);
             }
-        } else {
+        } else if (warp == 10) {
             // ----------------------------------------------------------------
-            // Q rows of each block; bf16: then the values of its partly seen tiles
+            // Q rows of each block, a lane per row
             // ----------------------------------------------------------------
-            constexpr int kChunks = D / 8;                // 16-byte pieces of a row
-            constexpr int kStep = 64 / kChunks;           // rows per pass of the two warps
-            const int t64 = tid & 63;
-            uint32_t n_q = 0, n_t = 0, dirty_phase = 0;
-            bool ok = true;
-            int blk = 0;
-            while (ok && work && k.next(p)) {
+            uint32_t n_q = 0;
+            for (;;) {
+                const volatile Blk* vb = take(ok);
+                if (!vb) break;
+                const int row0 = vb->row0, m0 = vb->m0, M = vb->M, hk = vb->hk;
+                const bool stacked = SMALL || (vb->flags & BLK_STACKED);
+                release();
                 if (n_q > 0) ok = wait_or_fail(p, &bar.q_empty, (n_q - 1) & 1);
                 ++n_q;
                 if (!ok) break;
-                const int c = t64 % kChunks;
-                int r = t64 / kChunks;
-                int wp = (k.g.m0 + r) / p.group, h = (k.g.m0 + r) % p.group;
-                for (; r < k.g.M; r += kStep) {
-                    const uint16_t* src = p.q + (k.w.row0 + wp) * p.q_stride +
-                                          static_cast<size_t>(k.hk * p.group + h) * D + c * 8;
-                    const int to = k.g.stacked ? (r >> 4) * 32 + (r & 15) : r;   // 16 rows keep r mod 8 and the swizzle
-                    uint8_t* dst = smem + (to >> 7) * C::kQBytes + (c >> 3) * (kTile * 128) + (to & 127) * 128 +
-                                   (((c & 7) ^ (to & 7)) << 4);
-                    cp_async_16(dst, src, 16u);
-                    if (k.g.stacked) cp_async_16(dst + 16 * 128, src, 16u);
-                    h += kStep;
-                    while (h >= p.group) {
-                        h -= p.group;
-                        ++wp;
+                for (int r = lane; r < M; r += 32) {
+                    const int m = m0 + r, wp = m / p.group;
+                    const uint16_t* src = p.q + (row0 + wp) * p.q_stride +
+                                          static_cast<size_t>(hk * p.group + (m - wp * p.group)) * D;
+                    const int to = stacked ? (r >> 4) * 32 + (r & 15) : r;   // 16 rows keep r mod 8 and the swizzle
+                    const uint32_t dst = (to >> 7) * C::kQBytes + (to & 127) * 128 + ((to & 7) << 4);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint8_t* d = smem + (c >> 3) * (kTile * 128) + (dst ^ ((c & 7) << 4));
+                        cp_async_16(d, src + c * 8, 16u);
+                        if (stacked) cp_async_16(d + 16 * 128, src + c * 8, 16u);
                     }
                 }
                 cp_async_wait_all();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.q_full);
+            }
+        } else {
+            // ----------------------------------------------------------------
+            // the share's blocks, in turn, for the other warps
+            // ----------------------------------------------------------------
+            Walk k;
+            k.init(st);
+            bool more = st.u0 < st.u1;
+            for (uint32_t n = 0;; ++n) {
+                more = more && k.next(p);
+                const int e = n % C::kRingBlocks;
+                if (n >= C::kRingBlocks && !wait_or_fail(p, &bar.blk_empty[e], ((n / C::kRingBlocks) - 1) & 1)) break;
+                if (lane == 0) {
+                    Blk b = {};
+                    if (more) {
+                        b.i = k.i;
+                        b.hk = k.hk;
+                        b.row0 = k.w.row0;
+                        b.n = k.w.n;
+                        b.ctx = k.w.ctx;
+                        b.m0 = k.g.m0;
+                        b.M = k.g.M;
+                        b.p0 = k.g.p0;
+                        b.p1 = k.g.p1;
+                        b.ns = k.g.ns;
+                        b.lo = k.g.lo;
+                        b.tiles = k.g.n;
+                        b.t0 = k.t0;
+                        b.t1 = k.t1;
+                        b.flags = (k.g.weight == 2 ? BLK_PAIR : 0) | (k.g.stacked ? BLK_STACKED : 0) |
+                                  (k.g.twice ? BLK_TWICE : 0);
+                    }
+                    blks[e] = b;
+                    mbar_arrive(&bar.blk_full[e]);
+                }
+                __syncwarp();
+                if (!more) break;
+            }
+        }
+    } else {
+        set_regs_down<kRegsRest>();
+        bool ok = true;
+        const int row = tid & 127;
+        int s = 0, rs = 0;
+        uint32_t turn = 0, raw_turn = 0, dirty_phase = 0;
+        for (;;) {
+            const volatile Blk* vb = take(ok);
+            if (!vb) break;
+            const Blk b = copy(vb);
+            const int len = b.ctx + b.n;
+            bool found = false;    // a value that is not finite, cleared
+            for (int t = b.t0; t < b.t1 && ok; ++t) {
+                const int key0 = tile_key(b, t);
+                const bool cleaned = tile_cleaned(p, b, key0);
                 if constexpr (!E4M3) {
-                    const int len = k.w.ctx + k.w.n;
-                    for (int t = k.t0; t < k.t1 && ok; ++t) {
-                        const int key0 = tile_key(k.g, t);
-                        if (!tile_cleaned(p, k.w, k.g, key0)) continue;
-                        const uint32_t idx = 2 * (n_t + (t - k.t0)) + 1;
-                        const int s = idx % C::kSlots;
-                        ok = wait_or_fail(p, &bar.dirty[s], (dirty_phase >> s) & 1);
-                        dirty_phase ^= 1u << s;
-                        if (!ok) break;
-                        uint4* v = reinterpret_cast<uint4*>(smem + C::kRing + s * C::kTileBytes);
-                        bool found = false;
-#pragma unroll 4
-                        for (int e = t64; e < C::kTileBytes / 16; e += 64) {
-                            uint4 x = v[e];
+                    // ------------------------------------------------------------
+                    // bf16: values of the tiles to be cleared, a key's row per thread
+                    // ------------------------------------------------------------
+                    const int sv = s + 1 >= C::kSlots ? s + 1 - C::kSlots : s + 1;
+                    s = s + 2 >= C::kSlots ? s + 2 - C::kSlots : s + 2;
+                    if (!cleaned) continue;
+                    ok = wait_or_fail(p, &bar.dirty[sv], (dirty_phase >> sv) & 1);
+                    dirty_phase ^= 1u << sv;
+                    if (!ok) break;
+                    uint8_t* v = smem + C::kRing + sv * C::kTileBytes + row * 128;
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            // pieces in an order that keeps the threads of a quarter-warp on different banks
+                            uint4* at = reinterpret_cast<uint4*>(v + h * (kTile * 128) + ((c ^ (row & 7)) << 4));
+                            uint4 x = *at;
                             if (nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) {
-                                uint32_t* u = reinterpret_cast<uint32_t*>(&x);
+                                uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
                                     const uint32_t bad = nonfinite2(u[j]);
                                     if (bad & 0x8000u) u[j] &= 0xffff0000u;
                                     if (bad & 0x80000000u) u[j] &= 0xffffu;
                                 }
-                                v[e] = x;
-                                found |= key0 + ((e >> 3) & (kTile - 1)) < len;
+                                *at = make_uint4(u[0], u[1], u[2], u[3]);
+                                found |= key0 + row < len;
                             }
                         }
-                        if (found) nonfin[blk & 15] = blk + 1;
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.clean[s]);
                     }
-                    n_t += k.t1 - k.t0;
-                }
-                ++blk;
-            }
-        }
-    } else {
-        // --------------------------------------------------------------------
-        // e4m3 codes -> bf16 values, one key's row per thread
-        // --------------------------------------------------------------------
-        if constexpr (E4M3) {
-            set_regs_down<C::kRegsRest>();
-            Walk k;
-            k.init(st);
-            const int row = tid & 127;
-            uint32_t n = 0;
-            bool ok = true;
-            int blk = 0;
-            while (ok && work && k.next(p)) {
-                const int len = k.w.ctx + k.w.n;
-                for (int t = k.t0; t < k.t1 && ok; ++t) {
-                    const int key0 = tile_key(k.g, t);
-                    const bool cleaned = tile_cleaned(p, k.w, k.g, key0);
-                    for (int v = 0; v < 2; ++v, ++n) {
-                        const int s = n % C::kSlots, rs = n % C::kRawSlots;
-                        if (n >= C::kSlots) ok = wait_or_fail(p, &bar.empty[s], ((n / C::kSlots) - 1) & 1);
-                        ok = ok && wait_or_fail(p, &bar.raw_full[rs], (n / C::kRawSlots) & 1);
+                    if (found) blks[rd.at()].nonfinite = 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.clean[sv]);
+                } else {
+                    // ------------------------------------------------------------
+                    // e4m3 codes -> bf16 values, a key's row per thread
+                    // ------------------------------------------------------------
+                    for (int v = 0; v < 2; ++v) {
+                        if (turn > 0) ok = wait_or_fail(p, &bar.empty[s], (turn - 1) & 1);
+                        ok = ok && wait_or_fail(p, &bar.raw_full[rs], raw_turn & 1);
                         if (!ok) break;
                         const uint8_t* src = smem + C::kRaw + rs * C::kRawBytes + row * D;
                         uint8_t* dst = smem + C::kRing + s * C::kTileBytes + row * 128;
@@ -1040,7 +1226,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                         const uint32_t sc = e << 7;
                         const uint32_t scale2 = sc | (sc << 16);
                         const bool clear = cleaned && v == 1;
-                        bool found = false;
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
                             // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
@@ -1053,9 +1238,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                             for (int j = 0; j < 8; ++j) {
                                 const float2 f = f16x2_to_f32x2(
                                     e4m3x2_to_f16x2(static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1)))));
-                                uint32_t b = f32x2_to_bf16x2(f.x, f.y);
-                                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(scale2));
-                                o[j] = b;
+                                uint32_t y = f32x2_to_bf16x2(f.x, f.y);
+                                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(scale2));
+                                o[j] = y;
                             }
                             if (clear) {
 #pragma unroll
@@ -1063,7 +1248,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                                     const uint32_t bad = nonfinite2(o[j]);
                                     if (bad & 0x8000u) o[j] &= 0xffff0000u;
                                     if (bad & 0x80000000u) o[j] &= 0xffffu;
-                                    found |= bad != 0;
+                                    found |= bad != 0 && key0 + row < len;
                                 }
                             }
 #pragma unroll
@@ -1074,17 +1259,26 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                                     make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
                             }
                         }
-                        if (found && key0 + row < len) nonfin[blk & 15] = blk + 1;
+                        if (found) blks[rd.at()].nonfinite = 1;
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(&bar.raw_empty[rs]);
                             mbar_arrive(&bar.full[s]);
                         }
+                        if (++s == C::kSlots) {
+                            s = 0;
+                            ++turn;
+                        }
+                        if (++rs == C::kRawSlots) {
+                            rs = 0;
+                            ++raw_turn;
+                        }
                     }
                 }
-                ++blk;
             }
+            if (!ok) break;
+            release();
         }
     }
 
@@ -1187,13 +1381,13 @@ bool encode(CUtensorMap* map, const CacheView& c, void* pool) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool SMALL>
 cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
-    using C = Cfg<D, E4M3>;
+    using C = Cfg<D, E4M3, SMALL>;
     static bool configured = false;
     if (!configured) {
-        const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   C::kTotal);
+        const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, E4M3, SMALL>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
         if (e != cudaSuccess) return e;
         configured = true;
     }
@@ -1208,7 +1402,8 @@ cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
     ws.ml = reinterpret_cast<float2*>(at);
     at += align256(2 * static_cast<size_t>(grid) * ws.cap * sizeof(float2));
     ws.o = reinterpret_cast<float*>(at);
-    cudaError_t e = launch_pdl(attend_kernel<D, E4M3>, dim3(grid), dim3(C::kThreads), C::kTotal, s, tmK, tmV, p, ws);
+    cudaError_t e =
+        launch_pdl(attend_kernel<D, E4M3, SMALL>, dim3(grid), dim3(kThreads), C::kTotal, s, tmK, tmV, p, ws);
     if (e != cudaSuccess) return e;
     return launch_pdl(attend_merge_kernel<D>, dim3(grid, std::min(4, (ws.cap + 7) / 8)), dim3(256), 0, s, p, ws, grid);
 }
@@ -1223,9 +1418,17 @@ size_t attend_workspace(int R, int max_window, int H, int D, int rows, int kv_he
     return align256(sizeof(Share) * grid) + align256(2 * grid * cap * sizeof(float2)) + 2 * grid * cap * D * 4;
 }
 
+// SMALL: every block has at most kStackRows rows, so one sub-tile of Q and the
+// stream form do, and the shared memory of the other goes to the ring.
+template <int D, bool E4M3>
+static cudaError_t launch_form(const AttendParams& p, void* ws, cudaStream_t s) {
+    const bool small = static_cast<long long>(p.max_window) * p.group <= kStackRows;
+    return small ? launch_one<D, E4M3, true>(p, ws, s) : launch_one<D, E4M3, false>(p, ws, s);
+}
+
 cudaError_t launch_attend(const AttendParams& p, void* ws, cudaStream_t s) {
-    if (p.c.D == 64) return p.c.e4m3 ? launch_one<64, true>(p, ws, s) : launch_one<64, false>(p, ws, s);
-    return p.c.e4m3 ? launch_one<128, true>(p, ws, s) : launch_one<128, false>(p, ws, s);
+    if (p.c.D == 64) return p.c.e4m3 ? launch_form<64, true>(p, ws, s) : launch_form<64, false>(p, ws, s);
+    return p.c.e4m3 ? launch_form<128, true>(p, ws, s) : launch_form<128, false>(p, ws, s);
 }
 
 }  // namespace sdm
