@@ -22,12 +22,12 @@
 // a cut splits leave (m, l, o) in the workspace and attend_merge_kernel joins
 // them in the order of the keys, so results do not depend on timing.
 //
-// Pipeline of a CTA (sixteen warps): one walks the share and hands each block
+// Pipeline of a CTA: one warp walks the share and hands each block
 // to the others; a producer brings K and V tiles page by page with TMA into a
-// ring; one gathers Q; one issues S = Q K^T and O += P V; eight do the
-// softmax, S from tensor memory to registers and P back over S; four clear
-// (bf16) or convert (e4m3: codes to bf16, exactly, the scale included, into a
-// second ring) the tiles.  Each softmax warpgroup's S, P and O are its own, so
+// ring; one gathers Q and clears values (below); one issues S = Q K^T and O +=
+// P V; eight do the softmax, S from tensor memory to registers and P back over
+// S; e4m3: four turn codes into bf16, exactly, the scale included, in a second
+// ring.  Each softmax warpgroup's S, P and O are its own, so
 // one's softmax runs beside the other's products.
 //
 // What a row does not see does not reach it: scores are replaced, not added
@@ -53,15 +53,12 @@ constexpr float kLazy = 8.0f;
 // multiplied too: as rows of the same product where the block leaves half of
 // the 128 lanes free (row r in lane r of its 16, the remainder 16 lanes on),
 // by a second product in blocks of at most kFineTiles key tiles.
+// What a block costs besides its tiles (Q, the first product, the last O), in
+// the units of the shares: one key tile of one sub-tile.
+constexpr int kBlockCost = 6;
 constexpr int kStackRows = 64;
 constexpr int kFineTiles = 9;
 constexpr int kTmemCols = 512;        // S0, S1, O0, O1 at columns 0, 128, 256, 384; P over S
-
-constexpr int kThreads = 512;
-// registers of a thread: the softmax warpgroups', the others' (together the
-// launch's own 4 x 128)
-constexpr int kRegsSoft = 184, kRegsRest = 72;
-static_assert(2 * kRegsSoft + 2 * kRegsRest == 4 * 128, "registers");
 
 // One block, as the walking warp hands it to the others.
 struct Blk {
@@ -74,6 +71,11 @@ enum { BLK_PAIR = 1, BLK_STACKED = 2, BLK_TWICE = 4 };
 
 template <int D, bool E4M3, bool SMALL>
 struct Cfg {
+    static constexpr int kThreads = E4M3 ? 512 : 384;
+    // registers of a thread: the softmax warpgroups', the others' (together
+    // the launch's own: 4 x 128 and 3 x 168)
+    static constexpr int kRegsSoft = E4M3 ? 184 : 208, kRegsRest = E4M3 ? 72 : 88;
+    static_assert(E4M3 ? 2 * kRegsSoft + 2 * kRegsRest == 4 * 128 : 2 * kRegsSoft + kRegsRest == 3 * 168, "registers");
     static constexpr int kQBytes = kTile * D * 2;            // one 128-row sub-tile
     static constexpr int kTileBytes = kTile * D * 2;         // one bf16 K or V tile
     static constexpr int kQs = SMALL ? 1 : 2;                // sub-tiles of Q
@@ -89,7 +91,7 @@ struct Cfg {
     static constexpr int kXch = kExps + kRawSlots * kTile;   // (m, l) of both warpgroups' rows
     static constexpr int kBlks = kXch + 2 * kXchRows * 8;
     static constexpr int kBars = kBlks + kRingBlocks * static_cast<int>(sizeof(Blk));
-    static constexpr int kNumBars = 4 * kSlots + 2 * (kRawSlots > 0 ? kRawSlots : 1) + 2 * kRingBlocks + 11;
+    static constexpr int kNumBars = (E4M3 ? 2 * kSlots + 2 : 4 * kSlots) + 2 * (kRawSlots > 0 ? kRawSlots : 1) + 2 * kRingBlocks + 13;
     static constexpr int kMisc = kBars + kNumBars * 8;
     static constexpr int kTotal = kMisc + 16;
     static_assert(kTotal <= 232448, "shared memory");
@@ -188,7 +190,7 @@ struct Walk {
     }
 
     __device__ __forceinline__ bool next(const AttendParams& p) {
-        if (have >= 0) us += static_cast<unsigned long long>(g.n) * g.weight;
+        if (have >= 0) us += kBlockCost + g.n * g.weight;
         for (;;) {
             if (us >= u1) return false;
             if (++hk >= p.c.heads) {
@@ -211,11 +213,12 @@ struct Walk {
                 have_b = b;
             }
             const unsigned wt = g.weight;   // 1 or 2
-            t0 = us < u0 ? static_cast<int>((u0 - us + wt - 1) >> (wt - 1)) : 0;
-            const unsigned long long left = (u1 - us + wt - 1) >> (wt - 1);
+            const unsigned long long at = us + kBlockCost;   // unit of the first tile
+            t0 = at < u0 ? static_cast<int>((u0 - at + wt - 1) >> (wt - 1)) : 0;
+            const unsigned long long left = at < u1 ? (u1 - at + wt - 1) >> (wt - 1) : 0;
             t1 = left < static_cast<unsigned long long>(g.n) ? static_cast<int>(left) : g.n;
             if (t0 < t1) return true;
-            us += static_cast<unsigned long long>(g.n) * wt;
+            us += kBlockCost + g.n * wt;
         }
     }
 };
@@ -226,6 +229,7 @@ __device__ __forceinline__ unsigned long long shfl_up64(unsigned long long v, in
 
 // This CTA's share of the units (key tiles times their weight) of all blocks,
 // and where it starts.  cost: shared memory for R entries.
+template <int kThreads>
 __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* cost, Start* start,
                                      unsigned long long* wsum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -239,7 +243,7 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
             unsigned long long c = 0;
             for (int b = 0; b < blocks_of(p, w); ++b) {
                 const Geom g = geom_of(p, w, b);
-                c += static_cast<unsigned long long>(g.n) * g.weight;
+                c += static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
             }
             cost[i] = c * p.c.heads;
         }
@@ -250,7 +254,7 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
             unsigned long long c = 0;
             for (int b = lane; b < blocks_of(p, w); b += 32) {
                 const Geom g = geom_of(p, w, b);
-                c += static_cast<unsigned long long>(g.n) * g.weight;
+                c += static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
@@ -305,7 +309,7 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
             unsigned long long one = 0;
             if (b < nb) {
                 const Geom g = geom_of(p, w, b);
-                one = static_cast<unsigned long long>(g.n) * g.weight;
+                one = static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
             }
             unsigned long long sum = one * p.c.heads;
 #pragma unroll
@@ -344,7 +348,7 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
 // ---------------------------------------------------------------------------
 // One short loop (the callers' loops have to fit the instruction cache).
 __device__ __forceinline__ bool wait_or_fail(const AttendParams& p, uint64_t* bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;   // one answer for the whole warp
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1)) return true;   // one answer a warp
     const uint64_t t0 = globaltimer();
 #pragma unroll 1
     do {
@@ -358,12 +362,12 @@ template <int SLOTS, int RAW, int BLOCKS>
 struct Bars {
     // a tile arrives at full, one to be cleaned at dirty and then, cleaned, at
     // clean: whoever waits on one of them waits for all its phases
-    uint64_t full[SLOTS], empty[SLOTS], dirty[SLOTS], clean[SLOTS];
+    uint64_t full[SLOTS], empty[SLOTS];
+    uint64_t dirty[RAW > 0 ? 1 : SLOTS], clean[RAW > 0 ? 1 : SLOTS];   // e4m3: the conversion cleans
     uint64_t raw_full[RAW > 0 ? RAW : 1], raw_empty[RAW > 0 ? RAW : 1];
     uint64_t blk_full[BLOCKS], blk_empty[BLOCKS];
-    uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], xch, xdone, drain;
+    uint64_t q_full, q_empty, s_full[2], p_ready[2], p_more[2], o_full[2], xch, xdone, drain;
 };
-constexpr int kBlkReaders = 8 + 3 + 4;   // warps that read a handed-out block
 
 // Nonzero if one of the two bf16 in x is an infinity or NaN (the exponent
 // field 0xff plus one carries into the sign's place).
@@ -461,18 +465,108 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Blk& blk
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
+// volatile: the order they are written in is kept
 __device__ __forceinline__ void ffma2(float& x, float& y, float a, float b) {   // (x, y) = (x, y) * a + b
-    asm("{\n\t.reg .b64 v, s, t;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %3};\n\t"
+    asm volatile(
+        "{\n\t.reg .b64 v, s, t;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %3};\n\t"
         "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
         : "+f"(x), "+f"(y)
         : "f"(a), "f"(b));
 }
 
 __device__ __forceinline__ void fadd2(float& x, float& y, float a, float b) {   // (x, y) += (a, b)
-    asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tadd.rn.f32x2 v, v, s;\n\t"
+    asm volatile(
+        "{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tadd.rn.f32x2 v, v, s;\n\t"
         "mov.b64 {%0, %1}, v;\n\t}"
         : "+f"(x), "+f"(y)
         : "f"(a), "f"(b));
+}
+
+__device__ __forceinline__ float exp2_in_order(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_in_order(float lo, float hi) {
+    uint32_t r;
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 32 scores of a row to weights 2^(x sl + neg), in place, their bf16 pairs
+// and their sums.  The order is the pipeline's: the exponentials (4 clocks of
+// a scheduler each) have the multiply-add of two pairs on and the sum and the
+// rounding of the pair before beside them.
+__device__ __forceinline__ void weights32(float* x, uint32_t (&w)[16], float sl, float neg, float (&l)[4]) {
+    ffma2(x[0], x[1], sl, neg);
+    ffma2(x[2], x[3], sl, neg);
+    x[0] = exp2_in_order(x[0]);
+    x[1] = exp2_in_order(x[1]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (i < 14) ffma2(x[2 * i + 4], x[2 * i + 5], sl, neg);
+        if (i < 15) {
+            x[2 * i + 2] = exp2_in_order(x[2 * i + 2]);
+            x[2 * i + 3] = exp2_in_order(x[2 * i + 3]);
+        }
+        fadd2(l[2 * (i & 1)], l[2 * (i & 1) + 1], x[2 * i], x[2 * i + 1]);
+        w[i] = pack_in_order(x[2 * i], x[2 * i + 1]);
+    }
+}
+
+enum { FORM_PLAIN = 0, FORM_STACKED = 1, FORM_TWICE = 2 };
+
+// A tile's scores at tS (this warp's 32 rows, 128 columns) to its weights P
+// (64 columns at tS); returns the row's sum.  The scores are read 32 at a time
+// and 32 ahead (held from the maximum on they would fill the registers); P is
+// handed over in two halves, the products of the first running beside the
+// exponentials of the second.  One copy per form: the loop of one has to lie
+// together in the instruction cache.
+template <int FORM>
+__device__ __forceinline__ float weights128(uint32_t tS, float sl, float neg, bool rest, uint64_t* some,
+                                            uint64_t* more) {
+    uint32_t xs[2][32], held[2][16];
+    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+    tmem_ld32(tS, xs[0]);
+    tmem_ld32(tS + 32, xs[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float(&x)[32] = reinterpret_cast<float(&)[32]>(xs[c & 1]);
+        uint32_t w[16];
+        weights32(x, w, sl, neg, ls);
+        if constexpr (FORM != FORM_PLAIN) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t u = f32x2_to_bf16x2(x[2 * j] - __uint_as_float(w[j] << 16),
+                                                   x[2 * j + 1] - __uint_as_float(w[j] & 0xffff0000u));
+                if constexpr (FORM == FORM_TWICE) held[c & 1][j] = u;
+                else w[j] = rest ? u : w[j];
+            }
+        }
+        tmem_st16(tS + c * 16, w);
+        if (c < 2) tmem_ld32(tS + (c + 2) * 32, xs[c]);
+        if (c & 1) {
+            if constexpr (FORM == FORM_TWICE) {   // beside P, where scores have been read by now
+                tmem_ld_wait();
+                tmem_st16(tS + 64 + (c - 1) * 16, held[0]);
+                tmem_st16(tS + 64 + c * 16, held[1]);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(c == 1 ? some : more);
+            if (c == 1) tmem_ld_wait();
+        }
+    }
+    return (ls[0] + ls[1]) + (ls[2] + ls[3]);
 }
 
 template <int N>
@@ -528,7 +622,7 @@ struct Reader {
 };
 
 template <int D, bool E4M3, bool SMALL>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ AttendParams p, const __grid_constant__ Scratch ws) {
     using C = Cfg<D, E4M3, SMALL>;
@@ -555,8 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = lane; k < C::kSlots; k += 32) {
             mbar_init(&bar.full[k], E4M3 ? 4 : 1);
             mbar_init(&bar.empty[k], 1);
-            mbar_init(&bar.dirty[k], 1);
-            mbar_init(&bar.clean[k], 4);
+            if (!E4M3) {
+                mbar_init(&bar.dirty[k], 1);
+                mbar_init(&bar.clean[k], 1);
+            }
         }
         for (int k = lane; k < C::kRawSlots; k += 32) {
             mbar_init(&bar.raw_full[k], 1);
@@ -564,11 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int k = lane; k < C::kRingBlocks; k += 32) {
             mbar_init(&bar.blk_full[k], 1);
-            mbar_init(&bar.blk_empty[k], kBlkReaders);
+            mbar_init(&bar.blk_empty[k], 8 + 3 + (E4M3 ? 4 : 0));   // the warps that read it
         }
         if (lane < 2) {
             mbar_init(&bar.s_full[lane], 1);
             mbar_init(&bar.p_ready[lane], 4);
+            mbar_init(&bar.p_more[lane], 4);
             mbar_init(&bar.o_full[lane], 1);
         }
         if (lane == 0) {
@@ -582,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    plan(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
+    plan<C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
     const Start st = *start;
     tc_fence_before();
     __syncthreads();
@@ -615,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------------
         // softmax warpgroups
         // ------------------------------------------------------------------
-        set_regs_up<kRegsSoft>();
+        set_regs_up<C::kRegsSoft>();
         const int wg = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + wg * 128;
@@ -653,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     if (busy) {
-                        if (mixed) {
+                        if (__builtin_expect(mixed, 0)) {
                             // few tiles: their scores are masked where they stand
 #pragma unroll 1
                             for (int c = 0; c < 4; ++c) {
@@ -668,29 +765,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             tmem_st_wait();
                         }
-                        // pass 1: the maximum.  The scores are read again for
-                        // pass 2, 32 at a time, the next 32 on their way: held
-                        // between the passes they would leave no registers to
-                        // overlap the exponentials with
                         float top;
                         {
-                            uint32_t x[4][32];
+                            uint32_t y[4][32];
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, x[c]);
+                            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, y[c]);
                             tmem_ld_wait();
-                            float y[4];
+                            float z[4];
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                y[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+                                z[c] = max3(__uint_as_float(y[c][0]), __uint_as_float(y[c][1]),
+                                            __uint_as_float(y[c][2]));
 #pragma unroll
-                                for (int j = 2; j < 32; j += 2)
-                                    y[c] = fmaxf(fmaxf(y[c], __uint_as_float(x[c][j])), __uint_as_float(x[c][j + 1]));
+                                for (int j = 3; j < 31; j += 2)
+                                    z[c] = max3(z[c], __uint_as_float(y[c][j]), __uint_as_float(y[c][j + 1]));
+                                z[c] = fmaxf(z[c], __uint_as_float(y[c][31]));
                             }
-                            top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * sl;
+                            top = fmaxf(max3(z[0], z[1], z[2]), z[3]) * sl;
                         }
-                        uint32_t xs[2][32];
-                        tmem_ld32(tS, xs[0]);
-                        if (__any_sync(0xffffffffu, top > m_ref + kLazy)) {
+                        if (__builtin_expect(__any_sync(0xffffffffu, top > m_ref + kLazy), 0)) {
                             const float to = fmaxf(m_ref, top);
                             const float corr = to == -INFINITY ? 1.f : fast_exp2(m_ref - to);
                             m_ref = to;
@@ -709,66 +802,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                             }
                         }
-                        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-                        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-                        uint32_t held[2][16];   // twice: remainders that wait for their columns
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            tmem_ld_wait();
-                            if (c < 3) tmem_ld32(tS + (c + 1) * 32, xs[(c + 1) & 1]);
-                            float y[32];
-                            uint32_t w[16];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(xs[c & 1][j]);
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) ffma2(y[j], y[j + 1], sl, neg);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) y[j] = fast_exp2(y[j]);
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                fadd2(l0, l1, y[j], y[j + 1]);
-                                fadd2(l2, l3, y[j + 2], y[j + 3]);
-                                w[j / 2] = f32x2_to_bf16x2(y[j], y[j + 1]);
-                                w[j / 2 + 1] = f32x2_to_bf16x2(y[j + 2], y[j + 3]);
-                            }
-                            if (stacked || twice) {
-                                uint32_t u[16];
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    u[j] = f32x2_to_bf16x2(y[2 * j] - __uint_as_float(w[j] << 16),
-                                                           y[2 * j + 1] - __uint_as_float(w[j] & 0xffff0000u));
-                                if (twice) {
-                                    // beside P, columns 64 .. 127: a piece waits until the scores there
-                                    // have been read
-                                    if (c >= 2) {
-#pragma unroll
-                                        for (int h = 0; h < (c == 2 ? 2 : 1); ++h)
-                                            tmem_st16(tS + 64 + (c == 2 ? h : 2) * 16, held[h]);
-                                    }
-                                    if (c == 3) tmem_st16(tS + 64 + 48, u);
-                                    else {
-#pragma unroll
-                                        for (int j = 0; j < 16; ++j) held[c & 1][j] = u[j];
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int j = 0; j < 16; ++j) w[j] = rest ? u[j] : w[j];
-                                }
-                            }
-                            tmem_st16(tS + c * 16, w);
-                        }
-                        l += (l0 + l1) + (l2 + l3);
-                        tmem_st_wait();
                     }
-                    if (x_open) {
+                    if (__builtin_expect(x_open, 0)) {
                         // the other warpgroup has read this one's O of the block before
                         ok = wait_or_fail(p, &bar.xdone, (n_x - 1) & 1);
                         x_open = false;
                         if (!ok) break;
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.p_ready[wg]);
+                    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                    if (busy) {
+                        uint64_t* some = &bar.p_ready[wg];
+                        uint64_t* more = &bar.p_more[wg];
+                        if (stacked) l += weights128<FORM_STACKED>(tS, sl, neg, rest, some, more);
+                        else if (twice) l += weights128<FORM_TWICE>(tS, sl, neg, rest, some, more);
+                        else l += weights128<FORM_PLAIN>(tS, sl, neg, rest, some, more);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bar.p_ready[wg]);
+                            mbar_arrive(&bar.p_more[wg]);
+                        }
+                    }
                 }
             }
             if (!ok) break;
@@ -903,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (tid == 0) ws.share[blockIdx.x] = share;
     } else if (warp < 12) {
-        set_regs_down<kRegsRest>();
+        set_regs_down<C::kRegsRest>();
         bool ok = true;
         if (warp == 8) {
             // ----------------------------------------------------------------
@@ -1011,22 +1066,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     issue_qk4(tmem + wg * 128, a + h * ((kTile * 128) >> 4), b + h * ((kTile * 128) >> 4), kIdQK, h > 0);
                 mma_commit_warp(&bar.s_full[wg]);
             };
+            // waits for P and issues O (+)= P V, half a tile at a time
             auto pv = [&](int wg, bool add, bool twice) {
                 const uint64_t b = v_desc + static_cast<uint64_t>(sv * (C::kTileBytes >> 4));
-                const uint32_t o = tmem + 256 + wg * 128, a = tmem + wg * 128;
-                issue_pv4(o, a, b, kIdPV, add);
-                issue_pv4(o, a + 32, b + 512, kIdPV, 1);
-                if (twice) {
-                    issue_pv4(o, a + 64, b, kIdPV, 1);
-                    issue_pv4(o, a + 96, b + 512, kIdPV, 1);
-                }
-            };
-            auto wait_p = [&](int wg) {
-                const bool r = wait_or_fail(p, &bar.p_ready[wg], (wg ? n_p1 : n_p0) & 1);
+                const uint32_t o = tmem + 256 + wg * 128, a = tmem + wg * 128, phase = (wg ? n_p1 : n_p0) & 1;
                 if (wg) ++n_p1;
                 else ++n_p0;
+                if (!wait_or_fail(p, &bar.p_ready[wg], phase)) return false;
                 tc_fence_after();
-                return r;
+                issue_pv4(o, a, b, kIdPV, add);
+                if (twice) issue_pv4(o, a + 64, b, kIdPV, 1);
+                if (!wait_or_fail(p, &bar.p_more[wg], phase)) return false;
+                tc_fence_after();
+                issue_pv4(o, a + 32, b + 512, kIdPV, 1);
+                if (twice) issue_pv4(o, a + 96, b + 512, kIdPV, 1);
+                return true;
             };
             for (;;) {
                 const volatile Blk* vb = take(ok);
@@ -1046,9 +1100,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int wg = 0; wg < 2; ++wg) {
                             if (t > 0) {
-                                ok = wait_p(wg);
+                                ok = pv(wg, t > 1, twice);
                                 if (!ok) break;
-                                pv(wg, t > 1, twice);
                                 if (t == n) mma_commit_warp(&bar.o_full[wg]);
                             }
                             if (t < n) qk(wg, wg);
@@ -1068,9 +1121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int t = 0; t < n + 2; ++t) {
                         const int wg = t & 1;
                         if (t >= 2) {
-                            ok = wait_v(tile_cleaned(p, b, tile_key(b, b.t0 + t - 2))) && wait_p(wg);
+                            ok = wait_v(tile_cleaned(p, b, tile_key(b, b.t0 + t - 2))) && pv(wg, t >= 4, twice);
                             if (!ok) break;
-                            pv(wg, t >= 4, twice);
                             if (t >= n) mma_commit_warp(&bar.o_full[wg]);
                             mma_commit_warp(&bar.empty[sv]);
                             sv = next(sv);
@@ -1093,15 +1145,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 10) {
             // ----------------------------------------------------------------
-            // Q rows of each block, a lane per row
+            // Q rows of each block, a lane per row; bf16: then the values of the
+            // tiles to be cleared, a key's row per lane
             // ----------------------------------------------------------------
-            uint32_t n_q = 0;
+            uint32_t n_q = 0, dirty_phase = 0;
+            int sv = 1;            // slot of the next V tile
             for (;;) {
                 const volatile Blk* vb = take(ok);
                 if (!vb) break;
                 const int row0 = vb->row0, m0 = vb->m0, M = vb->M, hk = vb->hk;
                 const bool stacked = SMALL || (vb->flags & BLK_STACKED);
-                release();
                 if (n_q > 0) ok = wait_or_fail(p, &bar.q_empty, (n_q - 1) & 1);
                 ++n_q;
                 if (!ok) break;
@@ -1122,6 +1175,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.q_full);
+                if constexpr (!E4M3) {
+                    const Blk b = copy(vb);
+                    const int len = b.ctx + b.n;
+                    for (int t = b.t0; t < b.t1; ++t) {
+                        const int key0 = tile_key(b, t), s = sv;
+                        sv = sv + 2 >= C::kSlots ? sv + 2 - C::kSlots : sv + 2;
+                        if (!tile_cleaned(p, b, key0)) continue;
+                        ok = wait_or_fail(p, &bar.dirty[s], (dirty_phase >> s) & 1);
+                        dirty_phase ^= 1u << s;
+                        if (!ok) break;
+                        bool found = false;
+#pragma unroll 1
+                        for (int row = lane; row < kTile * (D / 64); row += 32) {
+                            uint8_t* v = smem + C::kRing + s * C::kTileBytes + row * 128;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                // pieces in an order that keeps the lanes of a quarter-warp on different banks
+                                uint4* at = reinterpret_cast<uint4*>(v + ((c ^ (row & 7)) << 4));
+                                uint4 x = *at;
+                                if (nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) {
+                                    uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        const uint32_t bad = nonfinite2(u[j]);
+                                        if (bad & 0x8000u) u[j] &= 0xffff0000u;
+                                        if (bad & 0x80000000u) u[j] &= 0xffffu;
+                                    }
+                                    *at = make_uint4(u[0], u[1], u[2], u[3]);
+                                    found |= key0 + (row & (kTile - 1)) < len;
+                                }
+                            }
+                        }
+                        if (found) blks[rd.at()].nonfinite = 1;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.clean[s]);
+                    }
+                    if (!ok) break;
+                }
+                release();
             }
         } else {
             // ----------------------------------------------------------------
@@ -1162,59 +1255,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        set_regs_down<kRegsRest>();
-        bool ok = true;
-        const int row = tid & 127;
-        int s = 0, rs = 0;
-        uint32_t turn = 0, raw_turn = 0, dirty_phase = 0;
-        for (;;) {
-            const volatile Blk* vb = take(ok);
-            if (!vb) break;
-            const Blk b = copy(vb);
-            const int len = b.ctx + b.n;
-            bool found = false;    // a value that is not finite, cleared
-            for (int t = b.t0; t < b.t1 && ok; ++t) {
-                const int key0 = tile_key(b, t);
-                const bool cleaned = tile_cleaned(p, b, key0);
-                if constexpr (!E4M3) {
-                    // ------------------------------------------------------------
-                    // bf16: values of the tiles to be cleared, a key's row per thread
-                    // ------------------------------------------------------------
-                    const int sv = s + 1 >= C::kSlots ? s + 1 - C::kSlots : s + 1;
-                    s = s + 2 >= C::kSlots ? s + 2 - C::kSlots : s + 2;
-                    if (!cleaned) continue;
-                    ok = wait_or_fail(p, &bar.dirty[sv], (dirty_phase >> sv) & 1);
-                    dirty_phase ^= 1u << sv;
-                    if (!ok) break;
-                    uint8_t* v = smem + C::kRing + sv * C::kTileBytes + row * 128;
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            // pieces in an order that keeps the threads of a quarter-warp on different banks
-                            uint4* at = reinterpret_cast<uint4*>(v + h * (kTile * 128) + ((c ^ (row & 7)) << 4));
-                            uint4 x = *at;
-                            if (nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) {
-                                uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const uint32_t bad = nonfinite2(u[j]);
-                                    if (bad & 0x8000u) u[j] &= 0xffff0000u;
-                                    if (bad & 0x80000000u) u[j] &= 0xffffu;
-                                }
-                                *at = make_uint4(u[0], u[1], u[2], u[3]);
-                                found |= key0 + row < len;
-                            }
-                        }
-                    }
-                    if (found) blks[rd.at()].nonfinite = 1;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.clean[sv]);
-                } else {
-                    // ------------------------------------------------------------
-                    // e4m3 codes -> bf16 values, a key's row per thread
-                    // ------------------------------------------------------------
+        // --------------------------------------------------------------------
+        // e4m3 codes -> bf16 values, a key's row per thread
+        // --------------------------------------------------------------------
+        if constexpr (E4M3) {
+            set_regs_down<C::kRegsRest>();
+            bool ok = true;
+            const int row = tid & 127;
+            int s = 0, rs = 0;
+            uint32_t turn = 0, raw_turn = 0;
+            for (;;) {
+                const volatile Blk* vb = take(ok);
+                if (!vb) break;
+                const Blk b = copy(vb);
+                const int len = b.ctx + b.n;
+                bool found = false;    // a value that is not finite, cleared
+                for (int t = b.t0; t < b.t1 && ok; ++t) {
+                    const int key0 = tile_key(b, t);
+                    const bool cleaned = tile_cleaned(p, b, key0);
+#pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
                         if (turn > 0) ok = wait_or_fail(p, &bar.empty[s], (turn - 1) & 1);
                         ok = ok && wait_or_fail(p, &bar.raw_full[rs], raw_turn & 1);
@@ -1276,9 +1335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                if (!ok) break;
+                release();
             }
-            if (!ok) break;
-            release();
         }
     }
 
@@ -1403,7 +1462,7 @@ cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
     at += align256(2 * static_cast<size_t>(grid) * ws.cap * sizeof(float2));
     ws.o = reinterpret_cast<float*>(at);
     cudaError_t e =
-        launch_pdl(attend_kernel<D, E4M3, SMALL>, dim3(grid), dim3(kThreads), C::kTotal, s, tmK, tmV, p, ws);
+        launch_pdl(attend_kernel<D, E4M3, SMALL>, dim3(grid), dim3(C::kThreads), C::kTotal, s, tmK, tmV, p, ws);
     if (e != cudaSuccess) return e;
     return launch_pdl(attend_merge_kernel<D>, dim3(grid, std::min(4, (ws.cap + 7) / 8)), dim3(256), 0, s, p, ws, grid);
 }
