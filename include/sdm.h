@@ -679,7 +679,7 @@ sdm_status sdm_cache_commit(const sdm_cache* cache, const int32_t* tok, const in
  * infinities included.
  * In:  cache; q [rows, H, head_dim] bf16, q_stride elements from row to row
  *      (a multiple of 8, at least H * head_dim, base 16-byte aligned); H a
- *      multiple of kv_heads; cu_seqlens [R+1], ctx_len [R]; max_window: the
+ *      multiple of kv_heads, at most 128 times it; cu_seqlens [R+1], ctx_len [R]; max_window: the
  *      longest window (a longer one is cut: SDM_DEV_BAD_WINDOW; with
  *      tree_mask at most tree_nodes); scale > 0; sinks >= 0; R <= 16384.
  * Out: out [rows, H, head_dim] bf16; lse [rows, H] fp32 (may be NULL).

@@ -11,8 +11,9 @@
 // the maximum serves, and o, which lives in tensor memory, is then rescaled
 // in the first tiles of a row and hardly ever after.
 //
-// Work.  A block is up to 256 rows (two 128-row sub-tiles) of one request and
-// kv head.  A block of more than 128 rows runs in `pair` form: both softmax
+// Work.  A block is up to two sub-tiles of one request and kv head, a sub-tile
+// the rows of as many whole tokens as 128 lanes hold.  A larger block than one
+// sub-tile runs in `pair` form: both softmax
 // warpgroups see every key tile, each for its own 128 rows.  A smaller one
 // runs in `stream` form: the warpgroups take alternate key tiles of the same
 // rows and their (m, l, o) are joined at its end.  The key tiles of all blocks
@@ -26,7 +27,7 @@
 // to the others; a producer brings K and V tiles page by page with TMA into a
 // ring; one gathers Q and clears values (below); one issues S = Q K^T and O +=
 // P V; eight do the softmax, S from tensor memory to registers and P back over
-// S; e4m3: four turn codes into bf16, exactly, the scale included, in a second
+// S; e4m3: eight turn codes into bf16, exactly, the scale included, in a second
 // ring.  Each softmax warpgroup's S, P and O are its own, so
 // one's softmax runs beside the other's products.
 //
@@ -44,20 +45,16 @@ namespace sdm {
 namespace {
 
 constexpr int kTile = 128;            // keys per tile, rows per sub-tile
-constexpr int kBlockRows = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;
 // The weights enter the second product as bf16.  Where a row sees few keys,
 // nothing averages that rounding out, so the remainder p - bf16(p) is
-// multiplied too: as rows of the same product where the block leaves half of
-// the 128 lanes free (row r in lane r of its 16, the remainder 16 lanes on),
-// by a second product in blocks of at most kFineTiles key tiles.
-// What a block costs besides its tiles (Q, the first product, the last O), in
-// the units of the shares: one key tile of one sub-tile.
-constexpr int kBlockCost = 6;
+// multiplied too: in blocks of at most kStackTiles key tiles that leave half of
+// the 128 lanes free as rows of the same product (row r in lane r of its 16,
+// the remainder 16 lanes on), in blocks of at most kFineTiles by a second one.
 constexpr int kStackRows = 64;
-constexpr int kFineTiles = 9;
+constexpr int kFineTiles = 9, kStackTiles = 16;
 constexpr int kTmemCols = 512;        // S0, S1, O0, O1 at columns 0, 128, 256, 384; P over S
 
 // One block, as the walking warp hands it to the others.
@@ -71,11 +68,11 @@ enum { BLK_PAIR = 1, BLK_STACKED = 2, BLK_TWICE = 4 };
 
 template <int D, bool E4M3, bool SMALL>
 struct Cfg {
-    static constexpr int kThreads = E4M3 ? 512 : 384;
+    static constexpr int kThreads = E4M3 ? 640 : 384;
     // registers of a thread: the softmax warpgroups', the others' (together
-    // the launch's own: 4 x 128 and 3 x 168)
-    static constexpr int kRegsSoft = E4M3 ? 184 : 208, kRegsRest = E4M3 ? 72 : 88;
-    static_assert(E4M3 ? 2 * kRegsSoft + 2 * kRegsRest == 4 * 128 : 2 * kRegsSoft + kRegsRest == 3 * 168, "registers");
+    // the launch's own: 5 x 96 and 3 x 168)
+    static constexpr int kRegsSoft = E4M3 ? 144 : 208, kRegsRest = E4M3 ? 64 : 88;
+    static_assert(E4M3 ? 2 * kRegsSoft + 3 * kRegsRest == 5 * 96 : 2 * kRegsSoft + kRegsRest == 3 * 168, "registers");
     static constexpr int kQBytes = kTile * D * 2;            // one 128-row sub-tile
     static constexpr int kTileBytes = kTile * D * 2;         // one bf16 K or V tile
     static constexpr int kQs = SMALL ? 1 : 2;                // sub-tiles of Q
@@ -115,24 +112,30 @@ struct Scratch {
 // ---------------------------------------------------------------------------
 // Geometry: a request's blocks, a block's key tiles, a CTA's share of them
 // ---------------------------------------------------------------------------
+// Costs of the shares' units, about half a microsecond each: a block besides
+// its tiles (Q, the first product, the last O), a key tile for two sub-tiles
+// (with remainders), for one.
+constexpr int kBlockCost = 10, kPairCost = 4, kPairTwiceCost = 7, kStreamCost = 3;
+
 struct Geom {
     int m0, M;             // first row and rows of the block
     int p0, p1;            // window positions of its first and last row
     int ns, lo, n;         // tiles 0 .. ns - 1 hold the sinks, tiles ns .. n - 1 are key tiles lo, lo + 1, ...
-    int weight;            // cost of a tile: the sub-tiles it is multiplied with
-    // how the weights' rounding to bf16 is made up for (kFineTiles)
-    bool stacked;          // M <= 64: their remainders are 64 more rows of the same product
-    bool twice;            // few keys: their remainders are multiplied in a second product
+    bool pair;             // two sub-tiles
+    int weight;            // cost of a key tile, in units of the shares (kBlockCost)
+    // how the weights' rounding to bf16 is made up for where there are few keys
+    bool stacked;          // their remainders are more rows of the same product
+    bool twice;            // their remainders are multiplied in a second product
 };
 
 __device__ __forceinline__ int blocks_of(const AttendParams& p, const Window& w) {
-    return (w.n * p.group + kBlockRows - 1) / kBlockRows;
+    return (w.n * p.group + 2 * p.sub - 1) / (2 * p.sub);
 }
 
 __device__ __forceinline__ Geom geom_of(const AttendParams& p, const Window& w, int b) {
     Geom g;
-    g.m0 = b * kBlockRows;
-    g.M = min(kBlockRows, w.n * p.group - g.m0);
+    g.m0 = b * 2 * p.sub;
+    g.M = min(2 * p.sub, w.n * p.group - g.m0);
     g.p0 = g.m0 / p.group;
     g.p1 = (g.m0 + g.M - 1) / p.group;
     const int end = p.tree ? w.ctx + w.n : w.ctx + g.p1 + 1;
@@ -142,9 +145,10 @@ __device__ __forceinline__ Geom geom_of(const AttendParams& p, const Window& w, 
         g.ns = min((p.sinks + kTile - 1) / kTile, g.lo);
     }
     g.n = g.ns + (end + kTile - 1) / kTile - g.lo;
-    g.weight = g.M > kTile ? 2 : 1;
-    g.stacked = g.M <= kStackRows;
+    g.pair = g.M > p.sub;
+    g.stacked = g.M <= kStackRows && g.n <= kStackTiles;
     g.twice = !g.stacked && g.n <= kFineTiles;
+    g.weight = g.pair ? (g.twice ? kPairTwiceCost : kPairCost) : kStreamCost;
     return g;
 }
 
@@ -168,6 +172,14 @@ struct Start {
     unsigned long long us, u0, u1;   // unit at which the first block begins, the CTA's units [u0, u1)
     int i, b, hk;
 };
+
+// How many of a block's n tiles begin before unit u, the first at unit `at`.
+__device__ __forceinline__ int tiles_before(unsigned long long u, unsigned long long at, unsigned wt, int n) {
+    if (u <= at) return 0;
+    const unsigned long long d = u - at;
+    if (d >= static_cast<unsigned long long>(n) * wt) return n;
+    return static_cast<int>((static_cast<unsigned>(d) + wt - 1) / wt);   // n * wt is below 2^32
+}
 
 // Walks the blocks of a CTA's share.
 struct Walk {
@@ -212,11 +224,10 @@ struct Walk {
                 g = geom_of(p, w, b);
                 have_b = b;
             }
-            const unsigned wt = g.weight;   // 1 or 2
+            const unsigned wt = g.weight;
             const unsigned long long at = us + kBlockCost;   // unit of the first tile
-            t0 = at < u0 ? static_cast<int>((u0 - at + wt - 1) >> (wt - 1)) : 0;
-            const unsigned long long left = at < u1 ? (u1 - at + wt - 1) >> (wt - 1) : 0;
-            t1 = left < static_cast<unsigned long long>(g.n) ? static_cast<int>(left) : g.n;
+            t0 = tiles_before(u0, at, wt, g.n);
+            t1 = tiles_before(u1, at, wt, g.n);
             if (t0 < t1) return true;
             us += kBlockCost + g.n * wt;
         }
@@ -235,7 +246,7 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
     const long long tokens = table_tokens(p.c);
-    const int most = (p.max_window * p.group + kBlockRows - 1) / kBlockRows;
+    const int most = (p.max_window * p.group + 2 * p.sub - 1) / (2 * p.sub);
     if (most <= 4) {
         for (int i = tid; i < p.R; i += kThreads) {
             const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
@@ -418,7 +429,7 @@ __device__ __forceinline__ RowView row_view(const AttendParams& p, int i, int ct
 }
 
 // Adds weight * value for the infinite and NaN values that a row sees in its
-// block's partly seen tiles (where shared memory holds zeros for them), to 32
+// block's partly seen tiles (where shared memory holds zeros for them), to 16
 // of its output columns.  Rare: one thread per row, straight from the cache.
 template <int D, bool E4M3>
 __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Blk& blk, int m, float m_ref, int col0,
@@ -434,7 +445,7 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Blk& blk
             const int pg = max(page_of(p.c, blk.i, j), 0);
             const size_t row = pool_row(p.c, pg, j) + (static_cast<size_t>(blk.hk) << p.c.page_shift);
             float weight = -1.0f;
-            for (int c = 0; c < 32; ++c) {
+            for (int c = 0; c < 16; ++c) {
                 float v;
                 if constexpr (E4M3) {
                     v = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.v[row * D + col0 + c])).x;
@@ -500,11 +511,40 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// 32 scores of a row to weights 2^(x sl + neg), in place, their bf16 pairs
-// and their sums.  The order is the pipeline's: the exponentials (4 clocks of
-// a scheduler each) have the multiply-add of two pairs on and the sum and the
+// The largest of a row's 128 scores, N * 32 of them in registers at a time.
+template <int N>
+__device__ __forceinline__ float tile_max(uint32_t tS) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 4; h += N) {
+        uint32_t y[N][32];
+#pragma unroll
+        for (int c = 0; c < N; ++c) tmem_ld32(tS + (h + c) * 32, y[c]);
+        tmem_ld_wait();
+        float z[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            z[c] = max3(__uint_as_float(y[c][0]), __uint_as_float(y[c][1]), __uint_as_float(y[c][2]));
+#pragma unroll
+            for (int j = 3; j < 31; j += 2)
+                z[c] = max3(z[c], __uint_as_float(y[c][j]), __uint_as_float(y[c][j + 1]));
+            top = max3(top, z[c], __uint_as_float(y[c][31]));
+        }
+    }
+    return top;
+}
+
+enum { FORM_PLAIN = 0, FORM_STACKED = 1, FORM_TWICE = 2 };
+
+// 32 scores of a row to weights 2^(x sl + neg), their bf16 pairs to tP and
+// their sums.  The order is the pipeline's: the exponentials (4 clocks of a
+// scheduler each) have the multiply-add of two pairs on and the sum and the
 // rounding of the pair before beside them.
-__device__ __forceinline__ void weights32(float* x, uint32_t (&w)[16], float sl, float neg, float (&l)[4]) {
+template <int FORM>
+__device__ __forceinline__ void weights32(uint32_t (&xs)[32], uint32_t tP, float sl, float neg, bool rest,
+                                          float (&l)[4], uint32_t (&held)[16]) {
+    float(&x)[32] = reinterpret_cast<float(&)[32]>(xs);
+    uint32_t w[16];
     ffma2(x[0], x[1], sl, neg);
     ffma2(x[2], x[3], sl, neg);
     x[0] = exp2_in_order(x[0]);
@@ -519,52 +559,48 @@ __device__ __forceinline__ void weights32(float* x, uint32_t (&w)[16], float sl,
         fadd2(l[2 * (i & 1)], l[2 * (i & 1) + 1], x[2 * i], x[2 * i + 1]);
         w[i] = pack_in_order(x[2 * i], x[2 * i + 1]);
     }
+    if constexpr (FORM != FORM_PLAIN) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const uint32_t u = f32x2_to_bf16x2(x[2 * j] - __uint_as_float(w[j] << 16),
+                                               x[2 * j + 1] - __uint_as_float(w[j] & 0xffff0000u));
+            if constexpr (FORM == FORM_TWICE) held[j] = u;
+            else w[j] = rest ? u : w[j];
+        }
+    }
+    tmem_st16(tP, w);
 }
-
-enum { FORM_PLAIN = 0, FORM_STACKED = 1, FORM_TWICE = 2 };
 
 // A tile's scores at tS (this warp's 32 rows, 128 columns) to its weights P
 // (64 columns at tS); returns the row's sum.  The scores are read 32 at a time
 // and 32 ahead (held from the maximum on they would fill the registers); P is
 // handed over in two halves, the products of the first running beside the
-// exponentials of the second.  One copy per form: the loop of one has to lie
-// together in the instruction cache.
+// exponentials of the second.  One copy per form, and a loop over the halves:
+// the code of a tile has to stay in the instruction cache.
 template <int FORM>
 __device__ __forceinline__ float weights128(uint32_t tS, float sl, float neg, bool rest, uint64_t* some,
                                             uint64_t* more) {
-    uint32_t xs[2][32], held[2][16];
+    uint32_t xa[32], xb[32], held[2][16];
     float ls[4] = {0.f, 0.f, 0.f, 0.f};
-    tmem_ld32(tS, xs[0]);
-    tmem_ld32(tS + 32, xs[1]);
+    tmem_ld32(tS, xa);
+    tmem_ld32(tS + 32, xb);
     tmem_ld_wait();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float(&x)[32] = reinterpret_cast<float(&)[32]>(xs[c & 1]);
-        uint32_t w[16];
-        weights32(x, w, sl, neg, ls);
-        if constexpr (FORM != FORM_PLAIN) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t u = f32x2_to_bf16x2(x[2 * j] - __uint_as_float(w[j] << 16),
-                                                   x[2 * j + 1] - __uint_as_float(w[j] & 0xffff0000u));
-                if constexpr (FORM == FORM_TWICE) held[c & 1][j] = u;
-                else w[j] = rest ? u : w[j];
-            }
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        weights32<FORM>(xa, tS + h * 32, sl, neg, rest, ls, held[0]);
+        if (h == 0) tmem_ld32(tS + 64, xa);
+        weights32<FORM>(xb, tS + h * 32 + 16, sl, neg, rest, ls, held[1]);
+        if (h == 0) tmem_ld32(tS + 96, xb);
+        if constexpr (FORM == FORM_TWICE) {   // beside P, where scores have been read by now
+            tmem_ld_wait();
+            tmem_st16(tS + 64 + h * 32, held[0]);
+            tmem_st16(tS + 80 + h * 32, held[1]);
         }
-        tmem_st16(tS + c * 16, w);
-        if (c < 2) tmem_ld32(tS + (c + 2) * 32, xs[c]);
-        if (c & 1) {
-            if constexpr (FORM == FORM_TWICE) {   // beside P, where scores have been read by now
-                tmem_ld_wait();
-                tmem_st16(tS + 64 + (c - 1) * 16, held[0]);
-                tmem_st16(tS + 64 + c * 16, held[1]);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) mbar_arrive(c == 1 ? some : more);
-            if (c == 1) tmem_ld_wait();
-        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(h == 0 ? some : more);
+        tmem_ld_wait();
     }
     return (ls[0] + ls[1]) + (ls[2] + ls[3]);
 }
@@ -613,6 +649,82 @@ __device__ __forceinline__ void store_v8(void* to, const uint32_t (&x)[8]) {   /
                  : "memory");
 }
 
+// Where a row's output goes: row `at` of out, or (a split block's) row `slot`
+// of the workspace.
+template <int D>
+struct Out {
+    bool valid, whole;
+    size_t at, slot;
+    float inv;             // 1 / l
+};
+
+// Columns 16 c0 .. 16 c1 - 1 of a warp's 32 rows of O, from tensor memory to
+// where they go.  JOINED: w0 O0 + w1 O1 (t1 = 0: no O1); STACKED: the lane 16
+// on holds the remainders' part.
+template <int D, bool E4M3, bool JOINED, bool STACKED>
+__device__ __forceinline__ void put_rows(const AttendParams& p, const Scratch& ws, const Out<D>& to, uint32_t t0,
+                                         uint32_t t1, int c0, int c1, float w0, float w1, const volatile Blk* odd,
+                                         int m, float m_ref) {
+    // out is 16-byte aligned: 32-byte stores where it is more
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+        uint32_t o[16], q[16];
+        float f[16];
+        tmem_ld16(t0 + c * 16, o);
+        if (JOINED && t1) tmem_ld16(t1 + c * 16, q);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]);
+        if constexpr (JOINED) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = w0 == 0.f ? 0.f : f[j] * w0;
+            if (t1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = w1 == 0.f ? f[j] : fmaf(__uint_as_float(q[j]), w1, f[j]);
+            }
+        }
+        if constexpr (STACKED) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float y = __shfl_down_sync(0xffffffffu, f[j], 16);
+                if (fabsf(f[j]) < INFINITY) f[j] += y;   // a remainder has either sign: not on infinities
+            }
+        }
+        if (__builtin_expect(odd != nullptr && to.valid, 0)) {
+            float g[16];
+            Blk blk;
+            const int4* src = reinterpret_cast<const int4*>(const_cast<const Blk*>(odd));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) reinterpret_cast<int4*>(&blk)[k] = src[k];
+            for (int j = 0; j < 16; ++j) g[j] = f[j];
+            add_nonfinite<D, E4M3>(p, blk, m, m_ref, c * 16, g);
+            for (int j = 0; j < 16; ++j) f[j] = g[j];
+        }
+        if (to.whole) {
+            uint32_t y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = f32x2_to_bf16x2(f[2 * j] * to.inv, f[2 * j + 1] * to.inv);
+            uint16_t* dst = p.out + to.at * D + c * 16;
+            if (to.valid && wide) store_v8(dst, y);
+            if (to.valid && !wide) {
+                reinterpret_cast<uint4*>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                reinterpret_cast<uint4*>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+        } else if (to.valid) {
+            float* dst = ws.o + to.slot * D + c * 16;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = __float_as_uint(f[8 * h + j]);
+                store_v8(dst + 8 * h, y);
+            }
+        }
+        __syncwarp();
+    }
+}
+
 // Reads the handed-out blocks in turn.
 template <int BLOCKS>
 struct Reader {
@@ -624,6 +736,7 @@ struct Reader {
 template <int D, bool E4M3, bool SMALL>
 __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ CUtensorMap tmQ,
                   const __grid_constant__ AttendParams p, const __grid_constant__ Scratch ws) {
     using C = Cfg<D, E4M3, SMALL>;
     using B = Bars<C::kSlots, C::kRawSlots, C::kRingBlocks>;
@@ -641,13 +754,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         if (lane == 0) {
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
+            if (!SMALL) tma_prefetch_desc(&tmQ);
         }
     } else if (warp == 9) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     } else if (warp == 10) {
         for (int k = lane; k < C::kSlots; k += 32) {
-            mbar_init(&bar.full[k], E4M3 ? 4 : 1);
+            mbar_init(&bar.full[k], E4M3 ? 8 : 1);
             mbar_init(&bar.empty[k], 1);
             if (!E4M3) {
                 mbar_init(&bar.dirty[k], 1);
@@ -656,11 +770,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         }
         for (int k = lane; k < C::kRawSlots; k += 32) {
             mbar_init(&bar.raw_full[k], 1);
-            mbar_init(&bar.raw_empty[k], 4);
+            mbar_init(&bar.raw_empty[k], 8);
         }
         for (int k = lane; k < C::kRingBlocks; k += 32) {
             mbar_init(&bar.blk_full[k], 1);
-            mbar_init(&bar.blk_empty[k], 8 + 3 + (E4M3 ? 4 : 0));   // the warps that read it
+            mbar_init(&bar.blk_empty[k], 8 + 3 + (E4M3 ? 8 : 0));   // the warps that read it
         }
         if (lane < 2) {
             mbar_init(&bar.s_full[lane], 1);
@@ -728,17 +842,18 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             if (!vb) break;
             const int flags = vb->flags, M = vb->M, m0 = vb->m0, t0 = vb->t0;
             const bool pair = !SMALL && (flags & BLK_PAIR);
-            const bool stacked = SMALL || (flags & BLK_STACKED), twice = !SMALL && (flags & BLK_TWICE);
+            const bool stacked = flags & BLK_STACKED, twice = !SMALL && (flags & BLK_TWICE);
             const int n_tiles = vb->t1 - t0;
             const bool rest = stacked && (lane & 16);             // this lane holds the weights' remainders
-            const int r = stacked ? (row >> 5) * 16 + (row & 15) : pair ? wg * kTile + row : row;   // row of the block
-            const bool busy = (stacked ? r & ~15 : r & ~31) < M;  // the warp has rows
+            const int r = stacked ? (row >> 5) * 16 + (row & 15) : pair ? wg * p.sub + row : row;   // row of the block
+            const int lim = pair ? min(M, (wg + 1) * p.sub) : M;  // its warpgroup's rows end here
+            const bool busy = (stacked ? r & ~15 : r - lane) < lim;   // the warp has rows
             float m_ref = -INFINITY, l = 0.f;
             {
                 const int ctx = vb->ctx, n_rows = vb->n, ns = vb->ns, lo = vb->lo;
-                const int first_m = m0 + (pair ? wg * kTile : 0);
+                const int first_m = m0 + (pair ? wg * p.sub : 0);
                 const int p0 = pair ? first_m / p.group : vb->p0;
-                const int p1 = pair ? (min(first_m + kTile, m0 + M) - 1) / p.group : vb->p1;
+                const int p1 = pair ? (min(first_m + p.sub, m0 + M) - 1) / p.group : vb->p1;
                 const RowView view = row_view(p, vb->i, ctx, n_rows, min((m0 + r) / p.group, n_rows - 1));
                 const int mine = pair ? n_tiles : (n_tiles + 1 - wg) >> 1;
                 for (int it = 0; it < mine; ++it) {
@@ -765,24 +880,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                             }
                             tmem_st_wait();
                         }
-                        float top;
-                        {
-                            uint32_t y[4][32];
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, y[c]);
-                            tmem_ld_wait();
-                            float z[4];
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                z[c] = max3(__uint_as_float(y[c][0]), __uint_as_float(y[c][1]),
-                                            __uint_as_float(y[c][2]));
-#pragma unroll
-                                for (int j = 3; j < 31; j += 2)
-                                    z[c] = max3(z[c], __uint_as_float(y[c][j]), __uint_as_float(y[c][j + 1]));
-                                z[c] = fmaxf(z[c], __uint_as_float(y[c][31]));
-                            }
-                            top = fmaxf(max3(z[0], z[1], z[2]), z[3]) * sl;
-                        }
+                        const float top = tile_max<E4M3 ? 2 : 4>(tS) * sl;
                         if (__builtin_expect(__any_sync(0xffffffffu, top > m_ref + kLazy), 0)) {
                             const float to = fmaxf(m_ref, top);
                             const float corr = to == -INFINITY ? 1.f : fast_exp2(m_ref - to);
@@ -848,12 +946,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                     x_open = false;
                     if (!ok) break;
                 }
-                if (!SMALL || !rest) xch[wg * C::kXchRows + (SMALL ? r : row)] = make_float2(m_ref, l);
+                if (!SMALL || (!rest && r < kStackRows)) xch[wg * C::kXchRows + (SMALL ? r : row)] = make_float2(m_ref, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.xch);
                 ok = wait_or_fail(p, &bar.xch, n_x & 1);
                 if (!ok) break;
-                const float2 other = xch[(wg ^ 1) * C::kXchRows + (SMALL ? r : row)];
+                const float2 other = xch[(wg ^ 1) * C::kXchRows + (SMALL ? min(r, kStackRows - 1) : row)];
                 const float mm = fmaxf(m_ref, other.x);
                 const float ref = mm == -INFINITY ? 0.f : mm;
                 const float b0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref);
@@ -874,77 +972,25 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (busy) {
-                const int m = m0 + r, hk = vb->hk;
-                const bool valid = r < M && !rest;
-                const int wp = m / p.group;
-                const size_t at = (static_cast<size_t>(vb->row0) + wp) * p.H + hk * p.group + (m - wp * p.group);
-                const bool odd = vb->nonfinite != 0;
-                const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
-                const bool other_o = joined && n_tiles > 1;   // else the second warpgroup's o was never written
-                const int c0 = joined ? wg * (D / 64) : 0, c1 = joined ? c0 + D / 64 : D / 32;
-#pragma unroll 1
-                for (int c = c0; c < c1; ++c) {
-                    uint32_t o[32], q[32];
-                    float f[32];
-                    tmem_ld32((joined ? tO0 : tO) + c * 32, o);
-                    if (other_o) tmem_ld32(tO1 + c * 32, q);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]);
-                    if (joined) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) f[j] = a0 == 0.f ? 0.f : f[j] * a0;
-                        if (other_o) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                f[j] = a1 == 0.f ? f[j] : fmaf(__uint_as_float(q[j]), a1, f[j]);
-                        }
-                    }
-                    if (stacked) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float y = __shfl_down_sync(0xffffffffu, f[j], 16);
-                            if (fabsf(f[j]) < INFINITY) f[j] += y;   // a remainder has either sign: not on infinities
-                        }
-                    }
-                    if (odd && valid) {
-                        float g[32];
-                        const Blk blk = copy(vb);
-                        for (int j = 0; j < 32; ++j) g[j] = f[j];
-                        add_nonfinite<D, E4M3>(p, blk, m, m_ref, c * 32, g);
-                        for (int j = 0; j < 32; ++j) f[j] = g[j];
-                    }
-                    if (valid && whole) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t y[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                y[j] = f32x2_to_bf16x2(f[16 * h + 2 * j] * inv, f[16 * h + 2 * j + 1] * inv);
-                            // out is 16-byte aligned: 32-byte stores where it is more
-                            uint16_t* dst = p.out + at * D + c * 32 + h * 16;
-                            if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
-                                store_v8(dst, y);
-                            } else {
-                                reinterpret_cast<uint4*>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-                                reinterpret_cast<uint4*>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
-                            }
-                        }
-                    } else if (valid) {
-                        float* dst = ws.o + (slot * ws.cap + r) * D + c * 32;
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            uint32_t y[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] = __float_as_uint(f[8 * h + j]);
-                            store_v8(dst + 8 * h, y);
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (valid && (!joined || wg == 0)) {
-                    if (!whole) ws.ml[slot * ws.cap + r] = make_float2(m_ref, l);
-                    else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : m_ref * kLn2 + logf(l);
+                const int m = m0 + r, wp = m / p.group;
+                Out<D> to;
+                to.valid = r < lim && !rest;
+                to.whole = whole;
+                to.at = (static_cast<size_t>(vb->row0) + wp) * p.H + vb->hk * p.group + (m - wp * p.group);
+                to.slot = slot * ws.cap + r;
+                to.inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+                const volatile Blk* odd = vb->nonfinite ? vb : nullptr;
+                const bool two = joined && n_tiles > 1;   // else the second warpgroup's o was never written
+                if (pair) put_rows<D, E4M3, false, false>(p, ws, to, tO, 0, 0, D / 16, 1.f, 0.f, odd, m, m_ref);
+                else if (stacked)
+                    put_rows<D, E4M3, true, true>(p, ws, to, tO0, two ? tO1 : 0, wg * (D / 32), (wg + 1) * (D / 32), a0,
+                                                  a1, odd, m, m_ref);
+                else
+                    put_rows<D, E4M3, true, false>(p, ws, to, tO0, two ? tO1 : 0, wg * (D / 32), (wg + 1) * (D / 32),
+                                                   a0, a1, odd, m, m_ref);
+                if (to.valid && (!joined || wg == 0)) {
+                    if (!whole) ws.ml[to.slot] = make_float2(m_ref, l);
+                    else if (p.lse) p.lse[to.at] = l == 0.f ? -INFINITY : m_ref * kLn2 + logf(l);
                 }
             }
             tc_fence_before();   // O has been read before the next block's products are let go
@@ -1145,8 +1191,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             }
         } else if (warp == 10) {
             // ----------------------------------------------------------------
-            // Q rows of each block, a lane per row; bf16: then the values of the
-            // tiles to be cleared, a key's row per lane
+            // Q rows of each block: a sub-tile is one box of whole tokens, the rows
+            // of a stacked block go to two places, a lane each; bf16: then the
+            // values of the tiles to be cleared, a key's row per lane
             // ----------------------------------------------------------------
             uint32_t n_q = 0, dirty_phase = 0;
             int sv = 1;            // slot of the next V tile
@@ -1154,16 +1201,29 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 const volatile Blk* vb = take(ok);
                 if (!vb) break;
                 const int row0 = vb->row0, m0 = vb->m0, M = vb->M, hk = vb->hk;
-                const bool stacked = SMALL || (vb->flags & BLK_STACKED);
+                const bool stacked = vb->flags & BLK_STACKED;
                 if (n_q > 0) ok = wait_or_fail(p, &bar.q_empty, (n_q - 1) & 1);
                 ++n_q;
                 if (!ok) break;
-                for (int r = lane; r < M; r += 32) {
+                const bool boxes = !SMALL && !stacked;
+                if (boxes) {
+                    if (lane == 0) {
+                        const int subs = (vb->flags & BLK_PAIR) ? 2 : 1;
+                        mbar_arrive_expect_tx(&bar.q_full, subs * p.sub * D * 2);
+                        for (int k = 0; k < subs; ++k)
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_3d(smem + k * C::kQBytes + h * (kTile * 128), &tmQ, &bar.q_full, h * 64,
+                                            hk * p.group, row0 + (m0 + k * p.sub) / p.group);
+                    }
+                    __syncwarp();
+                }
+                for (int r = lane; !boxes && r < M; r += 32) {
                     const int m = m0 + r, wp = m / p.group;
                     const uint16_t* src = p.q + (row0 + wp) * p.q_stride +
                                           static_cast<size_t>(hk * p.group + (m - wp * p.group)) * D;
-                    const int to = stacked ? (r >> 4) * 32 + (r & 15) : r;   // 16 rows keep r mod 8 and the swizzle
-                    const uint32_t dst = (to >> 7) * C::kQBytes + (to & 127) * 128 + ((to & 7) << 4);
+                    const int to = stacked ? (r >> 4) * 32 + (r & 15) : r;   // 16 rows on keeps r mod 8 and the swizzle
+                    const uint32_t dst = to * 128 + ((to & 7) << 4);
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
                         uint8_t* d = smem + (c >> 3) * (kTile * 128) + (dst ^ ((c & 7) << 4));
@@ -1171,10 +1231,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         if (stacked) cp_async_16(d + 16 * 128, src + c * 8, 16u);
                     }
                 }
-                cp_async_wait_all();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.q_full);
+                if (!boxes) {
+                    cp_async_wait_all();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.q_full);
+                }
                 if constexpr (!E4M3) {
                     const Blk b = copy(vb);
                     const int len = b.ctx + b.n;
@@ -1188,23 +1250,25 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         bool found = false;
 #pragma unroll 1
                         for (int row = lane; row < kTile * (D / 64); row += 32) {
-                            uint8_t* v = smem + C::kRing + s * C::kTileBytes + row * 128;
+                            uint4* v = reinterpret_cast<uint4*>(smem + C::kRing + s * C::kTileBytes + row * 128);
+                            uint4 x[8];
+                            // pieces in an order that keeps the lanes of a quarter-warp on different banks
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                // pieces in an order that keeps the lanes of a quarter-warp on different banks
-                                uint4* at = reinterpret_cast<uint4*>(v + ((c ^ (row & 7)) << 4));
-                                uint4 x = *at;
-                                if (nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) {
-                                    uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                            for (int c = 0; c < 8; ++c) x[c] = v[c ^ (row & 7)];
+                            uint32_t any = 0;
 #pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        const uint32_t bad = nonfinite2(u[j]);
-                                        if (bad & 0x8000u) u[j] &= 0xffff0000u;
-                                        if (bad & 0x80000000u) u[j] &= 0xffffu;
-                                    }
-                                    *at = make_uint4(u[0], u[1], u[2], u[3]);
-                                    found |= key0 + (row & (kTile - 1)) < len;
+                            for (int c = 0; c < 8; ++c)
+                                any |= nonfinite2(x[c].x) | nonfinite2(x[c].y) | nonfinite2(x[c].z) |
+                                       nonfinite2(x[c].w);
+                            if (__builtin_expect(any != 0, 0)) {
+                                uint32_t* u = reinterpret_cast<uint32_t*>(v);
+#pragma unroll 1
+                                for (int j = 0; j < 32; ++j) {
+                                    const uint32_t bad = nonfinite2(u[j]);
+                                    if (bad & 0x8000u) u[j] &= 0xffff0000u;
+                                    if (bad & 0x80000000u) u[j] &= 0xffffu;
                                 }
+                                found |= key0 + (row & (kTile - 1)) < len;
                             }
                         }
                         if (found) blks[rd.at()].nonfinite = 1;
@@ -1216,6 +1280,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 }
                 release();
             }
+            if (!ok && n_q > 0) mbar_wait(&bar.q_full, (n_q - 1) & 1);   // a copy in flight lands first
         } else {
             // ----------------------------------------------------------------
             // the share's blocks, in turn, for the other warps
@@ -1244,7 +1309,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         b.tiles = k.g.n;
                         b.t0 = k.t0;
                         b.t1 = k.t1;
-                        b.flags = (k.g.weight == 2 ? BLK_PAIR : 0) | (k.g.stacked ? BLK_STACKED : 0) |
+                        b.flags = (k.g.pair ? BLK_PAIR : 0) | (k.g.stacked ? BLK_STACKED : 0) |
                                   (k.g.twice ? BLK_TWICE : 0);
                     }
                     blks[e] = b;
@@ -1256,12 +1321,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         }
     } else {
         // --------------------------------------------------------------------
-        // e4m3 codes -> bf16 values, a key's row per thread
+        // e4m3 codes -> bf16 values, half a key's row per thread
         // --------------------------------------------------------------------
         if constexpr (E4M3) {
             set_regs_down<C::kRegsRest>();
             bool ok = true;
-            const int row = tid & 127;
+            const int row = tid & 127, part = (tid >> 7) - 3;
             int s = 0, rs = 0;
             uint32_t turn = 0, raw_turn = 0;
             for (;;) {
@@ -1285,8 +1350,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         const uint32_t sc = e << 7;
                         const uint32_t scale2 = sc | (sc << 16);
                         const bool clear = cleaned && v == 1;
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
+#pragma unroll 2
+                        for (int k = 0; k < D / 32; ++k) {
+                            const int c = part * (D / 32) + k;
                             // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
                             // bytes at c ^ (r / 2 mod 4)
                             const int at = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
@@ -1412,10 +1478,10 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int slot_rows(int max_window, int group) {
     const long long m = static_cast<long long>(max_window) * group;
-    return m >= kBlockRows ? kBlockRows : static_cast<int>((m + 7) & ~7ll);
+    return m >= 2 * kTile ? 2 * kTile : static_cast<int>((m + 7) & ~7ll);
 }
 
-bool encode(CUtensorMap* map, const CacheView& c, void* pool) {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     if (!fn) {
         void* f = nullptr;
@@ -1425,6 +1491,26 @@ bool encode(CUtensorMap* map, const CacheView& c, void* pool) {
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     }
+    return fn;
+}
+
+// q as (dim, head, row): a box is 64 dims of the heads of one kv head and as
+// many tokens as a sub-tile holds, which land as the sub-tile's rows.
+bool encode_q(CUtensorMap* map, const AttendParams& p) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.c.D), static_cast<cuuint64_t>(p.H),
+                          static_cast<cuuint64_t>(p.rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.c.D) * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
+    cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.sub / p.group)};
+    cuuint32_t el[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, el,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode(CUtensorMap* map, const CacheView& c, void* pool) {
+    auto fn = encode_fn();
     if (!fn) return false;
     // rows = (page, head, slot); a box is one page of one head, 128 bytes (e4m3 with 64-wide heads: 64) across
     const int es = c.e4m3 ? 1 : 2;
@@ -1452,6 +1538,8 @@ cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
     }
     CUtensorMap tmK, tmV;
     if (!encode(&tmK, p.c, p.c.k) || !encode(&tmV, p.c, p.c.v)) return cudaErrorInvalidValue;
+    CUtensorMap tmQ = tmK;
+    if (!SMALL && !encode_q(&tmQ, p)) return cudaErrorInvalidValue;
     const int grid = num_sms();
     Scratch ws;
     uint8_t* at = static_cast<uint8_t*>(work);
@@ -1462,7 +1550,8 @@ cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
     at += align256(2 * static_cast<size_t>(grid) * ws.cap * sizeof(float2));
     ws.o = reinterpret_cast<float*>(at);
     cudaError_t e =
-        launch_pdl(attend_kernel<D, E4M3, SMALL>, dim3(grid), dim3(C::kThreads), C::kTotal, s, tmK, tmV, p, ws);
+        launch_pdl(attend_kernel<D, E4M3, SMALL>, dim3(grid), dim3(C::kThreads), C::kTotal, s, tmK, tmV, tmQ,
+                   p, ws);
     if (e != cudaSuccess) return e;
     return launch_pdl(attend_merge_kernel<D>, dim3(grid, std::min(4, (ws.cap + 7) / 8)), dim3(256), 0, s, p, ws, grid);
 }

@@ -123,6 +123,7 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
     if (H % p.c.heads != 0) return SDM_ERR_INVALID_ARG;
     if (R > 16384 || !stride_ok(q_stride, static_cast<long long>(H) * p.c.D) || !aligned16(q) || !aligned16(out))
         return SDM_ERR_UNSUPPORTED;
+    if (H / p.c.heads > 128) return SDM_ERR_UNSUPPORTED;   // a token's rows have to fit one tile
     // rows of one request and kv head are counted in 32 bits
     if (static_cast<long long>(max_window) * (H / p.c.heads) >= (1ll << 30)) return SDM_ERR_UNSUPPORTED;
     if (rows == 0) return SDM_OK;
@@ -137,6 +138,7 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
     p.max_window = max_window;
     p.H = H;
     p.group = H / p.c.heads;
+    p.sub = 128 / p.group * p.group;
     p.scale = scale;
     p.window = std::max(window, 0);
     p.sinks = sinks;

@@ -509,7 +509,8 @@ struct AttendParams {
     int64_t q_stride;     // elements
     const int32_t* cu;
     const int32_t* ctx;
-    int R, rows, max_window, H, group;   // group = query heads per kv head
+    int R, rows, max_window, H, group;   // group = query heads per kv head (at most 128)
+    int sub;              // rows of a sub-tile: group times the tokens that 128 rows hold
     float scale;
     int window, sinks;
     const uint32_t* tree;   // [R, nodes, words] or NULL
