@@ -76,7 +76,7 @@ struct Cfg {
     static constexpr int kQBytes = kTile * D * 2;            // one 128-row sub-tile
     static constexpr int kTileBytes = kTile * D * 2;         // one bf16 K or V tile
     static constexpr int kQs = SMALL ? 1 : 2;                // sub-tiles of Q
-    static constexpr int kRawSlots = E4M3 ? (D == 128 ? 4 : 6) : 0;
+    static constexpr int kRawSlots = !E4M3 ? 0 : D == 64 ? 6 : SMALL ? 4 : 2;
     static constexpr int kFit = (224 * 1024 - kQs * kQBytes - kRawSlots * kTile * D) / kTileBytes;
     static constexpr int kSlots = kFit < 8 ? kFit : 8;
     static constexpr int kRingBlocks = E4M3 && D == 128 && !SMALL ? 3 : 8;   // blocks handed out ahead
@@ -92,7 +92,9 @@ struct Cfg {
     static constexpr int kMisc = kBars + kNumBars * 8;
     static constexpr int kTotal = kMisc + 16;
     static_assert(kTotal <= 232448, "shared memory");
-    static_assert(kSlots >= 3, "a K tile, the V tile before it and the next");
+    static_assert(kSlots >= 4, "a K tile beside the two V tiles before it");
+    // K and V are converted apart: each kind has slots of its own, whose every phase its warps wait for
+    static_assert(!E4M3 || (kSlots % 2 == 0 && kRawSlots % 2 == 0), "slots of a kind");
 };
 
 struct Share {             // per CTA, for the merge: the block its last segment starts, and how its first goes on
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         tmem_relinquish();
     } else if (warp == 10) {
         for (int k = lane; k < C::kSlots; k += 32) {
-            mbar_init(&bar.full[k], E4M3 ? 8 : 1);
+            mbar_init(&bar.full[k], E4M3 ? 4 : 1);
             mbar_init(&bar.empty[k], 1);
             if (!E4M3) {
                 mbar_init(&bar.dirty[k], 1);
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         }
         for (int k = lane; k < C::kRawSlots; k += 32) {
             mbar_init(&bar.raw_full[k], 1);
-            mbar_init(&bar.raw_empty[k], 8);
+            mbar_init(&bar.raw_empty[k], 4);
         }
         for (int k = lane; k < C::kRingBlocks; k += 32) {
             mbar_init(&bar.blk_full[k], 1);
@@ -865,22 +867,33 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     if (busy) {
+                        float top;
                         if (__builtin_expect(mixed, 0)) {
                             // few tiles: their scores are masked where they stand
+                            top = -INFINITY;
 #pragma unroll 1
                             for (int c = 0; c < 4; ++c) {
                                 const uint32_t see = seen32(view, key0 + 32 * c);
                                 uint32_t y[32];
                                 tmem_ld32(tS + c * 32, y);
                                 tmem_ld_wait();
+                                float z = -INFINITY;
 #pragma unroll
-                                for (int j = 0; j < 32; ++j)
+                                for (int j = 0; j < 32; ++j) {
                                     if (!((see >> j) & 1u)) y[j] = 0xff800000u;
+                                    if (j & 1) {
+                                        if (j & 2) top = max3(top, __uint_as_float(y[j - 1]), __uint_as_float(y[j]));
+                                        else z = max3(z, __uint_as_float(y[j - 1]), __uint_as_float(y[j]));
+                                    }
+                                }
+                                top = fmaxf(top, z);
                                 tmem_st32(tS + c * 32, y);
                             }
+                            top *= sl;
                             tmem_st_wait();
+                        } else {
+                            top = tile_max<E4M3 ? 2 : 4>(tS) * sl;
                         }
-                        const float top = tile_max<E4M3 ? 2 : 4>(tS) * sl;
                         if (__builtin_expect(__any_sync(0xffffffffu, top > m_ref + kLazy), 0)) {
                             const float to = fmaxf(m_ref, top);
                             const float corr = to == -INFINITY ? 1.f : fast_exp2(m_ref - to);
@@ -1321,13 +1334,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         }
     } else {
         // --------------------------------------------------------------------
-        // e4m3 codes -> bf16 values, half a key's row per thread
+        // e4m3 codes -> bf16 values, a key's row per thread; one warpgroup takes
+        // the K tiles, the other the V tiles
         // --------------------------------------------------------------------
         if constexpr (E4M3) {
             set_regs_down<C::kRegsRest>();
             bool ok = true;
-            const int row = tid & 127, part = (tid >> 7) - 3;
-            int s = 0, rs = 0;
+            const int row = tid & 127, v = (tid >> 7) - 3;
+            int s = v, rs = v;
             uint32_t turn = 0, raw_turn = 0;
             for (;;) {
                 const volatile Blk* vb = take(ok);
@@ -1335,13 +1349,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 const Blk b = copy(vb);
                 const int len = b.ctx + b.n;
                 bool found = false;    // a value that is not finite, cleared
-                for (int t = b.t0; t < b.t1 && ok; ++t) {
+                for (int t = b.t0; t < b.t1; ++t) {
                     const int key0 = tile_key(b, t);
-                    const bool cleaned = tile_cleaned(p, b, key0);
-#pragma unroll 1
-                    for (int v = 0; v < 2; ++v) {
-                        if (turn > 0) ok = wait_or_fail(p, &bar.empty[s], (turn - 1) & 1);
-                        ok = ok && wait_or_fail(p, &bar.raw_full[rs], raw_turn & 1);
+                    const bool clear = v == 1 && tile_cleaned(p, b, key0);
+                    {
+                        ok = wait_or_fail(p, &bar.raw_full[rs], raw_turn & 1);
+                        if (ok && turn > 0) ok = wait_or_fail(p, &bar.empty[s], (turn - 1) & 1);
                         if (!ok) break;
                         const uint8_t* src = smem + C::kRaw + rs * C::kRawBytes + row * D;
                         uint8_t* dst = smem + C::kRing + s * C::kTileBytes + row * 128;
@@ -1349,10 +1362,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         // 2^(e - 127) as bf16, twice: every e a write leaves is in bf16's range
                         const uint32_t sc = e << 7;
                         const uint32_t scale2 = sc | (sc << 16);
-                        const bool clear = cleaned && v == 1;
 #pragma unroll 2
-                        for (int k = 0; k < D / 32; ++k) {
-                            const int c = part * (D / 32) + k;
+                        for (int c = 0; c < D / 16; ++c) {
                             // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
                             // bytes at c ^ (r / 2 mod 4)
                             const int at = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
@@ -1391,12 +1402,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                             mbar_arrive(&bar.raw_empty[rs]);
                             mbar_arrive(&bar.full[s]);
                         }
-                        if (++s == C::kSlots) {
-                            s = 0;
+                        s += 2;
+                        if (s >= C::kSlots) {
+                            s -= C::kSlots;
                             ++turn;
                         }
-                        if (++rs == C::kRawSlots) {
-                            rs = 0;
+                        rs += 2;
+                        if (rs >= C::kRawSlots) {
+                            rs -= C::kRawSlots;
                             ++raw_turn;
                         }
                     }
