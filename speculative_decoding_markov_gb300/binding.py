@@ -556,6 +556,7 @@ class PagedCache:
             raise ValueError("table must be [requests, columns] int32")
         self.k, self.v, self.table, self.k_exp, self.v_exp = k, v, table, k_exp, v_exp
         self.requests = table.shape[0]
+        self.device = k.get_device()
         self.kv_heads, self.page, self.head_dim = k.shape[1:]
         self.c = SdmCache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
                           v_exp.data_ptr() if e4m3 else None, table.data_ptr(), E4M3 if e4m3 else BF16, k.shape[0],
@@ -574,10 +575,14 @@ class PagedCache:
         return PagedCache(*(x.view(dtype) for x in pool), table, *exps)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _need_rows(what, x, heads, head_dim):
     """Packed rows [rows, heads, head dim] bf16, contiguous within a row (a
     slice of a fused projection's output will do); returns the row stride."""
-    if x.dtype != torch.bfloat16 or not x.is_cuda:
+    if x.dtype is not torch.bfloat16 or not x.is_cuda:
         raise TypeError(f"{what} must be a bf16 CUDA tensor")
     shape, st = x.shape, x.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
@@ -588,7 +593,7 @@ def _need_rows(what, x, heads, head_dim):
 
 
 def _need_i32(what, x, n):
-    if x.dtype != torch.int32 or x.numel() < n or not x.is_cuda or not x.is_contiguous():
+    if x.dtype is not torch.int32 or x.numel() < n or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 CUDA tensor of at least {n} entries")
     return x.data_ptr()
 
@@ -604,8 +609,9 @@ def cache_write(cache, k, v, cu_seqlens, ctx_len, dev_status=None):
     dev_status = new_status(k.device) if dev_status is None else dev_status
     st = lib().sdm_cache_write(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, _need_i32("cu_seqlens", cu_seqlens, R + 1),
                                _need_i32("ctx_len", ctx_len, R), R, k.shape[0], dev_status.data_ptr(),
-                               torch.cuda.current_stream().cuda_stream)
-    _check(st, "sdm_cache_write")
+                               _raw_stream(cache.device))
+    if st:
+        _check(st, "sdm_cache_write")
     return dev_status
 
 
@@ -616,15 +622,16 @@ def cache_read(cache, cu_rows, rows, first=None, out=None, dev_status=None):
     if out is None:
         out = {n: torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.k.device)
                for n in ("k", "v")}
-    for n in ("k", "v"):
-        if out[n].shape != (rows, cache.kv_heads, cache.head_dim) or not out[n].is_contiguous() \
-                or out[n].dtype != torch.bfloat16:
+    ko, vo = out["k"], out["v"]
+    for o in (ko, vo):
+        if o.dtype is not torch.bfloat16 or not o.is_contiguous() or o.shape != (rows, cache.kv_heads, cache.head_dim):
             raise ValueError("out must hold contiguous bf16 [rows, kv heads, head dim] tensors")
     dev_status = new_status(cache.k.device) if dev_status is None else dev_status
     st = lib().sdm_cache_read(cache.ref, _need_i32("cu_rows", cu_rows, R + 1),
-                              None if first is None else _need_i32("first", first, R), R, rows, out["k"].data_ptr(),
-                              out["v"].data_ptr(), dev_status.data_ptr(), torch.cuda.current_stream().cuda_stream)
-    _check(st, "sdm_cache_read")
+                              None if first is None else _need_i32("first", first, R), R, rows, ko.data_ptr(),
+                              vo.data_ptr(), dev_status.data_ptr(), _raw_stream(cache.device))
+    if st:
+        _check(st, "sdm_cache_read")
     return out
 
 
@@ -643,8 +650,9 @@ def cache_commit(cache, tok, parent, n_nodes, out_tok, accept, ctx_len, out=None
                                 _need_i32("n_nodes", n_nodes, R), _need_i32("out_tok", out_tok, R * (B + 1)),
                                 _need_i32("accept", accept, R), _need_i32("ctx_len", ctx_len, R), R, S - 1, B,
                                 _need_i32("path", out["path"], R * (B + 1)), _need_i32("length", out["length"], R),
-                                dev_status.data_ptr(), torch.cuda.current_stream().cuda_stream)
-    _check(st, "sdm_cache_commit")
+                                dev_status.data_ptr(), _raw_stream(cache.device))
+    if st:
+        _check(st, "sdm_cache_commit")
     return out
 
 
@@ -685,6 +693,7 @@ def attend(cache, q, cu_seqlens, ctx_len, max_window, scale=None, window=0, sink
                           _need_i32("ctx_len", ctx_len, R), R, rows, max_window, H,
                           D ** -0.5 if scale is None else scale, window, sinks, mask, nodes, o.data_ptr(),
                           None if z is None else z.data_ptr(), ws.data_ptr(), ws.numel(), dev_status.data_ptr(),
-                          torch.cuda.current_stream().cuda_stream)
-    _check(st, "sdm_attend")
+                          _raw_stream(cache.device))
+    if st:
+        _check(st, "sdm_attend")
     return out

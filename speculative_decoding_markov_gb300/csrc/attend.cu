@@ -240,39 +240,138 @@ __device__ __forceinline__ unsigned long long shfl_up64(unsigned long long v, in
     return __shfl_up_sync(0xffffffffu, v, d);
 }
 
-// This CTA's share of the units (key tiles times their weight) of all blocks,
-// and where it starts.  cost: shared memory for R entries.
+// The units of a request's blocks, for one kv head.
+__device__ __forceinline__ unsigned long long units_of(const AttendParams& p, const Window& w, int b0, int step) {
+    unsigned long long c = 0;
+    for (int b = b0; b < blocks_of(p, w); b += step) {
+        const Geom g = geom_of(p, w, b);
+        c += static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
+    }
+    return c;
+}
+
+// The units [u0, u1) of this CTA, of `total`: the first (total mod grid) CTAs
+// get one more than the others.
+__device__ __forceinline__ void share_of(unsigned long long total, unsigned long long& u0, unsigned long long& u1) {
+    const unsigned long long each = total >> 32 ? total / gridDim.x : static_cast<unsigned>(total) / gridDim.x;
+    const unsigned more = static_cast<unsigned>(total - each * gridDim.x);
+    u0 = each * blockIdx.x + min(blockIdx.x, more);
+    u1 = u0 + each + (blockIdx.x < more ? 1 : 0);
+}
+
+// The block of request i in which unit u0 lies; `us` is the request's first
+// unit.  Run by a whole warp.
+__device__ __forceinline__ void locate(const AttendParams& p, const Window& w, int i, unsigned long long us,
+                                       unsigned long long u0, Start& st) {
+    const int lane = threadIdx.x & 31;
+    const int nb = blocks_of(p, w);
+    int found = -1;
+    unsigned long long step = 1;
+    for (int b0 = 0; b0 < nb && found < 0; b0 += 32) {
+        const int b = b0 + lane;
+        unsigned long long one = 0;
+        if (b < nb) {
+            const Geom g = geom_of(p, w, b);
+            one = static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
+        }
+        unsigned long long sum = one * p.c.heads;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long v = shfl_up64(sum, o);
+            if (lane >= o) sum += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, us + sum > u0);
+        const int at = hit ? __ffs(hit) - 1 : 31;
+        const unsigned long long before = __shfl_sync(0xffffffffu, sum - one * p.c.heads, at);
+        const unsigned long long all = __shfl_sync(0xffffffffu, sum, 31);
+        step = __shfl_sync(0xffffffffu, one, at);
+        if (hit) {
+            found = b0 + at;
+            us += before;
+        } else {
+            us += all;
+        }
+    }
+    const unsigned long long into = u0 - us;
+    const unsigned long long k = step == 0 ? 0
+                                 : (into | step) >> 32 ? into / step
+                                                       : static_cast<unsigned>(into) / static_cast<unsigned>(step);
+    st.i = i;
+    st.b = max(found, 0);
+    st.hk = static_cast<int>(k);
+    st.us = us + k * step;
+}
+
+// Where this CTA's share starts, by one warp, 32 requests at a time: first
+// the total, then the request.
+__device__ __forceinline__ void plan_by_warp(const AttendParams& p, Start& st) {
+    const int lane = threadIdx.x & 31;
+    const long long tokens = table_tokens(p.c);
+    st.u0 = st.u1 = st.us = 0;
+    st.i = st.b = st.hk = 0;
+    unsigned long long total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        unsigned long long us = 0;
+        for (int i0 = 0; i0 < p.R; i0 += 32) {
+            const int i = i0 + lane;
+            Window w = {0, 0, 0, 0};
+            if (i < p.R) w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
+            if (pass == 0 && w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
+            const bool big = blocks_of(p, w) > 2;
+            unsigned long long c = big ? 0 : units_of(p, w, 0, 1);
+            for (unsigned todo = __ballot_sync(0xffffffffu, big); todo; todo &= todo - 1) {
+                const int k = __ffs(todo) - 1;     // a long window: its blocks a lane each
+                Window v;
+                v.n = __shfl_sync(0xffffffffu, w.n, k);
+                v.ctx = __shfl_sync(0xffffffffu, w.ctx, k);
+                v.row0 = v.bad = 0;
+                unsigned long long part = units_of(p, v, lane, 32);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+                if (lane == k) c = part;
+            }
+            unsigned long long sum = c * p.c.heads;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long v = shfl_up64(sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (pass == 1) {
+                const unsigned hit = __ballot_sync(0xffffffffu, us + sum > st.u0);
+                if (hit) {
+                    const int k = __ffs(hit) - 1;
+                    Window v;
+                    v.n = __shfl_sync(0xffffffffu, w.n, k);
+                    v.ctx = __shfl_sync(0xffffffffu, w.ctx, k);
+                    v.row0 = v.bad = 0;
+                    locate(p, v, i0 + k, us + __shfl_sync(0xffffffffu, sum - c * p.c.heads, k), st.u0, st);
+                    return;
+                }
+            }
+            us += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (pass == 0) {
+            total = us;
+            share_of(total, st.u0, st.u1);
+            if (st.u0 == st.u1) return;
+        }
+    }
+}
+
+// The same by all warps, for more requests than kWarpPlan.  cost: shared
+// memory for R entries.
+constexpr int kWarpPlan = 512;
+
 template <int kThreads>
 __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* cost, Start* start,
                                      unsigned long long* wsum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
     const long long tokens = table_tokens(p.c);
-    const int most = (p.max_window * p.group + 2 * p.sub - 1) / (2 * p.sub);
-    if (most <= 4) {
-        for (int i = tid; i < p.R; i += kThreads) {
-            const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
-            if (w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
-            unsigned long long c = 0;
-            for (int b = 0; b < blocks_of(p, w); ++b) {
-                const Geom g = geom_of(p, w, b);
-                c += static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
-            }
-            cost[i] = c * p.c.heads;
-        }
-    } else {
-        for (int i = warp; i < p.R; i += kWarps) {
-            const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
-            if (w.bad && blockIdx.x == 0 && lane == 0) set_status(p.dev_status, w.bad);
-            unsigned long long c = 0;
-            for (int b = lane; b < blocks_of(p, w); b += 32) {
-                const Geom g = geom_of(p, w, b);
-                c += static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-            if (lane == 0) cost[i] = c * p.c.heads;
-        }
+    for (int i = tid; i < p.R; i += kThreads) {
+        const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
+        if (w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
+        cost[i] = units_of(p, w, 0, 1) * p.c.heads;
     }
     __syncthreads();
     const int per = (p.R + kThreads - 1) / kThreads;
@@ -294,11 +393,8 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
         if (k < warp) base += v;
         total += v;
     }
-    // the first (total mod grid) shares are one unit longer
-    const unsigned long long each = total >> 32 ? total / gridDim.x : static_cast<unsigned>(total) / gridDim.x;
-    const unsigned more = static_cast<unsigned>(total - each * gridDim.x);
-    const unsigned long long u0 = each * blockIdx.x + min(blockIdx.x, more);
-    const unsigned long long u1 = u0 + each + (blockIdx.x < more ? 1 : 0);
+    unsigned long long u0, u1;
+    share_of(total, u0, u1);
     if (tid == 0) {
         start->u0 = u0;
         start->u1 = u1;
@@ -312,44 +408,15 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
     __syncthreads();
     if (warp == 0 && u0 < u1) {
         const int i = start->i;
-        unsigned long long us = start->us;
+        const unsigned long long us = start->us;
         const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
-        const int nb = blocks_of(p, w);
-        int found = -1;
-        unsigned long long step = 1;
-        for (int b0 = 0; b0 < nb && found < 0; b0 += 32) {
-            const int b = b0 + lane;
-            unsigned long long one = 0;
-            if (b < nb) {
-                const Geom g = geom_of(p, w, b);
-                one = static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
-            }
-            unsigned long long sum = one * p.c.heads;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long v = shfl_up64(sum, o);
-                if (lane >= o) sum += v;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, us + sum > u0);
-            const int at = hit ? __ffs(hit) - 1 : 31;
-            const unsigned long long before = __shfl_sync(0xffffffffu, sum - one * p.c.heads, at);
-            const unsigned long long all = __shfl_sync(0xffffffffu, sum, 31);
-            step = __shfl_sync(0xffffffffu, one, at);
-            if (hit) {
-                found = b0 + at;
-                us += before;
-            } else {
-                us += all;
-            }
-        }
-        const unsigned long long into = u0 - us;
-        const unsigned long long k = step == 0 ? 0
-                                     : (into | step) >> 32 ? into / step
-                                                           : static_cast<unsigned>(into) / static_cast<unsigned>(step);
+        Start st = {};
+        __syncwarp();
+        locate(p, w, i, us, u0, st);
         if (lane == 0) {
-            start->b = max(found, 0);
-            start->hk = static_cast<int>(k);
-            start->us = us + k * step;
+            start->b = st.b;
+            start->hk = st.hk;
+            start->us = st.us;
         }
     }
     __syncthreads();
@@ -669,22 +736,25 @@ __device__ __forceinline__ void put_rows(const AttendParams& p, const Scratch& w
                                          int m, float m_ref) {
     // out is 16-byte aligned: 32-byte stores where it is more
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+    uint32_t o[16], q[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) q[j] = 0;
+    tmem_ld16(t0 + c0 * 16, o);
+    if (JOINED && t1) tmem_ld16(t1 + c0 * 16, q);
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
-        uint32_t o[16], q[16];
         float f[16];
-        tmem_ld16(t0 + c * 16, o);
-        if (JOINED && t1) tmem_ld16(t1 + c * 16, q);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]);
         if constexpr (JOINED) {
+            // a weight is 0 only where that o is 0 too (no key seen) or absent
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = w0 == 0.f ? 0.f : f[j] * w0;
-            if (t1) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = w1 == 0.f ? f[j] : fmaf(__uint_as_float(q[j]), w1, f[j]);
-            }
+            for (int j = 0; j < 16; ++j) f[j] = fmaf(__uint_as_float(q[j]), w1, f[j] * w0);
+        }
+        if (c + 1 < c1) {   // the next columns on their way
+            tmem_ld16(t0 + (c + 1) * 16, o);
+            if (JOINED && t1) tmem_ld16(t1 + (c + 1) * 16, q);
         }
         if constexpr (STACKED) {
 #pragma unroll
@@ -795,8 +865,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    plan<C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
-    const Start st = *start;
+    // a few requests: the walking warp finds its own start, later
+    const bool by_all = p.R > kWarpPlan;
+    if (by_all) plan<C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
+    Start st = *start;   // read before the roles use its place
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1298,6 +1370,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             // ----------------------------------------------------------------
             // the share's blocks, in turn, for the other warps
             // ----------------------------------------------------------------
+            if (!by_all) plan_by_warp(p, st);
             Walk k;
             k.init(st);
             bool more = st.u0 < st.u1;
