@@ -302,76 +302,65 @@ __device__ __forceinline__ void locate(const AttendParams& p, const Window& w, i
     st.us = us + k * step;
 }
 
-// Where this CTA's share starts, by one warp, 32 requests at a time: first
-// the total, then the request.
-__device__ __forceinline__ void plan_by_warp(const AttendParams& p, Start& st) {
+// Where this CTA's share starts, for at most 32 requests of at most two blocks
+// each: by one warp, a lane per request (the walking warp's first steps are on
+// the path of the smallest calls, so they are few).
+__device__ __forceinline__ void plan_few(const AttendParams& p, Start& st) {
     const int lane = threadIdx.x & 31;
-    const long long tokens = table_tokens(p.c);
-    st.u0 = st.u1 = st.us = 0;
-    st.i = st.b = st.hk = 0;
-    unsigned long long total = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        unsigned long long us = 0;
-        for (int i0 = 0; i0 < p.R; i0 += 32) {
-            const int i = i0 + lane;
-            Window w = {0, 0, 0, 0};
-            if (i < p.R) w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
-            if (pass == 0 && w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
-            const bool big = blocks_of(p, w) > 2;
-            unsigned long long c = big ? 0 : units_of(p, w, 0, 1);
-            for (unsigned todo = __ballot_sync(0xffffffffu, big); todo; todo &= todo - 1) {
-                const int k = __ffs(todo) - 1;     // a long window: its blocks a lane each
-                Window v;
-                v.n = __shfl_sync(0xffffffffu, w.n, k);
-                v.ctx = __shfl_sync(0xffffffffu, w.ctx, k);
-                v.row0 = v.bad = 0;
-                unsigned long long part = units_of(p, v, lane, 32);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-                if (lane == k) c = part;
-            }
-            unsigned long long sum = c * p.c.heads;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long v = shfl_up64(sum, o);
-                if (lane >= o) sum += v;
-            }
-            if (pass == 1) {
-                const unsigned hit = __ballot_sync(0xffffffffu, us + sum > st.u0);
-                if (hit) {
-                    const int k = __ffs(hit) - 1;
-                    Window v;
-                    v.n = __shfl_sync(0xffffffffu, w.n, k);
-                    v.ctx = __shfl_sync(0xffffffffu, w.ctx, k);
-                    v.row0 = v.bad = 0;
-                    locate(p, v, i0 + k, us + __shfl_sync(0xffffffffu, sum - c * p.c.heads, k), st.u0, st);
-                    return;
-                }
-            }
-            us += __shfl_sync(0xffffffffu, sum, 31);
-        }
-        if (pass == 0) {
-            total = us;
-            share_of(total, st.u0, st.u1);
-            if (st.u0 == st.u1) return;
-        }
+    Window w = {0, 0, 0, 0};
+    if (lane < p.R) w = window_of(p.cu, p.ctx, lane, p.rows, p.max_window, table_tokens(p.c));
+    if (w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
+    const int nb = blocks_of(p, w);
+    unsigned c[2] = {0, 0};
+#pragma unroll 1
+    for (int b = 0; b < nb; ++b) {
+        const Geom g = geom_of(p, w, b);
+        (b ? c[1] : c[0]) = kBlockCost + g.n * g.weight;
     }
+    const unsigned long long mine = static_cast<unsigned long long>(c[0] + c[1]) * p.c.heads;
+    unsigned long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = shfl_up64(sum, o);
+        if (lane >= o) sum += v;
+    }
+    share_of(__shfl_sync(0xffffffffu, sum, 31), st.u0, st.u1);
+    const unsigned hit = __ballot_sync(0xffffffffu, sum > st.u0);
+    const int k = hit ? __ffs(hit) - 1 : 0;
+    const unsigned c0 = __shfl_sync(0xffffffffu, c[0], k), c1 = __shfl_sync(0xffffffffu, c[1], k);
+    unsigned long long us = __shfl_sync(0xffffffffu, sum - mine, k);
+    const unsigned long long first = static_cast<unsigned long long>(c0) * p.c.heads;
+    st.i = k;
+    st.b = st.u0 - us >= first ? 1 : 0;
+    if (st.b) us += first;
+    const unsigned one = st.b ? c1 : c0;
+    const unsigned long long into = st.u0 - us;
+    st.hk = one == 0 ? 0 : static_cast<int>(into >> 32 ? into / one : static_cast<unsigned>(into) / one);
+    st.us = us + static_cast<unsigned long long>(st.hk) * one;
 }
 
-// The same by all warps, for more requests than kWarpPlan.  cost: shared
-// memory for R entries.
-constexpr int kWarpPlan = 512;
-
+// The same by all warps.  cost: shared memory for R entries.
 template <int kThreads>
 __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* cost, Start* start,
                                      unsigned long long* wsum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
     const long long tokens = table_tokens(p.c);
-    for (int i = tid; i < p.R; i += kThreads) {
-        const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
-        if (w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
-        cost[i] = units_of(p, w, 0, 1) * p.c.heads;
+    if (p.max_window * p.group <= 8 * p.sub) {
+        for (int i = tid; i < p.R; i += kThreads) {
+            const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
+            if (w.bad && blockIdx.x == 0) set_status(p.dev_status, w.bad);
+            cost[i] = units_of(p, w, 0, 1) * p.c.heads;
+        }
+    } else {   // long windows: their blocks a lane each
+        for (int i = warp; i < p.R; i += kWarps) {
+            const Window w = window_of(p.cu, p.ctx, i, p.rows, p.max_window, tokens);
+            if (w.bad && blockIdx.x == 0 && lane == 0) set_status(p.dev_status, w.bad);
+            unsigned long long c = units_of(p, w, lane, 32);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            if (lane == 0) cost[i] = c * p.c.heads;
+        }
     }
     __syncthreads();
     const int per = (p.R + kThreads - 1) / kThreads;
@@ -865,8 +854,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    // a few requests: the walking warp finds its own start, later
-    const bool by_all = p.R > kWarpPlan;
+    // a few small requests: the walking warp finds the start by itself, later
+    const bool by_all = p.R > 32 || p.max_window * p.group > 4 * p.sub;
     if (by_all) plan<C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
     Start st = *start;   // read before the roles use its place
     tc_fence_before();
@@ -1370,7 +1359,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             // ----------------------------------------------------------------
             // the share's blocks, in turn, for the other warps
             // ----------------------------------------------------------------
-            if (!by_all) plan_by_warp(p, st);
+            if (!by_all) plan_few(p, st);
             Walk k;
             k.init(st);
             bool more = st.u0 < st.u1;
