@@ -435,7 +435,7 @@ struct Bars {
     uint64_t dirty[RAW > 0 ? 1 : SLOTS], clean[RAW > 0 ? 1 : SLOTS];   // e4m3: the conversion cleans
     uint64_t raw_full[RAW > 0 ? RAW : 1], raw_empty[RAW > 0 ? RAW : 1];
     uint64_t blk_full[BLOCKS], blk_empty[BLOCKS];
-    uint64_t q_full, q_empty, s_full[2], p_ready[2], p_more[2], o_full[2], xch, xdone, drain;
+    uint64_t q_full, q_empty, s_full[2], p_half[2][2], o_full[2], xch, xdone, drain;   // [warpgroup], [warpgroup][half]
 };
 
 // Nonzero if one of the two bf16 in x is an infinity or NaN (the exponent
@@ -573,7 +573,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <int N>
 __device__ __forceinline__ float tile_max(uint32_t tS) {
     float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 4; h += N) {
         uint32_t y[N][32];
 #pragma unroll
@@ -631,34 +631,48 @@ __device__ __forceinline__ void weights32(uint32_t (&xs)[32], uint32_t tP, float
 
 // A tile's scores at tS (this warp's 32 rows, 128 columns) to its weights P
 // (64 columns at tS); returns the row's sum.  The scores are read 32 at a time
-// and 32 ahead (held from the maximum on they would fill the registers); P is
-// handed over in two halves, the products of the first running beside the
+// (held from the maximum on they would fill the registers); P is handed over in two halves, the products of the first running beside the
 // exponentials of the second.  One copy per form, and a loop over the halves:
 // the code of a tile has to stay in the instruction cache.
 template <int FORM>
 __device__ __forceinline__ float weights128(uint32_t tS, float sl, float neg, bool rest, uint64_t* some,
                                             uint64_t* more) {
-    uint32_t xa[32], xb[32], held[2][16];
     float ls[4] = {0.f, 0.f, 0.f, 0.f};
-    tmem_ld32(tS, xa);
-    tmem_ld32(tS + 32, xb);
-    tmem_ld_wait();
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        weights32<FORM>(xa, tS + h * 32, sl, neg, rest, ls, held[0]);
-        if (h == 0) tmem_ld32(tS + 64, xa);
-        weights32<FORM>(xb, tS + h * 32 + 16, sl, neg, rest, ls, held[1]);
-        if (h == 0) tmem_ld32(tS + 96, xb);
-        if constexpr (FORM == FORM_TWICE) {   // beside P, where scores have been read by now
-            tmem_ld_wait();
-            tmem_st16(tS + 64 + h * 32, held[0]);
-            tmem_st16(tS + 80 + h * 32, held[1]);
-        }
+    auto hand_over = [&](int half) {
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(h == 0 ? some : more);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(half == 0 ? some : more);
+    };
+    if constexpr (FORM != FORM_TWICE) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], none[16];
+            tmem_ld32(tS + c * 32, x);
+            tmem_ld_wait();
+            weights32<FORM>(x, tS + c * 16, sl, neg, rest, ls, none);
+            if (c & 1) hand_over(c >> 1);
+        }
+    } else {
+        // the remainders lie beside P, in columns 64 .. 127: a half's wait
+        // until the scores there are in registers
+        uint32_t xa[32], xb[32], held[2][16];
+        tmem_ld32(tS, xa);
+        tmem_ld32(tS + 32, xb);
         tmem_ld_wait();
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            weights32<FORM>(xa, tS + h * 32, sl, neg, rest, ls, held[0]);
+            weights32<FORM>(xb, tS + h * 32 + 16, sl, neg, rest, ls, held[1]);
+            if (h == 0) {
+                tmem_ld32(tS + 64, xa);
+                tmem_ld32(tS + 96, xb);
+                tmem_ld_wait();
+            }
+            tmem_st16(tS + 64 + h * 32, held[0]);
+            tmem_st16(tS + 80 + h * 32, held[1]);
+            hand_over(h);
+        }
     }
     return (ls[0] + ls[1]) + (ls[2] + ls[3]);
 }
@@ -839,8 +853,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         }
         if (lane < 2) {
             mbar_init(&bar.s_full[lane], 1);
-            mbar_init(&bar.p_ready[lane], 4);
-            mbar_init(&bar.p_more[lane], 4);
+            mbar_init(&bar.p_half[lane][0], 4);
+            mbar_init(&bar.p_half[lane][1], 4);
             mbar_init(&bar.o_full[lane], 1);
         }
         if (lane == 0) {
@@ -953,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                             top *= sl;
                             tmem_st_wait();
                         } else {
-                            top = tile_max<E4M3 ? 2 : 4>(tS) * sl;
+                            top = tile_max<2>(tS) * sl;
                         }
                         if (__builtin_expect(__any_sync(0xffffffffu, top > m_ref + kLazy), 0)) {
                             const float to = fmaxf(m_ref, top);
@@ -983,8 +997,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                     }
                     const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
                     if (busy) {
-                        uint64_t* some = &bar.p_ready[wg];
-                        uint64_t* more = &bar.p_more[wg];
+                        uint64_t* some = &bar.p_half[wg][0];
+                        uint64_t* more = &bar.p_half[wg][1];
                         if (stacked) l += weights128<FORM_STACKED>(tS, sl, neg, rest, some, more);
                         else if (twice) l += weights128<FORM_TWICE>(tS, sl, neg, rest, some, more);
                         else l += weights128<FORM_PLAIN>(tS, sl, neg, rest, some, more);
@@ -992,8 +1006,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(&bar.p_ready[wg]);
-                            mbar_arrive(&bar.p_more[wg]);
+                            mbar_arrive(&bar.p_half[wg][0]);
+                            mbar_arrive(&bar.p_half[wg][1]);
                         }
                     }
                 }
@@ -1163,7 +1177,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::kRing), 16, 1024);
             const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kRing), kTile * 128, 1024);
-            uint32_t n_q = 0, n_p0 = 0, n_p1 = 0, full_phase = 0, clean_phase = 0;
+            uint32_t n_q = 0, p_phase = 0, full_phase = 0, clean_phase = 0;
             int sk = 0, sv = 1;    // slots of the next K tile and the next V tile to be multiplied
             auto wait_full = [&](int s) {
                 const bool r = wait_or_fail(p, &bar.full[s], (full_phase >> s) & 1);
@@ -1177,29 +1191,32 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 return r;
             };
             auto next = [&](int s) { return s + 2 >= C::kSlots ? s + 2 - C::kSlots : s + 2; };
+            // S = Q K^T
             auto qk = [&](int wg, int q) {
-                const uint64_t a = q_desc + static_cast<uint64_t>(q * (C::kQBytes >> 4));
-                const uint64_t b = k_desc + static_cast<uint64_t>(sk * (C::kTileBytes >> 4));
+                uint64_t a = q_desc + static_cast<uint64_t>(q * (C::kQBytes >> 4));
+                uint64_t b = k_desc + static_cast<uint64_t>(sk * (C::kTileBytes >> 4));
                 tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h)
-                    issue_qk4(tmem + wg * 128, a + h * ((kTile * 128) >> 4), b + h * ((kTile * 128) >> 4), kIdQK, h > 0);
+#pragma unroll 1
+                for (int d = 0; d < D / 64; ++d, a += (kTile * 128) >> 4, b += (kTile * 128) >> 4)
+                    issue_qk4(tmem + wg * 128, a, b, kIdQK, d > 0);
                 mma_commit_warp(&bar.s_full[wg]);
             };
-            // waits for P and issues O (+)= P V, half a tile at a time
+            // waits for P and issues O (+)= P V, half a tile at a time; with
+            // the remainders' P, 64 columns on, too
             auto pv = [&](int wg, bool add, bool twice) {
-                const uint64_t b = v_desc + static_cast<uint64_t>(sv * (C::kTileBytes >> 4));
-                const uint32_t o = tmem + 256 + wg * 128, a = tmem + wg * 128, phase = (wg ? n_p1 : n_p0) & 1;
-                if (wg) ++n_p1;
-                else ++n_p0;
-                if (!wait_or_fail(p, &bar.p_ready[wg], phase)) return false;
-                tc_fence_after();
-                issue_pv4(o, a, b, kIdPV, add);
-                if (twice) issue_pv4(o, a + 64, b, kIdPV, 1);
-                if (!wait_or_fail(p, &bar.p_more[wg], phase)) return false;
-                tc_fence_after();
-                issue_pv4(o, a + 32, b + 512, kIdPV, 1);
-                if (twice) issue_pv4(o, a + 96, b + 512, kIdPV, 1);
+                uint64_t b = v_desc + static_cast<uint64_t>(sv * (C::kTileBytes >> 4));
+                uint32_t a = tmem + wg * 128;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h, a += 32, b += 512) {
+                    if (!wait_or_fail(p, &bar.p_half[wg][h], (p_phase >> wg) & 1)) return false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int r = 0; r <= static_cast<int>(twice); ++r) {
+                        issue_pv4(tmem + 256 + wg * 128, a + r * 64, b, kIdPV, add);
+                        add = true;
+                    }
+                }
+                p_phase ^= 1u << wg;
                 return true;
             };
             for (;;) {
@@ -1212,50 +1229,39 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 ok = wait_or_fail(p, &bar.q_full, n_q & 1);
                 ++n_q;
                 if (!ok) break;
-                if (!SMALL && (b.flags & BLK_PAIR)) {
-                    for (int t = 0; t <= n; ++t) {
-                        if (t < n) ok = wait_full(sk);
-                        if (ok && t > 0) ok = wait_v(tile_cleaned(p, b, tile_key(b, b.t0 + t - 1)));
-                        if (!ok) break;
-#pragma unroll
-                        for (int wg = 0; wg < 2; ++wg) {
-                            if (t > 0) {
-                                ok = pv(wg, t > 1, twice);
-                                if (!ok) break;
-                                if (t == n) mma_commit_warp(&bar.o_full[wg]);
-                            }
-                            if (t < n) qk(wg, wg);
-                        }
-                        if (!ok) break;
-                        if (t < n) {
-                            mma_commit_warp(&bar.empty[sk]);
-                            sk = next(sk);
-                        }
-                        if (t > 0) {
-                            mma_commit_warp(&bar.empty[sv]);
-                            sv = next(sv);
-                        }
-                        if (t == n - 1) mma_commit_warp(&bar.q_empty);
-                    }
-                } else {
-                    for (int t = 0; t < n + 2; ++t) {
-                        const int wg = t & 1;
-                        if (t >= 2) {
-                            ok = wait_v(tile_cleaned(p, b, tile_key(b, b.t0 + t - 2))) && pv(wg, t >= 4, twice);
+                // Per tile and warpgroup: P V of its tile before, then the scores
+                // that take its place.  A pair's warpgroups have every tile,
+                // else they take turns.
+                const bool pair = !SMALL && (b.flags & BLK_PAIR);
+                const int lag = pair ? 1 : 2;
+#pragma unroll 1
+                for (int t = 0; t < n + lag; ++t) {
+                    if (t >= lag) ok = wait_v(tile_cleaned(p, b, tile_key(b, b.t0 + t - lag)));
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int k = 0; k < (pair ? 2 : 1); ++k) {
+                        const int wg = pair ? k : t & 1;
+                        if (t >= lag) {
+                            ok = pv(wg, t >= 2 * lag, twice);
                             if (!ok) break;
                             if (t >= n) mma_commit_warp(&bar.o_full[wg]);
-                            mma_commit_warp(&bar.empty[sv]);
-                            sv = next(sv);
                         }
                         if (t < n) {
-                            ok = wait_full(sk);
+                            if (k == 0) ok = wait_full(sk);
                             if (!ok) break;
-                            qk(wg, 0);
-                            mma_commit_warp(&bar.empty[sk]);
-                            sk = next(sk);
-                            if (t == n - 1) mma_commit_warp(&bar.q_empty);
+                            qk(wg, pair ? k : 0);
                         }
                     }
+                    if (!ok) break;
+                    if (t < n) {
+                        mma_commit_warp(&bar.empty[sk]);
+                        sk = next(sk);
+                    }
+                    if (t >= lag) {
+                        mma_commit_warp(&bar.empty[sv]);
+                        sv = next(sv);
+                    }
+                    if (t == n - 1) mma_commit_warp(&bar.q_empty);
                 }
                 if (!ok) break;
             }
@@ -1424,7 +1430,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         // 2^(e - 127) as bf16, twice: every e a write leaves is in bf16's range
                         const uint32_t sc = e << 7;
                         const uint32_t scale2 = sc | (sc << 16);
-#pragma unroll 2
+#pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
                             // bytes at c ^ (r / 2 mod 4)
@@ -1628,7 +1634,7 @@ cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
         launch_pdl(attend_kernel<D, E4M3, SMALL>, dim3(grid), dim3(C::kThreads), C::kTotal, s, tmK, tmV, tmQ,
                    p, ws);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attend_merge_kernel<D>, dim3(grid, std::min(4, (ws.cap + 7) / 8)), dim3(256), 0, s, p, ws, grid);
+    return launch_pdl(attend_merge_kernel<D>, dim3(grid, (ws.cap + 7) / 8), dim3(256), 0, s, p, ws, grid);
 }
 
 }  // namespace
