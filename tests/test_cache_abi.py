@@ -95,3 +95,9 @@ def test_the_binding_refuses_what_the_kernels_cannot_check():
 def test_device_bit_of_a_bad_page(lib):
     assert lib.sdm_status_of_device(binding.DEV_BAD_PAGE) == 6
     assert lib.sdm_workspace_size(binding.OP_ATTEND, 64, 8, 32, 128, 512, 8, 0) > 0
+
+
+def test_attend_refuses_more_heads_per_kv_head_than_a_tile_holds(lib):
+    assert attend(lib, H=2 * 129, qs=2 * 129 * 128) == 2
+    assert attend(lib, H=2 * 128, qs=2 * 128 * 128, ws_bytes=0) == 5      # accepted up to the workspace
+    assert attend(lib, ws=FAKE + 16) == 5                                 # the workspace starts on 256 bytes

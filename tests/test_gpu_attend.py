@@ -258,3 +258,41 @@ def test_device_checks(gpu_lib):
     assert run(ctx=[2 ** 31 - 1, 20]) & sdm.DEV_BAD_PAGE
     s.cache.table[1, 0] = -7
     assert run() == sdm.DEV_BAD_PAGE
+
+
+def test_outputs_on_a_16_byte_boundary(gpu_lib):
+    """out 16 but not 32 bytes aligned: the narrower stores, the same bits."""
+    s = ref.Setup([3, 130], [70, 0], 2, 64, 16, False)
+    s.write_all()
+    q = torch.randn((s.rows, 8, 64), generator=s.gen).to(torch.bfloat16).cuda()
+    want = sdm.attend(s.cache, q, s.cu, s.ctx, 130, dev_status=s.status)["out"]
+    room = torch.zeros(q.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    out = room[8:].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    sdm.attend(s.cache, q, s.cu, s.ctx, 130, out=dict(out=out), dev_status=s.status)
+    assert torch.equal(out, want) and not room[:8].any()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_long_windows(gpu_lib, e4m3):
+    """More requests than a warp plans, windows of several blocks, the most
+    query heads per kv head, empty requests between."""
+    rng = np.random.default_rng(2)
+    w = [int(x) for x in rng.integers(0, 30, 40)]
+    ctx = [int(x) for x in rng.integers(0, 300, 40)]
+    s = ref.Setup(w, ctx, 1, 64, 32, e4m3, seed=9)
+    s.write_all()
+    check(s, 128, max_window=29)
+    check(s, 33, max_window=29)
+    s = ref.Setup([40, 0, 700, 3], [500, 3, 0, 90], 2, 128, 64, e4m3, seed=10)
+    s.write_all()
+    check(s, 14)
+
+
+def test_splits_of_every_length(gpu_lib):
+    """One request at lengths that cut its tiles between CTAs in every way."""
+    for n in (1, 2, 127, 129, 255, 385, 1000, 2600, 4999):
+        for w in (1, 20, 70):
+            s = ref.Setup([w], [max(0, n - w)], 2, 64, 64, n % 2 == 0, seed=n + w)
+            s.write_all()
+            check(s, 8)
