@@ -88,7 +88,7 @@ struct Cfg {
     static constexpr int kXch = kExps + kRawSlots * kTile;   // (m, l) of both warpgroups' rows
     static constexpr int kBlks = kXch + 2 * kXchRows * 8;
     static constexpr int kBars = kBlks + kRingBlocks * static_cast<int>(sizeof(Blk));
-    static constexpr int kNumBars = (E4M3 ? 2 * kSlots + 2 : 4 * kSlots) + 2 * (kRawSlots > 0 ? kRawSlots : 1) + 2 * kRingBlocks + 13;
+    static constexpr int kNumBars = (E4M3 ? 2 * kSlots + 1 : 3 * kSlots) + 2 * (kRawSlots > 0 ? kRawSlots : 1) + 2 * kRingBlocks + 13;
     static constexpr int kMisc = kBars + kNumBars * 8;
     static constexpr int kTotal = kMisc + 16;
     static_assert(kTotal <= 232448, "shared memory");
@@ -114,17 +114,12 @@ struct Scratch {
 // ---------------------------------------------------------------------------
 // Geometry: a request's blocks, a block's key tiles, a CTA's share of them
 // ---------------------------------------------------------------------------
-// Costs of the shares' units, about half a microsecond each: a block besides
-// its tiles (Q, the first product, the last O), a key tile for two sub-tiles
-// (with remainders), for one.
-constexpr int kBlockCost = 10, kPairCost = 4, kPairTwiceCost = 7, kStreamCost = 3;
-
 struct Geom {
     int m0, M;             // first row and rows of the block
     int p0, p1;            // window positions of its first and last row
     int ns, lo, n;         // tiles 0 .. ns - 1 hold the sinks, tiles ns .. n - 1 are key tiles lo, lo + 1, ...
     bool pair;             // two sub-tiles
-    int weight;            // cost of a key tile, in units of the shares (kBlockCost)
+    int weight;            // cost of a key tile, in units of the shares
     // how the weights' rounding to bf16 is made up for where there are few keys
     bool stacked;          // their remainders are more rows of the same product
     bool twice;            // their remainders are multiplied in a second product
@@ -150,7 +145,7 @@ __device__ __forceinline__ Geom geom_of(const AttendParams& p, const Window& w, 
     g.pair = g.M > p.sub;
     g.stacked = g.M <= kStackRows && g.n <= kStackTiles;
     g.twice = !g.stacked && g.n <= kFineTiles;
-    g.weight = g.pair ? (g.twice ? kPairTwiceCost : kPairCost) : kStreamCost;
+    g.weight = g.pair ? (g.twice ? p.cost_twice : p.cost_pair) : p.cost_stream;
     return g;
 }
 
@@ -204,7 +199,7 @@ struct Walk {
     }
 
     __device__ __forceinline__ bool next(const AttendParams& p) {
-        if (have >= 0) us += kBlockCost + g.n * g.weight;
+        if (have >= 0) us += p.cost_block + g.n * g.weight;
         for (;;) {
             if (us >= u1) return false;
             if (++hk >= p.c.heads) {
@@ -227,11 +222,11 @@ struct Walk {
                 have_b = b;
             }
             const unsigned wt = g.weight;
-            const unsigned long long at = us + kBlockCost;   // unit of the first tile
+            const unsigned long long at = us + p.cost_block;   // unit of the first tile
             t0 = tiles_before(u0, at, wt, g.n);
             t1 = tiles_before(u1, at, wt, g.n);
             if (t0 < t1) return true;
-            us += kBlockCost + g.n * wt;
+            us += p.cost_block + g.n * wt;
         }
     }
 };
@@ -245,7 +240,7 @@ __device__ __forceinline__ unsigned long long units_of(const AttendParams& p, co
     unsigned long long c = 0;
     for (int b = b0; b < blocks_of(p, w); b += step) {
         const Geom g = geom_of(p, w, b);
-        c += static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
+        c += static_cast<unsigned long long>(p.cost_block + g.n * g.weight);
     }
     return c;
 }
@@ -272,7 +267,7 @@ __device__ __forceinline__ void locate(const AttendParams& p, const Window& w, i
         unsigned long long one = 0;
         if (b < nb) {
             const Geom g = geom_of(p, w, b);
-            one = static_cast<unsigned long long>(kBlockCost + g.n * g.weight);
+            one = static_cast<unsigned long long>(p.cost_block + g.n * g.weight);
         }
         unsigned long long sum = one * p.c.heads;
 #pragma unroll
@@ -315,7 +310,7 @@ __device__ __forceinline__ void plan_few(const AttendParams& p, Start& st) {
 #pragma unroll 1
     for (int b = 0; b < nb; ++b) {
         const Geom g = geom_of(p, w, b);
-        (b ? c[1] : c[0]) = kBlockCost + g.n * g.weight;
+        (b ? c[1] : c[0]) = p.cost_block + g.n * g.weight;
     }
     const unsigned long long mine = static_cast<unsigned long long>(c[0] + c[1]) * p.c.heads;
     unsigned long long sum = mine;
@@ -429,10 +424,10 @@ __device__ __forceinline__ bool wait_or_fail(const AttendParams& p, uint64_t* ba
 
 template <int SLOTS, int RAW, int BLOCKS>
 struct Bars {
-    // a tile arrives at full, one to be cleaned at dirty and then, cleaned, at
-    // clean: whoever waits on one of them waits for all its phases
+    // a tile arrives at full; one to be cleaned at dirty, and whoever cleans it
+    // arrives at full
     uint64_t full[SLOTS], empty[SLOTS];
-    uint64_t dirty[RAW > 0 ? 1 : SLOTS], clean[RAW > 0 ? 1 : SLOTS];   // e4m3: the conversion cleans
+    uint64_t dirty[RAW > 0 ? 1 : SLOTS];   // e4m3: the conversion cleans
     uint64_t raw_full[RAW > 0 ? RAW : 1], raw_empty[RAW > 0 ? RAW : 1];
     uint64_t blk_full[BLOCKS], blk_empty[BLOCKS];
     uint64_t q_full, q_empty, s_full[2], p_half[2][2], o_full[2], xch, xdone, drain;   // [warpgroup], [warpgroup][half]
@@ -838,10 +833,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         for (int k = lane; k < C::kSlots; k += 32) {
             mbar_init(&bar.full[k], E4M3 ? 4 : 1);
             mbar_init(&bar.empty[k], 1);
-            if (!E4M3) {
-                mbar_init(&bar.dirty[k], 1);
-                mbar_init(&bar.clean[k], 1);
-            }
+            if (!E4M3) mbar_init(&bar.dirty[k], 1);
         }
         for (int k = lane; k < C::kRawSlots; k += 32) {
             mbar_init(&bar.raw_full[k], 1);
@@ -948,21 +940,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                             top = -INFINITY;
 #pragma unroll 1
                             for (int c = 0; c < 4; ++c) {
-                                const uint32_t see = seen32(view, key0 + 32 * c);
                                 uint32_t y[32];
                                 tmem_ld32(tS + c * 32, y);
+                                const uint32_t see = seen32(view, key0 + 32 * c);
                                 tmem_ld_wait();
+                                if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j)
+                                        if (!((see >> j) & 1u)) y[j] = 0xff800000u;
+                                    tmem_st32(tS + c * 32, y);
+                                }
                                 float z = -INFINITY;
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    if (!((see >> j) & 1u)) y[j] = 0xff800000u;
-                                    if (j & 1) {
-                                        if (j & 2) top = max3(top, __uint_as_float(y[j - 1]), __uint_as_float(y[j]));
-                                        else z = max3(z, __uint_as_float(y[j - 1]), __uint_as_float(y[j]));
-                                    }
+                                for (int j = 0; j < 32; j += 4) {
+                                    top = max3(top, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                                    z = max3(z, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
                                 }
                                 top = fmaxf(top, z);
-                                tmem_st32(tS + c * 32, y);
                             }
                             top *= sl;
                             tmem_st_wait();
@@ -1134,7 +1128,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         const uint32_t bit = 1u << s;
                         dirty = to_dirty ? dirty | bit : dirty & ~bit;
                         if (to_dirty) odd_dirty ^= bit;
-                        else odd_full ^= bit;
+                        odd_full ^= bit;
                         if (lane == 0) mbar_arrive_expect_tx(arrive, bytes);
                         __syncwarp();
                         if (lane < live) {
@@ -1177,17 +1171,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::kRing), 16, 1024);
             const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kRing), kTile * 128, 1024);
-            uint32_t n_q = 0, p_phase = 0, full_phase = 0, clean_phase = 0;
+            uint32_t n_q = 0, p_phase = 0, full_phase = 0;
             int sk = 0, sv = 1;    // slots of the next K tile and the next V tile to be multiplied
             auto wait_full = [&](int s) {
                 const bool r = wait_or_fail(p, &bar.full[s], (full_phase >> s) & 1);
                 full_phase ^= 1u << s;
-                return r;
-            };
-            auto wait_v = [&](bool cleaned) {
-                if (E4M3 || !cleaned) return wait_full(sv);
-                const bool r = wait_or_fail(p, &bar.clean[sv], (clean_phase >> sv) & 1);
-                clean_phase ^= 1u << sv;
                 return r;
             };
             auto next = [&](int s) { return s + 2 >= C::kSlots ? s + 2 - C::kSlots : s + 2; };
@@ -1222,21 +1210,20 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             for (;;) {
                 const volatile Blk* vb = take(ok);
                 if (!vb) break;
-                const Blk b = copy(vb);
+                const int n = vb->t1 - vb->t0, flags = vb->flags;
                 release();
-                const int n = b.t1 - b.t0;
-                const bool twice = !SMALL && (b.flags & BLK_TWICE);
+                const bool twice = !SMALL && (flags & BLK_TWICE);
                 ok = wait_or_fail(p, &bar.q_full, n_q & 1);
                 ++n_q;
                 if (!ok) break;
                 // Per tile and warpgroup: P V of its tile before, then the scores
                 // that take its place.  A pair's warpgroups have every tile,
                 // else they take turns.
-                const bool pair = !SMALL && (b.flags & BLK_PAIR);
+                const bool pair = !SMALL && (flags & BLK_PAIR);
                 const int lag = pair ? 1 : 2;
 #pragma unroll 1
                 for (int t = 0; t < n + lag; ++t) {
-                    if (t >= lag) ok = wait_v(tile_cleaned(p, b, tile_key(b, b.t0 + t - lag)));
+                    if (t >= lag) ok = wait_full(sv);
                     if (!ok) break;
 #pragma unroll 1
                     for (int k = 0; k < (pair ? 2 : 1); ++k) {
@@ -1354,7 +1341,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         if (found) blks[rd.at()].nonfinite = 1;
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.clean[s]);
+                        if (lane == 0) mbar_arrive(&bar.full[s]);
                     }
                     if (!ok) break;
                 }
@@ -1497,19 +1484,24 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
 }
 
 // Joins the segments of split blocks, in key order: the CTA whose share
-// starts a block and the next ones that continue it.  One warp per row.
-template <int D>
+// starts a block and the next ones that continue it.  kRows rows a warp, the
+// loads of kSegs segments together: the kernel is a chain of a few L2 round
+// trips.
+template <int D, int kRows, int kSegs>
 __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p, const Scratch ws, int grid) {
+    constexpr int kV = D / 32;
     pdl_wait();
     pdl_trigger();
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const Share s = ws.share[c];
-    if (s.rows == 0) return;
     // slots of the block: 2c + 1, then slot 0 of the CTAs after c up to the one that finishes it
     int end = c + 1;
-    for (;;) {
+    unsigned none = 0;     // of the first 32 of them: without work
+    for (bool first = true;; first = false) {
         const int at = end + lane;
         const int head = at < grid ? ws.share[at].head : 1;
+        if (s.rows == 0) return;
+        if (first) none = __ballot_sync(0xffffffffu, head == 3);
         const unsigned stop = __ballot_sync(0xffffffffu, head == 1 || head == 0);
         if (stop) {
             end += __ffs(stop);
@@ -1518,40 +1510,66 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p,
         end += 32;
     }
     end = min(end, grid);
-    constexpr int kV = D / 32;
-    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < s.rows; r += gridDim.y * 8) {
-        float m = -INFINITY, l = 0.f, o[kV] = {};
-        for (int k = c; k < end; ++k) {
-            if (k > c && ws.share[k].head == 3) continue;
-            const size_t slot = k == c ? 2 * static_cast<size_t>(c) + 1 : 2 * static_cast<size_t>(k);
-            const float2 ml = ws.ml[slot * ws.cap + r];
-            const float* src = ws.o + (slot * ws.cap + r) * D + lane * kV;
-            float x[kV];
-            if constexpr (kV == 4) {
-                const float4 t = *reinterpret_cast<const float4*>(src);
-                x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
-            } else {
-                const float2 t = *reinterpret_cast<const float2*>(src);
-                x[0] = t.x, x[1] = t.y;
-            }
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;
-            const float to = fmaxf(m, ml.x);
-            const float a = m == -INFINITY ? 0.f : fast_exp2(m - to), b = fast_exp2(ml.x - to);
-            m = to;
-            l = l * a + ml.y * b;
+    const int r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kRows;
+    if (r0 >= s.rows) return;
+    float m[kRows], l[kRows], o[kRows][kV];
 #pragma unroll
-            for (int j = 0; j < kV; ++j) o[j] = o[j] * a + x[j] * b;
+    for (int r = 0; r < kRows; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) o[r][j] = 0.f;
+    }
+    for (int k0 = c; k0 < end; k0 += kSegs) {
+        float2 ml[kSegs][kRows];
+        float x[kSegs][kRows][kV];
+#pragma unroll
+        for (int g = 0; g < kSegs; ++g) {
+            const int k = k0 + g;
+            const bool work = k == c || (k < end && !(k - c <= 32 ? (none >> (k - c - 1)) & 1u : ws.share[k].head == 3));
+            const size_t slot = (k == c ? 2 * static_cast<size_t>(c) + 1 : 2 * static_cast<size_t>(k)) * ws.cap + r0;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                ml[g][r] = make_float2(-INFINITY, 0.f);
+                if (!work || r0 + r >= s.rows) continue;
+                ml[g][r] = ws.ml[slot + r];
+                const float* src = ws.o + (slot + r) * D + lane * kV;
+                if constexpr (kV == 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(src);
+                    x[g][r][0] = t.x, x[g][r][1] = t.y, x[g][r][2] = t.z, x[g][r][3] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2*>(src);
+                    x[g][r][0] = t.x, x[g][r][1] = t.y;
+                }
+            }
         }
-        const int mm = s.m0 + r;
+#pragma unroll
+        for (int g = 0; g < kSegs; ++g) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                if (ml[g][r].x == -INFINITY && ml[g][r].y == 0.f) continue;
+                const float to = fmaxf(m[r], ml[g][r].x);
+                const float a = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - to), b = fast_exp2(ml[g][r].x - to);
+                m[r] = to;
+                l[r] = l[r] * a + ml[g][r].y * b;
+#pragma unroll
+                for (int j = 0; j < kV; ++j) o[r][j] = o[r][j] * a + x[g][r][j] * b;
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        if (r0 + r >= s.rows) break;
+        const int mm = s.m0 + r0 + r;
         const size_t at = (static_cast<size_t>(s.row0) + mm / p.group) * p.H + s.hk * p.group + mm % p.group;
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const float inv = l[r] > 0.f ? 1.f / l[r] : (l[r] == 0.f ? 0.f : l[r]);
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * kV);
         if constexpr (kV == 4)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(f32x2_to_bf16x2(o[0] * inv, o[1] * inv), f32x2_to_bf16x2(o[2] * inv, o[3] * inv));
+            *reinterpret_cast<uint2*>(dst) = make_uint2(f32x2_to_bf16x2(o[r][0] * inv, o[r][1] * inv),
+                                                        f32x2_to_bf16x2(o[r][2] * inv, o[r][3] * inv));
         else
-            *dst = f32x2_to_bf16x2(o[0] * inv, o[1] * inv);
-        if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+            *dst = f32x2_to_bf16x2(o[r][0] * inv, o[r][1] * inv);
+        if (lane == 0 && p.lse) p.lse[at] = l[r] == 0.f ? -INFINITY : m[r] * kLn2 + logf(l[r]);
     }
 }
 
@@ -1634,7 +1652,9 @@ cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
         launch_pdl(attend_kernel<D, E4M3, SMALL>, dim3(grid), dim3(C::kThreads), C::kTotal, s, tmK, tmV, tmQ,
                    p, ws);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attend_merge_kernel<D>, dim3(grid, (ws.cap + 7) / 8), dim3(256), 0, s, p, ws, grid);
+    constexpr int kRows = SMALL ? 1 : 2, kSegs = SMALL ? 8 : 1;
+    return launch_pdl(attend_merge_kernel<D, kRows, kSegs>, dim3(grid, (ws.cap + 8 * kRows - 1) / (8 * kRows)),
+                      dim3(256), 0, s, p, ws, grid);
 }
 
 }  // namespace
@@ -1651,8 +1671,16 @@ size_t attend_workspace(int R, int max_window, int H, int D, int rows, int kv_he
 // stream form do, and the shared memory of the other goes to the ring.
 template <int D, bool E4M3>
 static cudaError_t launch_form(const AttendParams& p, void* ws, cudaStream_t s) {
+    // Costs of the shares' units, about 0.1 us each, fitted to the blocks' times:
+    // a block besides its tiles (Q, the first product, the last O), a key tile
+    // for two sub-tiles (with remainders: twice), for one.
     const bool small = static_cast<long long>(p.max_window) * p.group <= kStackRows;
-    return small ? launch_one<D, E4M3, true>(p, ws, s) : launch_one<D, E4M3, false>(p, ws, s);
+    AttendParams q = p;
+    q.cost_block = 35;
+    q.cost_pair = (D == 128 ? 16 : 12) + (E4M3 ? 4 : 0);
+    q.cost_twice = q.cost_pair * 3 / 2;
+    q.cost_stream = (D == 128 ? 13 : 8) + (E4M3 ? 3 : 0);
+    return small ? launch_one<D, E4M3, true>(q, ws, s) : launch_one<D, E4M3, false>(q, ws, s);
 }
 
 cudaError_t launch_attend(const AttendParams& p, void* ws, cudaStream_t s) {

@@ -511,6 +511,7 @@ struct AttendParams {
     const int32_t* ctx;
     int R, rows, max_window, H, group;   // group = query heads per kv head (at most 128)
     int sub;              // rows of a sub-tile: group times the tokens that 128 rows hold
+    int cost_block, cost_pair, cost_twice, cost_stream;   // units of the CTAs' shares (set at the launch)
     float scale;
     int window, sinks;
     const uint32_t* tree;   // [R, nodes, words] or NULL
