@@ -1417,13 +1417,15 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         // 2^(e - 127) as bf16, twice: every e a write leaves is in bf16's range
                         const uint32_t sc = e << 7;
                         const uint32_t scale2 = sc | (sc << 16);
+                        // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
+                        // bytes at c ^ (r / 2 mod 4)
+                        const int turn_of = D == 128 ? (row & 7) : ((row >> 1) & 3);
+                        uint4 x = *reinterpret_cast<const uint4*>(src + turn_of * 16);
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
-                            // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
-                            // bytes at c ^ (r / 2 mod 4)
-                            const int at = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
-                            const uint4 x = *reinterpret_cast<const uint4*>(src + at * 16);
                             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                            // the next piece's load runs under this one's arithmetic
+                            x = *reinterpret_cast<const uint4*>(src + ((((c + 1) & (D / 16 - 1)) ^ turn_of) << 4));
                             uint32_t o[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
