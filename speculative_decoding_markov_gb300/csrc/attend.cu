@@ -1403,7 +1403,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 if (!vb) break;
                 const Blk b = copy(vb);
                 const int len = b.ctx + b.n;
-                bool found = false;    // a value that is not finite, cleared
                 for (int t = b.t0; t < b.t1; ++t) {
                     const int key0 = tile_key(b, t);
                     const bool clear = v == 1 && tile_cleaned(p, b, key0);
@@ -1421,7 +1420,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         // bytes at c ^ (r / 2 mod 4)
                         const int turn_of = D == 128 ? (row & 7) : ((row >> 1) & 3);
                         uint4 x = *reinterpret_cast<const uint4*>(src + turn_of * 16);
-#pragma unroll 1
+#pragma unroll 2
                         for (int c = 0; c < D / 16; ++c) {
                             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                             // the next piece's load runs under this one's arithmetic
@@ -1435,24 +1434,28 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                                 asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(scale2));
                                 o[j] = y;
                             }
-                            if (clear) {
+                            uint8_t* half = dst + (c >> 2) * (kTile * 128);
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const uint32_t bad = nonfinite2(o[j]);
-                                    if (bad & 0x8000u) o[j] &= 0xffff0000u;
-                                    if (bad & 0x80000000u) o[j] &= 0xffffu;
-                                    found |= bad != 0 && key0 + row < len;
+                            for (int h = 0; h < 2; ++h)
+                                *reinterpret_cast<uint4*>(half + (((((2 * c) & 7) | h) ^ (row & 7)) << 4)) =
+                                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+                            if (clear) {
+                                uint32_t bad = 0;   // bits 15 and 31: an exponent field of ones
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) bad |= (o[j] & 0x7fff7fffu) + 0x00800080u;
+                                if (__builtin_expect((bad & 0x80008000u) != 0, 0)) {
+                                    if (key0 + row < len) blks[rd.at()].nonfinite = 1;
+#pragma unroll 1
+                                    for (int j = 0; j < 8; ++j) {
+                                        uint32_t* y = reinterpret_cast<uint32_t*>(
+                                            half + (((((2 * c) & 7) | (j >> 2)) ^ (row & 7)) << 4) + (j & 3) * 4);
+                                        bad = nonfinite2(*y);
+                                        if (bad & 0x8000u) *y &= 0xffff0000u;
+                                        if (bad & 0x80000000u) *y &= 0xffffu;
+                                    }
                                 }
                             }
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int oc = 2 * c + h;
-                                *reinterpret_cast<uint4*>(dst + (oc >> 3) * (kTile * 128) +
-                                                          (((oc & 7) ^ (row & 7)) << 4)) =
-                                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
-                            }
                         }
-                        if (found) blks[rd.at()].nonfinite = 1;
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
