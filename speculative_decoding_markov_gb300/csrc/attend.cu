@@ -726,12 +726,13 @@ struct Out {
 };
 
 // Columns 16 c0 .. 16 c1 - 1 of a warp's 32 rows of O, from tensor memory to
-// where they go.  JOINED: w0 O0 + w1 O1 (t1 = 0: no O1); STACKED: the lane 16
-// on holds the remainders' part.
-template <int D, bool E4M3, bool JOINED, bool STACKED>
+// where they go.  JOINED: w0 O0 + w1 O1 (t1 = 0: no O1); stacked: the lane 16
+// on holds the remainders' part.  It runs once a block, so its time is the
+// instructions' way into the cache: no copy for each form.
+template <int D, bool E4M3, bool JOINED>
 __device__ __forceinline__ void put_rows(const AttendParams& p, const Scratch& ws, const Out<D>& to, uint32_t t0,
-                                         uint32_t t1, int c0, int c1, float w0, float w1, const volatile Blk* odd,
-                                         int m, float m_ref) {
+                                         uint32_t t1, int c0, int c1, float w0, float w1, bool stacked,
+                                         const volatile Blk* odd, int m, float m_ref) {
     // out is 16-byte aligned: 32-byte stores where it is more
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     uint32_t o[16], q[16];
@@ -754,7 +755,7 @@ __device__ __forceinline__ void put_rows(const AttendParams& p, const Scratch& w
             tmem_ld16(t0 + (c + 1) * 16, o);
             if (JOINED && t1) tmem_ld16(t1 + (c + 1) * 16, q);
         }
-        if constexpr (STACKED) {
+        if (JOINED && stacked) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float y = __shfl_down_sync(0xffffffffu, f[j], 16);
@@ -1063,13 +1064,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 to.inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
                 const volatile Blk* odd = vb->nonfinite ? vb : nullptr;
                 const bool two = joined && n_tiles > 1;   // else the second warpgroup's o was never written
-                if (pair) put_rows<D, E4M3, false, false>(p, ws, to, tO, 0, 0, D / 16, 1.f, 0.f, odd, m, m_ref);
-                else if (stacked)
-                    put_rows<D, E4M3, true, true>(p, ws, to, tO0, two ? tO1 : 0, wg * (D / 32), (wg + 1) * (D / 32), a0,
-                                                  a1, odd, m, m_ref);
+                if (pair) put_rows<D, E4M3, false>(p, ws, to, tO, 0, 0, D / 16, 1.f, 0.f, false, odd, m, m_ref);
                 else
-                    put_rows<D, E4M3, true, false>(p, ws, to, tO0, two ? tO1 : 0, wg * (D / 32), (wg + 1) * (D / 32),
-                                                   a0, a1, odd, m, m_ref);
+                    put_rows<D, E4M3, true>(p, ws, to, tO0, two ? tO1 : 0, wg * (D / 32), (wg + 1) * (D / 32), a0, a1,
+                                            stacked, odd, m, m_ref);
                 if (to.valid && (!joined || wg == 0)) {
                     if (!whole) ws.ml[to.slot] = make_float2(m_ref, l);
                     else if (p.lse) p.lse[to.at] = l == 0.f ? -INFINITY : m_ref * kLn2 + logf(l);
