@@ -1408,21 +1408,21 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         ok = wait_or_fail(p, &bar.raw_full[rs], raw_turn & 1);
                         if (ok && turn > 0) ok = wait_or_fail(p, &bar.empty[s], (turn - 1) & 1);
                         if (!ok) break;
-                        const uint8_t* src = smem + C::kRaw + rs * C::kRawBytes + row * D;
-                        uint8_t* dst = smem + C::kRing + s * C::kTileBytes + row * 128;
+                        // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
+                        // bytes at c ^ (r / 2 mod 4); a bf16 row's pieces 2 c and 2 c + 1 likewise
+                        const int src = C::kRaw + rs * C::kRawBytes + row * D +
+                                        (D == 128 ? (row & 7) : ((row >> 1) & 3)) * 16;
+                        const int dst = C::kRing + s * C::kTileBytes + row * 128 + (row & 7) * 16;
                         const uint32_t e = smem[C::kExps + rs * kTile + row];
                         // 2^(e - 127) as bf16, twice: every e a write leaves is in bf16's range
                         const uint32_t sc = e << 7;
                         const uint32_t scale2 = sc | (sc << 16);
-                        // the TMA swizzle: 16-byte piece c of row r sits at c ^ (r mod 8), rows of 64
-                        // bytes at c ^ (r / 2 mod 4)
-                        const int turn_of = D == 128 ? (row & 7) : ((row >> 1) & 3);
-                        uint4 x = *reinterpret_cast<const uint4*>(src + turn_of * 16);
+                        uint4 x = *reinterpret_cast<const uint4*>(smem + src);
 #pragma unroll 2
-                        for (int c = 0; c < D / 16; ++c) {
+                        for (int c = 0; c < D; c += 16) {
                             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                             // the next piece's load runs under this one's arithmetic
-                            x = *reinterpret_cast<const uint4*>(src + ((((c + 1) & (D / 16 - 1)) ^ turn_of) << 4));
+                            x = *reinterpret_cast<const uint4*>(smem + (src ^ ((c + 16) & (D - 1))));
                             uint32_t o[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
@@ -1432,11 +1432,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                                 asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(scale2));
                                 o[j] = y;
                             }
-                            uint8_t* half = dst + (c >> 2) * (kTile * 128);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                *reinterpret_cast<uint4*>(half + (((((2 * c) & 7) | h) ^ (row & 7)) << 4)) =
-                                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+                            const int to = (dst + (c >> 6) * (kTile * 128)) ^ ((2 * c) & 127);
+                            *reinterpret_cast<uint4*>(smem + to) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(smem + (to ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                             if (clear) {
                                 uint32_t bad = 0;   // bits 15 and 31: an exponent field of ones
 #pragma unroll
@@ -1445,8 +1443,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                                     if (key0 + row < len) blks[rd.at()].nonfinite = 1;
 #pragma unroll 1
                                     for (int j = 0; j < 8; ++j) {
-                                        uint32_t* y = reinterpret_cast<uint32_t*>(
-                                            half + (((((2 * c) & 7) | (j >> 2)) ^ (row & 7)) << 4) + (j & 3) * 4);
+                                        uint32_t* y = reinterpret_cast<uint32_t*>(smem + (to ^ (j * 4)));
                                         bad = nonfinite2(*y);
                                         if (bad & 0x8000u) *y &= 0xffff0000u;
                                         if (bad & 0x80000000u) *y &= 0xffffu;
