@@ -12,24 +12,38 @@
 // in the first tiles of a row and hardly ever after.
 //
 // Work.  A block is up to two sub-tiles of one request and kv head, a sub-tile
-// the rows of as many whole tokens as 128 lanes hold.  A larger block than one
-// sub-tile runs in `pair` form: both softmax
-// warpgroups see every key tile, each for its own 128 rows.  A smaller one
-// runs in `stream` form: the warpgroups take alternate key tiles of the same
-// rows and their (m, l, o) are joined at its end.  The key tiles of all blocks
-// laid end to end are cut into equal shares, one per CTA (one CTA per SM,
-// persistent): a long context is split over as many SMs as it fills, many
-// short ones share an SM, and no schedule is kept between calls.  Blocks that
-// a cut splits leave (m, l, o) in the workspace and attend_merge_kernel joins
-// them in the order of the keys, so results do not depend on timing.
+// the rows of as many whole tokens as 128 lanes hold.  A block larger than one
+// sub-tile runs in `pair` form: both softmax warpgroups see every key tile,
+// each for its own 128 rows.  A smaller one runs in `stream` form: the
+// warpgroups take alternate key tiles of the same rows and their (m, l, o) are
+// joined at its end.  The key tiles of all blocks laid end to end are cut into
+// shares of equal cost, one per CTA (one CTA per SM, persistent): a long
+// context is split over as many SMs as it fills, many short ones share an SM,
+// and no schedule is kept between calls.  Blocks that a cut splits leave (m,
+// l, o) in the workspace and attend_merge_kernel joins them in the order of
+// the keys, so results do not depend on timing.
 //
-// Pipeline of a CTA: one warp walks the share and hands each block
-// to the others; a producer brings K and V tiles page by page with TMA into a
-// ring; one gathers Q and clears values (below); one issues S = Q K^T and O +=
-// P V; eight do the softmax, S from tensor memory to registers and P back over
-// S; e4m3: eight turn codes into bf16, exactly, the scale included, in a second
-// ring.  Each softmax warpgroup's S, P and O are its own, so
-// one's softmax runs beside the other's products.
+// Pipeline of a CTA: one warp walks the share and hands each block to the
+// others; a producer brings K and V tiles page by page with TMA into a ring;
+// one brings Q and clears values (below); one issues S = Q K^T and O += P V;
+// eight do the softmax, S from tensor memory to registers and P back over S;
+// e4m3: a warpgroup each turns K's and V's codes into bf16, exactly, the scale
+// included, in a second ring.  Each softmax warpgroup's S, P and O are its
+// own, so one's softmax runs beside the other's products.
+//
+// What bounds it (32 query heads on 8 kv heads of 128, bf16, unless said):
+//   64 windows of 1 to 8 tokens over 300 to 8000: HBM, 5.7 TB/s (107 us).
+//   A prompt of 8192 tokens: the softmax between its two products, 1.31
+//   PFLOP/s, tensor pipe 56 % (419 us).  A 128 x 128 tile's softmax takes 1112
+//   clocks alone and 1800 beside the other warpgroup's, its two products with
+//   their hand-overs 1460; S has no room for a second buffer beside O.
+//   e4m3 windows: turning the codes into bf16, about 6000 warp instructions a
+//   tile of 128 keys and 50 % of the issue slots: 3.3 TB/s of codes at two
+//   contexts of 150001 to 199999 (28 heads on 4, 104 us).
+//   One token over 500 keys: the chain of plan, loads, two products and merge
+//   (12.8 us).
+// The warps' loops together have to stay in the instruction cache: unrolling
+// one of them twice more than now cost 5 to 40 %, wherever it was tried.
 //
 // What a row does not see does not reach it: scores are replaced, not added
 // to; values of a tile that some row sees only in part are cleared of NaN and
@@ -48,11 +62,17 @@ constexpr int kTile = 128;            // keys per tile, rows per sub-tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;
-// The weights enter the second product as bf16.  Where a row sees few keys,
-// nothing averages that rounding out, so the remainder p - bf16(p) is
+// The weights enter the second product as bf16: an error of at most 2^-8 of a
+// weight, which the sum over many keys averages out.  Where a row sees few
+// keys, or few that count, it does not, so the remainder p - bf16(p) is
 // multiplied too: in blocks of at most kStackTiles key tiles that leave half of
 // the 128 lanes free as rows of the same product (row r in lane r of its 16,
 // the remainder 16 lanes on), in blocks of at most kFineTiles by a second one.
+// With these the error stays below 2^-8 of sum p |v| (that of rounding the
+// result) on peaked rows of about 1000 keys; with 4 and 4 tiles it did not.
+// Cost against no remainders at all: 256 e4m3 windows over 200 to 4000 tokens
+// 137 -> 149 us, five e4m3 windows of 37 to 1500 tokens 56 -> 66 us, 32 trees
+// of 65 slots 131 -> 133 us, a prompt of 8192 414 -> 419 us.
 constexpr int kStackRows = 64;
 constexpr int kFineTiles = 9, kStackTiles = 16;
 constexpr int kTmemCols = 512;        // S0, S1, O0, O1 at columns 0, 128, 256, 384; P over S
@@ -66,6 +86,11 @@ struct Blk {
 };
 enum { BLK_PAIR = 1, BLK_STACKED = 2, BLK_TWICE = 4 };
 
+// SMALL: all windows of the call fit in kStackRows rows.  Their calls are
+// bound by loads, and the second sub-tile of Q that they do not need holds two
+// more tiles of the rings: 64 windows of 1 to 8 tokens 107 us against 120, 256
+// e4m3 windows 149 against 184, two e4m3 contexts of 150001 to 199999 104
+// against 144, one token over 500 keys 12.8 against 13.3.
 template <int D, bool E4M3, bool SMALL>
 struct Cfg {
     static constexpr int kThreads = E4M3 ? 640 : 384;
@@ -88,7 +113,8 @@ struct Cfg {
     static constexpr int kXch = kExps + kRawSlots * kTile;   // (m, l) of both warpgroups' rows
     static constexpr int kBlks = kXch + 2 * kXchRows * 8;
     static constexpr int kBars = kBlks + kRingBlocks * static_cast<int>(sizeof(Blk));
-    static constexpr int kNumBars = (E4M3 ? 2 * kSlots + 1 : 3 * kSlots) + 2 * (kRawSlots > 0 ? kRawSlots : 1) + 2 * kRingBlocks + 13;
+    static constexpr int kNumBars = (E4M3 ? 2 * kSlots + 1 : 3 * kSlots) + 2 * (kRawSlots > 0 ? kRawSlots : 1) +
+                                    2 * kRingBlocks + 13;
     static constexpr int kMisc = kBars + kNumBars * 8;
     static constexpr int kTotal = kMisc + 16;
     static_assert(kTotal <= 232448, "shared memory");
@@ -626,9 +652,10 @@ __device__ __forceinline__ void weights32(uint32_t (&xs)[32], uint32_t tP, float
 
 // A tile's scores at tS (this warp's 32 rows, 128 columns) to its weights P
 // (64 columns at tS); returns the row's sum.  The scores are read 32 at a time
-// (held from the maximum on they would fill the registers); P is handed over in two halves, the products of the first running beside the
-// exponentials of the second.  One copy per form, and a loop over the halves:
-// the code of a tile has to stay in the instruction cache.
+// (held from the maximum on they would fill the registers); P is handed over
+// in two halves, the products of the first running beside the exponentials of
+// the second.  One copy per form, and a loop over the halves: the code of a
+// tile has to stay in the instruction cache.
 template <int FORM>
 __device__ __forceinline__ float weights128(uint32_t tS, float sl, float neg, bool rest, uint64_t* some,
                                             uint64_t* more) {
@@ -862,6 +889,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     pdl_wait();
     pdl_trigger();
     // a few small requests: the walking warp finds the start by itself, later
+    // (one token over 500 keys 12.8 us against 14.4 with all warps, 32 trees of
+    // 65 slots 133 against 135); beyond 32 it would need several rounds
     const bool by_all = p.R > 32 || p.max_window * p.group > 4 * p.sub;
     if (by_all) plan<C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
     Start st = *start;   // read before the roles use its place
@@ -1029,7 +1058,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                     x_open = false;
                     if (!ok) break;
                 }
-                if (!SMALL || (!rest && r < kStackRows)) xch[wg * C::kXchRows + (SMALL ? r : row)] = make_float2(m_ref, l);
+                if (!SMALL || (!rest && r < kStackRows))
+                    xch[wg * C::kXchRows + (SMALL ? r : row)] = make_float2(m_ref, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.xch);
                 ok = wait_or_fail(p, &bar.xch, n_x & 1);
@@ -1388,7 +1418,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     } else {
         // --------------------------------------------------------------------
         // e4m3 codes -> bf16 values, a key's row per thread; one warpgroup takes
-        // the K tiles, the other the V tiles
+        // the K tiles, the other the V tiles.  A tile takes a warpgroup about
+        // 1900 clocks, its instructions' rate beside the other's (two warpgroups
+        // a tile: slower, 106 -> 118 us for two contexts of 150001 to 199999);
+        // two pieces a step is what the instruction cache holds (one: 110 us,
+        // four: 104 us there, but 256 windows 155 -> 188 us)
         // --------------------------------------------------------------------
         if constexpr (E4M3) {
             set_regs_down<C::kRegsRest>();
@@ -1486,7 +1520,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
 // Joins the segments of split blocks, in key order: the CTA whose share
 // starts a block and the next ones that continue it.  kRows rows a warp, the
 // loads of kSegs segments together: the kernel is a chain of a few L2 round
-// trips.
+// trips (bytes: at most 2 x 256 rows x 4 D per CTA, written and read once).
+// Small windows are long contexts over many CTAs, so 8 segments of a row: one
+// token's merge over two contexts of 150001 to 199999 (38 segments) takes 8.7
+// us and the call 119 against 129 with a segment at a time; 4 and 16 are 2 us
+// slower.  Larger ones have two or three segments and many rows, so 2 rows: 12
+// us of a call of 66 for five e4m3 windows (a row at a time: 13).
 template <int D, int kRows, int kSegs>
 __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p, const Scratch ws, int grid) {
     constexpr int kV = D / 32;
@@ -1526,7 +1565,8 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p,
 #pragma unroll
         for (int g = 0; g < kSegs; ++g) {
             const int k = k0 + g;
-            const bool work = k == c || (k < end && !(k - c <= 32 ? (none >> (k - c - 1)) & 1u : ws.share[k].head == 3));
+            const bool idle = k > c && k < end && (k - c <= 32 ? (none >> (k - c - 1)) & 1u : ws.share[k].head == 3);
+            const bool work = k < end && !idle;
             const size_t slot = (k == c ? 2 * static_cast<size_t>(c) + 1 : 2 * static_cast<size_t>(k)) * ws.cap + r0;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
@@ -1671,9 +1711,13 @@ size_t attend_workspace(int R, int max_window, int H, int D, int rows, int kv_he
 // stream form do, and the shared memory of the other goes to the ring.
 template <int D, bool E4M3>
 static cudaError_t launch_form(const AttendParams& p, void* ws, cudaStream_t s) {
-    // Costs of the shares' units, about 0.1 us each, fitted to the blocks' times:
-    // a block besides its tiles (Q, the first product, the last O), a key tile
-    // for two sub-tiles (with remainders: twice), for one.
+    // Costs of the shares' units, about 0.1 us each, fitted to the times of the
+    // CTAs' shares: a block besides its tiles (Q, the first product, the last
+    // O; 3.5 to 8 us), a key tile for two sub-tiles (bf16 1.6 us at 128 wide,
+    // 1.3 at 64; e4m3 2.0; with remainders half as much again), for one (1.3 us
+    // at 128, the HBM's rate; 0.75 at 64; e4m3 1.5).  Against a block at 2.5
+    // tiles of one cost for both types: five e4m3 windows 73.5 -> 66 us, a
+    // prompt of 8192 429 -> 422 us.
     const bool small = static_cast<long long>(p.max_window) * p.group <= kStackRows;
     AttendParams q = p;
     q.cost_block = 35;

@@ -17,6 +17,11 @@ constexpr int kWarps = kThreads / 32;
 // One warp per packed row, its loads in flight before the row's slot is
 // known.  D / 8 lanes hold one (K or V, head) vector of D elements, 16 bytes
 // each, so the maximum of a vector is a shuffle reduction over those lanes.
+// e4m3: the smallest scale 2^e with max |x| <= 448 2^e, so that a code's error
+// is 2^-4 of its value, or 2^-10 2^e where that is more; scaling is exact.
+// 24831 rows of 8 heads x 128 as e4m3: 39 us, 3.9 TB/s, the conversion's 68 %
+// of the issue slots beside it; small calls are the chain cu_seqlens -> request
+// -> page -> slot (7 us for 2080 rows).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteParams p) {
     constexpr int kLanes = D / 8;           // lanes per vector
@@ -107,7 +112,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
 }
 
 // One warp per output row; D / 8 lanes read 8 elements each of one vector and
-// write them as 16 bytes of bf16.
+// write them as 16 bytes of bf16: code x 2^e is exact in bf16.  46418
+// tokens of 8 heads x 128 from e4m3: 48 us, 5.9 TB/s, bound by HBM.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadParams p) {
     constexpr int kLanes = D / 8;
@@ -175,7 +181,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
     }
 }
 
-// One CTA per request.  The first warp walks the tree (one ballot per 32
+// One CTA per request: path[0] = the root, path[j + 1] = the child of path[j]
+// whose token is out_tok[j]; then row path[j] moves to row j.  The bytes are
+// few, so the time is a chain of dependent loads: 10 us for 32 trees of 65
+// slots, 8 heads x 128.  The first warp walks the tree (one ballot per 32
 // slots and level), then all threads move the path's rows in order of their
 // destination: a batch is loaded whole, then stored.  A source slot path[j]
 // is never below its destination j, so a store cannot reach a slot that a
