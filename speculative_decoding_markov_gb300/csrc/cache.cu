@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCommitThreads = 512;     // 32 trees of 65 slots, written and committed: 8.3 us (256: 9.2, 1024: 8.5)
 
 // One warp per packed row, its loads in flight before the row's slot is
 // known.  D / 8 lanes hold one (K or V, head) vector of D elements, 16 bytes
@@ -183,13 +184,13 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
 
 // One CTA per request: path[0] = the root, path[j + 1] = the child of path[j]
 // whose token is out_tok[j]; then row path[j] moves to row j.  The bytes are
-// few, so the time is a chain of dependent loads: 10 us for 32 trees of 65
+// few, so the time is a chain of dependent loads: 9 us for 32 trees of 65
 // slots, 8 heads x 128.  The first warp walks the tree (one ballot per 32
 // slots and level), then all threads move the path's rows in order of their
 // destination: a batch is loaded whole, then stored.  A source slot path[j]
 // is never below its destination j, so a store cannot reach a slot that a
 // later batch still reads.
-__global__ void __launch_bounds__(kThreads) cache_commit_kernel(const CacheCommitParams p) {
+__global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const CacheCommitParams p) {
     extern __shared__ int32_t s_tree[];   // parent [N + 1], tok [N + 1], path [B + 1]
     __shared__ int s_len;
     const int S = p.N + 1;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) cache_commit_kernel(const CacheCommi
     const int i = blockIdx.x;
     pdl_wait();
     pdl_trigger();
-    for (int c = threadIdx.x; c < S; c += kThreads) {
+    for (int c = threadIdx.x; c < S; c += kCommitThreads) {
         s_parent[c] = __ldg(p.parent + static_cast<size_t>(i) * S + c);
         s_tok[c] = __ldg(p.tok + static_cast<size_t>(i) * S + c);
     }
@@ -237,19 +238,19 @@ __global__ void __launch_bounds__(kThreads) cache_commit_kernel(const CacheCommi
     }
     __syncthreads();
     const int len = s_len;
-    for (int j = threadIdx.x; j <= p.B; j += kThreads) p.path[static_cast<size_t>(i) * (p.B + 1) + j] = s_path[j];
+    for (int j = threadIdx.x; j <= p.B; j += kCommitThreads) p.path[static_cast<size_t>(i) * (p.B + 1) + j] = s_path[j];
     // 16-byte pieces of a (slot, K or V, head) row, then the scale exponents
     const int row_bytes = p.c.D * (p.c.e4m3 ? 1 : 2);
     const int pieces = row_bytes >> 4;
     const int per_slot = 2 * p.c.heads * (pieces + (p.c.e4m3 ? 1 : 0));
     const long long total = static_cast<long long>(len) * per_slot;   // the root stays where it is
     constexpr int kBatch = 4;
-    for (long long t0 = 0; t0 < total; t0 += kThreads * kBatch) {
+    for (long long t0 = 0; t0 < total; t0 += kCommitThreads * kBatch) {
         uint4 x[kBatch];
         uint8_t* to[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const long long t = t0 + b * kThreads + threadIdx.x;
+            const long long t = t0 + b * kCommitThreads + threadIdx.x;
             to[b] = nullptr;
             if (t >= total) continue;
             const int j = 1 + static_cast<int>(t / per_slot);
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) cache_commit_kernel(const CacheCommi
         __syncthreads();
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const long long t = t0 + b * kThreads + threadIdx.x;
+            const long long t = t0 + b * kCommitThreads + threadIdx.x;
             if (!to[b]) continue;
             if (static_cast<int>(t % per_slot) >= 2 * p.c.heads * pieces) *to[b] = static_cast<uint8_t>(x[b].x);
             else *reinterpret_cast<uint4*>(to[b]) = x[b];
@@ -322,7 +323,7 @@ cudaError_t launch_cache_commit(const CacheCommitParams& p, cudaStream_t s) {
                                                    static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(cache_commit_kernel, dim3(p.R), dim3(kThreads), smem, s, p);
+    return launch_pdl(cache_commit_kernel, dim3(p.R), dim3(kCommitThreads), smem, s, p);
 }
 
 }  // namespace sdm
