@@ -71,7 +71,7 @@ constexpr float kLazy = 8.0f;
 // With these the error stays below 2^-8 of sum p |v| (that of rounding the
 // result) on peaked rows of about 1000 keys; with 4 and 4 tiles it did not.
 // Cost against no remainders at all: 256 e4m3 windows over 200 to 4000 tokens
-// 137 -> 149 us, five e4m3 windows of 37 to 1500 tokens 56 -> 66 us, 32 trees
+// 137 -> 149 us, five e4m3 windows of 37 to 1500 tokens 55 -> 65 us, 32 trees
 // of 65 slots 131 -> 133 us, a prompt of 8192 414 -> 419 us.
 constexpr int kStackRows = 64;
 constexpr int kFineTiles = 9, kStackTiles = 16;
@@ -749,8 +749,22 @@ template <int D>
 struct Out {
     bool valid, whole;
     size_t at, slot;
-    float inv;             // 1 / l
 };
+
+// Two at a time: (f0, f1) = (a0, a1) w; (f0, f1) += (a0, a1) w.
+__device__ __forceinline__ void scale2(float& f0, float& f1, float a0, float a1, float w) {
+    asm("{\n\t.reg .b64 a, w;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 w, {%4, %4};\n\t"
+        "mul.rn.f32x2 a, a, w;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(f0), "=f"(f1)
+        : "f"(a0), "f"(a1), "f"(w));
+}
+
+__device__ __forceinline__ void add_scaled2(float& f0, float& f1, float a0, float a1, float w) {
+    asm("{\n\t.reg .b64 a, f, w;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 f, {%0, %1};\n\tmov.b64 w, {%4, %4};\n\t"
+        "fma.rn.f32x2 f, a, w, f;\n\tmov.b64 {%0, %1}, f;\n\t}"
+        : "+f"(f0), "+f"(f1)
+        : "f"(a0), "f"(a1), "f"(w));
+}
 
 // Columns 16 c0 .. 16 c1 - 1 of a warp's 32 rows of O, from tensor memory to
 // where they go.  JOINED: w0 O0 + w1 O1 (t1 = 0: no O1); stacked: the lane 16
@@ -771,12 +785,14 @@ __device__ __forceinline__ void put_rows(const AttendParams& p, const Scratch& w
     for (int c = c0; c < c1; ++c) {
         float f[16];
         tmem_ld_wait();
+        // a weight is 0 only where that o is 0 too (no key seen) or absent
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]);
+        for (int j = 0; j < 16; j += 2)
+            scale2(f[j], f[j + 1], __uint_as_float(o[j]), __uint_as_float(o[j + 1]), w0);
         if constexpr (JOINED) {
-            // a weight is 0 only where that o is 0 too (no key seen) or absent
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = fmaf(__uint_as_float(q[j]), w1, f[j] * w0);
+            for (int j = 0; j < 16; j += 2)
+                add_scaled2(f[j], f[j + 1], __uint_as_float(q[j]), __uint_as_float(q[j + 1]), w1);
         }
         if (c + 1 < c1) {   // the next columns on their way
             tmem_ld16(t0 + (c + 1) * 16, o);
@@ -795,14 +811,14 @@ __device__ __forceinline__ void put_rows(const AttendParams& p, const Scratch& w
             const int4* src = reinterpret_cast<const int4*>(const_cast<const Blk*>(odd));
 #pragma unroll
             for (int k = 0; k < 4; ++k) reinterpret_cast<int4*>(&blk)[k] = src[k];
-            for (int j = 0; j < 16; ++j) g[j] = f[j];
+            for (int j = 0; j < 16; ++j) g[j] = 0.f;
             add_nonfinite<D, E4M3>(p, blk, m, m_ref, c * 16, g);
-            for (int j = 0; j < 16; ++j) f[j] = g[j];
+            for (int j = 0; j < 16; ++j) f[j] += g[j];   // scaling would change neither infinities nor NaN
         }
         if (to.whole) {
             uint32_t y[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = f32x2_to_bf16x2(f[2 * j] * to.inv, f[2 * j + 1] * to.inv);
+            for (int j = 0; j < 8; ++j) y[j] = f32x2_to_bf16x2(f[2 * j], f[2 * j + 1]);
             uint16_t* dst = p.out + to.at * D + c * 16;
             if (to.valid && wide) store_v8(dst, y);
             if (to.valid && !wide) {
@@ -1091,10 +1107,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 to.whole = whole;
                 to.at = (static_cast<size_t>(vb->row0) + wp) * p.H + vb->hk * p.group + (m - wp * p.group);
                 to.slot = slot * ws.cap + r;
-                to.inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+                if (whole) {
+                    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+                    a0 *= inv;
+                    a1 *= inv;
+                }
                 const volatile Blk* odd = vb->nonfinite ? vb : nullptr;
                 const bool two = joined && n_tiles > 1;   // else the second warpgroup's o was never written
-                if (pair) put_rows<D, E4M3, false>(p, ws, to, tO, 0, 0, D / 16, 1.f, 0.f, false, odd, m, m_ref);
+                if (pair) put_rows<D, E4M3, false>(p, ws, to, tO, 0, 0, D / 16, a0, 0.f, false, odd, m, m_ref);
                 else
                     put_rows<D, E4M3, true>(p, ws, to, tO0, two ? tO1 : 0, wg * (D / 32), (wg + 1) * (D / 32), a0, a1,
                                             stacked, odd, m, m_ref);
@@ -1525,7 +1545,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
 // token's merge over two contexts of 150001 to 199999 (38 segments) takes 8.7
 // us and the call 119 against 129 with a segment at a time; 4 and 16 are 2 us
 // slower.  Larger ones have two or three segments and many rows, so 2 rows: 12
-// us of a call of 66 for five e4m3 windows (a row at a time: 13).
+// us of a call of 65 for five e4m3 windows (a row at a time: 13).
 template <int D, int kRows, int kSegs>
 __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p, const Scratch ws, int grid) {
     constexpr int kV = D / 32;
@@ -1716,7 +1736,7 @@ static cudaError_t launch_form(const AttendParams& p, void* ws, cudaStream_t s) 
     // O; 3.5 to 8 us), a key tile for two sub-tiles (bf16 1.6 us at 128 wide,
     // 1.3 at 64; e4m3 2.0; with remainders half as much again), for one (1.3 us
     // at 128, the HBM's rate; 0.75 at 64; e4m3 1.5).  Against a block at 2.5
-    // tiles of one cost for both types: five e4m3 windows 73.5 -> 66 us, a
+    // tiles of one cost for both types: five e4m3 windows 73.5 -> 66 us then, a
     // prompt of 8192 429 -> 422 us.
     const bool small = static_cast<long long>(p.max_window) * p.group <= kStackRows;
     AttendParams q = p;
