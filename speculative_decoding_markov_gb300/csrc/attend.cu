@@ -38,8 +38,8 @@
 //   clocks alone and 1800 beside the other warpgroup's, its two products with
 //   their hand-overs 1460; S has no room for a second buffer beside O.
 //   e4m3 windows: turning the codes into bf16, about 6000 warp instructions a
-//   tile of 128 keys and 50 % of the issue slots: 3.3 TB/s of codes at two
-//   contexts of 150001 to 199999 (28 heads on 4, 104 us).
+//   tile of 128 keys and 50 % of the issue slots: 3.4 TB/s of codes at two
+//   contexts of 150001 to 199999 (28 heads on 4, 101 us).
 //   One token over 500 keys: the chain of plan, loads, two products and merge
 //   (12.8 us).
 // The warps' loops together have to stay in the instruction cache: unrolling
@@ -1136,9 +1136,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     } else if (warp < 12) {
         set_regs_down<C::kRegsRest>();
         bool ok = true;
-        if (warp == 8) {
+        if (warp == 11) {
             // ----------------------------------------------------------------
-            // producer: K and V tiles in turn, a lane per page
+            // producer: K and V tiles in turn, a lane per page.  Not the warp that
+            // shares its scheduler with the first warps of the softmax, the only
+            // busy ones of small windows (two contexts of 150001 to 199999 101 us
+            // against 104.5)
             // ----------------------------------------------------------------
             const int pages = kTile >> p.c.page_shift, page = 1 << p.c.page_shift;
             constexpr int kN = E4M3 ? C::kRawSlots : C::kSlots;
