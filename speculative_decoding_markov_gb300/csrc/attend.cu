@@ -1009,7 +1009,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         } else {
                             top = tile_max<2>(tS) * sl;
                         }
-                        if (__builtin_expect(__any_sync(0xffffffffu, top > m_ref + kLazy), 0)) {
+                        // only lanes that hold a row of the block have a say: what the others'
+                        // scores come from is left in shared memory by whatever ran before
+                        if (__builtin_expect(__any_sync(0xffffffffu, r < lim && top > m_ref + kLazy), 0)) {
                             const float to = fmaxf(m_ref, top);
                             const float corr = to == -INFINITY ? 1.f : fast_exp2(m_ref - to);
                             m_ref = to;
