@@ -141,7 +141,7 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
     p.sub = 128 / p.group * p.group;
     p.scale = scale;
     p.window = std::max(window, 0);
-    p.sinks = sinks;
+    p.sinks = std::min(sinks, kMaxTokens);   // no cache holds more, and the kernel rounds it up to whole tiles
     p.tree = reinterpret_cast<const uint32_t*>(tree_mask);
     p.nodes = tree_mask ? tree_nodes : 0;
     p.words = (p.nodes + 31) / 32;

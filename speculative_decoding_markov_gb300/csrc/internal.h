@@ -458,6 +458,10 @@ cudaError_t launch_threshold_sweep(const float* conf, const int32_t* ceiling, in
 // ---------------------------------------------------------------------------
 // Paged key/value cache (cache.cu) and attention over it (attend.cu)
 // ---------------------------------------------------------------------------
+// Tokens of a request that the kernels reach: positions rounded up to whole
+// tiles of 128 keys, and a tile's last key, stay within 32 bits.
+constexpr int32_t kMaxTokens = 0x7fffff00;
+
 struct CacheView {
     uint8_t* k;            // [n_pages, heads, page, D] bf16 or e4m3
     uint8_t* v;

@@ -42,3 +42,15 @@ def test_the_same_bits_whatever_ran_before(gpu_lib, e4m3, w, before, G):
         got.append(sdm.attend(s.cache, q, s.cu, s.ctx, w, lse=True, dev_status=s.status))
     assert torch.equal(got[0]["lse"], got[1]["lse"]) and torch.equal(got[0]["out"], got[1]["out"])
     assert s.status.item() == 0
+
+
+@pytest.mark.parametrize("sinks", [2 ** 31 - 1, 2 ** 31 - 128, 2 ** 31 - 129, 10 ** 6])
+@pytest.mark.parametrize("e4m3,w,ctx,tree", [(False, [3, 1], [700, 2500], False), (True, [3, 1], [700, 2500], False),
+                                             (False, [150, 20], [333, 900], False), (False, [33], [600], True)])
+def test_all_tokens_as_sinks(gpu_lib, sinks, e4m3, w, ctx, tree):
+    """The largest numbers of first tokens that stay visible: every one does."""
+    mask = ref.random_trees(1, w[0], 6, np.random.default_rng(4))["mask"] if tree else None
+    s = ref.Setup(w, ctx, 2, 64, 32, e4m3, seed=7)
+    s.write_all()
+    check(s, 8, window=20, sinks=sinks, mask=mask)
+    assert s.status.item() == 0
