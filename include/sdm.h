@@ -599,10 +599,10 @@ sdm_status sdm_observe(const float* conf, const int32_t* cu_seqlens, const int32
  * row count, an upper bound on cu_seqlens[R]; rows past cu_seqlens[R] are
  * neither read nor written.  Device checks (OR-ed into *dev_status): a window
  * that is not within [0, rows] or not monotone counts as empty, a negative
- * ctx_len as 0 (SDM_DEV_BAD_WINDOW); tokens past max_pages * page are left
- * out, and a token whose page id is outside [0, n_pages) is skipped when
- * written and moved, read back as zeros, and as page 0 by sdm_attend
- * (SDM_DEV_BAD_PAGE).
+ * ctx_len as 0 (SDM_DEV_BAD_WINDOW); tokens past max_pages * page, or past
+ * 2^31 - 256, are left out, and a token whose page id is outside [0, n_pages)
+ * is skipped when written and moved, read back as zeros, and as page 0 by
+ * sdm_attend (SDM_DEV_BAD_PAGE).
  */
 typedef struct {
     void* k;              /* device pool */

@@ -59,7 +59,7 @@ __device__ __forceinline__ Window window_of(const int32_t* cu, const int32_t* ct
 
 __device__ __forceinline__ long long table_tokens(const CacheView& c) {
     const long long t = static_cast<long long>(c.max_pages) << c.page_shift;
-    return t < 0x7fffffffll ? t : 0x7fffffffll;
+    return t < kMaxTokens ? t : kMaxTokens;
 }
 
 // Page id of token `pos` of request i, or -1 (past the table or outside the pool).

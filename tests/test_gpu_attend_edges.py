@@ -54,3 +54,29 @@ def test_all_tokens_as_sinks(gpu_lib, sinks, e4m3, w, ctx, tree):
     s.write_all()
     check(s, 8, window=20, sinks=sinks, mask=mask)
     assert s.status.item() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_the_last_positions_of_32_bits(gpu_lib, e4m3):
+    """A page table of 2^31 tokens over four pages in turn: windows that end at
+    the last position in use, 2^31 - 257, and one that runs past it."""
+    page, G, H, D, w, last = 128, 2, 8, 64, 5, 2 ** 31 - 256
+    s = ref.Setup([4 * page], [0], G, D, page, e4m3, seed=11, spare=0)
+    s.write_all()
+    order = s.cache.table[0, :4]
+    table = order.repeat(2 ** 31 // page // 4)[None].contiguous()
+    cache = sdm.PagedCache(s.cache.k, s.cache.v, table, s.cache.k_exp, s.cache.v_exp)
+    q = torch.randn((w, H, D), generator=s.gen).to(torch.bfloat16).cuda()
+    k, v = s.held(0, "k"), s.held(0, "v")
+    for ctx, rows, status in ((last - w, w, 0), (last - 3, 3, sdm.DEV_BAD_PAGE)):
+        for window in (1, 64, 300):
+            flag = sdm.new_status()
+            got = sdm.attend(cache, q, i32([0, w]), i32([ctx]), w, window=window, dev_status=flag)["out"]
+            at = torch.arange(ctx - 300, last) % (4 * page)                    # the tokens' places in the four pages
+            see = ref.visible(rows, 300, window)
+            o, _, big = ref.attend(q[:rows], k[at], v[at], see, D ** -0.5)
+            err = np.abs(got[:rows].double().cpu().numpy() - o)
+            assert (err <= (2.0 ** -7 + 2.0 ** -12) * big).all(), err.max()
+            assert flag.item() == status
+    flag = sdm.cache_write(cache, s.packed("k")[:w], s.packed("v")[:w], i32([0, w]), i32([last - 3]))
+    assert flag.item() == sdm.DEV_BAD_PAGE
