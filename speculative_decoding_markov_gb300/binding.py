@@ -127,7 +127,7 @@ def load(path: str = LIB_PATH):
 
 
 def lib():
-    return load()
+    return _lib or load()
 
 
 def _ptr(t):
@@ -541,6 +541,8 @@ class PagedCache:
 
     def __init__(self, k, v, table, k_exp=None, v_exp=None):
         _need_cuda(k, v, table, k_exp, v_exp)
+        if any(x is not None and x.get_device() != k.get_device() for x in (v, table, k_exp, v_exp)):
+            raise ValueError("a cache's tensors must be on one device")
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("k and v must be [pages, kv heads, page, head dim] alike")
         e4m3 = k.dtype == torch.float8_e4m3fn
@@ -577,13 +579,27 @@ class PagedCache:
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_this_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def _need_rows(what, x, heads, head_dim):
+def _stream_of(cache):
+    """The current stream of the cache's device, which has to be the current one."""
+    if _this_device() != cache.device:
+        raise ValueError(f"the cache is on device {cache.device}, not on the current one")
+    return _raw_stream(cache.device)
+
+
+# The checks of a call's tensors are on the path of the smallest calls (a step's
+# write and read: 11 us), so each is one expression without calls of its own.
+# `device`: the CUDA device a tensor has to be on (None: any).
+_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+
+
+def _need_rows(what, x, heads, head_dim, device=None):
     """Packed rows [rows, heads, head dim] bf16, contiguous within a row (a
     slice of a fused projection's output will do); returns the row stride."""
-    if x.dtype is not torch.bfloat16 or not x.is_cuda:
-        raise TypeError(f"{what} must be a bf16 CUDA tensor")
+    if x.dtype is not _BF16 or (x.get_device() != device and (device is not None or not x.is_cuda)):
+        raise TypeError(f"{what} must be a bf16 CUDA tensor on the cache's device")
     shape, st = x.shape, x.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         raise ValueError(f"{what} must be [rows, {heads}, {head_dim}]")
@@ -592,24 +608,38 @@ def _need_rows(what, x, heads, head_dim):
     return st[0] if shape[0] > 1 else max(st[0], heads * head_dim)
 
 
-def _need_i32(what, x, n):
-    if x.dtype is not torch.int32 or x.numel() < n or not x.is_cuda or not x.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 CUDA tensor of at least {n} entries")
+def _need_i32(what, x, n, device=None):
+    if (x.dtype is not _I32 or (x.get_device() != device and (device is not None or not x.is_cuda)) or x.numel() < n or
+            not x.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous int32 tensor of at least {n} entries on the cache's device")
     return x.data_ptr()
+
+
+def _need_out(what, x, shape, dtype, device):
+    """A buffer the kernels fill: exactly this shape and type, on the cache's device."""
+    if x.dtype is not dtype or x.get_device() != device or x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on the cache's device")
+    return x.data_ptr()
+
+
+def _need_ws(ws, device):
+    if ws.dtype is not _U8 or ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on the cache's device")
+    return ws.data_ptr()
 
 
 def cache_write(cache, k, v, cu_seqlens, ctx_len, dev_status=None):
     """The windows' keys and values [rows, kv heads, head dim] into their slots
     (tokens ctx_len[i], ctx_len[i] + 1, ...), quantised if the cache is e4m3."""
-    R = cache.requests
-    ks = _need_rows("k", k, cache.kv_heads, cache.head_dim)
-    vs = _need_rows("v", v, cache.kv_heads, cache.head_dim)
+    R, dev = cache.requests, cache.device
+    ks = _need_rows("k", k, cache.kv_heads, cache.head_dim, dev)
+    vs = _need_rows("v", v, cache.kv_heads, cache.head_dim, dev)
     if v.shape[0] != k.shape[0]:
         raise ValueError("k and v must have the same rows")
     dev_status = new_status(k.device) if dev_status is None else dev_status
-    st = lib().sdm_cache_write(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, _need_i32("cu_seqlens", cu_seqlens, R + 1),
-                               _need_i32("ctx_len", ctx_len, R), R, k.shape[0], dev_status.data_ptr(),
-                               _raw_stream(cache.device))
+    st = lib().sdm_cache_write(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs,
+                               _need_i32("cu_seqlens", cu_seqlens, R + 1, dev), _need_i32("ctx_len", ctx_len, R, dev),
+                               R, k.shape[0], _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_cache_write")
     return dev_status
@@ -618,18 +648,15 @@ def cache_write(cache, k, v, cu_seqlens, ctx_len, dev_status=None):
 def cache_read(cache, cu_rows, rows, first=None, out=None, dev_status=None):
     """Tokens first[i], first[i] + 1, ... (first None: from 0) of every request
     back as bf16 rows cu_rows[i] .. cu_rows[i+1] - 1 of out["k"], out["v"]."""
-    R = cache.requests
+    R, dev = cache.requests, cache.device
+    shape = (rows, cache.kv_heads, cache.head_dim)
     if out is None:
-        out = {n: torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.k.device)
-               for n in ("k", "v")}
-    ko, vo = out["k"], out["v"]
-    for o in (ko, vo):
-        if o.dtype is not torch.bfloat16 or not o.is_contiguous() or o.shape != (rows, cache.kv_heads, cache.head_dim):
-            raise ValueError("out must hold contiguous bf16 [rows, kv heads, head dim] tensors")
+        out = {n: torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) for n in ("k", "v")}
+    ko, vo = _need_out("out['k']", out["k"], shape, _BF16, dev), _need_out("out['v']", out["v"], shape, _BF16, dev)
     dev_status = new_status(cache.k.device) if dev_status is None else dev_status
-    st = lib().sdm_cache_read(cache.ref, _need_i32("cu_rows", cu_rows, R + 1),
-                              None if first is None else _need_i32("first", first, R), R, rows, ko.data_ptr(),
-                              vo.data_ptr(), dev_status.data_ptr(), _raw_stream(cache.device))
+    st = lib().sdm_cache_read(cache.ref, _need_i32("cu_rows", cu_rows, R + 1, dev),
+                              None if first is None else _need_i32("first", first, R, dev), R, rows, ko, vo,
+                              _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_cache_read")
     return out
@@ -639,18 +666,19 @@ def cache_commit(cache, tok, parent, n_nodes, out_tok, accept, ctx_len, out=None
     """Moves a verified tree's accepted path (verify_tree's out_tok, accept) to
     follow the committed tokens; returns the path's slots and the new lengths."""
     R, S = tok.shape
-    B = out_tok.shape[1] - 1
+    B, dev = out_tok.shape[1] - 1, cache.device
     if R != cache.requests:
         raise ValueError("tok must have one row per request of the cache")
     if out is None:
         out = dict(path=torch.empty((R, B + 1), dtype=torch.int32, device=tok.device),
                    length=torch.empty((R,), dtype=torch.int32, device=tok.device))
     dev_status = new_status(tok.device) if dev_status is None else dev_status
-    st = lib().sdm_cache_commit(cache.ref, _need_i32("tok", tok, R * S), _need_i32("parent", parent, R * S),
-                                _need_i32("n_nodes", n_nodes, R), _need_i32("out_tok", out_tok, R * (B + 1)),
-                                _need_i32("accept", accept, R), _need_i32("ctx_len", ctx_len, R), R, S - 1, B,
-                                _need_i32("path", out["path"], R * (B + 1)), _need_i32("length", out["length"], R),
-                                dev_status.data_ptr(), _raw_stream(cache.device))
+    st = lib().sdm_cache_commit(cache.ref, _need_i32("tok", tok, R * S, dev), _need_i32("parent", parent, R * S, dev),
+                                _need_i32("n_nodes", n_nodes, R, dev), _need_i32("out_tok", out_tok, R * (B + 1), dev),
+                                _need_i32("accept", accept, R, dev), _need_i32("ctx_len", ctx_len, R, dev), R, S - 1, B,
+                                _need_i32("path", out["path"], R * (B + 1), dev),
+                                _need_i32("length", out["length"], R, dev),
+                                _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_cache_commit")
     return out
@@ -667,33 +695,30 @@ def attend(cache, q, cu_seqlens, ctx_len, max_window, scale=None, window=0, sink
     cached tokens: causal, or by a draft tree's ancestor mask (draft_tree's
     mask); window > 0 limits it to that many last tokens and the first
     `sinks`.  Returns out (and the log-sum-exp if lse)."""
-    R, D = cache.requests, cache.head_dim
+    R, D, dev = cache.requests, cache.head_dim, cache.device
     rows, H = q.shape[0], q.shape[1]
-    qs = _need_rows("q", q, H, D)
+    qs = _need_rows("q", q, H, D, dev)
     if H % cache.kv_heads:
         raise ValueError("q's heads must be a multiple of the cache's")
     if out is None:
         out = dict(out=torch.empty((rows, H, D), dtype=torch.bfloat16, device=q.device))
         if lse:
             out["lse"] = torch.empty((rows, H), dtype=torch.float32, device=q.device)
-    o, z = out["out"], out.get("lse")
-    if o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous():
-        raise ValueError("out must be contiguous bf16 of q's shape")
-    if z is not None and (z.shape != (rows, H) or z.dtype != torch.float32 or not z.is_contiguous()):
-        raise ValueError("lse must be contiguous fp32 [rows, H]")
+    o, z = _need_out("out", out["out"], q.shape, _BF16, dev), out.get("lse")
+    if z is not None:
+        z = _need_out("lse", z, (rows, H), torch.float32, dev)
     nodes, mask = 0, None
     if tree_mask is not None:
         nodes = tree_mask.shape[1]
-        mask = _need_i32("tree_mask", tree_mask, R * nodes * ((nodes + 31) // 32))
+        mask = _need_i32("tree_mask", tree_mask, R * nodes * ((nodes + 31) // 32), dev)
         if tree_mask.shape != (R, nodes, (nodes + 31) // 32):
             raise ValueError("tree_mask must be [requests, nodes, ceil(nodes / 32)]")
     ws = attend_workspace(cache, rows, max_window, H) if ws is None else ws
     dev_status = new_status(q.device) if dev_status is None else dev_status
-    st = lib().sdm_attend(cache.ref, q.data_ptr(), qs, _need_i32("cu_seqlens", cu_seqlens, R + 1),
-                          _need_i32("ctx_len", ctx_len, R), R, rows, max_window, H,
-                          D ** -0.5 if scale is None else scale, window, sinks, mask, nodes, o.data_ptr(),
-                          None if z is None else z.data_ptr(), ws.data_ptr(), ws.numel(), dev_status.data_ptr(),
-                          _raw_stream(cache.device))
+    st = lib().sdm_attend(cache.ref, q.data_ptr(), qs, _need_i32("cu_seqlens", cu_seqlens, R + 1, dev),
+                          _need_i32("ctx_len", ctx_len, R, dev), R, rows, max_window, H,
+                          D ** -0.5 if scale is None else scale, window, sinks, mask, nodes, o, z, _need_ws(ws, dev),
+                          ws.numel(), _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_attend")
     return out
