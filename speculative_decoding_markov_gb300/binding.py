@@ -707,6 +707,8 @@ def attend(cache, q, cu_seqlens, ctx_len, max_window, scale=None, window=0, sink
     o, z = _need_out("out", out["out"], q.shape, _BF16, dev), out.get("lse")
     if z is not None:
         z = _need_out("lse", z, (rows, H), torch.float32, dev)
+    elif lse:
+        raise ValueError("lse was asked for, but out has no \"lse\" to hold it")
     nodes, mask = 0, None
     if tree_mask is not None:
         nodes = tree_mask.shape[1]

@@ -177,3 +177,11 @@ def test_a_cache_on_two_devices_is_refused():
     with pytest.raises(ValueError):
         binding.PagedCache(k, k, Tensor((2, 4), device=DEV + 1))
     assert binding.PagedCache(k, k, Tensor((2, 4))).device == DEV
+
+
+def test_an_lse_without_a_place_is_refused(called):
+    with pytest.raises(ValueError):
+        binding.attend(**attend_args(lse=True))
+    assert not called.calls
+    binding.attend(**attend_args(lse=True, out=dict(out=Tensor((6, 4, 64), **bf), lse=Tensor((6, 4), torch.float32))))
+    assert len(called.calls) == 1
