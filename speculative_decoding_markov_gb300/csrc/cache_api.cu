@@ -47,13 +47,13 @@ sdm_status sdm_cache_write(const sdm_cache* cache, const uint16_t* k, const uint
                            int64_t v_stride, const int32_t* cu_seqlens, const int32_t* ctx_len, int R, int rows,
                            int32_t* dev_status, void* stream) {
     CacheWriteParams p = {};
-    if (!k || !v || !cu_seqlens || !ctx_len || R <= 0 || rows < 0) return SDM_ERR_INVALID_ARG;
+    if (!cu_seqlens || !ctx_len || R <= 0 || rows < 0) return SDM_ERR_INVALID_ARG;
     const sdm_status st = view_of(cache, &p.c);
-    if (st != SDM_OK) return st;
+    if (st != SDM_OK || rows == 0) return st;   // arrays without rows may have no address
+    if (!k || !v) return SDM_ERR_INVALID_ARG;
     const long long width = static_cast<long long>(p.c.heads) * p.c.D;
     if (!stride_ok(k_stride, width) || !stride_ok(v_stride, width) || !aligned16(k) || !aligned16(v))
         return SDM_ERR_UNSUPPORTED;
-    if (rows == 0) return SDM_OK;
     p.k = k;
     p.v = v;
     p.k_stride = k_stride;
@@ -69,11 +69,11 @@ sdm_status sdm_cache_write(const sdm_cache* cache, const uint16_t* k, const uint
 sdm_status sdm_cache_read(const sdm_cache* cache, const int32_t* cu_rows, const int32_t* first, int R, int rows,
                           uint16_t* k_out, uint16_t* v_out, int32_t* dev_status, void* stream) {
     CacheReadParams p = {};
-    if (!cu_rows || !k_out || !v_out || R <= 0 || rows < 0) return SDM_ERR_INVALID_ARG;
+    if (!cu_rows || R <= 0 || rows < 0) return SDM_ERR_INVALID_ARG;
     const sdm_status st = view_of(cache, &p.c);
-    if (st != SDM_OK) return st;
+    if (st != SDM_OK || rows == 0) return st;
+    if (!k_out || !v_out) return SDM_ERR_INVALID_ARG;
     if (!aligned16(k_out) || !aligned16(v_out)) return SDM_ERR_UNSUPPORTED;
-    if (rows == 0) return SDM_OK;
     p.cu = cu_rows;
     p.first = first;
     p.k_out = k_out;
@@ -114,19 +114,19 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
                       int sinks, const int32_t* tree_mask, int tree_nodes, uint16_t* out, float* lse, void* ws,
                       size_t ws_bytes, int32_t* dev_status, void* stream) {
     AttendParams p = {};
-    if (!q || !cu_seqlens || !ctx_len || !out || R <= 0 || rows < 0 || max_window <= 0 || H <= 0)
-        return SDM_ERR_INVALID_ARG;
+    if (!cu_seqlens || !ctx_len || R <= 0 || rows < 0 || max_window < 0 || H <= 0) return SDM_ERR_INVALID_ARG;
+    if (rows > 0 && (!q || !out || max_window == 0)) return SDM_ERR_INVALID_ARG;
     if (!(scale > 0.f) || scale > 3.0e38f || sinks < 0) return SDM_ERR_INVALID_ARG;
     if (tree_mask && tree_nodes < max_window) return SDM_ERR_INVALID_ARG;
     const sdm_status st = view_of(cache, &p.c);
     if (st != SDM_OK) return st;
     if (H % p.c.heads != 0) return SDM_ERR_INVALID_ARG;
+    if (rows == 0) return SDM_OK;
     if (R > 16384 || !stride_ok(q_stride, static_cast<long long>(H) * p.c.D) || !aligned16(q) || !aligned16(out))
         return SDM_ERR_UNSUPPORTED;
     if (H / p.c.heads > 128) return SDM_ERR_UNSUPPORTED;   // a token's rows have to fit one tile
     // rows of one request and kv head are counted in 32 bits
     if (static_cast<long long>(max_window) * (H / p.c.heads) >= (1ll << 30)) return SDM_ERR_UNSUPPORTED;
-    if (rows == 0) return SDM_OK;
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attend_workspace(R, max_window, H, p.c.D, rows, p.c.heads))
         return SDM_ERR_WORKSPACE;
     p.q = q;

@@ -8,7 +8,7 @@ import ctypes
 import pytest
 import torch
 
-from speculative_decoding_markov_gb300 import binding
+from speculative_decoding_markov_gb300 import binding, build
 
 DEV = 0
 
@@ -185,3 +185,35 @@ def test_an_lse_without_a_place_is_refused(called):
     assert not called.calls
     binding.attend(**attend_args(lse=True, out=dict(out=Tensor((6, 4, 64), **bf), lse=Tensor((6, 4), torch.float32))))
     assert len(called.calls) == 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load()
+
+
+def test_batches_without_rows(lib):
+    """Tensors without rows have no address: nothing to do, nothing refused."""
+    FAKE = 0x1000
+    c = ctypes.byref(binding.SdmCache(FAKE, FAKE, None, None, FAKE, 0, 4, 2, 16, 64, 2))
+    assert lib.sdm_cache_write(c, None, None, 128, 128, FAKE, FAKE, 1, 0, None, None) == 0
+    assert lib.sdm_cache_read(c, FAKE, None, 1, 0, None, None, None, None) == 0
+    for longest in (0, 4):
+        assert lib.sdm_attend(c, None, 512, FAKE, FAKE, 1, 0, longest, 8, 1.0, 0, 0, None, 0, None, None, None, 0,
+                              None, None) == 0
+    # the rest is still looked at
+    assert lib.sdm_cache_write(c, None, None, 128, 128, None, FAKE, 1, 0, None, None) == 1
+    assert lib.sdm_cache_write(c, None, None, 128, 128, FAKE, FAKE, 1, 1, None, None) == 1
+    assert lib.sdm_cache_read(c, FAKE, None, 0, 0, None, None, None, None) == 1
+    assert lib.sdm_attend(c, None, 512, FAKE, FAKE, 1, 0, 4, 7, 1.0, 0, 0, None, 0, None, None, None, 0, None,
+                          None) == 1
+    assert lib.sdm_attend(c, FAKE, 512, FAKE, FAKE, 1, 1, 0, 8, 1.0, 0, 0, None, 0, FAKE, None, FAKE, 1 << 30, None,
+                          None) == 1
+
+
+def test_calls_without_rows_pass_the_binding(called):
+    none = Tensor((0, 4, 64), **bf)
+    binding.attend(**attend_args(q=none, out=dict(out=Tensor((0, 4, 64), **bf)), max_window=0))
+    binding.cache_write(**write_args(k=Tensor((0, 2, 64), **bf), v=Tensor((0, 2, 64), **bf)))
+    assert len(called.calls) == 2 and called.calls[0][1][1] == 0
