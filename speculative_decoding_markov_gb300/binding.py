@@ -605,7 +605,7 @@ def _need_rows(what, x, heads, head_dim, device=None):
         raise ValueError(f"{what} must be [rows, {heads}, {head_dim}]")
     if st[2] != 1 or (heads > 1 and st[1] != head_dim):
         raise ValueError(f"{what} must be contiguous within a row")
-    return st[0] if shape[0] > 1 else max(st[0], heads * head_dim)
+    return st[0] if shape[0] > 1 else heads * head_dim   # one row has no next one
 
 
 def _need_i32(what, x, n, device=None):

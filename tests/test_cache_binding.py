@@ -217,3 +217,10 @@ def test_calls_without_rows_pass_the_binding(called):
     binding.attend(**attend_args(q=none, out=dict(out=Tensor((0, 4, 64), **bf)), max_window=0))
     binding.cache_write(**write_args(k=Tensor((0, 2, 64), **bf), v=Tensor((0, 2, 64), **bf)))
     assert len(called.calls) == 2 and called.calls[0][1][1] == 0
+
+
+def test_the_stride_of_a_single_row(called):
+    """It leads nowhere: any value will do."""
+    for stride in (1, 7, 128, 1001):
+        assert binding._need_rows("k", Tensor((1, 2, 64), torch.bfloat16, stride=(stride, 64, 1)), 2, 64, DEV) == 128
+    assert binding._need_rows("k", Tensor((2, 2, 64), torch.bfloat16, stride=(1000, 64, 1)), 2, 64, DEV) == 1000

@@ -31,3 +31,19 @@ def test_batches_without_rows(gpu_lib, e4m3):
         got = sdm.attend(s.cache, q, s.cu, s.ctx, longest, lse=True, dev_status=s.status)
         assert got["out"].shape == (0, 8, 64) and got["lse"].shape == (0, 8)
     assert s.status.item() == 0 and torch.equal(before.view(torch.uint8), s.cache.k.view(torch.uint8))
+
+
+def test_a_single_row_of_an_odd_projection(gpu_lib):
+    """One token's query, key and value as slices of a row of an odd width."""
+    s = ref.Setup([1], [40], 2, 64, 16, False, seed=2)
+    s.write_all()
+    wide = torch.zeros((1, 8 * 64 + 2 * 128 + 1), dtype=torch.bfloat16, device="cuda")
+    q, k, v = (wide.as_strided((1, n, 64), (769, 64, 1), at) for n, at in ((8, 0), (2, 512), (2, 640)))
+    q.copy_(torch.randn((1, 8, 64), generator=s.gen))
+    k.copy_(s.packed("k"))
+    v.copy_(s.packed("v"))
+    assert q.stride(0) % 8
+    sdm.cache_write(s.cache, k, v, s.cu, s.ctx, dev_status=s.status)
+    got = sdm.attend(s.cache, q, s.cu, s.ctx, 1, dev_status=s.status)["out"]
+    want = sdm.attend(s.cache, q.contiguous(), s.cu, s.ctx, 1, dev_status=s.status)["out"]
+    assert torch.equal(got, want) and s.status.item() == 0
