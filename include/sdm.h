@@ -587,7 +587,9 @@ sdm_status sdm_observe(const float* conf, const int32_t* cu_seqlens, const int32
  * Pools are [n_pages, kv_heads, page, head_dim], K and V apart, in bf16 or
  * e4m3.  An e4m3 cache holds one scale per token and kv head, a power of two:
  * k_exp / v_exp [n_pages, kv_heads, page] hold its exponent + 127, and the
- * value that a code stands for is code * 2^(exp - 127), exact in bf16.
+ * value that a code stands for is code * 2^(exp - 127) in bf16: exact for what
+ * cache_write leaves (17 to 246), rounded for what else a caller may put there
+ * (0 and 255 are read as 1 and 254).
  * Constraints: head_dim 64 or 128; page 16, 32, 64 or 128; n_pages * kv_heads
  * * page < 2^31; pools and exponents 16-byte aligned.  Else
  * SDM_ERR_UNSUPPORTED.

@@ -526,8 +526,8 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Blk& blk
             float weight = -1.0f;
             for (int c = 0; c < 16; ++c) {
                 float v;
-                if constexpr (E4M3) {
-                    v = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.v[row * D + col0 + c])).x;
+                if constexpr (E4M3) {   // past bf16's range in one case only: past fp32's, too
+                    v = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.v[row * D + col0 + c])).x * scale_of(p.c.v_exp[row]);
                 } else {
                     v = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p.c.v)[row * D + col0 + c]);
                 }
@@ -537,8 +537,7 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Blk& blk
                     for (int d = 0; d < D; ++d) {
                         float k;
                         if constexpr (E4M3) {
-                            k = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.k[row * D + d])).x *
-                                pow2f(static_cast<int>(p.c.k_exp[row]) - 127);
+                            k = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.k[row * D + d])).x * scale_of(p.c.k_exp[row]);
                         } else {
                             k = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p.c.k)[row * D + d]);
                         }
@@ -1473,8 +1472,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                                         (D == 128 ? (row & 7) : ((row >> 1) & 3)) * 16;
                         const int dst = C::kRing + s * C::kTileBytes + row * 128 + (row & 7) * 16;
                         const uint32_t e = smem[C::kExps + rs * kTile + row];
-                        // 2^(e - 127) as bf16, twice: every e a write leaves is in bf16's range
-                        const uint32_t sc = e << 7;
+                        // 2^(e - 127) as bf16, twice
+                        const uint32_t sc = scale_byte(e) << 7;
                         const uint32_t scale2 = sc | (sc << 16);
                         uint4 x = *reinterpret_cast<const uint4*>(smem + src);
 #pragma unroll 2

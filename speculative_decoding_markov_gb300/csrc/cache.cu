@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
         for (int v0 = 0; v0 < vectors; v0 += kPer * kBatch) {
             uint4 x[kBatch];
             uint2 code[kBatch];
-            int e[kBatch];
+            uint32_t e[kBatch];
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 const int vec = v0 + b * kPer + sub;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
                 const bool is_v = vec >= p.c.heads;
                 const int h = is_v ? vec - p.c.heads : vec;
                 if constexpr (E4M3) {
-                    const float s = pow2f(min(max(e[b] - 127, -126), 127));
+                    const float s = scale_of(e[b]);
                     uint32_t o[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {

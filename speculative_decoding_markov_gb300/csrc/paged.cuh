@@ -84,6 +84,11 @@ __device__ __forceinline__ float pow2f(int e) {   // -126 <= e <= 127
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// The exponent byte of a stored scale: 0 and 255, which no write leaves and
+// for which 2^(byte - 127) is no normal bf16, are read as 1 and 254.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t byte) { return min(max(byte, 1u), 254u); }
+__device__ __forceinline__ float scale_of(uint32_t byte) { return pow2f(static_cast<int>(scale_byte(byte)) - 127); }
+
 // Two codes (low byte first) as two fp16 values (every e4m3 value is one).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
     uint32_t r;

@@ -80,3 +80,41 @@ def test_the_last_positions_of_32_bits(gpu_lib, e4m3):
             assert flag.item() == status
     flag = sdm.cache_write(cache, s.packed("k")[:w], s.packed("v")[:w], i32([0, w]), i32([last - 3]))
     assert flag.item() == sdm.DEV_BAD_PAGE
+
+
+# The scales of an e4m3 cache: every reader takes a byte for the same factor.
+BYTES = [0, 1, 2, 16, 17, 126, 127, 200, 246, 247, 253, 254, 255]
+
+
+def test_every_exponent_byte_reads_alike(gpu_lib):
+    """A row that sees its own token alone gives that token's values, as
+    cache_read has them: infinities where code and scale leave bf16's range,
+    NaN codes, and zeros under any scale."""
+    n, D = len(BYTES), 64
+    s = ref.Setup([1] * n, [0] * n, 1, D, 16, True, seed=1, fill=0.0)
+    codes = torch.arange(256, dtype=torch.uint8)[torch.randperm(256, generator=s.gen)][:D]
+    codes[:6] = torch.tensor([0, 0x80, 0x7f, 0x7e, 0x38, 0xb8])             # zeros, NaN, 448, 1, -1
+    for i, byte in enumerate(BYTES):
+        page = s.table_cpu[i, 0].item()
+        s.cache.v.view(torch.uint8)[page, 0, 0] = codes.cuda()
+        s.cache.v_exp[page, 0, 0] = byte
+        s.cache.k.view(torch.uint8)[page, 0, 0] = 0                          # scores of zero: NaN if a scale is infinite
+        s.cache.k_exp[page, 0, 0] = byte
+    held = sdm.cache_read(s.cache, s.cu, n, dev_status=s.status)["v"].double().cpu().numpy()[:, 0]
+    value = codes.view(torch.float8_e4m3fn).double().numpy()
+    for i, byte in enumerate(BYTES):                                         # cache_read: the definition
+        want = torch.from_numpy(value * 2.0 ** (min(max(byte, 1), 254) - 127)).to(torch.bfloat16).double().numpy()
+        assert np.array_equal(held[i], want, equal_nan=True), byte
+    q = torch.randn((n, 4, D), generator=s.gen).to(torch.bfloat16).cuda()
+    got = sdm.attend(s.cache, q, s.cu, s.ctx, 1, lse=True, dev_status=s.status)
+    out = got["out"].double().cpu().numpy()
+    assert (got["lse"] == 0).all()
+    for i, byte in enumerate(BYTES):
+        for h in range(4):
+            assert np.array_equal(np.isnan(out[i, h]), np.isnan(held[i])), byte
+            assert np.array_equal(np.isinf(out[i, h]), np.isinf(held[i])), byte
+            fine = np.isfinite(held[i])
+            # products of subnormal numbers may count as zero
+            assert (np.abs(out[i, h] - held[i])[fine] <= 2.0 ** -126).all(), byte
+            assert np.array_equal(np.sign(out[i, h])[np.isinf(held[i])], np.sign(held[i])[np.isinf(held[i])])
+    assert s.status.item() == 0
