@@ -676,9 +676,10 @@ sdm_status sdm_cache_commit(const sdm_cache* cache, const int32_t* tok, const in
  * mask of sdm_draft_tree, [R, tree_nodes, words], words = ceil(tree_nodes /
  * 32): bit c of node p set if c is p or an ancestor) the window's tokens are
  * seen as the row's bits say, whatever their distance, and t = ctx_len[i] +
- * depth, depth = max(0, bits set - 1).  A row that sees nothing gives out 0,
- * lse -inf.  What a row does not see does not touch its result, NaN and
- * infinities included.
+ * depth, depth = max(0, bits set - 1).  A row that sees nothing, or only
+ * scores of -inf, gives out 0, lse -inf; one that sees a score of +inf and no
+ * NaN gives out NaN, lse +inf.  What a row does not see does not touch its
+ * result, NaN and infinities included.
  * In:  cache; q [rows, H, head_dim] bf16, q_stride elements from row to row
  *      (a multiple of 8, at least H * head_dim, base 16-byte aligned); H a
  *      multiple of kv_heads, at most 128 times it; cu_seqlens [R+1], ctx_len

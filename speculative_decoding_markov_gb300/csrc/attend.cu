@@ -62,6 +62,9 @@ constexpr int kTile = 128;            // keys per tile, rows per sub-tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;
+// The running maximum stays finite, so that the weight of an infinite score is
+// infinite (not 2^(inf - inf)) and the row's log-sum-exp with it.
+constexpr float kMaxRef = 3.0e38f;
 // The weights enter the second product as bf16: an error of at most 2^-8 of a
 // weight, which the sum over many keys averages out.  Where a row sees few
 // keys, or few that count, it does not, so the remainder p - bf16(p) is
@@ -1011,7 +1014,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         // only lanes that hold a row of the block have a say: what the others'
                         // scores come from is left in shared memory by whatever ran before
                         if (__builtin_expect(__any_sync(0xffffffffu, r < lim && top > m_ref + kLazy), 0)) {
-                            const float to = fmaxf(m_ref, top);
+                            const float to = fminf(fmaxf(m_ref, top), kMaxRef);
                             const float corr = to == -INFINITY ? 1.f : fast_exp2(m_ref - to);
                             m_ref = to;
                             l *= corr;

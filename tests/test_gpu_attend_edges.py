@@ -118,3 +118,65 @@ def test_every_exponent_byte_reads_alike(gpu_lib):
             assert (np.abs(out[i, h] - held[i])[fine] <= 2.0 ** -126).all(), byte
             assert np.array_equal(np.sign(out[i, h])[np.isinf(held[i])], np.sign(held[i])[np.isinf(held[i])])
     assert s.status.item() == 0
+
+
+def by_scores(q, k, v, see, scale):
+    """ref.attend by the definition where keys hold infinities: lse is NaN if a
+    score is, else +inf if one is; out is NaN in both cases; a row with scores
+    of -inf alone is one that sees nothing."""
+    out, lse, size = ref.attend(q, k, v, see, scale)
+    rep = q.shape[1] // k.shape[1]
+    q, k = q.double().cpu().numpy(), k.double().numpy()
+    for p in range(q.shape[0]):
+        at = np.nonzero(see[p])[0]
+        for h in range(q.shape[1]):
+            with np.errstate(invalid="ignore"):
+                s = scale * (k[at, h // rep] @ q[p, h]) if at.size else np.array([-np.inf])
+            if np.isnan(s).any() or np.isposinf(s).any():
+                out[p, h], lse[p, h] = np.nan, np.nan if np.isnan(s).any() else np.inf
+            elif np.isneginf(s).all():
+                out[p, h], lse[p, h] = 0.0, -np.inf
+    return out, lse, size
+
+
+@pytest.mark.parametrize("w,ctx", [([6], [140]), ([6, 1], [3, 1]), ([200], [100]), ([5], [6000]), ([300], [2000])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 1)])
+def test_infinite_keys(gpu_lib, w, ctx, window, sinks):
+    """Scores of +inf, -inf and (two of either sign together) NaN, for the rows
+    that see them and no other."""
+    s = ref.Setup(w, ctx, 2, 128, 16, False, seed=3)
+    k = s.kv[0]["k"]
+    k[ctx[0] + 3, 1, 5] = float("inf")
+    k[ctx[0] // 2, 0, 17] = -float("inf")
+    k[ctx[0] + 2, 0, 17] = k[ctx[0] + 2, 0, 18] = float("inf")
+    s.write_all()
+    q = torch.randn((s.rows, 8, 128), generator=s.gen).to(torch.bfloat16).cuda()
+    got = sdm.attend(s.cache, q, s.cu, s.ctx, max(w), window=window, sinks=sinks, lse=True, dev_status=s.status)
+    out, lse = got["out"].double().cpu().numpy(), got["lse"].double().cpu().numpy()
+    at, kinds = 0, set()
+    for i, (a, c) in enumerate(zip(w, ctx)):
+        with np.errstate(invalid="ignore"):
+            o, z, big = by_scores(q[at:at + a], s.held(i, "k"), s.held(i, "v"), ref.visible(a, c, window, sinks),
+                                  128 ** -0.5)
+        mine, zm = out[at:at + a], lse[at:at + a]
+        at += a
+        assert np.array_equal(np.isnan(mine), np.isnan(o)) and np.array_equal(np.isnan(zm), np.isnan(z))
+        assert np.array_equal(np.isposinf(zm), np.isposinf(z)) and np.array_equal(np.isneginf(zm), np.isneginf(z))
+        fine = np.isfinite(o)
+        assert (np.abs(mine - o)[fine] <= (2.0 ** -7 + 2.0 ** -12) * big[fine]).all()
+        fine = np.isfinite(z)
+        assert (np.abs(zm - z)[fine] <= 3e-5).all()
+        kinds |= {"nan"} if np.isnan(z).any() else set()
+        kinds |= {"inf"} if np.isposinf(z).any() else set()
+        kinds |= {"fine"} if fine.any() else set()
+    assert kinds == {"nan", "inf", "fine"} and s.status.item() == 0
+
+
+def test_rows_of_scores_of_minus_infinity(gpu_lib):
+    s = ref.Setup([2, 1], [3, 400], 1, 64, 16, False, seed=5)
+    for kv in s.kv:
+        kv["k"][:, 0, 7] = -float("inf")
+    s.write_all()
+    q = torch.rand((3, 4, 64), generator=s.gen).add(0.5).to(torch.bfloat16).cuda()
+    got = sdm.attend(s.cache, q, s.cu, s.ctx, 2, lse=True, dev_status=s.status)
+    assert not got["out"].any() and torch.isneginf(got["lse"]).all()
