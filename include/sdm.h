@@ -598,7 +598,7 @@ sdm_status sdm_observe(const float* conf, const int32_t* cu_seqlens, const int32
  * its window of new tokens: rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 of the
  * packed arrays (sdm_pack_ragged's layout; a tree's window is its N + 1 slots)
  * sit at tokens ctx_len[i], ctx_len[i] + 1, ....  `rows` is the packed arrays'
- * row count, an upper bound on cu_seqlens[R]; rows past cu_seqlens[R] are
+ * row count, an upper bound on cu_seqlens[R]; rows that no window holds are
  * neither read nor written, and with rows = 0 the packed arrays may be NULL.  Device checks (OR-ed into *dev_status): a window
  * that is not within [0, rows] or not monotone counts as empty, a negative
  * ctx_len as 0 (SDM_DEV_BAD_WINDOW); tokens past max_pages * page, or past

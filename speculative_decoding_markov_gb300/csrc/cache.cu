@@ -15,6 +15,23 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCommitThreads = 512;     // 32 trees of 65 slots, written and committed: 8.3 us (256: 9.2, 1024: 8.5)
 
+// The windows are looked at apart from the rows, by one block more than the
+// rows have (a window that counts as empty need not have a row in use): it
+// flags what is wrong with them and returns whether one of them is unsound, in
+// which case the rows' own search in cu_seqlens proves nothing and the block
+// takes every window's rows itself.
+__device__ __forceinline__ bool check_windows(const int32_t* cu, const int32_t* ctx, int R, int rows,
+                                              long long tokens, int32_t* dev_status) {
+    int bad = 0, unsound = 0;
+    for (int i = threadIdx.x; i < R; i += kThreads) {
+        const Window w = window_of(cu, ctx, i, rows, 0x7fffffff, tokens);
+        bad |= w.bad;
+        unsound |= w.n == 0 && (w.bad & SDM_DEV_BAD_WINDOW);
+    }
+    if (bad) set_status(dev_status, bad);
+    return __syncthreads_or(unsound);
+}
+
 // One warp per packed row, its loads in flight before the row's slot is
 // known.  D / 8 lanes hold one (K or V, head) vector of D elements, 16 bytes
 // each, so the maximum of a vector is a shuffle reduction over those lanes.
@@ -34,8 +51,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
     const int sub = lane / kLanes, part = lane % kLanes;
     const int vectors = 2 * p.c.heads;      // K's heads, then V's
     const long long tokens = table_tokens(p.c);
-    const int n_rows = min(p.rows, __ldg(p.cu + p.R));
-    for (int row = blockIdx.x * kWarps + (threadIdx.x >> 5); row < n_rows; row += gridDim.x * kWarps) {
+    // row's request: `known`, or (-1) the one that the search gives
+    auto write_row = [&](int row, int known) {
         size_t at = 0;
         bool found = false, ok = false;
         for (int v0 = 0; v0 < vectors; v0 += kPer * kBatch) {
@@ -51,19 +68,15 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
             }
             if (!found) {
                 found = true;
-                const int i = warp_find_request(p.cu, p.R, row);
+                const int i = known >= 0 ? known : warp_find_request(p.cu, p.R, row);
                 const Window w = window_of(p.cu, p.ctx, i, p.rows, 0x7fffffff, tokens);
-                int bad = w.bad;
                 if (row >= w.row0 && row < w.row0 + w.n) {
                     const int pos = w.ctx + (row - w.row0);
                     const int pg = page_of(p.c, i, pos);
                     ok = pg >= 0;
                     if (ok) at = pool_row(p.c, pg, pos);
-                    else bad |= SDM_DEV_BAD_PAGE;
-                } else if (!bad) {
-                    bad = SDM_DEV_BAD_WINDOW;   // a row that no window holds
+                    else if (lane == 0) set_status(p.dev_status, SDM_DEV_BAD_PAGE);
                 }
-                if (bad && lane == 0) set_status(p.dev_status, bad);
             }
             if (!ok) break;
 #pragma unroll
@@ -109,6 +122,16 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
                 }
             }
         }
+    };
+    const int warp = threadIdx.x >> 5, blocks = gridDim.x - 1;
+    if (static_cast<int>(blockIdx.x) < blocks) {
+        const int n_rows = min(p.rows, __ldg(p.cu + p.R));
+        for (int row = blockIdx.x * kWarps + warp; row < n_rows; row += blocks * kWarps) write_row(row, -1);
+    } else if (check_windows(p.cu, p.ctx, p.R, p.rows, tokens, p.dev_status)) {
+        for (int i = 0; i < p.R; ++i) {
+            const Window w = window_of(p.cu, p.ctx, i, p.rows, 0x7fffffff, tokens);
+            for (int k = warp; k < w.n; k += kWarps) write_row(w.row0 + k, i);
+        }
     }
 }
 
@@ -125,17 +148,13 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
     const int lane = threadIdx.x & 31;
     const int sub = lane / kLanes, part = lane % kLanes;
     const int vectors = 2 * p.c.heads;
-    const int n_rows = min(p.rows, __ldg(p.cu + p.R));
-    for (int row = blockIdx.x * kWarps + (threadIdx.x >> 5); row < n_rows; row += gridDim.x * kWarps) {
-        const int i = warp_find_request(p.cu, p.R, row);
+    auto read_row = [&](int row, int known) {
+        const int i = known >= 0 ? known : warp_find_request(p.cu, p.R, row);
         const Window w = window_of(p.cu, p.first, i, p.rows, 0x7fffffff, 0x7fffffffll);
-        int bad = w.bad;
-        const bool mine = row >= w.row0 && row < w.row0 + w.n;
+        if (row < w.row0 || row >= w.row0 + w.n) return;
         const int pos = w.ctx + (row - w.row0);
-        const int pg = mine ? page_of(p.c, i, pos) : -1;
-        if (pg < 0 && !bad) bad = mine ? SDM_DEV_BAD_PAGE : SDM_DEV_BAD_WINDOW;
-        if (bad && lane == 0) set_status(p.dev_status, bad);
-        if (!mine) continue;
+        const int pg = page_of(p.c, i, pos);
+        if (pg < 0 && lane == 0) set_status(p.dev_status, SDM_DEV_BAD_PAGE);
         const size_t at = pg >= 0 ? pool_row(p.c, pg, pos) : 0;
         for (int v0 = 0; v0 < vectors; v0 += kPer * kBatch) {
             uint4 x[kBatch];
@@ -178,6 +197,16 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
                     reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) +
                                              (static_cast<size_t>(row) * p.c.heads + h) * D)[part] = x[b];
             }
+        }
+    };
+    const int warp = threadIdx.x >> 5, blocks = gridDim.x - 1;
+    if (static_cast<int>(blockIdx.x) < blocks) {
+        const int n_rows = min(p.rows, __ldg(p.cu + p.R));
+        for (int row = blockIdx.x * kWarps + warp; row < n_rows; row += blocks * kWarps) read_row(row, -1);
+    } else if (check_windows(p.cu, p.first, p.R, p.rows, 0x7fffffffll, p.dev_status)) {
+        for (int i = 0; i < p.R; ++i) {
+            const Window w = window_of(p.cu, p.first, i, p.rows, 0x7fffffff, 0x7fffffffll);
+            for (int k = warp; k < w.n; k += kWarps) read_row(w.row0 + k, i);
         }
     }
 }
@@ -299,7 +328,7 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const Cach
 template <typename P>
 cudaError_t launch_rows(void (*const (&k)[4])(const P), const P& p, cudaStream_t s) {
     const int blocks = static_cast<int>(std::min<long long>((p.rows + kWarps - 1) / kWarps, 8LL * num_sms()));
-    return launch_pdl(k[(p.c.D == 128 ? 2 : 0) + (p.c.e4m3 ? 1 : 0)], dim3(blocks), dim3(kThreads), 0, s, p);
+    return launch_pdl(k[(p.c.D == 128 ? 2 : 0) + (p.c.e4m3 ? 1 : 0)], dim3(blocks + 1), dim3(kThreads), 0, s, p);
 }
 
 }  // namespace

@@ -47,3 +47,74 @@ def test_a_single_row_of_an_odd_projection(gpu_lib):
     got = sdm.attend(s.cache, q, s.cu, s.ctx, 1, dev_status=s.status)["out"]
     want = sdm.attend(s.cache, q.contiguous(), s.cu, s.ctx, 1, dev_status=s.status)["out"]
     assert torch.equal(got, want) and s.status.item() == 0
+
+
+# Offsets that are not sound: what is wrong is flagged, whether or not a row
+# leads to it, and windows that are valid by themselves are done all the same.
+def slots(s, name, i, first, n):
+    """Tokens first .. first + n - 1 of request i as the pool holds them [n, G, D]."""
+    page = s.page
+    pool = s.cache.k if name == "k" else s.cache.v
+    return torch.stack([pool[s.table_cpu[i, t // page].item(), :, t % page] for t in range(first, first + n)])
+
+
+@pytest.mark.parametrize("cu,valid", [([0, 5, 3], {0: (0, 5)}), ([0, 3, -1], {0: (0, 3)}), ([0, -1, 4], {}),
+                                      ([2, 2, 7], {1: (2, 5)}), ([0, 5, 3, 7], {0: (0, 5), 2: (3, 4)}),
+                                      ([0, 9, 4, 7], {2: (4, 3)}), ([0, 2 ** 31 - 1, 7], {}), ([-1, 2, 4], {1: (2, 2)})])
+@pytest.mark.parametrize("G", [2, 40])
+def test_windows_that_are_not_sound(gpu_lib, cu, valid, G):
+    R, rows = len(cu) - 1, 7
+    sound = all(0 <= a <= b <= rows for a, b in zip(cu, cu[1:]))
+    s = ref.Setup([7] * R, [10 + i for i in range(R)], G, 64, 16, False, seed=R, fill=7.0)
+    x = torch.randn((rows, G, 64), generator=s.gen).to(torch.bfloat16).cuda()
+    want = [p.clone() for p in (s.cache.k, s.cache.v)]
+    for i, (at, n) in valid.items():
+        for t in range(n):
+            pos = s.ctx_list[i] + t
+            page, slot = s.table_cpu[i, pos // 16].item(), pos % 16
+            want[0][page, :, slot], want[1][page, :, slot] = x[at + t], -x[at + t]
+    flag = sdm.cache_write(s.cache, x, -x, i32(cu), s.ctx)
+    assert torch.equal(s.cache.k, want[0]) and torch.equal(s.cache.v, want[1])
+    assert flag.item() == (0 if sound else sdm.DEV_BAD_WINDOW)
+    out = {n: torch.full((rows, G, 64), 3.0, dtype=torch.bfloat16, device="cuda") for n in "kv"}
+    back = sdm.new_status()
+    sdm.cache_read(s.cache, i32(cu), rows, first=s.ctx, out=out, dev_status=back)
+    want = torch.full_like(x, 3.0)
+    for at, n in valid.values():
+        want[at:at + n] = x[at:at + n]
+    assert torch.equal(out["k"], want) and back.item() == flag.item()
+
+
+def test_windows_are_checked_without_rows_in_use(gpu_lib):
+    """A negative length of an empty window, one past the table's end, and
+    offsets that end below zero."""
+    s = ref.Setup([0, 3], [5, 20], 2, 64, 16, False, fill=0.0)
+    end = s.cache.table.shape[1] * 16
+    k = s.packed("k")
+    for cu, ctx, status in (([0, 0, 3], [-4, 20], sdm.DEV_BAD_WINDOW), ([0, 0, 3], [end + 1, 20], sdm.DEV_BAD_PAGE),
+                            ([0, 0, 3], [end, 20], 0), ([0, -5, -5], [5, 20], sdm.DEV_BAD_WINDOW),
+                            ([0, 0, 3], [0, 20], 0), ([0, 0, 0], [0, 20], 0)):
+        assert sdm.cache_write(s.cache, k, k, i32(cu), i32(ctx)).item() == status, (cu, ctx)
+    for cu, first, status in (([0, 0, 3], [-4, 20], sdm.DEV_BAD_WINDOW), ([0, -5, -5], [5, 20], sdm.DEV_BAD_WINDOW),
+                              ([0, 0, 3], [4, 20], 0)):
+        flag = sdm.new_status()
+        sdm.cache_read(s.cache, i32(cu), 3, first=i32(first), dev_status=flag)
+        assert flag.item() == status, (cu, first)
+
+
+def test_the_checks_over_many_requests(gpu_lib):
+    """The last of more windows than a block has threads is the wrong one."""
+    R = 1500
+    w = [i % 2 for i in range(R)]
+    s = ref.Setup(w, [3] * R, 1, 64, 16, False, seed=6)
+    s.write_all()
+    assert s.status.item() == 0
+    cu = s.cu.clone()
+    cu[R] = s.rows + 1                                     # past the packed rows: its row is not written
+    before = s.cache.k.clone()
+    flag = sdm.cache_write(s.cache, -s.packed("k"), s.packed("v"), cu, s.ctx)
+    assert flag.item() == sdm.DEV_BAD_WINDOW
+    got, want = s.cache.k, before.clone()
+    for i in range(1, R - 1, 2):
+        want[s.table_cpu[i, 0].item(), :, 3] *= -1
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))    # bits: what no token holds is NaN
