@@ -655,7 +655,7 @@ sdm_status sdm_cache_read(const sdm_cache* cache, const int32_t* cu_rows, const 
  * moves to ctx_len[i] + j.  (A chain's accepted drafts are a prefix of its
  * window and need no move.)
  * In:  tok, parent [R, N+1], n_nodes [R] (sdm_draft_tree), out_tok [R, B+1],
- *      accept [R] (sdm_verify_tree), ctx_len [R].  N < 16384.
+ *      accept [R] (sdm_verify_tree), ctx_len [R].  N < 16384, B <= 16384.
  * Out: path [R, B+1] int32 (-1 past the path); length [R] = ctx_len +
  *      accepted + 1, the next ctx_len (may be NULL; may be ctx_len itself).
  * A path that breaks off (no such slot) is cut there: SDM_DEV_BAD_TOKEN.

@@ -346,12 +346,13 @@ cudaError_t launch_cache_read(const CacheReadParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_cache_commit(const CacheCommitParams& p, cudaStream_t s) {
+    // the limit is the process's, so it is raised once, to what the largest call needs
+    constexpr int kMost = (2 * kCommitMost + kCommitMost + 1) * sizeof(int32_t);
+    static_assert(kMost <= 224 * 1024, "shared memory");
+    static const cudaError_t raised =
+        cudaFuncSetAttribute(cache_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (raised != cudaSuccess) return raised;
     const size_t smem = (2 * static_cast<size_t>(p.N + 1) + p.B + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(cache_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
     return launch_pdl(cache_commit_kernel, dim3(p.R), dim3(kCommitThreads), smem, s, p);
 }
 

@@ -93,7 +93,7 @@ sdm_status sdm_cache_commit(const sdm_cache* cache, const int32_t* tok, const in
         return SDM_ERR_INVALID_ARG;
     const sdm_status st = view_of(cache, &p.c);
     if (st != SDM_OK) return st;
-    if (N >= 16384 || B > 16384) return SDM_ERR_UNSUPPORTED;   // the tree and the path are held in shared memory
+    if (N >= kCommitMost || B > kCommitMost) return SDM_ERR_UNSUPPORTED;   // held in shared memory
     p.tok = tok;
     p.parent = parent;
     p.n_nodes = n_nodes;

@@ -490,6 +490,7 @@ struct CacheReadParams {
     int R, rows;
     int32_t* dev_status;
 };
+constexpr int kCommitMost = 16384;   // a tree's slots, and the steps of a path
 struct CacheCommitParams {
     CacheView c;
     const int32_t* tok;

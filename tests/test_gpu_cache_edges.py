@@ -118,3 +118,30 @@ def test_the_checks_over_many_requests(gpu_lib):
     for i in range(1, R - 1, 2):
         want[s.table_cpu[i, 0].item(), :, 3] *= -1
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))    # bits: what no token holds is NaN
+
+
+@pytest.mark.parametrize("S,B", [(6140, 7), (6139, 9), (6140, 6), (6000, 287), (6140, 8), (16384, 16384), (3, 2)])
+def test_commits_of_large_trees(gpu_lib, S, B):
+    """Sizes around what fits 48 KB of shared memory (the tree's two arrays and
+    the path, beside the kernel's own few bytes), and the largest."""
+    depth = 40
+    t = ref.random_trees(1, 65, depth, np.random.default_rng(8), vocab=S + 70)
+    if S > 65:                                                       # the rest of the slots: children of the root
+        parent, tok = np.zeros((1, S), np.int32), np.arange(100000, 100000 + S, dtype=np.int32)[None]
+        parent[:, :65], tok[:, :65] = t["parent"], t["tok"]
+    else:
+        parent, tok = t["parent"][:, :S].copy(), t["tok"][:, :S].copy()
+    path, end = [], min(64, S - 1)
+    while end > 0:
+        path.insert(0, end)
+        end = int(parent[0, end])
+    path = path[:B]
+    s = ref.Setup([65], [20], 1, 64, 16, False, seed=9)
+    s.write_all()
+    out_tok = np.full((1, B + 1), -1, np.int32)
+    out_tok[0, :len(path)] = tok[0, path]
+    got = sdm.cache_commit(s.cache, torch.as_tensor(tok).cuda(), torch.as_tensor(parent.copy()).cuda(), i32([S]),
+                           torch.as_tensor(out_tok).cuda(), i32([len(path)]), s.ctx, dev_status=s.status)
+    assert got["path"][0].tolist() == [0] + path + [-1] * (B - len(path))
+    assert got["length"].tolist() == [21 + len(path)] and s.status.item() == 0
+    assert torch.equal(slots(s, "k", 0, 20, 1 + len(path)).cpu(), s.kv[0]["k"][[20] + [20 + c for c in path]])
