@@ -181,17 +181,18 @@ __device__ __forceinline__ Geom geom_of(const AttendParams& p, const Window& w, 
 __device__ __forceinline__ int tile_key(const Blk& b, int t) { return (t < b.ns ? t : b.lo + t - b.ns) * kTile; }
 
 // Whether some row at window positions p0 .. p1 does not see all of the tile's keys.
-__device__ __forceinline__ bool tile_mixed(const AttendParams& p, int ctx, int n, int p0, int p1, int key0) {
+__device__ __forceinline__ bool tile_mixed(const AttendParams& p, int ctx, int p0, int p1, int key0) {
     const int last = key0 + kTile - 1;
     if (last > (p.tree ? ctx - 1 : ctx + p0)) return true;
     if (p.window <= 0 || last < p.sinks) return false;
-    return key0 <= ctx + (p.tree ? n - 1 : p1) - p.window;
+    // a tree row's depth is what its bits say, those past the window's tokens counted
+    return key0 <= ctx + (p.tree ? p.words * 32 - 1 : p1) - p.window;
 }
 
 // Whether the tile's values are cleared of NaN and infinities: a row may not
 // see them, or a remainder (of either sign) may meet an infinity.
 __device__ __forceinline__ bool tile_cleaned(const AttendParams& p, const Blk& b, int key0) {
-    return (b.flags & BLK_TWICE) || tile_mixed(p, b.ctx, b.n, b.p0, b.p1, key0);
+    return (b.flags & BLK_TWICE) || tile_mixed(p, b.ctx, b.p0, b.p1, key0);
 }
 
 struct Start {
@@ -976,7 +977,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 for (int it = 0; it < mine; ++it) {
                     const int t = t0 + (pair ? it : 2 * it + wg);
                     const int key0 = (t < ns ? t : lo + t - ns) * kTile;
-                    const bool mixed = tile_mixed(p, ctx, n_rows, p0, p1, key0);
+                    const bool mixed = tile_mixed(p, ctx, p0, p1, key0);
                     ok = wait_or_fail(p, &bar.s_full[wg], n_s & 1);
                     ++n_s;
                     if (!ok) break;

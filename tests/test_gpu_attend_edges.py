@@ -180,3 +180,17 @@ def test_rows_of_scores_of_minus_infinity(gpu_lib):
     q = torch.rand((3, 4, 64), generator=s.gen).add(0.5).to(torch.bfloat16).cuda()
     got = sdm.attend(s.cache, q, s.cu, s.ctx, 2, lse=True, dev_status=s.status)
     assert not got["out"].any() and torch.isneginf(got["lse"]).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("w,ctx", [([5, 3], [384, 300]), ([40], [513])])
+def test_bits_past_the_window(gpu_lib, e4m3, w, ctx):
+    """Mask rows with more bits than the window has tokens: they count as
+    depth, and so move the sliding window, and show no token."""
+    t = ref.random_trees(len(w), 70, 9, np.random.default_rng(3))["mask"]
+    t[:, 1::2, 1:] = -1
+    t[:, 2::3] = -1
+    s = ref.Setup(w, ctx, 2, 64, 32, e4m3, seed=12)
+    s.write_all()
+    for window, sinks in ((140, 0), (140, 3), (70, 0), (300, 200)):
+        check(s, 8, mask=t, window=window, sinks=sinks, max_window=max(w))
