@@ -684,8 +684,8 @@ sdm_status sdm_cache_commit(const sdm_cache* cache, const int32_t* tok, const in
  *      (a multiple of 8, at least H * head_dim, base 16-byte aligned); H a
  *      multiple of kv_heads, at most 128 times it; cu_seqlens [R+1], ctx_len
  *      [R]; max_window: the longest window (a longer one is cut:
- *      SDM_DEV_BAD_WINDOW; with tree_mask at most tree_nodes); scale > 0;
- *      sinks >= 0; R <= 16384.
+ *      SDM_DEV_BAD_WINDOW; with tree_mask at most tree_nodes); 0 < scale
+ *      <= 2e38; sinks >= 0; R <= 16384.
  * Out: out [rows, H, head_dim] bf16; lse [rows, H] fp32 (may be NULL).
  * Scores, statistics and sums are fp32; the weights exp(s - m) are rounded to
  * bf16 for the second product (the tensor cores' operand type); over few keys

@@ -116,7 +116,8 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
     AttendParams p = {};
     if (!cu_seqlens || !ctx_len || R <= 0 || rows < 0 || max_window < 0 || H <= 0) return SDM_ERR_INVALID_ARG;
     if (rows > 0 && (!q || !out || max_window == 0)) return SDM_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || scale > 3.0e38f || sinks < 0) return SDM_ERR_INVALID_ARG;
+    // the kernel works with scale * log2 e, which has to stay finite
+    if (!(scale > 0.f) || scale > 2.0e38f || sinks < 0) return SDM_ERR_INVALID_ARG;
     if (tree_mask && tree_nodes < max_window) return SDM_ERR_INVALID_ARG;
     const sdm_status st = view_of(cache, &p.c);
     if (st != SDM_OK) return st;

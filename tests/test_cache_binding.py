@@ -224,3 +224,14 @@ def test_the_stride_of_a_single_row(called):
     for stride in (1, 7, 128, 1001):
         assert binding._need_rows("k", Tensor((1, 2, 64), torch.bfloat16, stride=(stride, 64, 1)), 2, 64, DEV) == 128
     assert binding._need_rows("k", Tensor((2, 2, 64), torch.bfloat16, stride=(1000, 64, 1)), 2, 64, DEV) == 1000
+
+
+def test_scales_whose_product_with_log2_e_is_infinite(lib):
+    FAKE = 0x1000
+    c = ctypes.byref(binding.SdmCache(FAKE, FAKE, None, None, FAKE, 0, 4, 2, 16, 64, 2))
+
+    def attend(scale):
+        return lib.sdm_attend(c, FAKE, 512, FAKE, FAKE, 1, 1, 4, 8, scale, 0, 0, None, 0, FAKE, None, None, 0, None, None)
+
+    assert attend(2.5e38) == attend(2.9e38) == 1
+    assert attend(1.9e38) == attend(1e-38) == 5                # accepted up to the workspace

@@ -194,3 +194,10 @@ def test_bits_past_the_window(gpu_lib, e4m3, w, ctx):
     s.write_all()
     for window, sinks in ((140, 0), (140, 3), (70, 0), (300, 200)):
         check(s, 8, mask=t, window=window, sinks=sinks, max_window=max(w))
+
+
+def test_the_largest_scale(gpu_lib):
+    """Scores of zero stay zero."""
+    s = ref.Setup([2], [200], 2, 64, 16, False, seed=4)
+    s.write_all()
+    check(s, 8, scale=1.99e38, q=torch.zeros((2, 8, 64), dtype=torch.bfloat16, device="cuda"))
