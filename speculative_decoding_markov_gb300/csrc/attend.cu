@@ -433,6 +433,7 @@ __device__ __forceinline__ void plan(const AttendParams& p, unsigned long long* 
             start->us = st.us;
         }
     }
+    fence_proxy_async_smem();   // `cost` lies where TMA is about to write
     __syncthreads();
 }
 
