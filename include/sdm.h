@@ -688,8 +688,12 @@ sdm_status sdm_cache_commit(const sdm_cache* cache, const int32_t* tok, const in
  *      <= 2e38; sinks >= 0; R <= 16384.
  * Out: out [rows, H, head_dim] bf16; lse [rows, H] fp32 (may be NULL).
  * Scores, statistics and sums are fp32; the weights exp(s - m) are rounded to
- * bf16 for the second product (the tensor cores' operand type); over few keys
- * what that rounding leaves is multiplied too.
+ * bf16 for the second product (the tensor cores' operand type).  An output is
+ * within 2^-8 |out| + 2^-8 sum_j softmax(s)_j |v_j| of the formula's, and the
+ * fp32 sums' own error: the result's rounding and the weights'.  The second
+ * part goes, because what the weights' rounding leaves is multiplied too,
+ * where a request's rows of a kv head (query heads times window) see at most
+ * 1152 keys, or 2048 if the rows are at most 64.
  * ws:  sdm_workspace_size(SDM_OP_ATTEND, R, max_window, H, head_dim, rows,
  *      kv_heads, 0).
  */
