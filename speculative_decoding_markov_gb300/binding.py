@@ -645,15 +645,23 @@ def cache_write(cache, k, v, cu_seqlens, ctx_len, dev_status=None):
     return dev_status
 
 
+def _new_status_in(out, device):
+    """A status word of the call's own, returned with its outputs."""
+    out["dev_status"] = new_status(device)
+    return out["dev_status"]
+
+
 def cache_read(cache, cu_rows, rows, first=None, out=None, dev_status=None):
     """Tokens first[i], first[i] + 1, ... (first None: from 0) of every request
-    back as bf16 rows cu_rows[i] .. cu_rows[i+1] - 1 of out["k"], out["v"]."""
+    back as bf16 rows cu_rows[i] .. cu_rows[i+1] - 1 of out["k"], out["v"].
+    Without a dev_status, out["dev_status"] is the call's own (as in
+    cache_commit and attend)."""
     R, dev = cache.requests, cache.device
     shape = (rows, cache.kv_heads, cache.head_dim)
     if out is None:
         out = {n: torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) for n in ("k", "v")}
     ko, vo = _need_out("out['k']", out["k"], shape, _BF16, dev), _need_out("out['v']", out["v"], shape, _BF16, dev)
-    dev_status = new_status(cache.k.device) if dev_status is None else dev_status
+    dev_status = _new_status_in(out, cache.k.device) if dev_status is None else dev_status
     st = lib().sdm_cache_read(cache.ref, _need_i32("cu_rows", cu_rows, R + 1, dev),
                               None if first is None else _need_i32("first", first, R, dev), R, rows, ko, vo,
                               _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
@@ -672,7 +680,7 @@ def cache_commit(cache, tok, parent, n_nodes, out_tok, accept, ctx_len, out=None
     if out is None:
         out = dict(path=torch.empty((R, B + 1), dtype=torch.int32, device=tok.device),
                    length=torch.empty((R,), dtype=torch.int32, device=tok.device))
-    dev_status = new_status(tok.device) if dev_status is None else dev_status
+    dev_status = _new_status_in(out, tok.device) if dev_status is None else dev_status
     st = lib().sdm_cache_commit(cache.ref, _need_i32("tok", tok, R * S, dev), _need_i32("parent", parent, R * S, dev),
                                 _need_i32("n_nodes", n_nodes, R, dev), _need_i32("out_tok", out_tok, R * (B + 1), dev),
                                 _need_i32("accept", accept, R, dev), _need_i32("ctx_len", ctx_len, R, dev), R, S - 1, B,
@@ -716,7 +724,7 @@ def attend(cache, q, cu_seqlens, ctx_len, max_window, scale=None, window=0, sink
         if tree_mask.shape != (R, nodes, (nodes + 31) // 32):
             raise ValueError("tree_mask must be [requests, nodes, ceil(nodes / 32)]")
     ws = attend_workspace(cache, rows, max_window, H) if ws is None else ws
-    dev_status = new_status(q.device) if dev_status is None else dev_status
+    dev_status = _new_status_in(out, q.device) if dev_status is None else dev_status
     st = lib().sdm_attend(cache.ref, q.data_ptr(), qs, _need_i32("cu_seqlens", cu_seqlens, R + 1, dev),
                           _need_i32("ctx_len", ctx_len, R, dev), R, rows, max_window, H,
                           D ** -0.5 if scale is None else scale, window, sinks, mask, nodes, o, z, _need_ws(ws, dev),

@@ -235,3 +235,16 @@ def test_scales_whose_product_with_log2_e_is_infinite(lib):
 
     assert attend(2.5e38) == attend(2.9e38) == 1
     assert attend(1.9e38) == attend(1e-38) == 5                # accepted up to the workspace
+
+
+@pytest.mark.parametrize("which", CALLS)
+def test_a_status_of_the_calls_own_comes_back(called, which, monkeypatch):
+    """What the device finds wrong is not lost when no dev_status is given."""
+    made = Tensor((1,), at=0x7700)
+    monkeypatch.setattr(binding, "new_status", lambda device: made)
+    call, args = CALLS[which]
+    got = call(**args(dev_status=None))
+    assert (got if which == "write" else got["dev_status"]) is made
+    assert 0x7700 in called.calls[0][1]
+    if which != "write":
+        assert "dev_status" not in call(**args())                    # a caller's own stays the caller's
