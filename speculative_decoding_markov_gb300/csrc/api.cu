@@ -273,7 +273,7 @@ size_t sdm_workspace_size(int op, int R, int B, int V, int r, int P, int k, int 
         case SDM_OP_VERIFY: return ws_verify(R, P, V);
         case SDM_OP_TV_LABEL: return ws_tv_label(R, B, V, P);
         case SDM_OP_DRAFT_CHAIN_RNN: return ws_chain_rnn(R, B, V, r);
-        case SDM_OP_ATTEND: return attend_workspace(R, B, V, r, P, k);
+        case SDM_OP_ATTEND: return attend_workspace(B, V, r, k);
         case SDM_OP_VERIFY_TREE:
             return align256(static_cast<size_t>(R) * (N + 1) * 8 * std::max(n_chunks_of(V, 0), n_chunks_of(V, 1)));
         default: return 0;

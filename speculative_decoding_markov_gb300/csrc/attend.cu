@@ -1731,9 +1731,7 @@ cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
 
 }  // namespace
 
-size_t attend_workspace(int R, int max_window, int H, int D, int rows, int kv_heads) {
-    (void)R;
-    (void)rows;
+size_t attend_workspace(int max_window, int H, int D, int kv_heads) {
     if (max_window <= 0 || H <= 0 || D <= 0 || kv_heads <= 0) return 0;
     const size_t grid = num_sms(), cap = slot_rows(max_window, (H + kv_heads - 1) / kv_heads);
     return align256(sizeof(Share) * grid) + align256(2 * grid * cap * sizeof(float2)) + 2 * grid * cap * D * 4;

@@ -128,7 +128,7 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
     if (H / p.c.heads > 128) return SDM_ERR_UNSUPPORTED;   // a token's rows have to fit one tile
     // rows of one request and kv head are counted in 32 bits
     if (static_cast<long long>(max_window) * (H / p.c.heads) >= (1ll << 30)) return SDM_ERR_UNSUPPORTED;
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attend_workspace(R, max_window, H, p.c.D, rows, p.c.heads))
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < attend_workspace(max_window, H, p.c.D, p.c.heads))
         return SDM_ERR_WORKSPACE;
     p.q = q;
     p.q_stride = q_stride;

@@ -525,7 +525,7 @@ struct AttendParams {
     float* lse;             // or NULL
     int32_t* dev_status;
 };
-size_t attend_workspace(int R, int max_window, int H, int D, int rows, int kv_heads);
+size_t attend_workspace(int max_window, int H, int D, int kv_heads);
 cudaError_t launch_attend(const AttendParams& p, void* ws, cudaStream_t s);
 
 }  // namespace sdm
