@@ -517,13 +517,35 @@ __device__ __forceinline__ RowView row_view(const AttendParams& p, int i, int ct
 
 // Adds weight * value for the infinite and NaN values that a row sees in its
 // block's partly seen tiles (where shared memory holds zeros for them), to 16
-// of its output columns.  Rare: one thread per row, straight from the cache.
+// of its output columns: one thread per row, straight from the cache.  The
+// weight of such a value changes nothing while it is a positive number, as it
+// is for any finite score, so the row's score is computed only for keys that
+// are not finite themselves (with a score for each value 1100 tokens whose
+// values are all infinite took 115 ms, and the other warps' waits end after 2 s).
 template <int D, bool E4M3>
 __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Blk& blk, int m, float m_ref, int col0,
                                            float* o) {
     const int wp = m / p.group;
     const RowView r = row_view(p, blk.i, blk.ctx, blk.n, wp);
     const uint16_t* q = p.q + (blk.row0 + wp) * p.q_stride + static_cast<size_t>(blk.hk * p.group + m % p.group) * D;
+    // element c of a cache row, as the products take it
+    auto value = [&](const uint8_t* pool, float scale, size_t row, int c) {
+        if constexpr (E4M3)   // past bf16's range in one case only: past fp32's, too
+            return f16x2_to_f32x2(e4m3x2_to_f16x2(pool[row * D + c])).x * scale;
+        else
+            return bf16_bits_to_float(reinterpret_cast<const uint16_t*>(pool)[row * D + c]);
+    };
+    // whether 16 bytes of a row may hold an infinity or NaN
+    auto odd16 = [&](uint4 x, float scale) {
+        if constexpr (E4M3) {
+            uint32_t bad = 0;   // bit 7 of a byte: a code of ones but for its sign
+            for (const uint32_t u : {x.x, x.y, x.z, x.w}) bad |= (u & 0x7f7f7f7fu) + 0x01010101u;
+            return (bad & 0x80808080u) != 0 || scale > 0x1p119f;   // 448 x 2^119 is the largest finite
+        } else {
+            return (nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) != 0;
+        }
+    };
+    constexpr int kSize = E4M3 ? 1 : 2;
     for (int t = blk.t0; t < blk.t1; ++t) {
         const int key0 = tile_key(blk, t);
         if (!tile_cleaned(p, blk, key0)) continue;
@@ -531,29 +553,24 @@ __device__ __noinline__ void add_nonfinite(const AttendParams& p, const Blk& blk
             if (!((seen32(r, j & ~31) >> (j & 31)) & 1u)) continue;
             const int pg = max(page_of(p.c, blk.i, j), 0);
             const size_t row = pool_row(p.c, pg, j) + (static_cast<size_t>(blk.hk) << p.c.page_shift);
-            float weight = -1.0f;
+            const float vs = E4M3 ? scale_of(p.c.v_exp[row]) : 1.0f;
+            const uint4* v16 = reinterpret_cast<const uint4*>(p.c.v + (row * D + col0) * kSize);
+            bool odd = odd16(v16[0], vs);
+            if constexpr (!E4M3) odd = odd || odd16(v16[1], vs);
+            if (!odd) continue;
+            const float ks = E4M3 ? scale_of(p.c.k_exp[row]) : 1.0f;
+            const uint4* k16 = reinterpret_cast<const uint4*>(p.c.k + row * D * kSize);
+            bool key_odd = false;
+            for (int c = 0; c < D * kSize / 16; ++c) key_odd |= odd16(k16[c], ks);
+            float weight = 1.0f;
+            if (key_odd) {
+                float s = 0.f;
+                for (int d = 0; d < D; ++d) s = fmaf(bf16_bits_to_float(q[d]), value(p.c.k, ks, row, d), s);
+                weight = fast_exp2(s * p.scale * kLog2e - m_ref);
+            }
             for (int c = 0; c < 16; ++c) {
-                float v;
-                if constexpr (E4M3) {   // past bf16's range in one case only: past fp32's, too
-                    v = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.v[row * D + col0 + c])).x * scale_of(p.c.v_exp[row]);
-                } else {
-                    v = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p.c.v)[row * D + col0 + c]);
-                }
-                if (fabsf(v) < INFINITY) continue;
-                if (weight < 0.f) {
-                    float s = 0.f;
-                    for (int d = 0; d < D; ++d) {
-                        float k;
-                        if constexpr (E4M3) {
-                            k = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.k[row * D + d])).x * scale_of(p.c.k_exp[row]);
-                        } else {
-                            k = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p.c.k)[row * D + d]);
-                        }
-                        s = fmaf(bf16_bits_to_float(q[d]), k, s);
-                    }
-                    weight = fast_exp2(s * p.scale * kLog2e - m_ref);
-                }
-                o[c] += weight * v;
+                const float x = value(p.c.v, vs, row, col0 + c);
+                if (!(fabsf(x) < INFINITY)) o[c] += weight * x;
             }
         }
     }
