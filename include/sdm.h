@@ -631,6 +631,7 @@ typedef struct {
  *      multiple of 8, at least kv_heads * head_dim; bases 16-byte aligned: a
  *      slice of a fused projection's output will do), cu_seqlens [R+1],
  *      ctx_len [R].
+ * Here and in cache_read R, rows <= 2^31 - 2^16.
  * Slots of different tokens must differ (they do when no two requests share
  * a page they write).
  */

@@ -36,6 +36,9 @@ sdm_status view_of(const sdm_cache* c, CacheView* v) {
     return SDM_OK;
 }
 
+// Whether the grids' strides over rows and requests (below 65536) stay within 32 bits.
+inline bool counts_ok(int R, int rows) { return R <= 0x7fff0000 && rows <= 0x7fff0000; }
+
 // A row stride in elements: 16-byte rows that hold `width` elements.
 inline bool stride_ok(int64_t stride, long long width) { return stride % 8 == 0 && stride >= width; }
 
@@ -51,6 +54,7 @@ sdm_status sdm_cache_write(const sdm_cache* cache, const uint16_t* k, const uint
     const sdm_status st = view_of(cache, &p.c);
     if (st != SDM_OK || rows == 0) return st;   // arrays without rows may have no address
     if (!k || !v) return SDM_ERR_INVALID_ARG;
+    if (!counts_ok(R, rows)) return SDM_ERR_UNSUPPORTED;
     const long long width = static_cast<long long>(p.c.heads) * p.c.D;
     if (!stride_ok(k_stride, width) || !stride_ok(v_stride, width) || !aligned16(k) || !aligned16(v))
         return SDM_ERR_UNSUPPORTED;
@@ -73,7 +77,7 @@ sdm_status sdm_cache_read(const sdm_cache* cache, const int32_t* cu_rows, const 
     const sdm_status st = view_of(cache, &p.c);
     if (st != SDM_OK || rows == 0) return st;
     if (!k_out || !v_out) return SDM_ERR_INVALID_ARG;
-    if (!aligned16(k_out) || !aligned16(v_out)) return SDM_ERR_UNSUPPORTED;
+    if (!counts_ok(R, rows) || !aligned16(k_out) || !aligned16(v_out)) return SDM_ERR_UNSUPPORTED;
     p.cu = cu_rows;
     p.first = first;
     p.k_out = k_out;

@@ -248,3 +248,11 @@ def test_a_status_of_the_calls_own_comes_back(called, which, monkeypatch):
     assert 0x7700 in called.calls[0][1]
     if which != "write":
         assert "dev_status" not in call(**args())                    # a caller's own stays the caller's
+
+
+@pytest.mark.parametrize("R,rows", [(2 ** 31 - 1, 1), (1, 2 ** 31 - 1), (2 ** 31 - 2 ** 16 + 1, 1)])
+def test_counts_that_the_grids_strides_would_pass(lib, R, rows):
+    FAKE = 0x1000
+    c = ctypes.byref(binding.SdmCache(FAKE, FAKE, None, None, FAKE, 0, 4, 2, 16, 64, 2))
+    assert lib.sdm_cache_write(c, FAKE, FAKE, 128, 128, FAKE, FAKE, R, rows, None, None) == 2
+    assert lib.sdm_cache_read(c, FAKE, None, R, rows, FAKE, FAKE, None, None) == 2
