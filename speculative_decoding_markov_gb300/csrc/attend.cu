@@ -31,17 +31,18 @@
 // included, in a second ring.  Each softmax warpgroup's S, P and O are its
 // own, so one's softmax runs beside the other's products.
 //
-// What bounds it (32 query heads on 8 kv heads of 128, bf16, unless said):
-//   64 windows of 1 to 8 tokens over 300 to 8000: HBM, 5.7 TB/s (107 us).
-//   A prompt of 8192 tokens: the softmax between its two products, 1.31
-//   PFLOP/s, tensor pipe 56 % (419 us).  A 128 x 128 tile's softmax takes 1112
+// What bounds it (32 query heads on 8 kv heads of 128, bf16, unless said; times
+// of whole calls among others of their kind, merge included):
+//   64 windows of 1 to 8 tokens over 300 to 8000: HBM, 5.8 TB/s (105 us).
+//   A prompt of 8192 tokens: the softmax between its two products, 1.26
+//   PFLOP/s (435 us; this kernel by itself 419, tensor pipe 56 %).  A 128 x 128 tile's softmax takes 1112
 //   clocks alone and 1800 beside the other warpgroup's, its two products with
 //   their hand-overs 1460; S has no room for a second buffer beside O.
-//   e4m3 windows: turning the codes into bf16, about 6000 warp instructions a
+//   e4m3 windows: turning the codes into bf16, about 5700 warp instructions a
 //   tile of 128 keys and 50 % of the issue slots: 3.4 TB/s of codes at two
-//   contexts of 150001 to 199999 (28 heads on 4, 101 us).
+//   contexts of 150001 to 199999 (28 heads on 4, 102 us).
 //   One token over 500 keys: the chain of plan, loads, two products and merge
-//   (12.8 us).
+//   (12.5 us, 12.0 in a graph).
 // The warps' loops together have to stay in the instruction cache: unrolling
 // one of them twice more than now cost 5 to 40 %, wherever it was tried.
 //
@@ -77,8 +78,9 @@ constexpr float kMaxRef = 3.0e38f;
 // the remainders 0.91 to 1.00; without, 1.24 over 2049 keys, 1.24 over 2500,
 // 1.18 over 40000.
 // Cost against no remainders at all: 256 e4m3 windows over 200 to 4000 tokens
-// 137 -> 149 us, five e4m3 windows of 37 to 1500 tokens 55 -> 65 us, 32 trees
-// of 65 slots 131 -> 133 us, a prompt of 8192 414 -> 419 us.
+// 137 -> 149 us, five e4m3 windows of 37 to 1500 tokens 57 -> 67 us, 32 trees
+// of 65 slots 132 -> 134 us, a prompt of 8192 430 -> 435 us, one token over 500
+// keys 12.0 -> 12.5 us.
 constexpr int kStackRows = 64;
 constexpr int kFineTiles = 9, kStackTiles = 16;
 constexpr int kTmemCols = 512;        // S0, S1, O0, O1 at columns 0, 128, 256, 384; P over S
@@ -94,9 +96,9 @@ enum { BLK_PAIR = 1, BLK_STACKED = 2, BLK_TWICE = 4 };
 
 // SMALL: all windows of the call fit in kStackRows rows.  Their calls are
 // bound by loads, and the second sub-tile of Q that they do not need holds two
-// more tiles of the rings: 64 windows of 1 to 8 tokens 107 us against 120, 256
-// e4m3 windows 149 against 184, two e4m3 contexts of 150001 to 199999 104
-// against 144, one token over 500 keys 12.8 against 13.3.
+// more tiles of the rings: 64 windows of 1 to 8 tokens 105 us against 119, 256
+// e4m3 windows 149 against 183, two e4m3 contexts of 150001 to 199999 102
+// against 143, one token over 500 keys 12.5 against 12.9.
 template <int D, bool E4M3, bool SMALL>
 struct Cfg {
     static constexpr int kThreads = E4M3 ? 640 : 384;
@@ -929,8 +931,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     pdl_wait();
     pdl_trigger();
     // a few small requests: the walking warp finds the start by itself, later
-    // (one token over 500 keys 12.8 us against 14.4 with all warps, 32 trees of
-    // 65 slots 133 against 135); beyond 32 it would need several rounds
+    // (one token over 500 keys 12.5 us against 14.0 with all warps, 32 trees of
+    // 65 slots 134 against 135); beyond 32 it would need several rounds
     const bool by_all = p.R > 32 || p.max_window * p.group > 4 * p.sub;
     if (by_all) plan<C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem + C::kRing), start, wsum);
     Start st = *start;   // read before the roles use its place
@@ -1166,8 +1168,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             // ----------------------------------------------------------------
             // producer: K and V tiles in turn, a lane per page.  Not the warp that
             // shares its scheduler with the first warps of the softmax, the only
-            // busy ones of small windows (two contexts of 150001 to 199999 101 us
-            // against 104.5)
+            // busy ones of small windows (two contexts of 150001 to 199999 101.6
+            // us against 104.3)
             // ----------------------------------------------------------------
             const int pages = kTile >> p.c.page_shift, page = 1 << p.c.page_shift;
             constexpr int kN = E4M3 ? C::kRawSlots : C::kSlots;
@@ -1570,11 +1572,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
 // starts a block and the next ones that continue it.  kRows rows a warp, the
 // loads of kSegs segments together: the kernel is a chain of a few L2 round
 // trips (bytes: at most 2 x 256 rows x 4 D per CTA, written and read once).
-// Small windows are long contexts over many CTAs, so 8 segments of a row: one
-// token's merge over two contexts of 150001 to 199999 (38 segments) takes 8.7
-// us and the call 119 against 129 with a segment at a time; 4 and 16 are 2 us
-// slower.  Larger ones have two or three segments and many rows, so 2 rows: 12
-// us of a call of 65 for five e4m3 windows (a row at a time: 13).
+// Small windows are long contexts over many CTAs, so 8 segments of a row: two
+// contexts of 150001 to 199999 (38 segments) take 102 us against 109 with a
+// segment at a time (4: 104; 16: 101, but 64 windows 108 against 106).  Larger
+// ones have two or three segments and many rows, so 2 rows: five e4m3 windows
+// 66.4 us (a row at a time: 67.5).
 template <int D, int kRows, int kSegs>
 __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p, const Scratch ws, int grid) {
     constexpr int kV = D / 32;

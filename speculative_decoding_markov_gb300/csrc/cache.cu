@@ -13,13 +13,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCommitThreads = 512;     // 32 trees of 65 slots, written and committed: 8.3 us (256: 9.2, 1024: 8.5)
+constexpr int kCommitThreads = 512;     // 32 trees of 65 slots, written and committed: 8.4 us (256: 9.2, 1024: 8.5)
 
 // The windows are looked at apart from the rows, by one block more than the
 // rows have (a window that counts as empty need not have a row in use): it
 // flags what is wrong with them and returns whether one of them is unsound, in
 // which case the rows' own search in cu_seqlens proves nothing and the block
-// takes every window's rows itself.
+// takes every window's rows itself.  0.4 us of the write and read of 64 windows
+// (6.2 us in a graph).
 __device__ __forceinline__ bool check_windows(const int32_t* cu, const int32_t* ctx, int R, int rows,
                                               long long tokens, int32_t* dev_status) {
     int bad = 0, unsound = 0;
@@ -37,9 +38,9 @@ __device__ __forceinline__ bool check_windows(const int32_t* cu, const int32_t* 
 // each, so the maximum of a vector is a shuffle reduction over those lanes.
 // e4m3: the smallest scale 2^e with max |x| <= 448 2^e, so that a code's error
 // is 2^-4 of its value, or 2^-10 2^e where that is more; scaling is exact.
-// 24831 rows of 8 heads x 128 as e4m3: 39 us, 3.9 TB/s, the conversion's 68 %
+// 24831 rows of 8 heads x 128 as e4m3: 41 us, 3.7 TB/s, the conversion's 62 %
 // of the issue slots beside it; small calls are the chain cu_seqlens -> request
-// -> page -> slot (7 us for 2080 rows).
+// -> page -> slot (8 us from cold caches for 2080 rows).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteParams p) {
     constexpr int kLanes = D / 8;           // lanes per vector
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
 
 // One warp per output row; D / 8 lanes read 8 elements each of one vector and
 // write them as 16 bytes of bf16: code x 2^e is exact in bf16.  46418
-// tokens of 8 heads x 128 from e4m3: 48 us, 5.9 TB/s, bound by HBM.
+// tokens of 8 heads x 128 from e4m3: 50 us, 5.7 TB/s, bound by HBM.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadParams p) {
     constexpr int kLanes = D / 8;
@@ -213,8 +214,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
 
 // One CTA per request: path[0] = the root, path[j + 1] = the child of path[j]
 // whose token is out_tok[j]; then row path[j] moves to row j.  The bytes are
-// few, so the time is a chain of dependent loads: 9 us for 32 trees of 65
-// slots, 8 heads x 128.  The first warp walks the tree (one ballot per 32
+// few, so the time is a chain of dependent loads: 8 to 9 us from cold caches for
+// 32 trees of 65 slots, 8 heads x 128.  The first warp walks the tree (one ballot per 32
 // slots and level), then all threads move the path's rows in order of their
 // destination: a batch is loaded whole, then stored.  A source slot path[j]
 // is never below its destination j, so a store cannot reach a slot that a
