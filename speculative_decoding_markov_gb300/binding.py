@@ -539,6 +539,8 @@ class PagedCache:
     exponents k_exp, v_exp [pages, kv heads, page] uint8) and the page table
     [requests, columns] int32.  Holds the tensors and their C description."""
 
+    alone = False   # whether its device is the only one, and so the current one
+
     def __init__(self, k, v, table, k_exp=None, v_exp=None):
         _need_cuda(k, v, table, k_exp, v_exp)
         if any(x is not None and x.get_device() != k.get_device() for x in (v, table, k_exp, v_exp)):
@@ -559,6 +561,7 @@ class PagedCache:
         self.k, self.v, self.table, self.k_exp, self.v_exp = k, v, table, k_exp, v_exp
         self.requests = table.shape[0]
         self.device = k.get_device()
+        self.alone = torch.cuda.device_count() == 1
         self.kv_heads, self.page, self.head_dim = k.shape[1:]
         self.c = SdmCache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
                           v_exp.data_ptr() if e4m3 else None, table.data_ptr(), E4M3 if e4m3 else BF16, k.shape[0],
@@ -584,20 +587,22 @@ _this_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") 
 
 def _stream_of(cache):
     """The current stream of the cache's device, which has to be the current one."""
-    if _this_device() != cache.device:
+    if not cache.alone and _this_device() != cache.device:
         raise ValueError(f"the cache is on device {cache.device}, not on the current one")
     return _raw_stream(cache.device)
 
 
 # The checks of a call's tensors are on the path of the smallest calls (a step's
 # write and read: 11 us), so each is one expression without calls of its own.
-# `device`: the CUDA device a tensor has to be on (None: any).
+# `device`: the CUDA device a tensor has to be on (None: any).  What costs is
+# reading a tensor's attributes, 50 to 100 ns each: a shape is read once.
 _BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
 
 
 def _need_rows(what, x, heads, head_dim, device=None):
     """Packed rows [rows, heads, head dim] bf16, contiguous within a row (a
-    slice of a fused projection's output will do); returns the row stride."""
+    slice of a fused projection's output will do); returns the rows and their
+    stride."""
     if x.dtype is not _BF16 or (x.get_device() != device and (device is not None or not x.is_cuda)):
         raise TypeError(f"{what} must be a bf16 CUDA tensor on the cache's device")
     shape, st = x.shape, x.stride()
@@ -605,13 +610,19 @@ def _need_rows(what, x, heads, head_dim, device=None):
         raise ValueError(f"{what} must be [rows, {heads}, {head_dim}]")
     if st[2] != 1 or (heads > 1 and st[1] != head_dim):
         raise ValueError(f"{what} must be contiguous within a row")
-    return st[0] if shape[0] > 1 else heads * head_dim   # one row has no next one
+    return shape[0], st[0] if shape[0] > 1 else heads * head_dim   # one row has no next one
 
 
 def _need_i32(what, x, n, device=None):
     if (x.dtype is not _I32 or (x.get_device() != device and (device is not None or not x.is_cuda)) or x.numel() < n or
             not x.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous int32 tensor of at least {n} entries on the cache's device")
+    return x.data_ptr()
+
+
+def _need_status(x, device):
+    if x.dtype is not _I32 or x.get_device() != device or x.numel() < 1:
+        raise ValueError("dev_status must be an int32 on the cache's device")
     return x.data_ptr()
 
 
@@ -632,14 +643,14 @@ def cache_write(cache, k, v, cu_seqlens, ctx_len, dev_status=None):
     """The windows' keys and values [rows, kv heads, head dim] into their slots
     (tokens ctx_len[i], ctx_len[i] + 1, ...), quantised if the cache is e4m3."""
     R, dev = cache.requests, cache.device
-    ks = _need_rows("k", k, cache.kv_heads, cache.head_dim, dev)
-    vs = _need_rows("v", v, cache.kv_heads, cache.head_dim, dev)
-    if v.shape[0] != k.shape[0]:
+    rows, ks = _need_rows("k", k, cache.kv_heads, cache.head_dim, dev)
+    v_rows, vs = _need_rows("v", v, cache.kv_heads, cache.head_dim, dev)
+    if v_rows != rows:
         raise ValueError("k and v must have the same rows")
     dev_status = new_status(k.device) if dev_status is None else dev_status
     st = lib().sdm_cache_write(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs,
                                _need_i32("cu_seqlens", cu_seqlens, R + 1, dev), _need_i32("ctx_len", ctx_len, R, dev),
-                               R, k.shape[0], _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
+                               R, rows, _need_status(dev_status, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_cache_write")
     return dev_status
@@ -664,7 +675,7 @@ def cache_read(cache, cu_rows, rows, first=None, out=None, dev_status=None):
     dev_status = _new_status_in(out, cache.k.device) if dev_status is None else dev_status
     st = lib().sdm_cache_read(cache.ref, _need_i32("cu_rows", cu_rows, R + 1, dev),
                               None if first is None else _need_i32("first", first, R, dev), R, rows, ko, vo,
-                              _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
+                              _need_status(dev_status, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_cache_read")
     return out
@@ -686,7 +697,7 @@ def cache_commit(cache, tok, parent, n_nodes, out_tok, accept, ctx_len, out=None
                                 _need_i32("accept", accept, R, dev), _need_i32("ctx_len", ctx_len, R, dev), R, S - 1, B,
                                 _need_i32("path", out["path"], R * (B + 1), dev),
                                 _need_i32("length", out["length"], R, dev),
-                                _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
+                                _need_status(dev_status, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_cache_commit")
     return out
@@ -704,15 +715,16 @@ def attend(cache, q, cu_seqlens, ctx_len, max_window, scale=None, window=0, sink
     mask); window > 0 limits it to that many last tokens and the first
     `sinks`.  Returns out (and the log-sum-exp if lse)."""
     R, D, dev = cache.requests, cache.head_dim, cache.device
-    rows, H = q.shape[0], q.shape[1]
-    qs = _need_rows("q", q, H, D, dev)
+    shape = q.shape
+    H = shape[1]
+    rows, qs = _need_rows("q", q, H, D, dev)
     if H % cache.kv_heads:
         raise ValueError("q's heads must be a multiple of the cache's")
     if out is None:
         out = dict(out=torch.empty((rows, H, D), dtype=torch.bfloat16, device=q.device))
         if lse:
             out["lse"] = torch.empty((rows, H), dtype=torch.float32, device=q.device)
-    o, z = _need_out("out", out["out"], q.shape, _BF16, dev), out.get("lse")
+    o, z = _need_out("out", out["out"], shape, _BF16, dev), out.get("lse")
     if z is not None:
         z = _need_out("lse", z, (rows, H), torch.float32, dev)
     elif lse:
@@ -728,7 +740,7 @@ def attend(cache, q, cu_seqlens, ctx_len, max_window, scale=None, window=0, sink
     st = lib().sdm_attend(cache.ref, q.data_ptr(), qs, _need_i32("cu_seqlens", cu_seqlens, R + 1, dev),
                           _need_i32("ctx_len", ctx_len, R, dev), R, rows, max_window, H,
                           D ** -0.5 if scale is None else scale, window, sinks, mask, nodes, o, z, _need_ws(ws, dev),
-                          ws.numel(), _need_i32("dev_status", dev_status, 1, dev), _stream_of(cache))
+                          ws.numel(), _need_status(dev_status, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_attend")
     return out

@@ -222,8 +222,8 @@ def test_calls_without_rows_pass_the_binding(called):
 def test_the_stride_of_a_single_row(called):
     """It leads nowhere: any value will do."""
     for stride in (1, 7, 128, 1001):
-        assert binding._need_rows("k", Tensor((1, 2, 64), torch.bfloat16, stride=(stride, 64, 1)), 2, 64, DEV) == 128
-    assert binding._need_rows("k", Tensor((2, 2, 64), torch.bfloat16, stride=(1000, 64, 1)), 2, 64, DEV) == 1000
+        assert binding._need_rows("k", Tensor((1, 2, 64), torch.bfloat16, stride=(stride, 64, 1)), 2, 64, DEV) == (1, 128)
+    assert binding._need_rows("k", Tensor((2, 2, 64), torch.bfloat16, stride=(1000, 64, 1)), 2, 64, DEV) == (2, 1000)
 
 
 def test_scales_whose_product_with_log2_e_is_infinite(lib):
