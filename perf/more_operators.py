@@ -299,7 +299,7 @@ def _paged(case, s, gen, w, ctx):
         return
     s["scale"] = 1.0 / math.sqrt(D)
     s["mass"] = torch.rand((R, G, s["len"]), generator=gen, device=DEV) * 4
-    s["out"] = torch.zeros((R, G, s["len"]), device=DEV)
+    s["out"] = dict(mass=torch.zeros((R, G, s["len"]), device=DEV))
     # what the attention left: the log-sum-exp of each row's scores
     s["lse"] = torch.ones((s["packed"], H), device=DEV)
     for h in range(G):
@@ -313,7 +313,6 @@ def _handles(case, s):
     from speculative_decoding_markov_gb300 import binding as sdm
     s["status"] = sdm.new_status()
     if case["op"] == "logprobs":
-        s["ws"] = sdm.token_logprobs_workspace(s["target"], s["tok"], case["top"])
         return
     s["handle"] = sdm.PagedCache(s["k"], s["v"], s["table"], s["k_exp"], s["v_exp"])
     if case["op"] == "rotate":
@@ -433,7 +432,7 @@ def _weight(s):
     key = torch.arange(L, device=DEV)[None, None]
     ctx, n = s["ctx"].long()[:, None, None], s["n"].long()[:, None, None]
     new = torch.where(key < ctx, s["mass"], 0.0) + got
-    s["out"].copy_(torch.where(key < ctx + n, new, s["out"]))
+    s["out"]["mass"].copy_(torch.where(key < ctx + n, new, s["out"]["mass"]))
     return s["out"]
 
 
@@ -483,8 +482,7 @@ def run(state):
             return [s["q_out"], s["back"]["k"], s["back"]["v"]]
         if op == "logprobs":
             return sdm.token_logprobs(s["target"], s["cu"], s["tok"], n=s["n"], path=s["path"],
-                                      temperature=case["temp"], top=case["top"], out=s["out"], ws=s["ws"],
-                                      dev_status=s["status"])
+                                      temperature=case["temp"], top=case["top"], out=s["out"], dev_status=s["status"])
         if op == "weight":
             return sdm.attend_weight(s["handle"], s["q"], s["lse"], s["cu"], s["ctx"], s["max_w"], mass=s["mass"],
                                      count=s["n"], path=s["path"], scale=s["scale"], window=case["window"],
@@ -569,7 +567,7 @@ def _exact_logprobs(case, s, w):
 
 def _exact_weight(case, s, w, ctx):
     G, D, page, group = case["G"], case["D"], case["page"], case["H"] // case["G"]
-    out, cu = s["out"].double(), s["cu"].tolist()
+    out, cu = s["out"]["mass"].double(), s["cu"].tolist()
     for i in range(case["R"]):
         n = w[i] + ctx[i]
         ids = s["table"].long()[i, :(n + page - 1) // page]
@@ -592,7 +590,7 @@ def _exact_weight(case, s, w, ctx):
                 x = torch.einsum("wgd,nd->wgn", q[part:part + 512, h], k[h]) * s["scale"]
                 x = torch.exp(x - lse[part:part + 512, h, :, None])
                 out[i, h, :n] += torch.where(see[:, None], x, 0.0).sum((0, 1))
-    return out
+    return dict(mass=out)
 
 
 def _exact_evict(case, s, w, ctx):
