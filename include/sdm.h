@@ -108,7 +108,9 @@ enum {
     SDM_OP_VERIFY_TREE = 5,
     SDM_OP_TV_LABEL = 6,
     SDM_OP_DRAFT_CHAIN_RNN = 7,
-    SDM_OP_ATTEND = 8
+    SDM_OP_ATTEND = 8,
+    SDM_OP_ATTEND_WEIGHT = 9,
+    SDM_OP_CACHE_EVICT = 10
 };
 
 /* Bytes of scratch the operation needs for these sizes (0 if none).  Pass the
@@ -702,6 +704,135 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
                       const int32_t* ctx_len, int R, int rows, int max_window, int H, float scale, int window,
                       int sinks, const int32_t* tree_mask, int tree_nodes, uint16_t* out, float* lse, void* ws,
                       size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * qk_rotate: what stands between the projections and the cache: every query
+ * and key head vector x normalised, y = x / sqrt(mean(x^2) + eps) * weight (no
+ * weight: y = x), and rotated by its position: pair j < rot_dim / 2 by the
+ * angle position * freq[j], (a, b) -> (a cos - b sin, b cos + a sin).  A pair is
+ * elements (j, j + rot_dim / 2), or (2 j, 2 j + 1) if interleaved; elements
+ * from rot_dim on are not rotated.  With a cache the keys, and the values as
+ * they are, go into its slots as by sdm_cache_write (the same bits as rotating
+ * into k_out and writing that); without one the keys go to k_out.
+ * The row at window position p of request i has the position start[i] + p, or
+ * start[i] + row_pos[row] (a tree's depths; sdm_pack_ragged's packed_pos);
+ * start NULL: ctx_len[i].  start differs from ctx_len where tokens were
+ * evicted.  Positions are exact to 2^53; the angle is reduced in fp64.
+ * In:  q [rows, H, head_dim], k [rows, kv_heads, head_dim], v (with a cache)
+ *      the same, bf16, strides in elements from row to row (multiples of 8,
+ *      at least a row, bases 16-byte aligned); q_weight, k_weight [head_dim]
+ *      fp32, 16-byte aligned, or NULL; eps >= 0; freq [rot_dim / 2] fp64
+ *      radians per token (NULL with rot_dim 0); rot_dim a multiple of 8, at
+ *      most head_dim; head_dim 64 or 128, and the cache's; kv_heads likewise;
+ *      cu_seqlens, ctx_len as in sdm_cache_write (without a cache ctx_len may
+ *      be NULL if start is given); R <= 2^31 - 2^16, rows * (H + 2 kv_heads)
+ *      < 2^31.
+ * Out: q_out, and k_out without a cache (NULL with one): rows with strides of
+ *      their own; each may be its input.  Rows that no window holds are left
+ *      as they were.  fp32 throughout, rounded to bf16 once.
+ * Device checks as in sdm_cache_write; a row whose page is bad still has its
+ * query rotated, one past the page table is left out.
+ */
+sdm_status sdm_qk_rotate(const sdm_cache* cache, const uint16_t* q, int64_t q_stride, int H, const uint16_t* k,
+                         int64_t k_stride, const uint16_t* v, int64_t v_stride, int kv_heads, int head_dim,
+                         const float* q_weight, const float* k_weight, float eps, const double* freq, int rot_dim,
+                         int interleaved, const int32_t* cu_seqlens, const int32_t* ctx_len, const int32_t* start,
+                         const int32_t* row_pos, int R, int rows, uint16_t* q_out, int64_t q_out_stride,
+                         uint16_t* k_out, int64_t k_out_stride, int32_t* dev_status, void* stream);
+
+/*
+ * token_logprobs: what a served request wants to know of its tokens, after
+ * sdm_verify or sdm_verify_tree.  Position p < n[i] of request i, with its
+ * target row z (row cu_seqlens[i] + p, or cu_seqlens[i] + path[i, p]) and
+ * token y = tok[i, p], has
+ *     logp = log softmax(z / T)[y],     entropy = -sum_v P_v log P_v,
+ *     rank = tokens ahead of y: a greater logit, or an equal one and a lower id,
+ *     top_tok, top_logp = the `top` first tokens in that order, and theirs.
+ * A tree's target [R, N+1, V] has cu_seqlens[i] = i (N + 1) and the path that
+ * sdm_cache_commit returns; a prompt is one window whose tok are its next tokens.
+ * In:  target [row_capacity, V] (dtT), cu_seqlens [R+1], path [R, W] or NULL,
+ *      tok [R, W] (sdm_verify's out_tok), n [R] (its n_out) or NULL: every row
+ *      of the windows, W at most.  V % 8 == 0, V >= 8, target 16-byte aligned;
+ *      R W <= 2^27; 0 <= top <= min(32, V); log2(e) / T within 1e-30 .. 1e30.
+ * Out: logp [R, W] fp32; entropy fp32, rank int32 [R, W] (each may be NULL);
+ *      top_tok int32, top_logp fp32 [R, W, top] (NULL if top = 0).  Positions
+ *      from n[i] on are left as they were.
+ * Sums are fp32 relative to a reference near the maximum.  A logit of -inf has
+ * logp -inf; a row of nothing else, or with a NaN, has logp and entropy NaN (a
+ * row with a NaN has some ranks and some `top` different tokens), one with
+ * +inf logp -inf but for those NaN, entropy NaN.
+ * Device checks: n[i] outside [0, W] (cut), a row outside its window
+ * (SDM_DEV_BAD_WINDOW) or past row_capacity (SDM_DEV_CAPACITY): left out; a
+ * token outside [0, V) has logp -inf and rank V (SDM_DEV_BAD_TOKEN).
+ */
+sdm_status sdm_token_logprobs(const void* target, sdm_dtype dtT, int row_capacity, int V, const int32_t* cu_seqlens,
+                              const int32_t* path, const int32_t* tok, const int32_t* n, int R, int W,
+                              float temperature, int top, float* logp, float* entropy, int32_t* rank,
+                              int32_t* top_tok, float* top_logp, int32_t* dev_status, void* stream);
+
+/*
+ * attend_weight: the attention weight that each cached token got from the
+ * committed rows of a call, per kv head, for sdm_cache_evict.  After
+ * sdm_attend (its lse) and, for trees, sdm_cache_commit (the keys have to be
+ * where they stay):
+ *     mass_out[i, g, j] = (j < ctx_len[i] ? mass[i, g, j] : 0)
+ *                         + sum_{p, h} exp(scale q . k_j - lse)
+ * over the rows p < count[i] that see token j and the query heads h of kv head
+ * g, for j < ctx_len[i] + count[i]; later entries are left as they were.  Row
+ * p is packed row cu_seqlens[i] + p, or cu_seqlens[i] + path[i, p] (count: the
+ * path's length, root included), and sits at token ctx_len[i] + p; it sees j
+ * <= ctx_len[i] + p within `window` or below `sinks`, as in sdm_attend.
+ * In:  cache (its values are not read); q and q_stride as in sdm_attend; lse
+ *      [rows, H] fp32; cu_seqlens [R+1], ctx_len [R]; count [R] or NULL (whole
+ *      windows); path [R, path_stride] or NULL, path_stride >= max_count;
+ *      max_count: the largest count (larger ones are cut); mass [R, kv_heads,
+ *      stride] fp32 or NULL (zeros), stride < 2^31; R <= 16384, H at most 128
+ *      kv_heads.
+ * Out: mass_out, the same shape; may be mass.
+ * Scores and sums are fp32, in an order that depends on the sizes alone.  A
+ * row with lse -inf saw nothing and adds nothing; one with lse +inf or NaN
+ * adds what the formula gives.
+ * ws:  sdm_workspace_size(SDM_OP_ATTEND_WEIGHT, R, max_count, H, head_dim, rows,
+ *      kv_heads, 0) bytes.
+ * Device checks as in sdm_attend; a count outside [0, max_count] or past the
+ * window is cut, a row of the path outside the window adds nothing
+ * (SDM_DEV_BAD_WINDOW); tokens past `stride` are left out (SDM_DEV_BAD_PAGE).
+ */
+sdm_status sdm_attend_weight(const sdm_cache* cache, const uint16_t* q, int64_t q_stride, const float* lse,
+                             const int32_t* cu_seqlens, const int32_t* ctx_len, const int32_t* count,
+                             const int32_t* path, int path_stride, int R, int rows, int max_count, int H, float scale,
+                             int window, int sinks, const float* mass, float* mass_out, int64_t stride, void* ws,
+                             size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * cache_evict: every request's cache cut to `keep` tokens, chosen for each kv
+ * head by itself: the positions below `sinks` and the last `recent` ones
+ * first, then those of the largest weight (equals: the lowest slot; a NaN
+ * last).  Request i holds n = ctx_len[i] + count[i] tokens; slot s < ctx_len[i]
+ * has the position pos[i, g, s] that an earlier cut left, slot ctx_len[i] + j
+ * the position start[i] + j.  A kept token in front of slot `keep` stays in its
+ * slot; the j-th of the others, in order, moves (key, value, scales, weight and
+ * position) to the j-th slot that becomes free there.  A request with n <= keep
+ * keeps all.  Keys carry their rotation, so a cache in another order attends
+ * alike; sdm_attend's `window` and `sinks` go by slots, so use neither then.
+ * In:  cache (its pools are written); mass, pos [R, kv_heads, stride] (pos is
+ *      not read from ctx_len on), stride < 2^31; ctx_len [R]; count [R] or NULL (0); start [R]
+ *      or NULL (ctx_len: nothing was evicted yet); 0 <= sinks, recent, sinks +
+ *      recent <= keep, keep >= 1; R * kv_heads <= 2^24.
+ * Out: mass_out, pos_out [R, kv_heads, stride], filled below length[i], entries
+ *      from there on left as they were; may be mass and pos.  length [R] =
+ *      min(n, keep), the next ctx_len; next [R] (may be NULL) = start + count,
+ *      the next start.  Neither may be an input: a request's heads read those
+ *      beside one another.
+ * ws:  sdm_workspace_size(SDM_OP_CACHE_EVICT, R, kv_heads, 0, 0, stride, 0, keep).
+ * Device checks: a negative ctx_len or count as 0 (SDM_DEV_BAD_WINDOW); tokens
+ * past the page table or `stride` are left out, a row whose page is bad is not
+ * moved (SDM_DEV_BAD_PAGE).
+ */
+sdm_status sdm_cache_evict(const sdm_cache* cache, const float* mass, const int32_t* pos, int64_t stride,
+                           const int32_t* ctx_len, const int32_t* count, const int32_t* start, int R, int keep,
+                           int sinks, int recent, float* mass_out, int32_t* pos_out, int32_t* length, int32_t* next,
+                           void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

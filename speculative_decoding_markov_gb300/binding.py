@@ -21,7 +21,7 @@ BF16, FP32, E4M3 = 0, 1, 2
 GREEDY, SAMPLE = 0, 1
 STATIC, COMPACT, CAP_ACCEPT = 0, 1, 2
 OP_DRAFT_CHAIN, OP_DRAFT_TREE, OP_SCHEDULE, OP_PACK, OP_VERIFY, OP_VERIFY_TREE, OP_TV_LABEL, OP_DRAFT_CHAIN_RNN = range(8)
-OP_ATTEND = 8
+OP_ATTEND, OP_ATTEND_WEIGHT, OP_CACHE_EVICT = 8, 9, 10
 DEV_BAD_TOKEN, DEV_TIER_UNCAPTURED, DEV_TIMEOUT, DEV_BAD_WINDOW, DEV_CAPACITY, DEV_BAD_CLASS = 1, 2, 4, 8, 16, 32
 DEV_TIER_OVERFLOW, DEV_BAD_PAGE = 64, 128
 
@@ -31,6 +31,7 @@ EXPORTS = ("sdm_workspace_size", "sdm_markov_prepared_size", "sdm_markov_prepare
            "sdm_threshold_sweep", "sdm_draft_chain_rnn", "sdm_status_str", "sdm_status_of_device", "sdm_check_timeout_path",
            "sdm_draft_chain_packed", "sdm_draft_chain_front",
            "sdm_cache_write", "sdm_cache_read", "sdm_cache_commit", "sdm_attend",
+           "sdm_qk_rotate", "sdm_token_logprobs", "sdm_attend_weight", "sdm_cache_evict",
            "sdm_version")
 
 
@@ -110,6 +111,18 @@ def _declare(lib):
     lib.sdm_attend.restype = _I
     lib.sdm_attend.argtypes = [cache, _VP, _I64, _VP, _VP, _I, _I, _I, _I, _F, _I, _I, _VP, _I, _VP, _VP, _VP, _SZ,
                                _VP, _VP]
+    lib.sdm_qk_rotate.restype = _I
+    lib.sdm_qk_rotate.argtypes = [cache, _VP, _I64, _I, _VP, _I64, _VP, _I64, _I, _I, _VP, _VP, _F, _VP, _I, _I, _VP,
+                                  _VP, _VP, _VP, _I, _I, _VP, _I64, _VP, _I64, _VP, _VP]
+    lib.sdm_token_logprobs.restype = _I
+    lib.sdm_token_logprobs.argtypes = [_VP, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _F, _I, _VP, _VP, _VP, _VP, _VP,
+                                       _VP, _VP]
+    lib.sdm_attend_weight.restype = _I
+    lib.sdm_attend_weight.argtypes = [cache, _VP, _I64, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _F, _I, _I, _VP,
+                                      _VP, _I64, _VP, _SZ, _VP, _VP]
+    lib.sdm_cache_evict.restype = _I
+    lib.sdm_cache_evict.argtypes = [cache, _VP, _VP, _I64, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _SZ,
+                                    _VP, _VP]
     lib.sdm_verify_tree.restype = _I
     lib.sdm_verify_tree.argtypes = [_VP, _I, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _SZ, _VP, _VP]
 
@@ -743,4 +756,185 @@ def attend(cache, q, cu_seqlens, ctx_len, max_window, scale=None, window=0, sink
                           ws.numel(), _need_status(dev_status, dev), _stream_of(cache))
     if st:
         _check(st, "sdm_attend")
+    return out
+
+
+def _need_f32(what, x, n, device):
+    if x.dtype is not torch.float32 or x.get_device() != device or x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor of {n} entries on the cache's device")
+    return x.data_ptr()
+
+
+def qk_rotate(q, k, cu_seqlens, ctx_len, freq, v=None, cache=None, start=None, row_pos=None, q_weight=None,
+              k_weight=None, eps=1e-6, interleaved=False, out=None, dev_status=None):
+    """Queries q [rows, H, head dim] and keys k [rows, kv heads, head dim]
+    normalised per head (where a weight [head dim] fp32 is given) and rotated:
+    pair j of a row at position start[i] + p (start None: ctx_len) by position *
+    freq[j] (fp64, rot_dim / 2 of them).  With a cache the keys and the values v
+    go into it, without one the keys are returned.  out["q"] (and out["k"]) may
+    be the inputs."""
+    if (cache is None) != (v is None):
+        raise ValueError("values go with a cache, and only with one")
+    H, G, D = q.shape[1], k.shape[1], q.shape[2]
+    if cache is not None:
+        dev, stream = cache.device, _stream_of(cache)
+        R = cache.requests
+        if G != cache.kv_heads or D != cache.head_dim:
+            raise ValueError("k's heads and the head dim must be the cache's")
+    else:
+        dev = q.get_device()
+        if dev < 0:
+            raise ValueError("q must be a CUDA tensor")
+        if _this_device() != dev:
+            raise ValueError(f"q is on device {dev}, not on the current one")
+        stream, R = _raw_stream(dev), cu_seqlens.numel() - 1
+    rows, qs = _need_rows("q", q, H, D, dev)
+    k_rows, ks = _need_rows("k", k, G, D, dev)
+    v_rows, vs = (rows, 0) if v is None else _need_rows("v", v, G, D, dev)
+    if k_rows != rows or v_rows != rows:
+        raise ValueError("q, k and v must have the same rows")
+    if freq is not None and (freq.dtype is not torch.float64 or freq.get_device() != dev or not freq.is_contiguous()):
+        raise ValueError("freq must be a contiguous float64 tensor on the cache's device")
+    rot = 0 if freq is None else 2 * freq.numel()
+    if out is None:
+        out = dict(q=torch.empty((rows, H, D), dtype=torch.bfloat16, device=q.device))
+        if cache is None:
+            out["k"] = torch.empty((rows, G, D), dtype=torch.bfloat16, device=q.device)
+    o_rows, qos = _need_rows("out['q']", out["q"], H, D, dev)
+    ko, kos = None, 0
+    if cache is None:
+        n, kos = _need_rows("out['k']", out["k"], G, D, dev)
+        o_rows, ko = min(o_rows, n), out["k"].data_ptr()
+    if o_rows < rows:
+        raise ValueError("the outputs must have the inputs' rows")
+    dev_status = _new_status_in(out, q.device) if dev_status is None else dev_status
+    st = lib().sdm_qk_rotate(None if cache is None else cache.ref, q.data_ptr(), qs, H, k.data_ptr(), ks,
+                             None if v is None else v.data_ptr(), vs, G, D,
+                             None if q_weight is None else _need_f32("q_weight", q_weight, D, dev),
+                             None if k_weight is None else _need_f32("k_weight", k_weight, D, dev), eps,
+                             freq.data_ptr() if rot else None, rot, interleaved,
+                             _need_i32("cu_seqlens", cu_seqlens, R + 1, dev),
+                             None if ctx_len is None else _need_i32("ctx_len", ctx_len, R, dev),
+                             None if start is None else _need_i32("start", start, R, dev),
+                             None if row_pos is None else _need_i32("row_pos", row_pos, rows, dev), R, rows,
+                             out["q"].data_ptr(), qos, ko, kos, _need_status(dev_status, dev), stream)
+    if st:
+        _check(st, "sdm_qk_rotate")
+    return out
+
+
+def token_logprobs(target, cu_seqlens, tok, n=None, path=None, temperature=1.0, top=0, out=None, dev_status=None):
+    """Log probability, rank and entropy [R, W] of the tokens tok [R, W] (their
+    first n[i]; None: the whole windows) at target rows cu_seqlens[i] + p, or
+    cu_seqlens[i] + path[i, p], and the `top` most probable tokens of each."""
+    _need_cuda(target)
+    dev, (R, W), V = target.get_device(), tok.shape, target.shape[-1]
+    if _this_device() != dev:
+        raise ValueError(f"the target is on device {dev}, not on the current one")
+    if not target.is_contiguous():
+        raise ValueError("target must be contiguous")
+    device = target.device
+    if out is None:   # positions that hold no token keep these
+        out = dict(logp=torch.zeros((R, W), dtype=torch.float32, device=device),
+                   entropy=torch.zeros((R, W), dtype=torch.float32, device=device),
+                   rank=torch.full((R, W), -1, dtype=torch.int32, device=device))
+        if top:
+            out.update(top_tok=torch.full((R, W, top), -1, dtype=torch.int32, device=device),
+                       top_logp=torch.zeros((R, W, top), dtype=torch.float32, device=device))
+    shape, best = (R, W), (R, W, top)
+    entropy, rank = out.get("entropy"), out.get("rank")
+    dev_status = _new_status_in(out, device) if dev_status is None else dev_status
+    st = lib().sdm_token_logprobs(
+        target.data_ptr(), _dt(target), target.numel() // V, V, _need_i32("cu_seqlens", cu_seqlens, R + 1, dev),
+        None if path is None else _need_i32("path", path, R * W, dev), _need_i32("tok", tok, R * W, dev),
+        None if n is None else _need_i32("n", n, R, dev), R, W, float(temperature), top,
+        _need_out("logp", out["logp"], shape, torch.float32, dev),
+        None if entropy is None else _need_out("entropy", entropy, shape, torch.float32, dev),
+        None if rank is None else _need_out("rank", rank, shape, _I32, dev),
+        _need_out("top_tok", out["top_tok"], best, _I32, dev) if top else None,
+        _need_out("top_logp", out["top_logp"], best, torch.float32, dev) if top else None,
+        _need_status(dev_status, dev), _raw_stream(dev))
+    if st:
+        _check(st, "sdm_token_logprobs")
+    return out
+
+
+def attend_weight_workspace(cache, max_count, H):
+    return workspace(OP_ATTEND_WEIGHT, cache.requests, max_count, H, cache.head_dim, 0, cache.kv_heads,
+                     device=cache.k.device)
+
+
+def attend_weight(cache, q, lse, cu_seqlens, ctx_len, max_count, mass=None, count=None, path=None, scale=None, window=0,
+                  sinks=0, out=None, ws=None, dev_status=None):
+    """The attention weight each cached token got from the committed rows (the
+    first count[i] of a window, or of the path's), on top of mass [R, kv heads,
+    tokens] fp32 (None: zeros): out["mass"], which may be mass.  lse is
+    attend's."""
+    R, D, G, dev = cache.requests, cache.head_dim, cache.kv_heads, cache.device
+    H = q.shape[1]
+    rows, qs = _need_rows("q", q, H, D, dev)
+    if H % G:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    if out is None:
+        if mass is None:
+            raise ValueError("mass or out has to say how many tokens a row holds")
+        out = dict(mass=torch.zeros_like(mass))
+    shape = out["mass"].shape
+    if len(shape) != 3 or shape[0] != R or shape[1] != G:
+        raise ValueError(f"out['mass'] must be [{R}, {G}, tokens]")
+    mo = _need_out("out['mass']", out["mass"], shape, torch.float32, dev)
+    mi = None if mass is None else _need_out("mass", mass, shape, torch.float32, dev)
+    stride = 0
+    if path is not None:
+        if path.dim() != 2 or path.shape[0] != R or path.shape[1] < max_count:
+            raise ValueError("path must be [requests, at least max_count]")
+        stride = path.shape[1]
+        path = _need_i32("path", path, R * stride, dev)
+    ws = attend_weight_workspace(cache, max_count, H) if ws is None else ws
+    dev_status = _new_status_in(out, q.device) if dev_status is None else dev_status
+    st = lib().sdm_attend_weight(cache.ref, q.data_ptr(), qs, _need_out("lse", lse, (rows, H), torch.float32, dev),
+                                 _need_i32("cu_seqlens", cu_seqlens, R + 1, dev),
+                                 _need_i32("ctx_len", ctx_len, R, dev),
+                                 None if count is None else _need_i32("count", count, R, dev), path, stride, R, rows,
+                                 max_count, H, D ** -0.5 if scale is None else scale, window, sinks, mi, mo, shape[2],
+                                 _need_ws(ws, dev), ws.numel(), _need_status(dev_status, dev), _stream_of(cache))
+    if st:
+        _check(st, "sdm_attend_weight")
+    return out
+
+
+def cache_evict_workspace(cache, tokens, keep):
+    return workspace(OP_CACHE_EVICT, cache.requests, cache.kv_heads, 0, 0, tokens, 0, keep, device=cache.k.device)
+
+
+def cache_evict(cache, mass, pos, ctx_len, start, keep, count=None, sinks=0, recent=0, out=None, ws=None,
+                dev_status=None):
+    """Cuts every request's cache to `keep` tokens per kv head: positions below
+    `sinks`, the last `recent`, then the largest mass [R, kv heads, tokens]; pos
+    int32 of the same shape holds the positions of slots below ctx_len, the
+    count[i] new ones are at start[i], start[i] + 1, ....  out["mass"] and
+    out["pos"] may be the inputs; out["length"] is the next ctx_len, out["next"]
+    (if there) the next start."""
+    R, G, dev = cache.requests, cache.kv_heads, cache.device
+    shape = mass.shape
+    if len(shape) != 3 or shape[0] != R or shape[1] != G:
+        raise ValueError(f"mass must be [{R}, {G}, tokens]")
+    device = mass.device
+    if out is None:
+        out = dict(mass=mass, pos=pos, length=torch.empty((R,), dtype=torch.int32, device=device),
+                   next=torch.empty((R,), dtype=torch.int32, device=device))
+    after = out.get("next")
+    ws = cache_evict_workspace(cache, shape[2], keep) if ws is None else ws
+    dev_status = _new_status_in(out, device) if dev_status is None else dev_status
+    st = lib().sdm_cache_evict(cache.ref, _need_out("mass", mass, shape, torch.float32, dev),
+                               _need_out("pos", pos, shape, _I32, dev), shape[2], _need_i32("ctx_len", ctx_len, R, dev),
+                               None if count is None else _need_i32("count", count, R, dev),
+                               None if start is None else _need_i32("start", start, R, dev), R, keep, sinks, recent,
+                               _need_out("out['mass']", out["mass"], shape, torch.float32, dev),
+                               _need_out("out['pos']", out["pos"], shape, _I32, dev),
+                               _need_i32("length", out["length"], R, dev),
+                               None if after is None else _need_i32("next", after, R, dev),
+                               _need_ws(ws, dev), ws.numel(), _need_status(dev_status, dev), _stream_of(cache))
+    if st:
+        _check(st, "sdm_cache_evict")
     return out

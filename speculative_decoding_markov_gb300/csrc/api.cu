@@ -274,6 +274,8 @@ size_t sdm_workspace_size(int op, int R, int B, int V, int r, int P, int k, int 
         case SDM_OP_TV_LABEL: return ws_tv_label(R, B, V, P);
         case SDM_OP_DRAFT_CHAIN_RNN: return ws_chain_rnn(R, B, V, r);
         case SDM_OP_ATTEND: return attend_workspace(B, V, r, k);
+        case SDM_OP_ATTEND_WEIGHT: return weigh_workspace(B, V, k);
+        case SDM_OP_CACHE_EVICT: return evict_workspace(R, B, P, N);
         case SDM_OP_VERIFY_TREE:
             return align256(static_cast<size_t>(R) * (N + 1) * 8 * std::max(n_chunks_of(V, 0), n_chunks_of(V, 1)));
         default: return 0;
@@ -1112,6 +1114,42 @@ sdm_status sdm_observe(const float* conf, const int32_t* cu_seqlens, const int32
     SDM_CHECK_CUDA(launch_observe(conf, cu_seqlens, ceiling, cls, R, gamma, n_class, n_bins, hist, reached, hits,
                                   bin_n, bin_hit, bin_conf, ece, dev_status, static_cast<cudaStream_t>(stream)));
     return SDM_OK;
+}
+
+sdm_status sdm_token_logprobs(const void* target, sdm_dtype dtT, int row_capacity, int V, const int32_t* cu_seqlens,
+                              const int32_t* path, const int32_t* tok, const int32_t* n, int R, int W,
+                              float temperature, int top, float* logp, float* entropy, int32_t* rank,
+                              int32_t* top_tok, float* top_logp, int32_t* dev_status, void* stream) {
+    if (!cu_seqlens || !tok || !logp || R <= 0 || W <= 0 || row_capacity < 0 || V <= 0) return SDM_ERR_INVALID_ARG;
+    if (dtT != SDM_BF16 && dtT != SDM_FP32) return SDM_ERR_INVALID_ARG;
+    if (top < 0 || top > V || (top > 0 && (!top_tok || !top_logp))) return SDM_ERR_INVALID_ARG;
+    const double scale = 1.4426950408889634 / static_cast<double>(temperature);
+    if (!(temperature > 0.f) || !(scale >= 1e-30 && scale <= 1e30)) return SDM_ERR_INVALID_ARG;
+    if (row_capacity > 0 && !target) return SDM_ERR_INVALID_ARG;
+    if (V % 8 != 0 || !aligned16(target) || top > 32 || static_cast<long long>(R) * W > (1ll << 27))
+        return SDM_ERR_UNSUPPORTED;
+    if (row_capacity == 0) return SDM_OK;
+    LogprobParams p = {};
+    p.target = target;
+    p.fp32 = dtT == SDM_FP32;
+    p.rows = row_capacity;
+    p.V = V;
+    p.inv_t = 1.0f / temperature;
+    p.scale = static_cast<float>(scale);
+    p.cu = cu_seqlens;
+    p.path = path;
+    p.tok = tok;
+    p.n = n;
+    p.R = R;
+    p.W = W;
+    p.top = top;
+    p.logp = logp;
+    p.entropy = entropy;
+    p.rank = rank;
+    p.top_tok = top_tok;
+    p.top_logp = top_logp;
+    p.dev_status = dev_status;
+    return launch_logprobs(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
 
 }  // extern "C"

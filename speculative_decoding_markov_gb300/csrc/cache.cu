@@ -15,24 +15,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCommitThreads = 512;     // 32 trees of 65 slots, written and committed: 8.4 us (256: 9.2, 1024: 8.5)
 
-// The windows are looked at apart from the rows, by one block more than the
-// rows have (a window that counts as empty need not have a row in use): it
-// flags what is wrong with them and returns whether one of them is unsound, in
-// which case the rows' own search in cu_seqlens proves nothing and the block
-// takes every window's rows itself.  0.4 us of the write and read of 64 windows
-// (6.2 us in a graph).
-__device__ __forceinline__ bool check_windows(const int32_t* cu, const int32_t* ctx, int R, int rows,
-                                              long long tokens, int32_t* dev_status) {
-    int bad = 0, unsound = 0;
-    for (int i = threadIdx.x; i < R; i += kThreads) {
-        const Window w = window_of(cu, ctx, i, rows, 0x7fffffff, tokens);
-        bad |= w.bad;
-        unsound |= w.n == 0 && (w.bad & SDM_DEV_BAD_WINDOW);
-    }
-    if (bad) set_status(dev_status, bad);
-    return __syncthreads_or(unsound);
-}
-
 // One warp per packed row, its loads in flight before the row's slot is
 // known.  D / 8 lanes hold one (K or V, head) vector of D elements, 16 bytes
 // each, so the maximum of a vector is a shuffle reduction over those lanes.
@@ -90,34 +72,10 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
                     if (vec < vectors) reinterpret_cast<uint4*>((is_v ? p.c.v : p.c.k) + r * D * 2)[part] = x[b];
                 } else {
                     const uint32_t u[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
-                    // the largest finite magnitude, on the bf16 bits
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t lo = u[j] & 0x7fffu, hi = (u[j] >> 16) & 0x7fffu;
-                        if (lo < 0x7f80u) top = max(top, lo);
-                        if (hi < 0x7f80u) top = max(top, hi);
-                    }
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // max |x| = 1.f 2^(E - 127) <= 448 2^e = 1.75 2^(8 + e)
-                    int e = static_cast<int>(top >> 7) - 135 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-                    e = min(max(e, kExpLo), kExpHi);
-                    const float inv = pow2f(-e);
-                    uint32_t code[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float f[4];
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const float y = bf16_bits_to_float((u[2 * j + (t >> 1)] >> (16 * (t & 1))) & 0xffffu);
-                            f[t] = __fmaf_rn(y, inv, y * 0.0f);   // the scaling is exact; an infinity becomes NaN
-                        }
-                        code[j] = f32x2_to_e4m3x2(f[0], f[1]) |
-                                  (static_cast<uint32_t>(f32x2_to_e4m3x2(f[2], f[3])) << 16);
-                    }
+                    const int e = e4m3_exponent<kLanes>(u);
+                    const uint2 code = e4m3_codes(u, e);
                     if (vec < vectors) {
-                        reinterpret_cast<uint2*>((is_v ? p.c.v : p.c.k) + r * D)[part] = make_uint2(code[0], code[1]);
+                        reinterpret_cast<uint2*>((is_v ? p.c.v : p.c.k) + r * D)[part] = code;
                         if (part == 0) (is_v ? p.c.v_exp : p.c.k_exp)[r] = static_cast<uint8_t>(e + 127);
                     }
                 }
@@ -128,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteP
     if (static_cast<int>(blockIdx.x) < blocks) {
         const int n_rows = min(p.rows, __ldg(p.cu + p.R));
         for (int row = blockIdx.x * kWarps + warp; row < n_rows; row += blocks * kWarps) write_row(row, -1);
-    } else if (check_windows(p.cu, p.ctx, p.R, p.rows, tokens, p.dev_status)) {
+    } else if (check_windows<kThreads>(p.cu, p.ctx, p.R, p.rows, tokens, p.dev_status)) {
         for (int i = 0; i < p.R; ++i) {
             const Window w = window_of(p.cu, p.ctx, i, p.rows, 0x7fffffff, tokens);
             for (int k = warp; k < w.n; k += kWarps) write_row(w.row0 + k, i);
@@ -204,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
     if (static_cast<int>(blockIdx.x) < blocks) {
         const int n_rows = min(p.rows, __ldg(p.cu + p.R));
         for (int row = blockIdx.x * kWarps + warp; row < n_rows; row += blocks * kWarps) read_row(row, -1);
-    } else if (check_windows(p.cu, p.first, p.R, p.rows, 0x7fffffffll, p.dev_status)) {
+    } else if (check_windows<kThreads>(p.cu, p.first, p.R, p.rows, 0x7fffffffll, p.dev_status)) {
         for (int i = 0; i < p.R; ++i) {
             const Window w = window_of(p.cu, p.first, i, p.rows, 0x7fffffff, 0x7fffffffll);
             for (int k = warp; k < w.n; k += kWarps) read_row(w.row0 + k, i);

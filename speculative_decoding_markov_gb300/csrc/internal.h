@@ -28,6 +28,27 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// The same with `cluster` neighbouring blocks of the grid's x as a thread-block cluster.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem,
+                                  cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // ---------------------------------------------------------------------------
 // Markov GEMM (tcgen05): one CTA = one 128-row M tile x a round-robin set of
 // 128-wide vocab tiles; K = r (<= 256, multiple of 64).
@@ -527,5 +548,93 @@ struct AttendParams {
 };
 size_t attend_workspace(int max_window, int H, int D, int kv_heads);
 cudaError_t launch_attend(const AttendParams& p, void* ws, cudaStream_t s);
+
+// Norm and rotation of queries and keys (rotate.cu)
+struct RotateParams {
+    CacheView c;             // if cached
+    int cached;
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;       // if cached
+    int64_t q_stride, k_stride, v_stride;   // elements
+    int H, G, parts;         // query heads, kv heads; warps a row (set at the launch)
+    const float* q_weight;   // [D] or NULL
+    const float* k_weight;
+    float eps;
+    const double* freq;      // [rot / 2] radians per token
+    int rot;
+    const int32_t* cu;
+    const int32_t* ctx;
+    const int32_t* start;    // or NULL
+    const int32_t* row_pos;  // or NULL
+    int R, rows;
+    uint16_t* q_out;
+    uint16_t* k_out;         // unless cached
+    int64_t q_out_stride, k_out_stride;
+    int32_t* dev_status;
+};
+cudaError_t launch_rotate(const RotateParams& p, int D, bool interleaved, cudaStream_t s);
+
+// Log probabilities of committed tokens (logprobs.cu)
+struct LogprobParams {
+    const void* target;      // [rows, V]
+    int fp32, rows, V;
+    float inv_t, scale;      // 1 / T, log2(e) / T
+    const int32_t* cu;
+    const int32_t* path;     // [R, W] or NULL
+    const int32_t* tok;      // [R, W]
+    const int32_t* n;        // [R] or NULL
+    int R, W, top;
+    float* logp;             // [R, W]
+    float* entropy;          // or NULL
+    int32_t* rank;           // or NULL
+    int32_t* top_tok;        // [R, W, top]
+    float* top_logp;
+    int32_t* dev_status;
+};
+cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s);
+
+// The attention weight that cached tokens got (weigh.cu)
+struct WeighParams {
+    CacheView c;
+    const uint16_t* q;
+    int64_t q_stride;        // elements
+    const float* lse;        // [rows, H]
+    const int32_t* cu;
+    const int32_t* ctx;
+    const int32_t* count;    // [R] or NULL
+    const int32_t* path;     // [R, path_stride] or NULL
+    int path_stride;
+    int R, rows, max_count, H, group;
+    float scale;
+    int window, sinks;
+    const float* mass;       // [R, heads, stride] or NULL
+    float* mass_out;
+    int64_t stride;
+    int32_t* dev_status;
+};
+size_t weigh_workspace(int max_count, int H, int kv_heads);
+cudaError_t launch_weigh(const WeighParams& p, void* ws, cudaStream_t s);
+
+// A cache cut to its tokens of largest weight (evict.cu)
+struct EvictParams {
+    CacheView c;
+    const float* mass;       // [R, heads, stride]
+    const int32_t* pos;      // the same
+    int64_t stride;
+    const int32_t* ctx;
+    const int32_t* count;    // or NULL
+    const int32_t* start;    // or NULL
+    int R, keep, sinks, recent;
+    float* mass_out;
+    int32_t* pos_out;
+    int32_t* length;
+    int32_t* next;           // or NULL
+    int32_t* moves;          // [R, heads, most] sources
+    int64_t most;
+    int32_t* dev_status;
+};
+size_t evict_workspace(int R, int kv_heads, int64_t stride, int keep);
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 
 }  // namespace sdm

@@ -1,0 +1,446 @@
+// logprobs.cu - log probabilities of committed tokens, the distributions'
+// entropy, the tokens' ranks and the most probable tokens.
+//
+// Mathematics, per row z of V logits, c = log2(e) / T and a reference m near
+// the row's maximum:  d_v = c z_v - m,  s = sum 2^d,  t = sum d 2^d
+//     log p(y) = ln 2 (d_y - log2 s)        H = ln 2 (log2 s - t / s)
+// (d <= a few, so H has no cancellation), in one pass over the row: every
+// thread keeps (m, s, t) of its own elements and moves m only when an element
+// exceeds it by more than kLazy.  The listed tokens come from the same pass:
+// a thread also keeps its largest element, and the top-th largest of (four a
+// warp of) those is a bound that at least `top` elements reach; only the
+// threads whose largest reaches it look at their elements again.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "device.cuh"
+#include "internal.h"
+
+namespace sdm {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTopMost = 32;
+constexpr int kCand = 2048;           // listed elements of a CTA
+constexpr int kMaxCluster = 8;
+constexpr float kLazy = 8.0f;         // in log2 units
+constexpr float kLn2 = 0.6931471805599453f;
+// A reference's rounding shifts every d of a row alike, by up to 2^-24 of it: no
+// matter for d itself, but 2^d has to stay finite.  Rows whose largest c z is
+// beyond this are summed with care.
+constexpr float kHuge = 1.0e8f;
+constexpr float kFar = 1.0e30f;       // a logit beside which log s does not count, and c z may overflow
+constexpr float kMaxRef = 3.0e38f;    // references stay finite
+
+struct Part {                          // one CTA's share of a row
+    float m, s, t, top;                // reference (scaled), sums, largest logit
+    int ahead;                         // elements ahead of the given token
+    int n;                             // entries of best
+    unsigned long long best[kTopMost];
+};
+
+struct Shared {
+    float m[kWarps], s[kWarps], t[kWarps], top[kWarps];
+    int ahead[kWarps];
+    uint32_t maxima[kWarps * 4];
+    uint32_t bound;
+    int count, strict;
+    unsigned long long round[kWarps];
+    double sd[kWarps], td[kWarps];
+    Part part;
+    unsigned long long cand[kCand];
+};
+
+__device__ __forceinline__ float logit8(const uint4& lo, const uint4& hi, int j, bool fp32) {
+    const uint32_t* a = reinterpret_cast<const uint32_t*>(&lo);
+    const uint32_t* b = reinterpret_cast<const uint32_t*>(&hi);
+    if (fp32) return __uint_as_float(j < 4 ? a[j] : b[j - 4]);
+    return bf16_bits_to_float((a[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+}
+
+// Eight logits of a row, from element 8 vec on.
+template <bool FP32>
+struct Vec {
+    uint4 lo, hi;
+    __device__ __forceinline__ void load(const uint8_t* row, int vec) {
+        const uint4* src = reinterpret_cast<const uint4*>(row) + (FP32 ? 2 * static_cast<size_t>(vec) : vec);
+        lo = __ldg(src);
+        if (FP32) hi = __ldg(src + 1);
+    }
+    __device__ __forceinline__ float at(int j) const { return logit8(lo, hi, j, FP32); }
+};
+
+// (s, t) of a reference m, for the reference `to` >= m.  A factor of zero ends
+// what may be infinite beside it.
+__device__ __forceinline__ void move_to(float& m, float& s, float& t, float to) {
+    const float k = m - to, a = fast_exp2(k);
+    t = a == 0.f ? 0.f : a * (t + k * s);
+    s = a != 0.f ? s * a : s != s ? s : 0.f;
+    m = to;
+}
+
+__device__ __forceinline__ void join(float& m, float& s, float& t, float m2, float s2, float t2) {
+    const float to = fmaxf(m, m2);
+    move_to(m, s, t, to);
+    move_to(m2, s2, t2, to);
+    s += s2;
+    t += t2;
+}
+
+// The largest key below `below` of elements [v0, v1) (in vectors), by the whole CTA.
+template <bool FP32>
+__device__ unsigned long long next_key(const uint8_t* row, int v0, int v1, unsigned long long below, Shared& sh) {
+    unsigned long long best = 0;
+    for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+        Vec<FP32> x;
+        x.load(row, v);
+        for (int j = 0; j < 8; ++j) {
+            const unsigned long long k = argmax_key(x.at(j), 8 * v + j);
+            if (k < below) best = umax64(best, k);
+        }
+    }
+    best = warp_max_u64(best);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh.round[threadIdx.x >> 5] = best;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) best = umax64(best, sh.round[w]);
+    return best;
+}
+
+// Lists the elements of the threads whose largest one reaches `bound` that
+// reach it themselves (`strict`: exceed it).
+template <bool FP32>
+__device__ __forceinline__ void list_candidates(const uint8_t* row, int v0, int v1, uint32_t mine, uint32_t bound,
+                                                bool strict, Shared& sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t from = strict ? bound + 1 : bound;
+    unsigned todo = __ballot_sync(0xffffffffu, mine >= from);
+    while (todo) {
+        const int l = __ffs(todo) - 1;
+        todo &= todo - 1;
+        for (int v = v0 + warp * 32 + l + lane * kThreads; v < v1; v += 32 * kThreads) {
+            Vec<FP32> x;
+            x.load(row, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float z = x.at(j);
+                if (ordered_bits(z) >= from) {
+                    const int at = atomicAdd(&sh.count, 1);
+                    if (at < kCand) sh.cand[at] = argmax_key(z, 8 * v + j);
+                }
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// The `top` largest keys of the CTA's elements, in order, into sh.part.best.
+template <bool FP32>
+__device__ void pick_top(const uint8_t* row, int v0, int v1, float largest, bool any, int top, Shared& sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n_out = min(top, 8 * (v1 - v0));
+    const uint32_t mine = any ? max(ordered_bits(largest), 1u) : 0u;
+    // four largest of the warp's maxima
+    uint32_t left = mine;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t w = __reduce_max_sync(0xffffffffu, left);
+        const unsigned who = __ballot_sync(0xffffffffu, left == w);
+        if (lane == __ffs(who) - 1) left = 0;
+        if (lane == 0) sh.maxima[warp * 4 + r] = w;
+    }
+    if (threadIdx.x == 0) {
+        sh.count = 0;
+        sh.bound = 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < kWarps * 4) {
+        const uint32_t x = sh.maxima[threadIdx.x];
+        int before = 0;
+        for (int k = 0; k < kWarps * 4; ++k) {
+            const uint32_t y = sh.maxima[k];
+            before += y > x || (y == x && k < static_cast<int>(threadIdx.x));
+        }
+        if (before == top - 1) sh.bound = x;
+    }
+    __syncthreads();
+    const uint32_t bound = sh.bound;
+    list_candidates<FP32>(row, v0, v1, mine, bound, false, sh);
+    int n = sh.count;
+    if (n > kCand) {
+        // more reach the bound than fit: those that exceed it, then its lowest ids
+        __syncthreads();
+        if (threadIdx.x == 0) sh.count = 0;
+        __syncthreads();
+        list_candidates<FP32>(row, v0, v1, mine, bound, true, sh);
+        n = sh.count;
+        if (n <= kCand - kThreads) {
+            for (int base = v0; base < v1 && n < n_out; base += kThreads) {
+                const int v = base + threadIdx.x;
+                Vec<FP32> x;
+                uint32_t hit = 0;
+                if (v < v1) {
+                    x.load(row, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) hit |= static_cast<uint32_t>(ordered_bits(x.at(j)) == bound) << j;
+                }
+                // their places, in the order of the ids
+                int incl = __popc(hit);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                __syncthreads();
+                if (lane == 31) sh.ahead[warp] = incl;
+                __syncthreads();
+                int at = n + incl - __popc(hit), all = 0;
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) at += sh.ahead[w];
+                    all += sh.ahead[w];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if ((hit >> j) & 1u) {
+                        if (at < n_out) sh.cand[at] = argmax_key(x.at(j), 8 * v + j);
+                        ++at;
+                    }
+                n = min(n + all, n_out);
+            }
+            __syncthreads();
+        } else {   // one pass a rank
+            unsigned long long below = ~0ull;
+            for (int r = 0; r < n_out; ++r) {
+                below = next_key<FP32>(row, v0, v1, below, sh);
+                if (threadIdx.x == 0) sh.part.best[r] = below;
+            }
+            if (threadIdx.x == 0) sh.part.n = n_out;
+            __syncthreads();
+            return;
+        }
+    }
+    for (int a = threadIdx.x; a < n; a += kThreads) {
+        const unsigned long long k = sh.cand[a];
+        int before = 0;
+        for (int b = 0; b < n; ++b) before += sh.cand[b] > k;
+        if (before < n_out) sh.part.best[before] = k;
+    }
+    if (threadIdx.x == 0) sh.part.n = n_out;
+    __syncthreads();
+}
+
+// A cluster of CTAs per row; each takes an equal share of it.
+template <bool FP32>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams p) {
+    __shared__ Shared sh;
+    __shared__ Part row_part;
+    pdl_wait();
+    pdl_trigger();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = cluster.num_blocks(), rank = cluster.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int item = blockIdx.x / C, i = item / p.W, pos = item % p.W;
+
+    // the row, or nothing
+    int n = p.n ? __ldg(p.n + i) : p.W;
+    int bad = 0;
+    if (n < 0 || n > p.W) {
+        n = min(max(n, 0), p.W);
+        bad = SDM_DEV_BAD_WINDOW;
+    }
+    const long long first = __ldg(p.cu + i), end = __ldg(p.cu + i + 1);
+    if (!p.n) n = static_cast<int>(min(static_cast<long long>(n), max(end - first, 0ll)));
+    bool live = pos < n;
+    long long r = 0;
+    if (live) {
+        const int off = p.path ? __ldg(p.path + item) : pos;
+        r = first + off;
+        if (first < 0 || off < 0 || r >= end) bad |= SDM_DEV_BAD_WINDOW, live = false;
+        else if (r >= p.rows) bad |= SDM_DEV_CAPACITY, live = false;
+    }
+    const int tok = live ? __ldg(p.tok + item) : 0;
+    const bool known = static_cast<unsigned>(tok) < static_cast<unsigned>(p.V);
+    if (!known) bad |= SDM_DEV_BAD_TOKEN;
+    if (bad && rank == 0 && threadIdx.x == 0) set_status(p.dev_status, bad);
+    if (!live) return;   // the whole cluster
+
+    const uint8_t* row = static_cast<const uint8_t*>(p.target) + static_cast<size_t>(r) * p.V * (FP32 ? 4 : 2);
+    const int vecs = p.V / 8;
+    const int v0 = static_cast<int>(static_cast<long long>(vecs) * rank / C);
+    const int v1 = static_cast<int>(static_cast<long long>(vecs) * (rank + 1) / C);
+    const float c = p.scale;
+    float said = 0.f;
+    if (known)
+        said = FP32 ? __ldg(reinterpret_cast<const float*>(row) + tok)
+                    : bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + tok));
+
+    float m = -kMaxRef, s = 0.f, t = 0.f, top = -INFINITY;
+    int ahead = 0;
+    bool any = false;
+#pragma unroll 4
+    for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+        Vec<FP32> x;
+        x.load(row, v);
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = x.at(j);
+        float vm = f[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) vm = fmaxf(vm, f[j]);
+        top = fmaxf(top, vm);
+        if (vm * c > m + kLazy) {
+            const float to = fminf(vm * c, kMaxRef);
+            move_to(m, s, t, to);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float d = fmaxf(fmaf(f[j], c, -m), -1000.f);   // -inf: 2^d is 0, and d 2^d
+            const float e = f[j] != f[j] ? f[j] : fast_exp2(d);
+            s += e;
+            t = fmaf(e, d, t);
+        }
+        const int id = 8 * v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ahead += f[j] > said || (f[j] == said && id + j < tok);
+        any = true;
+    }
+    const float mine = top;
+
+    // the CTA's sums, in the order of lanes and warps
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        const float t2 = __shfl_xor_sync(0xffffffffu, t, o);
+        join(m, s, t, m2, s2, t2);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+    }
+    if (lane == 0) {
+        sh.m[warp] = m;
+        sh.s[warp] = s;
+        sh.t[warp] = t;
+        sh.top[warp] = top;
+        sh.ahead[warp] = ahead;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        Part& q = sh.part;
+        q.m = sh.m[0], q.s = sh.s[0], q.t = sh.t[0], q.top = sh.top[0], q.ahead = sh.ahead[0], q.n = 0;
+        for (int w = 1; w < kWarps; ++w) {
+            join(q.m, q.s, q.t, sh.m[w], sh.s[w], sh.t[w]);
+            q.top = fmaxf(q.top, sh.top[w]);
+            q.ahead += sh.ahead[w];
+        }
+    }
+    __syncthreads();
+    if (p.top > 0 && v1 > v0) pick_top<FP32>(row, v0, v1, mine, any, p.top, sh);
+    if (C > 1) cluster.sync();
+
+    // joined by every CTA alike
+    if (threadIdx.x == 0) {
+        Part q = sh.part;
+        if (C > 1) {
+            const Part* a = cluster.map_shared_rank(&sh.part, 0);
+            q.m = a->m, q.s = a->s, q.t = a->t, q.top = a->top, q.ahead = a->ahead;
+            for (int k = 1; k < C; ++k) {
+                const Part* b = cluster.map_shared_rank(&sh.part, k);
+                join(q.m, q.s, q.t, b->m, b->s, b->t);
+                q.top = fmaxf(q.top, b->top);
+                q.ahead += b->ahead;
+            }
+        }
+        row_part.m = q.m, row_part.s = q.s, row_part.t = q.t, row_part.top = q.top, row_part.ahead = q.ahead;
+    }
+    __syncthreads();
+    const float M = row_part.top;
+    float S = row_part.s, T = row_part.t, ref = row_part.m;
+    // a row of logits whose products with c leave fp32: summed again in fp64,
+    // relative to its largest (the type's lowest value in every place is one)
+    const bool careful = fabsf(M) * c >= kHuge && fabsf(M) < INFINITY && S == S;
+    const double cd = static_cast<double>(p.inv_t);
+    if (careful) {
+        double sd = 0, td = 0;
+        for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+            Vec<FP32> x;
+            x.load(row, v);
+            for (int j = 0; j < 8; ++j) {
+                const double d = (static_cast<double>(x.at(j)) - M) * cd;
+                const double e = exp(d);
+                sd += e;
+                if (e > 0) td += e * d;
+            }
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            sd += __shfl_xor_sync(0xffffffffu, sd, o);
+            td += __shfl_xor_sync(0xffffffffu, td, o);
+        }
+        if (lane == 0) sh.sd[warp] = sd, sh.td[warp] = td;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int w = 1; w < kWarps; ++w) sh.sd[0] += sh.sd[w], sh.td[0] += sh.td[w];
+        if (C > 1) cluster.sync();
+        else __syncthreads();
+        sd = td = 0;
+        for (int k = 0; k < C; ++k) {
+            sd += C > 1 ? *cluster.map_shared_rank(&sh.sd[0], k) : sh.sd[0];
+            td += C > 1 ? *cluster.map_shared_rank(&sh.td[0], k) : sh.td[0];
+        }
+        S = static_cast<float>(sd);
+        T = static_cast<float>(td);
+    }
+    // log p of a logit of the row
+    auto logp = [&](float z) {
+        if (careful) return static_cast<float>((static_cast<double>(z) - M) * cd - log(static_cast<double>(S)));
+        if (fabsf(M) == INFINITY && S == S) return z - M;   // -inf beside +inf, else NaN
+        if (fabsf(z) * c >= kFar && S == S) return static_cast<float>((static_cast<double>(z) - M) * cd);
+        return kLn2 * (fmaf(z, c, -ref) - log2f(S));
+    };
+    if (rank == 0 && threadIdx.x == 0) {
+        p.logp[item] = known ? logp(said) : -INFINITY;
+        if (p.entropy) {
+            float h = careful ? logf(S) - T / S : kLn2 * (log2f(S) - T / S);
+            if (fabsf(M) == INFINITY) h = __int_as_float(0x7fffffff);
+            p.entropy[item] = h;
+        }
+        if (p.rank) p.rank[item] = known ? row_part.ahead : p.V;
+    }
+    if (p.top > 0) {
+        // a listed token's place: how many of all CTAs' come before it
+        const Part& own = sh.part;
+        for (int a = threadIdx.x; a < own.n; a += kThreads) {
+            const unsigned long long k = own.best[a];
+            int before = a;
+            for (int b = 0; b < C; ++b) {
+                if (b == rank) continue;
+                const Part* o = cluster.map_shared_rank(&sh.part, b);
+                for (int e = 0; e < o->n && o->best[e] > k; ++e) ++before;
+            }
+            if (before < p.top) {
+                const size_t at = static_cast<size_t>(item) * p.top + before;
+                const int id = static_cast<int>(key_token(k));
+                p.top_tok[at] = id;
+                const float z = FP32 ? __ldg(reinterpret_cast<const float*>(row) + id)
+                                     : bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + id));
+                p.top_logp[at] = logp(z);
+            }
+        }
+    }
+    if (C > 1) cluster.sync();   // nobody leaves while its share is read
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
+    const long long items = static_cast<long long>(p.R) * p.W;
+    // few rows: several SMs a row, as long as each has some thousand elements
+    int C = 1;
+    while (C < kMaxCluster && items * C * 2 <= 2LL * num_sms() && p.V / (2 * C) >= 4096) C *= 2;
+    return launch_cluster(p.fp32 ? logprobs_kernel<true> : logprobs_kernel<false>, dim3(static_cast<unsigned>(items * C)),
+                          dim3(kThreads), C, 0, s, p);
+}
+
+}  // namespace sdm
