@@ -1,11 +1,38 @@
 // weigh.cu - the attention weight that every cached token got from a call's
-// committed rows, added to what it had.
+// committed rows, added to what it had, on the tcgen05 tensor cores.
 //
 // Mathematics, for token j of a request and kv head g:
 //     out_j = (j < ctx ? in_j : 0) + sum over rows p and heads h of g with j
 //             visible of exp(scale q_ph . k_j - lse_ph)
 // with the log-sum-exp that the attention left.  No maximum is needed: every
 // term is a softmax weight, at most 1.
+//
+// Layout.  A product's 128 lanes are keys, its columns the query rows of one kv
+// head (heads side by side, token by token): S = K Q^T.  A thread then owns a
+// key, its sum over the columns never leaves its registers, a column's -lse is
+// a broadcast read, and no result depends on an order of arrival.
+//
+// Work.  A unit is 256 keys of one request and kv head, a tile of 128 for each
+// of two warpgroups, which share every tile of query rows.  Units laid end to
+// end are cut into shares of equal cost, one per CTA (one CTA per SM).  If all
+// rows of a head fit one tile (SMALL: decoding, verification), a cut never
+// splits a unit, and the rows stay in shared memory while the keys of their
+// head go by.  Else shares are cut between tiles of rows: the parts of a unit
+// leave their sums in the workspace, and weigh_join_kernel adds them in order.
+//
+// A CTA: a warp walks the share, hands units out and loads keys page by page by
+// TMA; one brings the query rows (by TMA, or gathered along a path); one their
+// -lse; one issues the products; eight turn S into weights.
+//
+// An e4m3 cache: if SMALL its codes are operands as they are.  A bf16 query
+// splits exactly into three e5m2 numbers (8 significant bits as 3 + 3 + 2,
+// under a power of two per row that puts its largest element below 2^15;
+// elements 2^24 smaller than that lose bits, at most 2^-31 of it), so S is
+// three products over the same codes, and the scales of row and key follow in
+// fp32.  Else, where a tile of keys meets many rows, its warpgroup turns the
+// codes into bf16 once.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 
 #include "paged.cuh"
@@ -13,9 +40,14 @@
 namespace sdm {
 namespace {
 
-constexpr int kTile = 128;            // keys of a tile, one a thread
-constexpr int kRows = 16;             // query rows staged together
+constexpr int kTile = 128;            // keys of a tile, query rows of a tile
+constexpr int kUnit = 2 * kTile;      // keys of a unit
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 384;
+constexpr int kTmemCols = 512;        // S of warpgroup w, buffer b at 256 w + 128 b
+constexpr int kRing = 4;              // units handed out ahead
+constexpr int kHeavy = 6, kBase = 2;  // costs: a unit with a product if SMALL (1 without); a unit beside its row tiles
+constexpr int kExpStages = 16;        // e4m3 exponents of tiles
 
 // A request's counted rows: window positions 0 .. n - 1 of its path (packed
 // rows row0 .. row0 + wide - 1 hold its window) at tokens ctx, ctx + 1, ....
@@ -52,80 +84,1048 @@ __device__ __forceinline__ long long row_of(const WeighParams& p, const Counted&
     return static_cast<unsigned>(off) < static_cast<unsigned>(w.wide) ? w.row0 + off : -1;
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kTile) weigh_kernel(const WeighParams p) {
-    __shared__ float q[kRows][D];
-    __shared__ float l2[kRows];
-    __shared__ int at[kRows];
-    pdl_wait();
-    pdl_trigger();
-    const int i = blockIdx.z, g = blockIdx.y, key0 = blockIdx.x * kTile;
-    const Counted w = counted_of(p, i);
-    if (w.bad && blockIdx.x == 0 && g == 0 && threadIdx.x == 0) set_status(p.dev_status, w.bad);
-    const int n = w.ctx + w.n;
-    if (key0 >= n) return;
-    const int j = key0 + threadIdx.x;
-    float k[D];
-    bool held = j < n;
-    if (held) {
-        int pg = page_of(p.c, i, j);
-        if (pg < 0) {
-            set_status(p.dev_status, SDM_DEV_BAD_PAGE);
-            pg = 0;
+// One unit, or the part of it that a CTA has.
+struct __align__(16) Blk {
+    int i, g, row0, wide;             // request, kv head, its window's packed rows
+    int ctx, n, M, k0;                // committed tokens, all tokens, rows, first key
+    int q0, q1, tiles, flags;         // tiles of rows q0 .. q1 - 1; tiles of keys (0: no more units)
+};
+enum { U_NEWQ = 1, U_FIRST = 2, U_LAST = 4, U_HAS = 8 };   // U_HAS: something is visible in it
+
+template <int D, bool E4M3, bool SMALL>
+struct Cfg {
+    static constexpr bool kPlanes = E4M3 && SMALL;
+    static constexpr int kKBytes = kTile * (kPlanes ? D : 2 * D);
+    static constexpr int kPlane = kTile * D;                   // one e5m2 plane of a tile of rows
+    static constexpr int kQBytes = kPlanes ? 3 * kPlane : kTile * 2 * D;
+    static constexpr int kQSlots = SMALL ? 2 : 3;
+    static constexpr int kLStages = SMALL ? 2 : 4;
+    static constexpr int kMiscBytes = kRing * sizeof(Blk) + kLStages * (kTile * 4 + 16) + (kPlanes ? 2 * kTile * 4 : 0) +
+                                      (kPlanes ? kExpStages * kTile : 0) + 704;
+    static constexpr int kFit = (232448 - kMiscBytes - kQSlots * kQBytes) / kKBytes;
+    static constexpr int kKSlots = kFit < (SMALL ? 12 : 8) ? kFit : (SMALL ? 12 : 8);
+    static_assert(kFit >= 4, "shared memory");
+    static constexpr int kQ = kKSlots * kKBytes;
+    static constexpr int kL = kQ + kQSlots * kQBytes;          // -lse log2 e of a tile's columns
+    static_assert(kL >= 16384 * 8, "the plan's costs of up to 16384 requests");
+    static constexpr int kCf = kL + kLStages * kTile * 4;      // planes: the columns' scales
+    static constexpr int kExps = kCf + (kPlanes ? 2 * kTile * 4 : 0);
+    static constexpr int kBlks = kExps + (kPlanes ? kExpStages * kTile : 0);
+    static constexpr int kBars = kBlks + kRing * static_cast<int>(sizeof(Blk));
+};
+
+template <int K, int Q, int L>
+struct Bars {
+    uint64_t k_full[K], k_empty[K], q_full[Q], q_empty[Q], l_full[L], l_empty[L];
+    uint64_t s_full[2][2], s_empty[2][2], blk_full[kRing], blk_empty[kRing], x_full[kExpStages], x_empty[kExpStages];
+    uint64_t drain;
+    uint32_t odd[L];                  // a column of the stage adds nothing
+    uint32_t tmem;
+};
+
+// What a share's ends leave for weigh_join_kernel.
+struct Part {
+    int rest;                         // the share starts a unit and does not finish it
+    int head;                         // its first part continues a unit: 0 no, 1 and finishes it, 2 and does not
+    int i, g, k0, n, ctx, pad;        // the started unit
+};
+struct Scratch {
+    Part* part;                       // [grid]
+    float* sum;                       // [grid][2][kUnit]: what continues a unit, what starts one
+};
+
+// ---------------------------------------------------------------------------
+// A request's units and their costs
+// ---------------------------------------------------------------------------
+struct Req {
+    Counted w;
+    int n, M, QT, units;              // tokens, rows, tiles of rows, units of a head
+    int us, ul;                       // units below us or from ul on have a product (SMALL)
+};
+
+__device__ __forceinline__ Req req_of(const WeighParams& p, int i) {
+    Req r;
+    r.w = counted_of(p, i);
+    r.n = r.w.ctx + r.w.n;
+    r.M = r.w.n * p.group;
+    r.QT = (r.M + p.sub - 1) / p.sub;
+    r.units = (r.n + kUnit - 1) / kUnit;
+    r.us = r.ul = r.units;
+    if (r.M == 0) {
+        r.us = 0;
+        r.ul = r.units;
+    } else if (p.window > 0) {
+        r.us = min(r.units, static_cast<int>((static_cast<long long>(p.sinks) + kUnit - 1) / kUnit));
+        r.ul = min(r.units, max(0, r.w.ctx + 1 - p.window) / kUnit);
+        r.ul = max(r.ul, r.us);
+    }
+    return r;
+}
+
+// Tiles of rows [q0, q1) that see some key of a unit.
+__device__ __forceinline__ void rows_of(const WeighParams& p, const Req& r, int u, int& q0, int& q1) {
+    const int k0 = u * kUnit;
+    q0 = k0 > r.w.ctx ? (k0 - r.w.ctx) * p.group / p.sub : 0;
+    q1 = r.QT;
+    if (p.window > 0 && k0 >= p.sinks) {
+        const long long last = min(k0 + kUnit, r.n) - 1;       // seen by the rows below last - ctx + window
+        const long long end = last - r.w.ctx + p.window;
+        if (end < r.w.n) q1 = end <= 0 ? 0 : static_cast<int>((end * p.group + p.sub - 1) / p.sub);
+    }
+    q1 = max(q0, q1);
+}
+
+template <bool SMALL>
+__device__ __forceinline__ int cost_of(const WeighParams& p, const Req& r, int u) {
+    if (SMALL) return u < r.us || u >= r.ul ? kHeavy : 1;
+    int q0, q1;
+    rows_of(p, r, u, q0, q1);
+    return kBase + q1 - q0;
+}
+
+// Cost of a head's units 0 .. u - 1 (SMALL).
+__device__ __forceinline__ long long before_unit(const Req& r, int u) {
+    return static_cast<long long>(min(u, r.us) + max(0, u - r.ul)) * kHeavy + min(max(u - r.us, 0), r.ul - r.us);
+}
+
+// Where a CTA's share starts: the unit in which its first cost unit lies.
+struct Start {
+    unsigned long long us, u0, u1;    // cost at which that unit begins, the share [u0, u1)
+    int i, g, u, pad;
+};
+
+// cost: shared memory for R entries.  By all warps.
+template <bool SMALL>
+__device__ __forceinline__ void plan(const WeighParams& p, unsigned long long* cost, unsigned long long* wsum,
+                                     Start* start) {
+    constexpr int kWarps = kThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (SMALL) {
+        for (int i = tid; i < p.R; i += kThreads) {
+            const Req r = req_of(p, i);
+            if (r.w.bad && blockIdx.x == 0) set_status(p.dev_status, r.w.bad);
+            cost[i] = before_unit(r, r.units) * p.c.heads;
         }
-        const size_t row = pool_row(p.c, pg, j) + (static_cast<size_t>(g) << p.c.page_shift);
-        const float s = E4M3 ? scale_of(__ldg(p.c.k_exp + row)) : 1.f;
+    } else {
+        for (int i = warp; i < p.R; i += kWarps) {
+            const Req r = req_of(p, i);
+            if (r.w.bad && blockIdx.x == 0 && lane == 0) set_status(p.dev_status, r.w.bad);
+            unsigned long long c = 0;
+            for (int u = lane; u < r.units; u += 32) c += cost_of<false>(p, r, u);
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if constexpr (E4M3)
-                k[d] = f16x2_to_f32x2(e4m3x2_to_f16x2(p.c.k[row * D + d])).x * s;
-            else
-                k[d] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p.c.k)[row * D + d]);
+            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            if (lane == 0) cost[i] = c * p.c.heads;
         }
     }
-    float sum = 0.f;
-    const int M = w.n * p.group;
-    const float c = p.scale * kLog2e;
-    for (int m0 = 0; m0 < M; m0 += kRows) {
-        __syncthreads();
-        for (int t = threadIdx.x; t < kRows * D; t += kTile) {
-            const int m = m0 + t / D, wp = m / p.group, h = g * p.group + m % p.group;
-            const long long row = m < M ? row_of(p, w, i, wp) : -1;
-            q[t / D][t % D] = row >= 0 ? bf16_bits_to_float(p.q[row * p.q_stride + static_cast<size_t>(h) * D + t % D]) : 0.f;
-            if (t % D == 0) {
-                float z = row >= 0 ? p.lse[row * p.H + h] : -INFINITY;
-                at[t / D] = z == -INFINITY ? -1 : w.ctx + wp;      // nothing seen: weighs nothing
-                l2[t / D] = z * kLog2e;
-                if (m < M && row < 0 && blockIdx.x == 0 && g == 0) set_status(p.dev_status, SDM_DEV_BAD_WINDOW);
+    __syncthreads();
+    const int per = (p.R + kThreads - 1) / kThreads;
+    const int a = min(p.R, tid * per), e = min(p.R, a + per);
+    unsigned long long mine = 0;
+    for (int i = a; i < e; ++i) mine += cost[i];
+    unsigned long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    unsigned long long base = incl - mine, total = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+        const unsigned long long v = wsum[k];
+        if (k < warp) base += v;
+        total += v;
+    }
+    const unsigned long long each = total / gridDim.x, more = total % gridDim.x;
+    const unsigned long long u0 = each * blockIdx.x + min(static_cast<unsigned long long>(blockIdx.x), more);
+    const unsigned long long u1 = u0 + each + (blockIdx.x < more ? 1 : 0);
+    if (tid == 0) {
+        start->u0 = u0;
+        start->u1 = u1;
+    }
+    if (u0 < u1 && base <= u0 && u0 < base + mine) {
+        int i = a;
+        for (; i < e - 1 && u0 >= base + cost[i]; ++i) base += cost[i];
+        start->i = i;
+        start->us = base;
+    }
+    __syncthreads();
+    if (warp == 0 && u0 < u1) {
+        const int i = start->i;
+        const Req r = req_of(p, i);
+        const unsigned long long c = cost[i] / p.c.heads;      // of a head; not 0, for the share's start lies in it
+        unsigned long long into = u0 - start->us;
+        const int g = static_cast<int>(into / c);
+        unsigned long long us = start->us + g * c;
+        into -= g * c;
+        int u = 0;
+        if (SMALL) {
+            const unsigned long long first = static_cast<unsigned long long>(r.us) * kHeavy;
+            const unsigned long long mid = first + (r.ul - r.us);
+            if (into < first) u = static_cast<int>(into / kHeavy);
+            else if (into < mid) u = r.us + static_cast<int>(into - first);
+            else u = r.ul + static_cast<int>((into - mid) / kHeavy);
+            us += before_unit(r, u);
+        } else {
+            for (int u0_ = 0; u0_ < r.units; u0_ += 32) {
+                const unsigned long long one = u0_ + lane < r.units ? cost_of<false>(p, r, u0_ + lane) : 0;
+                unsigned long long sum = one;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned long long v = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += v;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, sum > into);
+                if (hit) {
+                    const int at = __ffs(hit) - 1;
+                    u = u0_ + at;
+                    us += __shfl_sync(0xffffffffu, sum - one, at);
+                    break;
+                }
+                const unsigned long long all = __shfl_sync(0xffffffffu, sum, 31);
+                into -= all;
+                us += all;
             }
         }
-        __syncthreads();
-        if (!held) continue;
-        for (int r = 0; r < min(kRows, M - m0); ++r) {
-            const int t = at[r];
-            if (j > t || (p.window > 0 && t - j >= p.window && j >= p.sinks)) continue;
-            float s = 0.f;
-#pragma unroll
-            for (int d = 0; d < D; ++d) s = fmaf(q[r][d], k[d], s);
-            sum += fast_exp2(fmaf(s, c, -l2[r]));
+        __syncwarp();
+        if (lane == 0) {
+            start->g = g;
+            start->u = u;
+            start->us = us;
         }
     }
-    if (held) {
-        const size_t o = (static_cast<size_t>(i) * p.c.heads + g) * p.stride + j;
-        p.mass_out[o] = (j < w.ctx && p.mass ? p.mass[o] : 0.f) + sum;
+    fence_proxy_async_smem();   // `cost` lies where TMA is about to write
+    __syncthreads();
+}
+
+__device__ __forceinline__ bool wait_or_fail(const WeighParams& p, uint64_t* bar, uint32_t parity) {
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1)) return true;   // one answer a warp
+    const uint64_t t0 = globaltimer();
+#pragma unroll 1
+    do {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    } while (__all_sync(0xffffffffu, globaltimer() - t0 < kWaitLimitNs));
+    set_status(p.dev_status, SDM_DEV_TIMEOUT);
+    return false;
+}
+
+// A place in a ring and the parity of the phase it is in.
+template <int N>
+struct Ring {
+    int at = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == N) {
+            at = 0;
+            ++turn;
+        }
     }
+    __device__ __forceinline__ uint32_t full() const { return turn & 1; }           // for the reader
+    __device__ __forceinline__ uint32_t empty() const { return (turn & 1) ^ 1; }    // for the writer: passes at first
+};
+
+// N products along the rows' bytes, 32 bytes a step, the lane elect.sync picks
+// issuing.
+template <bool F8>
+__device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    if constexpr (F8)
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(add)
+            : "memory");
+}
+
+// kind::f8f6f4: e4m3 A (0 at bit 7), e5m2 B (1 at bit 10), fp32 accumulator
+__device__ __forceinline__ uint32_t idesc_f8(int M, int N) {
+    return (1u << 4) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Descriptor of 64-byte rows, 64-byte swizzle (mode 4).
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(512 >> 4) << 32) |
+           (1ull << 46) | (4ull << 61);
+}
+
+__device__ __forceinline__ uint32_t f32x2_to_e5m2x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 e5m2x2_to_f32x2(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+    return f16x2_to_f32x2(r);
+}
+
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+template <int D, bool E4M3, bool SMALL>
+__global__ void __launch_bounds__(kThreads, 1)
+    weigh_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
+                 const __grid_constant__ WeighParams p, const __grid_constant__ Scratch ws) {
+    using C = Cfg<D, E4M3, SMALL>;
+    constexpr bool kPlanes = C::kPlanes;
+    using B = Bars<C::kKSlots, C::kQSlots, C::kLStages>;
+    static_assert(C::kBars + sizeof(B) <= 232448, "shared memory");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    B& bar = *reinterpret_cast<B*>(smem + C::kBars);
+    Blk* blks = reinterpret_cast<Blk*>(smem + C::kBlks);
+    float* l2 = reinterpret_cast<float*>(smem + C::kL);
+    float* cf = reinterpret_cast<float*>(smem + C::kCf);
+    Start* start = reinterpret_cast<Start*>(smem + C::kL);     // only until the roles begin
+    unsigned long long* wsum = reinterpret_cast<unsigned long long*>(smem + C::kL + 64);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == 8) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmK);
+            if (!SMALL) tma_prefetch_desc(&tmQ);
+        }
+    } else if (warp == 9) {
+        tmem_alloc(&bar.tmem, kTmemCols);
+        tmem_relinquish();
+    } else if (warp == 10) {
+        for (int k = lane; k < C::kKSlots; k += 32) {
+            mbar_init(&bar.k_full[k], E4M3 && !SMALL ? 4 : 1);
+            mbar_init(&bar.k_empty[k], 1);
+        }
+        if (lane < C::kQSlots) {
+            mbar_init(&bar.q_full[lane], 1);
+            mbar_init(&bar.q_empty[lane], SMALL ? 9 : 1);
+        }
+        if (lane < C::kLStages) {
+            mbar_init(&bar.l_full[lane], 1);
+            mbar_init(&bar.l_empty[lane], 8);
+        }
+        if (lane < 4) {
+            mbar_init(&bar.s_full[0][0] + lane, 1);
+            mbar_init(&bar.s_empty[0][0] + lane, 4);
+        }
+        if (lane < kRing) {
+            mbar_init(&bar.blk_full[lane], 1);
+            mbar_init(&bar.blk_empty[lane], 8 + (SMALL ? 2 : 3));
+        }
+        if (lane < kExpStages) {
+            mbar_init(&bar.x_full[lane], 1);
+            mbar_init(&bar.x_empty[lane], 4);
+        }
+        if (lane == 0) mbar_init(&bar.drain, 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    plan<SMALL>(p, reinterpret_cast<unsigned long long*>(smem), wsum, start);
+    const Start st = *start;          // read before the roles use its place
+    // rows of a tile that no query row fills are zeros, so that their columns are finite
+    for (int k = tid; k < C::kQSlots * C::kQBytes / 16; k += kThreads)
+        reinterpret_cast<uint4*>(smem + C::kQ)[k] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+
+    Ring<kRing> rd;
+    // waits for the next unit; false at the end (or with ok false)
+    auto take = [&](bool& ok, Blk& b) {
+        ok = wait_or_fail(p, &bar.blk_full[rd.at], rd.full());
+        if (!ok) return false;
+        const int4* src = reinterpret_cast<const int4*>(blks + rd.at);
+        int4* dst = reinterpret_cast<int4*>(&b);
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(Blk) / 16); ++k) dst[k] = src[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.blk_empty[rd.at]);
+        rd.step();
+        return b.tiles > 0;
+    };
+
+    if (warp == 8) {
+        // ------------------------------------------------------------------
+        // walker: the share's units, and their keys
+        // ------------------------------------------------------------------
+        bool ok = true;
+        unsigned long long us = st.us;
+        int i = st.i, g = st.g, u = st.u, have = -1, loaded_i = -1, loaded_g = -1;
+        Req r;
+        Ring<kRing> wr;
+        Ring<C::kKSlots> kr;
+        Ring<kExpStages> xr;
+        bool live = st.u0 < st.u1;
+        Part part = {};
+        while (ok) {
+            Blk b = {};
+            bool got = false;
+            while (live && us < st.u1) {
+                if (have != i) {
+                    if (i >= p.R) break;
+                    r = req_of(p, i);
+                    have = i;
+                }
+                if (u >= r.units) {
+                    u = 0;
+                    if (++g >= p.c.heads) {
+                        g = 0;
+                        ++i;
+                    }
+                    continue;
+                }
+                int q0 = 0, q1 = 1;
+                const int cost = cost_of<SMALL>(p, r, u);
+                b.flags = U_FIRST | U_LAST;
+                bool mine;
+                if (SMALL) {
+                    mine = us >= st.u0;
+                    if (cost == kHeavy) b.flags |= U_HAS;
+                } else {
+                    rows_of(p, r, u, q0, q1);
+                    const int all = q1 - q0;
+                    if (all == 0) {
+                        mine = us >= st.u0;
+                    } else {
+                        // tile k of the rows stands at cost us + kBase + k
+                        const unsigned long long at = us + kBase;
+                        const int t0 = st.u0 <= at ? 0 : static_cast<int>(min(st.u0 - at, static_cast<unsigned long long>(all)));
+                        const int t1 = st.u1 <= at ? 0 : static_cast<int>(min(st.u1 - at, static_cast<unsigned long long>(all)));
+                        mine = t1 > t0;
+                        b.flags = U_HAS | (t0 == 0 ? U_FIRST : 0) | (t1 == all ? U_LAST : 0);
+                        if (mine && t0 > 0) part.head = t1 == all ? 1 : 2;
+                        if (mine && t0 == 0 && t1 < all) {
+                            part.rest = 1;
+                            part.i = i, part.g = g, part.k0 = u * kUnit, part.n = r.n, part.ctx = r.w.ctx;
+                        }
+                        q1 = q0 + t1;
+                        q0 += t0;
+                    }
+                }
+                b.i = i, b.g = g, b.row0 = r.w.row0, b.wide = r.w.wide;
+                b.ctx = r.w.ctx, b.n = r.n, b.M = r.M, b.k0 = u * kUnit;
+                b.q0 = q0, b.q1 = q1;
+                b.tiles = r.n - b.k0 > kTile ? 2 : 1;
+                us += cost;
+                ++u;
+                if (mine) {
+                    got = true;
+                    break;
+                }
+            }
+            if (!got) b.tiles = 0;
+            if (got && (b.flags & U_HAS) && (loaded_i != b.i || loaded_g != b.g)) {
+                b.flags |= U_NEWQ;
+                loaded_i = b.i;
+                loaded_g = b.g;
+            }
+            ok = wait_or_fail(p, &bar.blk_empty[wr.at], wr.empty());
+            if (!ok) break;
+            if (lane == 0) {
+                blks[wr.at] = b;
+                mbar_arrive(&bar.blk_full[wr.at]);
+            }
+            wr.step();
+            if (!got) break;
+            if (!(b.flags & U_HAS) || (E4M3 && !SMALL)) continue;
+            // its keys, a lane per page
+            const int pages = kTile >> p.c.page_shift, page = 1 << p.c.page_shift;
+            for (int t = 0; t < b.tiles && ok; ++t) {
+                const int key0 = b.k0 + t * kTile;
+                const int pages_live = min(pages, (b.n - key0 + page - 1) >> p.c.page_shift);
+                int pg = 0;
+                if (lane < pages_live) {
+                    pg = page_of(p.c, b.i, key0 + lane * page);
+                    if (pg < 0) {
+                        set_status(p.dev_status, SDM_DEV_BAD_PAGE);
+                        pg = 0;
+                    }
+                }
+                const int y = (pg * p.c.heads + b.g) << p.c.page_shift;
+                ok = wait_or_fail(p, &bar.k_empty[kr.at], kr.empty());
+                if (kPlanes && ok) ok = wait_or_fail(p, &bar.x_empty[xr.at], xr.empty());
+                if (!ok) break;
+                uint8_t* slot = smem + kr.at * C::kKBytes;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar.k_full[kr.at], static_cast<uint32_t>(pages_live) * page * (kPlanes ? D : 2 * D));
+                    if (kPlanes) mbar_arrive_expect_tx(&bar.x_full[xr.at], static_cast<uint32_t>(pages_live) * page);
+                }
+                __syncwarp();
+                if (lane < pages_live) {
+                    if constexpr (kPlanes) {
+                        tma_load_2d(slot + lane * page * D, &tmK, &bar.k_full[kr.at], 0, y);
+                        bulk_load(smem + C::kExps + xr.at * kTile + lane * page, p.c.k_exp + y, page, &bar.x_full[xr.at]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_2d(slot + h * (kTile * 128) + lane * page * 128, &tmK, &bar.k_full[kr.at], h * 64, y);
+                    }
+                }
+                __syncwarp();
+                kr.step();
+                if (kPlanes) xr.step();
+            }
+        }
+        if (!SMALL && lane == 0) ws.part[blockIdx.x] = part;
+        if (!ok) {
+            // copies in flight land before the CTA may exit
+            for (int k = 0; k < C::kKSlots; ++k)
+                if (kr.turn > 0 || k < kr.at) mbar_wait(&bar.k_full[k], k < kr.at ? kr.turn & 1 : (kr.turn & 1) ^ 1);
+            if (kPlanes)
+                for (int k = 0; k < kExpStages; ++k)
+                    if (xr.turn > 0 || k < xr.at) mbar_wait(&bar.x_full[k], k < xr.at ? xr.turn & 1 : (xr.turn & 1) ^ 1);
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------------
+        // products
+        // ------------------------------------------------------------------
+        bool ok = true;
+        Ring<C::kKSlots> kr;
+        Ring<C::kQSlots> qr;          // SMALL: the slot in use
+        Ring<2> sr[2];
+        bool any_q = false;
+        Blk b;
+        while (take(ok, b)) {
+            if (!(b.flags & U_HAS)) continue;
+            if (SMALL && (b.flags & U_NEWQ)) {
+                if (any_q) {
+                    mma_commit_warp(&bar.q_empty[qr.at]);
+                    qr.step();
+                }
+                any_q = true;
+                ok = wait_or_fail(p, &bar.q_full[qr.at], qr.full());
+                if (!ok) break;
+            }
+            const int k_at[2] = {kr.at, kr.at + 1 == C::kKSlots ? 0 : kr.at + 1};
+            for (int q = b.q0; q < b.q1 && ok; ++q) {
+                if (!SMALL) ok = wait_or_fail(p, &bar.q_full[qr.at], qr.full());
+                const int N = SMALL ? (b.M + 31) & ~31 : kTile;   // what the weights read
+                for (int t = 0; t < b.tiles && ok; ++t) {
+                    if (q == b.q0) {
+                        ok = wait_or_fail(p, &bar.k_full[kr.at], kr.full());
+                        kr.step();
+                    }
+                    if (ok) ok = wait_or_fail(p, &bar.s_empty[t][sr[t].at], sr[t].empty());
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + t * 256 + sr[t].at * 128;
+                    const uint32_t ka = smem_u32(smem + k_at[t] * C::kKBytes), qa = smem_u32(smem + C::kQ + qr.at * C::kQBytes);
+                    if constexpr (kPlanes) {
+                        const uint64_t a = D == 128 ? smem_desc_sw128(ka, 16, 1024) : smem_desc_sw64(ka);
+                        const uint64_t q_ = D == 128 ? smem_desc_sw128(qa, 16, 1024) : smem_desc_sw64(qa);
+#pragma unroll
+                        for (int pl = 0; pl < 3; ++pl)
+#pragma unroll
+                            for (int k = 0; k < D / 32; ++k)
+                                issue<true>(d, a + 2 * k, q_ + ((pl * C::kPlane) >> 4) + 2 * k, idesc_f8(kTile, N), pl + k > 0);
+                    } else {
+                        const uint64_t a = smem_desc_sw128(ka, 16, 1024), q_ = smem_desc_sw128(qa, 16, 1024);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t off = (k / 4) * ((kTile * 128) >> 4) + (k % 4) * 2;
+                            issue<false>(d, a + off, q_ + off, idesc_bf16_f32(kTile, N, false), k > 0);
+                        }
+                    }
+                    mma_commit_warp(&bar.s_full[t][sr[t].at]);
+                    sr[t].step();
+                    if (q == b.q1 - 1) mma_commit_warp(&bar.k_empty[k_at[t]]);
+                }
+                if (!SMALL && ok) {
+                    mma_commit_warp(&bar.q_empty[qr.at]);
+                    qr.step();
+                }
+            }
+            if (!ok) break;
+        }
+        // products in flight end before the tensor memory goes
+        mma_commit_warp(&bar.drain);
+        mbar_wait(&bar.drain, 0);
+    } else if (warp == 10 || (warp == 11 && !SMALL)) {
+        // ------------------------------------------------------------------
+        // the query rows (warp 10) and their -lse (warp 11; SMALL: warp 10 too)
+        // ------------------------------------------------------------------
+        bool ok = true;
+        Ring<C::kQSlots> qr;
+        Ring<C::kLStages> lr;
+        Blk b;
+        int sent = 0;
+        // four columns a lane: -lse log2 e, -infinity for those that add nothing
+        auto columns = [&](const Blk& b, int q, float* to, uint32_t* odd) {
+            bool none = false;
+            Counted w;
+            w.row0 = b.row0;
+            w.wide = b.wide;
+            float z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int col = k * 32 + lane, m = q * p.sub + col;
+                z[k] = -INFINITY;
+                if (col < p.sub && m < b.M) {
+                    const long long row = row_of(p, w, b.i, m / p.group);
+                    if (row >= 0) z[k] = __ldg(p.lse + row * p.H + b.g * p.group + m % p.group);
+                    else set_status(p.dev_status, SDM_DEV_BAD_WINDOW);
+                    none |= z[k] == -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) to[k * 32 + lane] = z[k] == -INFINITY ? -INFINITY : -z[k] * kLog2e;
+            none = __any_sync(0xffffffffu, none);
+            // a tile that its rows do not fill has columns of what follows them
+            if (lane == 0) *odd = none || (!SMALL && b.M - q * p.sub < p.sub);
+        };
+        // rows q * sub .. of the head into a slot, gathered
+        auto gather = [&](const Blk& b, int q, uint8_t* slot, float* scale) {
+            const int M = min(p.sub, b.M - q * p.sub), N = (M + 31) & ~31;
+            Counted w;
+            w.row0 = b.row0;
+            w.wide = b.wide;
+            if constexpr (kPlanes) {
+                constexpr int kPer = D / 32;   // elements of a lane
+                for (int r0 = 0; r0 < N; r0 += 4) {
+                    uint32_t x[4][kPer / 2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int m = q * p.sub + r0 + e;
+                        const long long row = r0 + e < M ? row_of(p, w, b.i, m / p.group) : -1;
+#pragma unroll
+                        for (int k = 0; k < kPer / 2; ++k) x[e][k] = 0;
+                        if (row >= 0) {
+                            const uint16_t* src = p.q + row * p.q_stride + static_cast<size_t>(b.g * p.group + m % p.group) * D;
+                            if constexpr (kPer == 4) {
+                                const uint2 y = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+                                x[e][0] = y.x;
+                                x[e][kPer / 2 - 1] = y.y;
+                            } else {
+                                x[e][0] = __ldg(reinterpret_cast<const uint32_t*>(src) + lane);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float f[kPer];
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int k = 0; k < kPer; ++k) {
+                            f[k] = bf16_bits_to_float((x[e][k >> 1] >> (16 * (k & 1))) & 0xffffu);
+                            f[k] = fmaf(f[k], 0.f, f[k]);            // an infinity becomes NaN
+                            const uint32_t u = __float_as_uint(f[k]) & 0x7fffffffu;
+                            if (u < 0x7f800000u) top = max(top, u);
+                        }
+                        top = __reduce_max_sync(0xffffffffu, top) >> 23;
+                        // 2^(141 - top) puts the largest into [2^14, 2^15); the factor stays normal
+                        const int shift = min(max(141 - static_cast<int>(top), -100), 100);
+                        const float mul = pow2f(shift);
+                        uint32_t code[3] = {0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < kPer; k += 2) {
+                            float a = f[k] * mul, c = f[k + 1] * mul;
+#pragma unroll
+                            for (int pl = 0; pl < 3; ++pl) {
+                                const uint32_t two = f32x2_to_e5m2x2(a, c);
+                                const float2 back = e5m2x2_to_f32x2(two);
+                                a -= back.x;
+                                c -= back.y;
+                                code[pl] |= two << (8 * k);
+                            }
+                        }
+                        const int r = r0 + e;
+                        // bytes kPer * lane .. of row r, swizzled as TMA would have it
+                        const int byte = kPer * lane, chunk = byte >> 4;
+                        const int at = D == 128 ? r * 128 + ((chunk ^ (r & 7)) << 4) + (byte & 15)
+                                                : r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4) + (byte & 15);
+#pragma unroll
+                        for (int pl = 0; pl < 3; ++pl) {
+                            if constexpr (kPer == 4) *reinterpret_cast<uint32_t*>(slot + pl * C::kPlane + at) = code[pl];
+                            else *reinterpret_cast<uint16_t*>(slot + pl * C::kPlane + at) = static_cast<uint16_t>(code[pl]);
+                        }
+                        if (lane == 0) scale[r] = pow2f(-shift);
+                    }
+                }
+            } else {
+                constexpr int kChunks = D / 8;   // 16-byte pieces of a row
+                for (int t = lane; t < N * kChunks; t += 32) {
+                    const int r = t / kChunks, c = t % kChunks, m = q * p.sub + r;
+                    const long long row = r < M ? row_of(p, w, b.i, m / p.group) : -1;
+                    const uint16_t* src = p.q;
+                    if (row >= 0) src += row * p.q_stride + static_cast<size_t>(b.g * p.group + m % p.group) * D + c * 8;
+                    cp_async_16(slot + (c / 8) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, row >= 0 ? 16 : 0);
+                }
+                cp_async_wait_all();
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        while (take(ok, b)) {
+            if (!(b.flags & U_HAS)) continue;
+            if constexpr (SMALL) {
+                if (!(b.flags & U_NEWQ)) continue;
+                ok = wait_or_fail(p, &bar.q_empty[qr.at], qr.empty());
+                if (!ok) break;
+                columns(b, 0, l2 + qr.at * kTile, &bar.odd[qr.at]);
+                gather(b, 0, smem + C::kQ + qr.at * C::kQBytes, cf + qr.at * kTile);
+                if (lane == 0) mbar_arrive(&bar.q_full[qr.at]);
+                qr.step();
+            } else
+            for (int q = b.q0; q < b.q1 && ok; ++q) {
+                if (warp == 11) {
+                    ok = wait_or_fail(p, &bar.l_empty[lr.at], lr.empty());
+                    if (!ok) break;
+                    columns(b, q, l2 + lr.at * kTile, &bar.odd[lr.at]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.l_full[lr.at]);
+                    lr.step();
+                    continue;
+                }
+                ok = wait_or_fail(p, &bar.q_empty[qr.at], qr.empty());
+                if (!ok) break;
+                uint8_t* slot = smem + C::kQ + qr.at * C::kQBytes;
+                if (p.path) {
+                    gather(b, q, slot, nullptr);
+                    if (lane == 0) mbar_arrive(&bar.q_full[qr.at]);
+                } else {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.q_full[qr.at], static_cast<uint32_t>(p.sub) * D * 2);
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(slot + h * (kTile * 128), &tmQ, &bar.q_full[qr.at], h * 64, b.g * p.group,
+                                        b.row0 + q * (p.sub / p.group));
+                    }
+                    __syncwarp();
+                    ++sent;
+                }
+                qr.step();
+            }
+            if (!ok) break;
+        }
+        if (!ok && !SMALL && warp == 10 && sent > 0)
+            for (int k = 0; k < C::kQSlots; ++k)
+                if (qr.turn > 0 || k < qr.at) mbar_wait(&bar.q_full[k], k < qr.at ? qr.turn & 1 : (qr.turn & 1) ^ 1);
+    } else if (warp < 8) {
+        // ------------------------------------------------------------------
+        // weights: a thread per key
+        // ------------------------------------------------------------------
+        const int wg = warp >> 2;
+        bool ok = true;
+        Ring<2> sr;
+        Ring<C::kQSlots> qr;
+        Ring<C::kLStages> lr;
+        Ring<kExpStages> xr;
+        Ring<C::kKSlots> kr;
+        bool any_q = false;
+        const float c0 = p.scale * kLog2e;
+        Blk b;
+        while (take(ok, b)) {
+            const int key = b.k0 + wg * kTile + (tid & 127);
+            const bool mine = wg < b.tiles, held = mine && key < b.n;
+            const bool has = b.flags & U_HAS;
+            const size_t o = (static_cast<size_t>(b.i) * p.c.heads + b.g) * p.stride + key;
+            float old = 0.f;
+            if (held && p.mass && key < b.ctx && (b.flags & U_FIRST) && (b.flags & U_LAST)) old = __ldcg(p.mass + o);
+            float sum = 0.f, lost = 0.f;
+            if (has) {
+                if (SMALL && (b.flags & U_NEWQ)) {
+                    if (any_q) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.q_empty[qr.at]);
+                        qr.step();
+                    }
+                    any_q = true;
+                    ok = wait_or_fail(p, &bar.q_full[qr.at], qr.full());   // its -lse
+                    if (!ok) break;
+                }
+                float c = c0;
+                if constexpr (kPlanes) {
+                    // this tile's exponents; the other warpgroup has the other's
+                    if (mine) {
+                        if (wg == 1) xr.step();
+                        ok = wait_or_fail(p, &bar.x_full[xr.at], xr.full());
+                        if (!ok) break;
+                        c *= scale_of(smem[C::kExps + xr.at * kTile + (tid & 127)]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.x_empty[xr.at]);
+                        xr.step();
+                        if (wg == 0 && b.tiles == 2) xr.step();
+                    } else {
+                        xr.step();
+                    }
+                }
+                if constexpr (E4M3 && !SMALL) {
+                    // the tile's codes as bf16, a key a thread
+                    const Ring<C::kKSlots> first = kr;
+                    if (wg == 1 && mine) kr.step();
+                    if (mine) {
+                        ok = wait_or_fail(p, &bar.k_empty[kr.at], kr.empty());
+                        if (!ok) break;
+                        uint8_t* slot = smem + kr.at * C::kKBytes;
+                        const int row = tid & 127;
+                        if (held) {
+                            int pg = page_of(p.c, b.i, key);
+                            if (pg < 0) {
+                                set_status(p.dev_status, SDM_DEV_BAD_PAGE);
+                                pg = 0;
+                            }
+                            const size_t at = pool_row(p.c, pg, key) + (static_cast<size_t>(b.g) << p.c.page_shift);
+                            const uint4* src = reinterpret_cast<const uint4*>(p.c.k + at * D);
+                            const float s = scale_of(__ldg(p.c.k_exp + at));
+                            uint4 x[D / 16];
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) x[k] = __ldg(src + k);
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                                uint32_t z[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(y[e >> 1] >> (16 * (e & 1)))));
+                                    z[e] = f32x2_to_bf16x2(f.x * s, f.y * s);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int chunk = 2 * k + e;
+                                    *reinterpret_cast<uint4*>(slot + (chunk / 8) * (kTile * 128) + row * 128 +
+                                                              (((chunk & 7) ^ (row & 7)) << 4)) =
+                                        make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+                                }
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.k_full[kr.at]);
+                    }
+                    kr = first;
+                    for (int t = 0; t < b.tiles; ++t) kr.step();
+                }
+                for (int q = b.q0; q < b.q1 && ok; ++q) {
+                    const float* lq = l2 + (SMALL ? qr.at : lr.at) * kTile;
+                    if (!SMALL) {
+                        ok = wait_or_fail(p, &bar.l_full[lr.at], lr.full());
+                        if (!ok) break;
+                    }
+                    if (mine) {
+                        const int cols = SMALL ? b.M : p.sub;
+                        // columns [lo, hi) see this key
+                        const int first = q * p.sub;
+                        int lo = 0, hi = min(cols, b.M - first);
+                        bool some = bar.odd[SMALL ? qr.at : lr.at];
+                        if (key > b.ctx) lo = (key - b.ctx) * p.group - first;
+                        if (p.window > 0 && key >= p.sinks) {
+                            const long long end = static_cast<long long>(key) - b.ctx + p.window;   // rows below it see the key
+                            if (end * p.group < b.M) hi = min(hi, static_cast<int>(max(end, 0ll)) * p.group - first);
+                        }
+                        some = __any_sync(0xffffffffu, some || lo > 0 || hi < min(cols, b.M - first));
+                        ok = wait_or_fail(p, &bar.s_full[wg][sr.at], sr.full());
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t s_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 256 + sr.at * 128;
+                        const int N = (cols + 31) & ~31;
+                        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        const float2 cc = make_float2(c, c);
+#pragma unroll 1
+                        for (int c1 = 0; c1 < N; c1 += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(s_at + c1, x);
+                            tmem_ld_wait();
+                            const float4* lp = reinterpret_cast<const float4*>(lq + c1);
+                            const float4* fp = reinterpret_cast<const float4*>(cf + qr.at * kTile + c1);
+                            uint32_t see = 0xffffffffu;
+                            if (some) {
+                                const int from = max(lo - c1, 0), to = hi - c1;
+                                see = (from >= 32 ? 0u : ~0u << from) & (to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 l = lp[k];
+                                float2 a = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+                                float2 d = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+                                if constexpr (kPlanes) {
+                                    const float4 f = fp[k];
+                                    a = fma2(mul2(a, cc), make_float2(f.x, f.y), make_float2(l.x, l.y));
+                                    d = fma2(mul2(d, cc), make_float2(f.z, f.w), make_float2(l.z, l.w));
+                                } else {
+                                    a = fma2(a, cc, make_float2(l.x, l.y));
+                                    d = fma2(d, cc, make_float2(l.z, l.w));
+                                }
+                                a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                                d = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+                                if (some) {
+                                    if (!((see >> (4 * k)) & 1u) || l.x == -INFINITY) a.x = 0.f;
+                                    if (!((see >> (4 * k + 1)) & 1u) || l.y == -INFINITY) a.y = 0.f;
+                                    if (!((see >> (4 * k + 2)) & 1u) || l.z == -INFINITY) d.x = 0.f;
+                                    if (!((see >> (4 * k + 3)) & 1u) || l.w == -INFINITY) d.y = 0.f;
+                                }
+                                acc[0] = add2(acc[0], a);
+                                acc[1] = add2(acc[1], d);
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.s_empty[wg][sr.at]);
+                        sr.step();
+                        // the tiles' sums with what each addition loses: a key of a long
+                        // prompt is the sum of thousands of weights
+                        const float one = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) - lost;
+                        const float to = sum + one;
+                        lost = (to - sum) - one;
+                        sum = to;
+                    }
+                    if (!SMALL) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.l_empty[lr.at]);
+                        lr.step();
+                    }
+                }
+                if (!ok) break;
+            }
+            if (held) {
+                if ((b.flags & U_FIRST) && (b.flags & U_LAST)) p.mass_out[o] = old + sum;
+                else ws.sum[(static_cast<size_t>(blockIdx.x) * 2 + ((b.flags & U_FIRST) ? 1 : 0)) * kUnit + wg * kTile + (tid & 127)] = sum;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Adds the parts of the unit that a share starts and does not finish, in order.
+__global__ void __launch_bounds__(kUnit) weigh_join_kernel(const WeighParams p, const Scratch ws, int grid) {
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x;
+    const Part s = ws.part[c];
+    if (!s.rest) return;
+    const int key = s.k0 + threadIdx.x;
+    const float* sums = ws.sum + threadIdx.x;
+    float sum = sums[(2 * static_cast<size_t>(c) + 1) * kUnit];
+    for (int k = c + 1; k < grid; ++k) {
+        const int head = ws.part[k].head;
+        if (head) sum += sums[2 * static_cast<size_t>(k) * kUnit];
+        if (head == 1) break;
+    }
+    if (key >= s.n) return;
+    const size_t o = (static_cast<size_t>(s.i) * p.c.heads + s.g) * p.stride + key;
+    p.mass_out[o] = (key < s.ctx && p.mass ? __ldcg(p.mass + o) : 0.f) + sum;
+}
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess && q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+    }();
+    return fn;
+}
+
+bool encode_q(CUtensorMap* map, const WeighParams& p) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.c.D), static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.c.D) * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
+    cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.sub / p.group)};
+    cuuint32_t el[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, el,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// rows = (page, head, slot); a box is one page of one head, 128 bytes (e4m3 with 64-wide heads: 64) across
+bool encode_k(CUtensorMap* map, const CacheView& c) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const int es = c.e4m3 ? 1 : 2, cols = c.e4m3 ? c.D : 64;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.n_pages) * c.heads << c.page_shift};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.D) * es};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(cols), 1u << c.page_shift};
+    cuuint32_t el[2] = {1, 1};
+    return fn(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.k, dims, strides, box,
+              el, CU_TENSOR_MAP_INTERLEAVE_NONE, cols * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool E4M3, bool SMALL>
+cudaError_t launch_one(const WeighParams& p, void* work, cudaStream_t s) {
+    using C = Cfg<D, E4M3, SMALL>;
+    constexpr int kTotal = C::kBars + static_cast<int>(sizeof(Bars<C::kKSlots, C::kQSlots, C::kLStages>));
+    static const cudaError_t raised = cudaFuncSetAttribute(weigh_kernel<D, E4M3, SMALL>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kTotal);
+    if (raised != cudaSuccess) return raised;
+    CUtensorMap tmK;
+    if (!encode_k(&tmK, p.c)) return cudaErrorInvalidValue;
+    CUtensorMap tmQ = tmK;
+    if (!SMALL && p.rows > 0 && !encode_q(&tmQ, p)) return cudaErrorInvalidValue;
+    const int grid = num_sms();
+    Scratch ws = {};
+    if (!SMALL) {
+        ws.part = static_cast<Part*>(work);
+        ws.sum = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + align256(sizeof(Part) * grid));
+    }
+    const cudaError_t e = launch_pdl(weigh_kernel<D, E4M3, SMALL>, dim3(grid), dim3(kThreads), kTotal, s, tmK, tmQ, p, ws);
+    if (e != cudaSuccess || SMALL) return e;
+    return launch_pdl(weigh_join_kernel, dim3(grid), dim3(kUnit), 0, s, p, ws, grid);
+}
+
+// Query rows of a tile: those of as many whole tokens as it holds.
+inline int tile_rows(int group) { return kTile / group * group; }
+
+template <int D, bool E4M3>
+cudaError_t launch_form(const WeighParams& p, void* ws, cudaStream_t s) {
+    const bool small = static_cast<long long>(p.max_count) * p.group <= p.sub;
+    return small ? launch_one<D, E4M3, true>(p, ws, s) : launch_one<D, E4M3, false>(p, ws, s);
 }
 
 }  // namespace
 
-size_t weigh_workspace(int max_count, int H, int kv_heads) { return 0; }
+size_t weigh_workspace(int max_count, int H, int kv_heads) {
+    if (max_count <= 0 || H <= 0 || kv_heads <= 0 || H / kv_heads > kTile || H < kv_heads) return 0;
+    const int group = H / kv_heads;
+    if (static_cast<long long>(max_count) * group <= tile_rows(group)) return 0;
+    const size_t grid = num_sms();
+    return align256(sizeof(Part) * grid) + grid * 2 * kUnit * sizeof(float);
+}
 
 cudaError_t launch_weigh(const WeighParams& p, void* ws, cudaStream_t s) {
-    const long long tokens = std::min<long long>(p.stride, static_cast<long long>(p.c.max_pages) << p.c.page_shift);
-    const dim3 grid(static_cast<unsigned>((tokens + kTile - 1) / kTile), p.c.heads, p.R);
-    auto k = p.c.D == 128 ? (p.c.e4m3 ? weigh_kernel<128, true> : weigh_kernel<128, false>)
-                          : (p.c.e4m3 ? weigh_kernel<64, true> : weigh_kernel<64, false>);
-    return launch_pdl(k, grid, dim3(kTile), 0, s, p);
+    WeighParams q = p;
+    q.sub = tile_rows(p.group);
+    if (p.c.D == 128) return p.c.e4m3 ? launch_form<128, true>(q, ws, s) : launch_form<128, false>(q, ws, s);
+    return p.c.e4m3 ? launch_form<64, true>(q, ws, s) : launch_form<64, false>(q, ws, s);
 }
 
 }  // namespace sdm
