@@ -753,7 +753,7 @@ sdm_status sdm_qk_rotate(const sdm_cache* cache, const uint16_t* q, int64_t q_st
  * In:  target [row_capacity, V] (dtT), cu_seqlens [R+1], path [R, W] or NULL,
  *      tok [R, W] (sdm_verify's out_tok), n [R] (its n_out) or NULL: every row
  *      of the windows, W at most.  V % 8 == 0, V >= 8, target 16-byte aligned;
- *      R W <= 2^27; 0 <= top <= min(32, V); log2(e) / T within 1e-30 .. 1e30.
+ *      R W <= 2^27; 0 <= top <= min(32, V); log2(e) / T within 1e-8 .. 1e8.
  * Out: logp [R, W] fp32; entropy fp32, rank int32 [R, W] (each may be NULL);
  *      top_tok int32, top_logp fp32 [R, W, top] (NULL if top = 0).  Positions
  *      from n[i] on are left as they were.

@@ -1124,7 +1124,7 @@ sdm_status sdm_token_logprobs(const void* target, sdm_dtype dtT, int row_capacit
     if (dtT != SDM_BF16 && dtT != SDM_FP32) return SDM_ERR_INVALID_ARG;
     if (top < 0 || top > V || (top > 0 && (!top_tok || !top_logp))) return SDM_ERR_INVALID_ARG;
     const double scale = 1.4426950408889634 / static_cast<double>(temperature);
-    if (!(temperature > 0.f) || !(scale >= 1e-30 && scale <= 1e30)) return SDM_ERR_INVALID_ARG;
+    if (!(temperature > 0.f) || !(scale >= 1e-8 && scale <= 1e8)) return SDM_ERR_INVALID_ARG;
     if (row_capacity > 0 && !target) return SDM_ERR_INVALID_ARG;
     if (V % 8 != 0 || !aligned16(target) || top > 32 || static_cast<long long>(R) * W > (1ll << 27))
         return SDM_ERR_UNSUPPORTED;

@@ -63,6 +63,7 @@ __device__ __forceinline__ Held held_of(const EvictParams& p, int i) {
 
 __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     __shared__ Shared sh;
+    extern __shared__ uint32_t keys[];
     pdl_wait();
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
@@ -88,20 +89,38 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     const int per = (((h.n + C - 1) / C) + 31) & ~31;
     const int s0 = static_cast<int>(min(static_cast<long long>(per) * rank, static_cast<long long>(h.n)));
     const int s1 = static_cast<int>(min(static_cast<long long>(s0) + per, static_cast<long long>(h.n)));
-    const bool same = mass_out == mass && pos_out == pos;
-    for (int s = s0 + tid; s < min(s1, keep); s += kThreads) {   // those that stay; the others' places are overwritten below
-        if (same && s < h.ctx) continue;
-        mass_out[s] = __ldcg(mass + s);
-        pos_out[s] = where(s);
-    }
-    if (h.n <= keep) return;   // the whole cluster
-
-    auto key_of = [&](int s) {
-        const int32_t at = where(s);
+    const bool same = mass_out == mass && pos_out == pos, cut = h.n > keep;
+    auto key = [&](int32_t at, float m) {
         if (at < p.sinks || at >= h.end - p.recent) return 0xffffffffu;
-        const float m = __ldcg(mass + s);
         return m == m ? min(ordered_bits(m), 0xfffffffeu) : 0u;
     };
+    // The keys stay in shared memory; a run of slots that does not fit is
+    // looked up again wherever its keys are wanted.
+    const bool fits = per <= p.room;
+    for (int b = s0; b < s1; b += 4 * kThreads) {
+        int32_t at[4];
+        float m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s = b + j * kThreads + tid;
+            if (s < s1) {
+                at[j] = where(s);
+                m[j] = __ldcg(mass + s);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s = b + j * kThreads + tid;
+            if (s >= s1) continue;
+            if (cut && fits) keys[s - s0] = key(at[j], m[j]);
+            if (s < keep && !(same && s < h.ctx)) {   // those that stay; the others' places are overwritten below
+                mass_out[s] = m[j];
+                pos_out[s] = at[j];
+            }
+        }
+    }
+    if (!cut) return;   // the whole cluster
+    auto key_of = [&](int s) { return fits ? keys[s - s0] : key(where(s), __ldcg(mass + s)); };
     // 1. the keep-th largest key
     uint32_t found = 0, mask = 0;
     int need = keep;       // rank of the wanted key among those that share the digits found
@@ -272,7 +291,13 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
     const long long items = static_cast<long long>(p.R) * p.c.heads;
     int C = 1;
     while (C < 8 && items * C * 2 <= 2LL * num_sms() && p.stride / (2 * C) >= 2048) C *= 2;
-    return launch_cluster(evict_kernel, dim3(static_cast<unsigned>(items * C)), dim3(kThreads), C, 0, s, q);
+    const long long per = ((p.stride + C - 1) / C + 31) / 32 * 32;
+    constexpr int kMost = 48 * 1024;   // keys a CTA can hold
+    static const cudaError_t raised =
+        cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4);
+    if (raised != cudaSuccess) return raised;
+    q.room = static_cast<int>(std::min<long long>(per, kMost));
+    return launch_cluster(evict_kernel, dim3(static_cast<unsigned>(items * C)), dim3(kThreads), C, q.room * 4, s, q);
 }
 
 }  // namespace sdm

@@ -631,8 +631,9 @@ struct EvictParams {
     int32_t* pos_out;
     int32_t* length;
     int32_t* next;           // or NULL
-    int32_t* moves;          // [R, heads, most] sources
+    int32_t* moves;          // [R, heads, 2, most]: sources, destinations
     int64_t most;
+    int room;                // keys that a CTA holds in shared memory (set at the launch)
     int32_t* dev_status;
 };
 size_t evict_workspace(int R, int kv_heads, int64_t stride, int keep);

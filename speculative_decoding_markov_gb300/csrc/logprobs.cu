@@ -25,6 +25,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTopMost = 32;
+constexpr int kBatch = 4;             // loads of a thread in flight together
 constexpr int kCand = 2048;           // listed elements of a CTA
 constexpr int kMaxCluster = 8;
 constexpr float kLazy = 8.0f;         // in log2 units
@@ -35,6 +36,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kHuge = 1.0e8f;
 constexpr float kFar = 1.0e30f;       // a logit beside which log s does not count, and c z may overflow
 constexpr float kMaxRef = 3.0e38f;    // references stay finite
+constexpr float kLowest = -1.0e30f;   // logits below it have a weight of 0 beside a largest one above -kHuge
 
 struct Part {                          // one CTA's share of a row
     float m, s, t, top;                // reference (scaled), sums, largest logit
@@ -55,23 +57,86 @@ struct Shared {
     unsigned long long cand[kCand];
 };
 
-__device__ __forceinline__ float logit8(const uint4& lo, const uint4& hi, int j, bool fp32) {
-    const uint32_t* a = reinterpret_cast<const uint32_t*>(&lo);
-    const uint32_t* b = reinterpret_cast<const uint32_t*>(&hi);
-    if (fp32) return __uint_as_float(j < 4 ? a[j] : b[j - 4]);
-    return bf16_bits_to_float((a[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
 }
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ __nv_bfloat162 pair_of(uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
 // Eight logits of a row, from element 8 vec on.
 template <bool FP32>
 struct Vec {
-    uint4 lo, hi;
+    uint32_t u[FP32 ? 8 : 4];
     __device__ __forceinline__ void load(const uint8_t* row, int vec) {
         const uint4* src = reinterpret_cast<const uint4*>(row) + (FP32 ? 2 * static_cast<size_t>(vec) : vec);
-        lo = __ldg(src);
-        if (FP32) hi = __ldg(src + 1);
+        const uint4 a = __ldg(src);
+        u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
+        if constexpr (FP32) {
+            const uint4 b = __ldg(src + 1);
+            u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+        }
     }
-    __device__ __forceinline__ float at(int j) const { return logit8(lo, hi, j, FP32); }
+    __device__ __forceinline__ float at(int j) const {
+        if constexpr (FP32) return __uint_as_float(u[j]);
+        else return bf16_bits_to_float((u[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+    }
+    // The largest; a NaN is left out.
+    __device__ __forceinline__ float largest() const {
+        if constexpr (FP32) {
+            float m = at(0);
+#pragma unroll
+            for (int j = 1; j < 8; ++j) m = fmaxf(m, at(j));
+            return m;
+        } else {
+            const uint32_t m = bits_of(__hmax2(__hmax2(pair_of(u[0]), pair_of(u[1])), __hmax2(pair_of(u[2]), pair_of(u[3]))));
+            return fmaxf(bf16_bits_to_float(m & 0xffffu), bf16_bits_to_float(m >> 16));
+        }
+    }
+    // Elements below kLowest, which weigh nothing, as that (finite: 0 d = 0); a NaN stays.
+    __device__ __forceinline__ void raise() {
+        if constexpr (FP32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(max_nan(at(j), kLowest));
+        } else {
+            const __nv_bfloat162 low = __float2bfloat162_rn(kLowest);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = bits_of(__hmax2_nan(pair_of(u[j]), low));
+        }
+    }
+    // How many exceed x, or (EQUAL) reach it.
+    template <bool EQUAL>
+    __device__ __forceinline__ int above(float x) const {
+        if constexpr (FP32) {
+            int n = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n += EQUAL ? at(j) >= x : at(j) > x;
+            return n;
+        } else {
+            const __nv_bfloat162 y = __float2bfloat162_rn(x);   // x is one of the row's: exact
+            __nv_bfloat162 n = EQUAL ? __hge2(pair_of(u[0]), y) : __hgt2(pair_of(u[0]), y);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) n = __hadd2(n, EQUAL ? __hge2(pair_of(u[j]), y) : __hgt2(pair_of(u[j]), y));
+            return static_cast<int>(__low2float(n) + __high2float(n));
+        }
+    }
 };
 
 // (s, t) of a reference m, for the reference `to` >= m.  A factor of zero ends
@@ -281,32 +346,37 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
     float m = -kMaxRef, s = 0.f, t = 0.f, top = -INFINITY;
     int ahead = 0;
     bool any = false;
-#pragma unroll 4
-    for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
-        Vec<FP32> x;
-        x.load(row, v);
-        float f[8];
+    const int said_in = tok >> 3;        // the vector that holds the token
+    for (int b = v0 + threadIdx.x; b < v1; b += kBatch * kThreads) {
+        Vec<FP32> xs[kBatch];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = x.at(j);
-        float vm = f[0];
+        for (int k = 0; k < kBatch; ++k)
+            if (b + k * kThreads < v1) xs[k].load(row, b + k * kThreads);
 #pragma unroll
-        for (int j = 1; j < 8; ++j) vm = fmaxf(vm, f[j]);
-        top = fmaxf(top, vm);
-        if (vm * c > m + kLazy) {
-            const float to = fminf(vm * c, kMaxRef);
-            move_to(m, s, t, to);
+        for (int k = 0; k < kBatch; ++k) {
+            const int v = b + k * kThreads;
+            if (v >= v1) break;
+            Vec<FP32>& x = xs[k];
+            const float vm = x.largest();
+            top = fmaxf(top, vm);
+            if (v < said_in) ahead += x.template above<true>(said);
+            else ahead += x.template above<false>(said);
+            if (v == said_in)
+                for (int j = 0; j < (tok & 7); ++j) ahead += x.at(j) == said;
+            if (vm * c > m + kLazy) move_to(m, s, t, fminf(vm * c, kMaxRef));
+            x.raise();
+            float2 sum = make_float2(0.f, 0.f), tsum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 d = fma2(make_float2(x.at(j), x.at(j + 1)), make_float2(c, c), make_float2(-m, -m));
+                const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+                sum = add2(sum, e);
+                tsum = fma2(e, d, tsum);
+            }
+            s += sum.x + sum.y;
+            t += tsum.x + tsum.y;
+            any = true;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float d = fmaxf(fmaf(f[j], c, -m), -1000.f);   // -inf: 2^d is 0, and d 2^d
-            const float e = f[j] != f[j] ? f[j] : fast_exp2(d);
-            s += e;
-            t = fmaf(e, d, t);
-        }
-        const int id = 8 * v;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ahead += f[j] > said || (f[j] == said && id + j < tok);
-        any = true;
     }
     const float mine = top;
 

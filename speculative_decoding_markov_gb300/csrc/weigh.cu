@@ -390,6 +390,44 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     return r;
 }
 
+// Adds the weights of 32 columns: 2^(c f x + l), f the columns' scales (planes),
+// l their -lse log2 e.  MASKED: only columns lo .. hi - 1, and none whose l is
+// -infinity, whatever x is.
+template <bool PLANES, bool MASKED>
+__device__ __forceinline__ void add_weights(const uint32_t (&x)[32], float c, const float4* l4, const float4* f4, int lo,
+                                            int hi, float2 (&acc)[4]) {
+    const float2 cc = make_float2(c, c);
+    uint32_t see = 0;
+    if (MASKED) {
+        const int from = max(lo, 0);
+        see = (from >= 32 ? 0u : ~0u << from) & (hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float4 l = l4[k];
+        float2 a = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+        float2 b = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+        if constexpr (PLANES) {
+            const float4 f = f4[k];
+            a = fma2(mul2(a, cc), make_float2(f.x, f.y), make_float2(l.x, l.y));
+            b = fma2(mul2(b, cc), make_float2(f.z, f.w), make_float2(l.z, l.w));
+        } else {
+            a = fma2(a, cc, make_float2(l.x, l.y));
+            b = fma2(b, cc, make_float2(l.z, l.w));
+        }
+        a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+        b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
+        if constexpr (MASKED) {
+            if (!((see >> (4 * k)) & 1u) || l.x == -INFINITY) a.x = 0.f;
+            if (!((see >> (4 * k + 1)) & 1u) || l.y == -INFINITY) a.y = 0.f;
+            if (!((see >> (4 * k + 2)) & 1u) || l.z == -INFINITY) b.x = 0.f;
+            if (!((see >> (4 * k + 3)) & 1u) || l.w == -INFINITY) b.y = 0.f;
+        }
+        acc[2 * (k & 1)] = add2(acc[2 * (k & 1)], a);
+        acc[2 * (k & 1) + 1] = add2(acc[2 * (k & 1) + 1], b);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
@@ -487,6 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring<kExpStages> xr;
         bool live = st.u0 < st.u1;
         Part part = {};
+        // page ids of a unit's keys, a lane per page, loaded a unit ahead: the
+        // table's latency would else stand before every unit's first copy
+        const int unit_pages = kUnit >> p.c.page_shift;
+        auto page_at = [&](int i, int u) {
+            const long long col = static_cast<long long>(u) * unit_pages + lane;
+            return lane < unit_pages && col < p.c.max_pages ? __ldg(p.c.table + static_cast<size_t>(i) * p.c.max_pages + col) : -1;
+        };
+        int ahead = -1, ahead_i = -1, ahead_u = -1;
         while (ok) {
             Blk b = {};
             bool got = false;
@@ -560,16 +606,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(b.flags & U_HAS) || (E4M3 && !SMALL)) continue;
             // its keys, a lane per page
             const int pages = kTile >> p.c.page_shift, page = 1 << p.c.page_shift;
+            const int this_u = b.k0 / kUnit;
+            const int ids = ahead_i == b.i && ahead_u == this_u ? ahead : page_at(b.i, this_u);
+            ahead_i = b.i;
+            ahead_u = this_u + 1;
+            ahead = page_at(ahead_i, ahead_u);
             for (int t = 0; t < b.tiles && ok; ++t) {
                 const int key0 = b.k0 + t * kTile;
                 const int pages_live = min(pages, (b.n - key0 + page - 1) >> p.c.page_shift);
-                int pg = 0;
-                if (lane < pages_live) {
-                    pg = page_of(p.c, b.i, key0 + lane * page);
-                    if (pg < 0) {
-                        set_status(p.dev_status, SDM_DEV_BAD_PAGE);
-                        pg = 0;
-                    }
+                int pg = __shfl_sync(0xffffffffu, ids, (t * pages + lane) & 31);
+                if (lane < pages_live && static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.n_pages)) {
+                    set_status(p.dev_status, SDM_DEV_BAD_PAGE);
+                    pg = 0;
                 }
                 const int y = (pg * p.c.heads + b.g) << p.c.page_shift;
                 ok = wait_or_fail(p, &bar.k_empty[kr.at], kr.empty());
@@ -948,44 +996,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
                         const uint32_t s_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 256 + sr.at * 128;
                         const int N = (cols + 31) & ~31;
-                        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                        const float2 cc = make_float2(c, c);
+                        float2 acc[4] = {};
+                        const float4* lp = reinterpret_cast<const float4*>(lq);
+                        const float4* fp = reinterpret_cast<const float4*>(cf + qr.at * kTile);
+                        // 32 columns are loaded while the 32 before them are summed
+                        uint32_t x[2][32];
+                        tmem_ld32(s_at, x[0]);
 #pragma unroll 1
-                        for (int c1 = 0; c1 < N; c1 += 32) {
-                            uint32_t x[32];
-                            tmem_ld32(s_at + c1, x);
+                        for (int c1 = 0; c1 < N; c1 += 64) {
                             tmem_ld_wait();
-                            const float4* lp = reinterpret_cast<const float4*>(lq + c1);
-                            const float4* fp = reinterpret_cast<const float4*>(cf + qr.at * kTile + c1);
-                            uint32_t see = 0xffffffffu;
-                            if (some) {
-                                const int from = max(lo - c1, 0), to = hi - c1;
-                                see = (from >= 32 ? 0u : ~0u << from) & (to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float4 l = lp[k];
-                                float2 a = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
-                                float2 d = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
-                                if constexpr (kPlanes) {
-                                    const float4 f = fp[k];
-                                    a = fma2(mul2(a, cc), make_float2(f.x, f.y), make_float2(l.x, l.y));
-                                    d = fma2(mul2(d, cc), make_float2(f.z, f.w), make_float2(l.z, l.w));
-                                } else {
-                                    a = fma2(a, cc, make_float2(l.x, l.y));
-                                    d = fma2(d, cc, make_float2(l.z, l.w));
-                                }
-                                a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-                                d = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-                                if (some) {
-                                    if (!((see >> (4 * k)) & 1u) || l.x == -INFINITY) a.x = 0.f;
-                                    if (!((see >> (4 * k + 1)) & 1u) || l.y == -INFINITY) a.y = 0.f;
-                                    if (!((see >> (4 * k + 2)) & 1u) || l.z == -INFINITY) d.x = 0.f;
-                                    if (!((see >> (4 * k + 3)) & 1u) || l.w == -INFINITY) d.y = 0.f;
-                                }
-                                acc[0] = add2(acc[0], a);
-                                acc[1] = add2(acc[1], d);
-                            }
+                            if (c1 + 32 < N) tmem_ld32(s_at + c1 + 32, x[1]);
+                            if (!some) add_weights<kPlanes, false>(x[0], c, lp + c1 / 4, fp + c1 / 4, 0, 0, acc);
+                            else add_weights<kPlanes, true>(x[0], c, lp + c1 / 4, fp + c1 / 4, lo - c1, hi - c1, acc);
+                            if (c1 + 32 >= N) break;
+                            tmem_ld_wait();
+                            if (c1 + 64 < N) tmem_ld32(s_at + c1 + 64, x[0]);
+                            if (!some) add_weights<kPlanes, false>(x[1], c, lp + c1 / 4 + 8, fp + c1 / 4 + 8, 0, 0, acc);
+                            else add_weights<kPlanes, true>(x[1], c, lp + c1 / 4 + 8, fp + c1 / 4 + 8, lo - c1 - 32, hi - c1 - 32, acc);
                         }
                         tc_fence_before();
                         __syncwarp();
@@ -993,7 +1020,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sr.step();
                         // the tiles' sums with what each addition loses: a key of a long
                         // prompt is the sum of thousands of weights
-                        const float one = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) - lost;
+                        const float2 half = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+                        const float one = half.x + half.y - lost;
                         const float to = sum + one;
                         lost = (to - sum) - one;
                         sum = to;
