@@ -606,7 +606,7 @@ struct WeighParams {
     const int32_t* path;     // [R, path_stride] or NULL
     int path_stride;
     int R, rows, max_count, H, group;
-    int sub;                 // query rows of a tile (set at the launch)
+    int sub, box;            // query rows of a tile, tokens of a TMA box (set at the launch)
     float scale;
     int window, sinks;
     const float* mass;       // [R, heads, stride] or NULL

@@ -45,7 +45,6 @@ constexpr int kUnit = 2 * kTile;      // keys of a unit
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;        // S of warpgroup w, buffer b at 256 w + 128 b
-constexpr int kRing = 4;              // units handed out ahead
 constexpr int kHeavy = 6, kBase = 2;  // costs: a unit with a product if SMALL (1 without); a unit beside its row tiles
 constexpr int kExpStages = 16;        // e4m3 exponents of tiles
 
@@ -100,6 +99,7 @@ struct Cfg {
     static constexpr int kQBytes = kPlanes ? 3 * kPlane : kTile * 2 * D;
     static constexpr int kQSlots = SMALL ? 2 : 3;
     static constexpr int kLStages = SMALL ? 2 : 4;
+    static constexpr int kRing = SMALL ? 8 : 4;                // units handed out ahead
     static constexpr int kMiscBytes = kRing * sizeof(Blk) + kLStages * (kTile * 4 + 16) + (kPlanes ? 2 * kTile * 4 : 0) +
                                       (kPlanes ? kExpStages * kTile : 0) + 704;
     static constexpr int kFit = (232448 - kMiscBytes - kQSlots * kQBytes) / kKBytes;
@@ -114,10 +114,10 @@ struct Cfg {
     static constexpr int kBars = kBlks + kRing * static_cast<int>(sizeof(Blk));
 };
 
-template <int K, int Q, int L>
+template <int K, int Q, int L, int U>
 struct Bars {
     uint64_t k_full[K], k_empty[K], q_full[Q], q_empty[Q], l_full[L], l_empty[L];
-    uint64_t s_full[2][2], s_empty[2][2], blk_full[kRing], blk_empty[kRing], x_full[kExpStages], x_empty[kExpStages];
+    uint64_t s_full[2][2], s_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages], x_empty[kExpStages];
     uint64_t drain;
     uint32_t odd[L];                  // a column of the stage adds nothing
     uint32_t tmem;
@@ -194,6 +194,52 @@ struct Start {
     int i, g, u, pad;
 };
 
+// The unit of a head that cost `into` of it lies in (SMALL).
+__device__ __forceinline__ int unit_at(int us, int ul, unsigned long long into) {
+    const unsigned long long first = static_cast<unsigned long long>(us) * kHeavy, mid = first + (ul - us);
+    if (into < first) return static_cast<int>(into / kHeavy);
+    if (into < mid) return us + static_cast<int>(into - first);
+    return ul + static_cast<int>((into - mid) / kHeavy);
+}
+
+__device__ __forceinline__ void share_of(unsigned long long total, unsigned long long& u0, unsigned long long& u1) {
+    const unsigned long long each = total >> 32 ? total / gridDim.x : static_cast<unsigned>(total) / gridDim.x;
+    const unsigned more = static_cast<unsigned>(total - each * gridDim.x);
+    u0 = each * blockIdx.x + min(blockIdx.x, more);
+    u1 = u0 + each + (blockIdx.x < more ? 1 : 0);
+}
+
+// Where the share starts, for at most 32 requests (SMALL): by the walking warp
+// alone, a lane per request, while the others set themselves up.
+__device__ __forceinline__ Start plan_few(const WeighParams& p) {
+    const int lane = threadIdx.x & 31;
+    Req r = {};
+    if (lane < p.R) r = req_of(p, lane);
+    if (r.w.bad && blockIdx.x == 0) set_status(p.dev_status, r.w.bad);
+    const unsigned long long head = before_unit(r, r.units), mine = head * p.c.heads;
+    unsigned long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    Start st = {};
+    share_of(__shfl_sync(0xffffffffu, sum, 31), st.u0, st.u1);
+    const unsigned hit = __ballot_sync(0xffffffffu, sum > st.u0);
+    const int k = hit ? __ffs(hit) - 1 : 0;
+    const unsigned long long c = max(__shfl_sync(0xffffffffu, head, k), 1ull);
+    const int us = __shfl_sync(0xffffffffu, r.us, k), ul = __shfl_sync(0xffffffffu, r.ul, k);
+    st.us = __shfl_sync(0xffffffffu, sum - mine, k);
+    unsigned long long into = st.u0 - st.us;
+    st.i = k;
+    st.g = into >> 32 || c >> 32 ? static_cast<int>(into / c) : static_cast<unsigned>(into) / static_cast<unsigned>(c);
+    into -= st.g * c;
+    st.u = unit_at(us, ul, into);
+    st.us += st.g * c + static_cast<unsigned long long>(min(st.u, us) + max(0, st.u - ul)) * kHeavy +
+             min(max(st.u - us, 0), ul - us);
+    return st;
+}
+
 // cost: shared memory for R entries.  By all warps.
 template <bool SMALL>
 __device__ __forceinline__ void plan(const WeighParams& p, unsigned long long* cost, unsigned long long* wsum,
@@ -237,9 +283,8 @@ __device__ __forceinline__ void plan(const WeighParams& p, unsigned long long* c
         if (k < warp) base += v;
         total += v;
     }
-    const unsigned long long each = total / gridDim.x, more = total % gridDim.x;
-    const unsigned long long u0 = each * blockIdx.x + min(static_cast<unsigned long long>(blockIdx.x), more);
-    const unsigned long long u1 = u0 + each + (blockIdx.x < more ? 1 : 0);
+    unsigned long long u0, u1;
+    share_of(total, u0, u1);
     if (tid == 0) {
         start->u0 = u0;
         start->u1 = u1;
@@ -261,11 +306,7 @@ __device__ __forceinline__ void plan(const WeighParams& p, unsigned long long* c
         into -= g * c;
         int u = 0;
         if (SMALL) {
-            const unsigned long long first = static_cast<unsigned long long>(r.us) * kHeavy;
-            const unsigned long long mid = first + (r.ul - r.us);
-            if (into < first) u = static_cast<int>(into / kHeavy);
-            else if (into < mid) u = r.us + static_cast<int>(into - first);
-            else u = r.ul + static_cast<int>((into - mid) / kHeavy);
+            u = unit_at(r.us, r.ul, into);
             us += before_unit(r, u);
         } else {
             for (int u0_ = 0; u0_ < r.units; u0_ += 32) {
@@ -325,22 +366,40 @@ struct Ring {
     __device__ __forceinline__ uint32_t empty() const { return (turn & 1) ^ 1; }    // for the writer: passes at first
 };
 
-// N products along the rows' bytes, 32 bytes a step, the lane elect.sync picks
-// issuing.
-template <bool F8>
+// N (2 or 4) products along the rows' bytes, 32 bytes a step, in one statement:
+// the lane elect.sync picks issues them with nothing but the descriptors' steps
+// between (one statement each: 930 clocks for the eight of a tile).
+template <bool F8, int N>
 __device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    if constexpr (F8)
+#define SDM_MMA4(KIND)                                                                                             \
+    asm volatile(                                                                                                  \
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\t"                         \
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"                                                        \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], %1, %2, %3, p;\n\t"                                      \
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"                                                               \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, q;\n\t"                                        \
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"                                                               \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, q;\n\t"                                        \
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"                                                               \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, q;\n\t}" ::"r"(d),                             \
+        "l"(a), "l"(b), "r"(idesc), "r"(add)                                                                       \
+        : "memory")
+    static_assert(N == 4 || (N == 2 && F8), "steps");
+    if constexpr (!F8) {
+        SDM_MMA4("f16");
+    } else if constexpr (N == 4) {
+        SDM_MMA4("f8f6f4");
+    } else {
         asm volatile(
-            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+            "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, q;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(add)
             : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(add)
-            : "memory");
+    }
+#undef SDM_MMA4
 }
 
 // kind::f8f6f4: e4m3 A (0 at bit 7), e5m2 B (1 at bit 10), fp32 accumulator
@@ -437,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ WeighParams p, const __grid_constant__ Scratch ws) {
     using C = Cfg<D, E4M3, SMALL>;
     constexpr bool kPlanes = C::kPlanes;
-    using B = Bars<C::kKSlots, C::kQSlots, C::kLStages>;
+    using B = Bars<C::kKSlots, C::kQSlots, C::kLStages, C::kRing>;
     static_assert(C::kBars + sizeof(B) <= 232448, "shared memory");
     extern __shared__ __align__(1024) uint8_t smem[];
     B& bar = *reinterpret_cast<B*>(smem + C::kBars);
@@ -451,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
         if (lane == 0) {
             tma_prefetch_desc(&tmK);
-            if (!SMALL) tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmQ);
         }
     } else if (warp == 9) {
         tmem_alloc(&bar.tmem, kTmemCols);
@@ -462,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.k_empty[k], 1);
         }
         if (lane < C::kQSlots) {
-            mbar_init(&bar.q_full[lane], 1);
+            mbar_init(&bar.q_full[lane], SMALL ? 2 : 1);
             mbar_init(&bar.q_empty[lane], SMALL ? 9 : 1);
         }
         if (lane < C::kLStages) {
@@ -473,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.s_full[0][0] + lane, 1);
             mbar_init(&bar.s_empty[0][0] + lane, 4);
         }
-        if (lane < kRing) {
+        if (lane < C::kRing) {
             mbar_init(&bar.blk_full[lane], 1);
-            mbar_init(&bar.blk_empty[lane], 8 + (SMALL ? 2 : 3));
+            mbar_init(&bar.blk_empty[lane], 8 + 3);   // the warps that read it
         }
         if (lane < kExpStages) {
             mbar_init(&bar.x_full[lane], 1);
@@ -486,8 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    plan<SMALL>(p, reinterpret_cast<unsigned long long*>(smem), wsum, start);
-    const Start st = *start;          // read before the roles use its place
+    const bool few = SMALL && p.R <= 32;
+    if (!few) plan<SMALL>(p, reinterpret_cast<unsigned long long*>(smem), wsum, start);
+    Start st = *start;                // read before the roles use its place
     // rows of a tile that no query row fills are zeros, so that their columns are finite
     for (int k = tid; k < C::kQSlots * C::kQBytes / 16; k += kThreads)
         reinterpret_cast<uint4*>(smem + C::kQ)[k] = make_uint4(0, 0, 0, 0);
@@ -497,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
 
-    Ring<kRing> rd;
+    Ring<C::kRing> rd;
     // waits for the next unit; false at the end (or with ok false)
     auto take = [&](bool& ok, Blk& b) {
         ok = wait_or_fail(p, &bar.blk_full[rd.at], rd.full());
@@ -517,10 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // walker: the share's units, and their keys
         // ------------------------------------------------------------------
         bool ok = true;
+        if (few) st = plan_few(p);
         unsigned long long us = st.us;
         int i = st.i, g = st.g, u = st.u, have = -1, loaded_i = -1, loaded_g = -1;
         Req r;
-        Ring<kRing> wr;
+        Ring<C::kRing> wr;
         Ring<C::kKSlots> kr;
         Ring<kExpStages> xr;
         bool live = st.u0 < st.u1;
@@ -691,18 +752,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (kPlanes) {
                         const uint64_t a = D == 128 ? smem_desc_sw128(ka, 16, 1024) : smem_desc_sw64(ka);
                         const uint64_t q_ = D == 128 ? smem_desc_sw128(qa, 16, 1024) : smem_desc_sw64(qa);
+                        const uint32_t id = idesc_f8(kTile, N);
 #pragma unroll
                         for (int pl = 0; pl < 3; ++pl)
-#pragma unroll
-                            for (int k = 0; k < D / 32; ++k)
-                                issue<true>(d, a + 2 * k, q_ + ((pl * C::kPlane) >> 4) + 2 * k, idesc_f8(kTile, N), pl + k > 0);
+                            issue<true, D / 32>(d, a, q_ + ((pl * C::kPlane) >> 4), id, pl > 0);
                     } else {
                         const uint64_t a = smem_desc_sw128(ka, 16, 1024), q_ = smem_desc_sw128(qa, 16, 1024);
+                        const uint32_t id = idesc_bf16_f32(kTile, N, false);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t off = (k / 4) * ((kTile * 128) >> 4) + (k % 4) * 2;
-                            issue<false>(d, a + off, q_ + off, idesc_bf16_f32(kTile, N, false), k > 0);
-                        }
+                        for (int h = 0; h < D / 64; ++h)
+                            issue<false, 4>(d, a + h * ((kTile * 128) >> 4), q_ + h * ((kTile * 128) >> 4), id, h > 0);
                     }
                     mma_commit_warp(&bar.s_full[t][sr[t].at]);
                     sr[t].step();
@@ -718,164 +777,212 @@ __global__ void __launch_bounds__(kThreads, 1)
         // products in flight end before the tensor memory goes
         mma_commit_warp(&bar.drain);
         mbar_wait(&bar.drain, 0);
-    } else if (warp == 10 || (warp == 11 && !SMALL)) {
+    } else if (warp == 10 || warp == 11) {
         // ------------------------------------------------------------------
-        // the query rows (warp 10) and their -lse (warp 11; SMALL: warp 10 too)
+        // the query rows (warp 10; split into planes: both) and their -lse (warp 11)
         // ------------------------------------------------------------------
         bool ok = true;
         Ring<C::kQSlots> qr;
         Ring<C::kLStages> lr;
         Blk b;
         int sent = 0;
-        // four columns a lane: -lse log2 e, -infinity for those that add nothing
-        auto columns = [&](const Blk& b, int q, float* to, uint32_t* odd) {
-            bool none = false;
+        const int tokens = p.sub / p.group;   // of a tile
+        // four columns a lane: window position in the tile, and head
+        int col_wp[4], col_h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            col_wp[k] = (k * 32 + lane) / p.group;
+            col_h[k] = (k * 32 + lane) - col_wp[k] * p.group;
+            if (k * 32 + lane >= p.sub) col_wp[k] = 1 << 30;
+        }
+        auto lse_of = [&](const Blk& b, int q, float (&z)[4]) {
             Counted w;
             w.row0 = b.row0;
             w.wide = b.wide;
-            float z[4];
+            const int rows = b.M / p.group - q * tokens;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int col = k * 32 + lane, m = q * p.sub + col;
                 z[k] = -INFINITY;
-                if (col < p.sub && m < b.M) {
-                    const long long row = row_of(p, w, b.i, m / p.group);
-                    if (row >= 0) z[k] = __ldg(p.lse + row * p.H + b.g * p.group + m % p.group);
+                if (col_wp[k] < rows) {
+                    const long long row = row_of(p, w, b.i, q * tokens + col_wp[k]);
+                    if (row >= 0) z[k] = __ldg(p.lse + row * p.H + b.g * p.group + col_h[k]);
                     else set_status(p.dev_status, SDM_DEV_BAD_WINDOW);
-                    none |= z[k] == -INFINITY;
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) to[k * 32 + lane] = z[k] == -INFINITY ? -INFINITY : -z[k] * kLog2e;
-            none = __any_sync(0xffffffffu, none);
-            // a tile that its rows do not fill has columns of what follows them
-            if (lane == 0) *odd = none || (!SMALL && b.M - q * p.sub < p.sub);
         };
-        // rows q * sub .. of the head into a slot, gathered
-        auto gather = [&](const Blk& b, int q, uint8_t* slot, float* scale) {
+        // -lse log2 e, -infinity for columns that add nothing; `odd`: there are
+        // such below column N, whose scores may be anything
+        auto put_lse = [&](const Blk& b, int q, int N, const float (&z)[4], float* to, uint32_t* odd) {
+            bool none = false;
+            const int live = min(b.M - q * p.sub, p.sub);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int col = k * 32 + lane;
+                none |= z[k] == -INFINITY && col < (live < p.sub ? N : p.sub);   // beyond a full tile's rows are zeros
+                to[col] = z[k] == -INFINITY ? -INFINITY : -z[k] * kLog2e;
+            }
+            none = __any_sync(0xffffffffu, none);
+            if (lane == 0) *odd = none;
+        };
+        // rows of tile q of the head into a slot, 16 bytes at a time, zeros up to N
+        auto gather = [&](const Blk& b, int q, uint8_t* slot) {
+            constexpr int kChunks = D / 8, kPer = 32 / kChunks;   // 16-byte pieces of a row; rows of a step
             const int M = min(p.sub, b.M - q * p.sub), N = (M + 31) & ~31;
             Counted w;
             w.row0 = b.row0;
             w.wide = b.wide;
-            if constexpr (kPlanes) {
-                constexpr int kPer = D / 32;   // elements of a lane
-                for (int r0 = 0; r0 < N; r0 += 4) {
-                    uint32_t x[4][kPer / 2];
+            const int c = lane % kChunks;
+            int wp = (lane / kChunks) / p.group, h = (lane / kChunks) - wp * p.group;
+            wp += q * tokens;
+#pragma unroll 4
+            for (int r = lane / kChunks; r < N; r += kPer) {
+                const long long row = r < M ? row_of(p, w, b.i, wp) : -1;
+                const uint16_t* src = p.q;
+                if (row >= 0) src += row * p.q_stride + static_cast<size_t>(b.g * p.group + h) * D + c * 8;
+                cp_async_16(slot + (c / 8) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, row >= 0 ? 16 : 0);
+                h += kPer;
+                while (h >= p.group) {
+                    h -= p.group;
+                    ++wp;
+                }
+            }
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        // the same as three planes of e5m2, and the rows' scales: this warp's groups of 4 rows
+        auto split = [&](const Blk& b, uint8_t* slot, float* scale) {
+            constexpr int kPer = D / 32;   // elements of a lane
+            const int M = b.M, N = (M + 31) & ~31;
+            Counted w;
+            w.row0 = b.row0;
+            w.wide = b.wide;
+            for (int r0 = 4 * (warp - 10); r0 < N; r0 += 8) {
+                uint32_t x[4][2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int m = q * p.sub + r0 + e;
-                        const long long row = r0 + e < M ? row_of(p, w, b.i, m / p.group) : -1;
-#pragma unroll
-                        for (int k = 0; k < kPer / 2; ++k) x[e][k] = 0;
-                        if (row >= 0) {
-                            const uint16_t* src = p.q + row * p.q_stride + static_cast<size_t>(b.g * p.group + m % p.group) * D;
-                            if constexpr (kPer == 4) {
-                                const uint2 y = __ldg(reinterpret_cast<const uint2*>(src) + lane);
-                                x[e][0] = y.x;
-                                x[e][kPer / 2 - 1] = y.y;
-                            } else {
-                                x[e][0] = __ldg(reinterpret_cast<const uint32_t*>(src) + lane);
-                            }
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    const int m = r0 + e;
+                    x[e][0] = x[e][1] = 0;
+                    if (m >= M) continue;
+                    const int wp = m / p.group, h = m - wp * p.group;
+                    const long long row = row_of(p, w, b.i, wp);
+                    if (row < 0) continue;
+                    const uint16_t* src = p.q + row * p.q_stride + static_cast<size_t>(b.g * p.group + h) * D;
+                    if constexpr (kPer == 4) {
+                        const uint2 y = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+                        x[e][0] = y.x;
+                        x[e][1] = y.y;
+                    } else {
+                        x[e][0] = __ldg(reinterpret_cast<const uint32_t*>(src) + lane);
                     }
+                }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float f[kPer];
-                        uint32_t top = 0;
+                for (int e = 0; e < 4; ++e) {
+                    float f[kPer];
+                    uint32_t top = 0;
 #pragma unroll
-                        for (int k = 0; k < kPer; ++k) {
-                            f[k] = bf16_bits_to_float((x[e][k >> 1] >> (16 * (k & 1))) & 0xffffu);
-                            f[k] = fmaf(f[k], 0.f, f[k]);            // an infinity becomes NaN
-                            const uint32_t u = __float_as_uint(f[k]) & 0x7fffffffu;
-                            if (u < 0x7f800000u) top = max(top, u);
-                        }
-                        top = __reduce_max_sync(0xffffffffu, top) >> 23;
-                        // 2^(141 - top) puts the largest into [2^14, 2^15); the factor stays normal
-                        const int shift = min(max(141 - static_cast<int>(top), -100), 100);
-                        const float mul = pow2f(shift);
-                        uint32_t code[3] = {0, 0, 0};
+                    for (int k = 0; k < kPer; ++k) {
+                        f[k] = bf16_bits_to_float((x[e][k >> 1] >> (16 * (k & 1))) & 0xffffu);
+                        f[k] = fmaf(f[k], 0.f, f[k]);            // an infinity becomes NaN
+                        const uint32_t u = __float_as_uint(f[k]) & 0x7fffffffu;
+                        if (u < 0x7f800000u) top = max(top, u);
+                    }
+                    top = __reduce_max_sync(0xffffffffu, top) >> 23;
+                    // 2^(141 - top) puts the largest into [2^14, 2^15); the factor stays normal
+                    const int shift = min(max(141 - static_cast<int>(top), -100), 100);
+                    const float mul = pow2f(shift);
+                    uint32_t code[3] = {0, 0, 0};
 #pragma unroll
-                        for (int k = 0; k < kPer; k += 2) {
-                            float a = f[k] * mul, c = f[k + 1] * mul;
-#pragma unroll
-                            for (int pl = 0; pl < 3; ++pl) {
-                                const uint32_t two = f32x2_to_e5m2x2(a, c);
-                                const float2 back = e5m2x2_to_f32x2(two);
-                                a -= back.x;
-                                c -= back.y;
-                                code[pl] |= two << (8 * k);
-                            }
-                        }
-                        const int r = r0 + e;
-                        // bytes kPer * lane .. of row r, swizzled as TMA would have it
-                        const int byte = kPer * lane, chunk = byte >> 4;
-                        const int at = D == 128 ? r * 128 + ((chunk ^ (r & 7)) << 4) + (byte & 15)
-                                                : r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4) + (byte & 15);
+                    for (int k = 0; k < kPer; k += 2) {
+                        float a = f[k] * mul, c = f[k + 1] * mul;
 #pragma unroll
                         for (int pl = 0; pl < 3; ++pl) {
-                            if constexpr (kPer == 4) *reinterpret_cast<uint32_t*>(slot + pl * C::kPlane + at) = code[pl];
-                            else *reinterpret_cast<uint16_t*>(slot + pl * C::kPlane + at) = static_cast<uint16_t>(code[pl]);
+                            const uint32_t two = f32x2_to_e5m2x2(a, c);
+                            const float2 back = e5m2x2_to_f32x2(two);
+                            a -= back.x;
+                            c -= back.y;
+                            code[pl] |= two << (8 * k);
                         }
-                        if (lane == 0) scale[r] = pow2f(-shift);
                     }
+                    const int r = r0 + e;
+                    // bytes kPer * lane .. of row r, swizzled as TMA would have it
+                    const int byte = kPer * lane, chunk = byte >> 4;
+                    const int at = D == 128 ? r * 128 + ((chunk ^ (r & 7)) << 4) + (byte & 15)
+                                            : r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4) + (byte & 15);
+#pragma unroll
+                    for (int pl = 0; pl < 3; ++pl) {
+                        if constexpr (kPer == 4) *reinterpret_cast<uint32_t*>(slot + pl * C::kPlane + at) = code[pl];
+                        else *reinterpret_cast<uint16_t*>(slot + pl * C::kPlane + at) = static_cast<uint16_t>(code[pl]);
+                    }
+                    if (lane == 0) scale[r] = pow2f(-shift);
                 }
-            } else {
-                constexpr int kChunks = D / 8;   // 16-byte pieces of a row
-                for (int t = lane; t < N * kChunks; t += 32) {
-                    const int r = t / kChunks, c = t % kChunks, m = q * p.sub + r;
-                    const long long row = r < M ? row_of(p, w, b.i, m / p.group) : -1;
-                    const uint16_t* src = p.q;
-                    if (row >= 0) src += row * p.q_stride + static_cast<size_t>(b.g * p.group + m % p.group) * D + c * 8;
-                    cp_async_16(slot + (c / 8) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, row >= 0 ? 16 : 0);
-                }
-                cp_async_wait_all();
             }
             fence_proxy_async_smem();
             __syncwarp();
+        };
+        // tile q by TMA: boxes of `box` whole tokens
+        auto fetch = [&](const Blk& b, int q, uint8_t* slot, uint64_t* full) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.box) * p.group * D * 2);
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                    tma_load_3d(slot + h * (kTile * 128), &tmQ, full, h * 64, b.g * p.group, b.row0 + q * tokens);
+            }
+            __syncwarp();
+            ++sent;
         };
         while (take(ok, b)) {
             if (!(b.flags & U_HAS)) continue;
             if constexpr (SMALL) {
                 if (!(b.flags & U_NEWQ)) continue;
-                ok = wait_or_fail(p, &bar.q_empty[qr.at], qr.empty());
-                if (!ok) break;
-                columns(b, 0, l2 + qr.at * kTile, &bar.odd[qr.at]);
-                gather(b, 0, smem + C::kQ + qr.at * C::kQBytes, cf + qr.at * kTile);
-                if (lane == 0) mbar_arrive(&bar.q_full[qr.at]);
-                qr.step();
-            } else
-            for (int q = b.q0; q < b.q1 && ok; ++q) {
-                if (warp == 11) {
-                    ok = wait_or_fail(p, &bar.l_empty[lr.at], lr.empty());
-                    if (!ok) break;
-                    columns(b, q, l2 + lr.at * kTile, &bar.odd[lr.at]);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.l_full[lr.at]);
-                    lr.step();
-                    continue;
-                }
+                float z[4];
+                if (warp == 11) lse_of(b, 0, z);
                 ok = wait_or_fail(p, &bar.q_empty[qr.at], qr.empty());
                 if (!ok) break;
                 uint8_t* slot = smem + C::kQ + qr.at * C::kQBytes;
-                if (p.path) {
-                    gather(b, q, slot, nullptr);
-                    if (lane == 0) mbar_arrive(&bar.q_full[qr.at]);
+                if (warp == 11) put_lse(b, 0, (b.M + 31) & ~31, z, l2 + qr.at * kTile, &bar.odd[qr.at]);
+                if constexpr (kPlanes) split(b, slot, cf + qr.at * kTile);
+                else if (warp == 10 && p.path) gather(b, 0, slot);
+                if (!kPlanes && warp == 10 && !p.path) {
+                    fetch(b, 0, slot, &bar.q_full[qr.at]);
                 } else {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&bar.q_full[qr.at], static_cast<uint32_t>(p.sub) * D * 2);
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_3d(slot + h * (kTile * 128), &tmQ, &bar.q_full[qr.at], h * 64, b.g * p.group,
-                                        b.row0 + q * (p.sub / p.group));
-                    }
                     __syncwarp();
-                    ++sent;
+                    if (lane == 0) mbar_arrive(&bar.q_full[qr.at]);
                 }
                 qr.step();
+            } else if (warp == 11) {
+                // a tile's are loaded while the ones before it wait for their place
+                float z[4];
+                lse_of(b, b.q0, z);
+                for (int q = b.q0; q < b.q1 && ok; ++q) {
+                    float next[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (q + 1 < b.q1) lse_of(b, q + 1, next);
+                    ok = wait_or_fail(p, &bar.l_empty[lr.at], lr.empty());
+                    if (!ok) break;
+                    put_lse(b, q, kTile, z, l2 + lr.at * kTile, &bar.odd[lr.at]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.l_full[lr.at]);
+                    lr.step();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) z[k] = next[k];
+                }
+            } else {
+                for (int q = b.q0; q < b.q1 && ok; ++q) {
+                    ok = wait_or_fail(p, &bar.q_empty[qr.at], qr.empty());
+                    if (!ok) break;
+                    uint8_t* slot = smem + C::kQ + qr.at * C::kQBytes;
+                    if (p.path) {
+                        gather(b, q, slot);
+                        if (lane == 0) mbar_arrive(&bar.q_full[qr.at]);
+                    } else {
+                        fetch(b, q, slot, &bar.q_full[qr.at]);
+                    }
+                    qr.step();
+                }
             }
             if (!ok) break;
         }
-        if (!ok && !SMALL && warp == 10 && sent > 0)
+        if (!ok && warp == 10 && sent > 0)   // copies in flight land before the CTA may exit
             for (int k = 0; k < C::kQSlots; ++k)
                 if (qr.turn > 0 || k < qr.at) mbar_wait(&bar.q_full[k], k < qr.at ? qr.turn & 1 : (qr.turn & 1) ^ 1);
     } else if (warp < 8) {
@@ -984,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // columns [lo, hi) see this key
                         const int first = q * p.sub;
                         int lo = 0, hi = min(cols, b.M - first);
-                        bool some = bar.odd[SMALL ? qr.at : lr.at];
+                        bool some = bar.odd[SMALL ? qr.at : lr.at];   // (junk columns, too)
                         if (key > b.ctx) lo = (key - b.ctx) * p.group - first;
                         if (p.window > 0 && key >= p.sinks) {
                             const long long end = static_cast<long long>(key) - b.ctx + p.window;   // rows below it see the key
@@ -1087,7 +1194,7 @@ bool encode_q(CUtensorMap* map, const WeighParams& p) {
     if (!fn) return false;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.c.D), static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.rows)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.c.D) * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
-    cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.sub / p.group)};
+    cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.box)};
     cuuint32_t el[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, el,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1111,14 +1218,14 @@ bool encode_k(CUtensorMap* map, const CacheView& c) {
 template <int D, bool E4M3, bool SMALL>
 cudaError_t launch_one(const WeighParams& p, void* work, cudaStream_t s) {
     using C = Cfg<D, E4M3, SMALL>;
-    constexpr int kTotal = C::kBars + static_cast<int>(sizeof(Bars<C::kKSlots, C::kQSlots, C::kLStages>));
+    constexpr int kTotal = C::kBars + static_cast<int>(sizeof(Bars<C::kKSlots, C::kQSlots, C::kLStages, C::kRing>));
     static const cudaError_t raised = cudaFuncSetAttribute(weigh_kernel<D, E4M3, SMALL>,
                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kTotal);
     if (raised != cudaSuccess) return raised;
     CUtensorMap tmK;
     if (!encode_k(&tmK, p.c)) return cudaErrorInvalidValue;
     CUtensorMap tmQ = tmK;
-    if (!SMALL && p.rows > 0 && !encode_q(&tmQ, p)) return cudaErrorInvalidValue;
+    if (!C::kPlanes && p.rows > 0 && !encode_q(&tmQ, p)) return cudaErrorInvalidValue;
     const int grid = num_sms();
     Scratch ws = {};
     if (!SMALL) {
@@ -1152,6 +1259,7 @@ size_t weigh_workspace(int max_count, int H, int kv_heads) {
 cudaError_t launch_weigh(const WeighParams& p, void* ws, cudaStream_t s) {
     WeighParams q = p;
     q.sub = tile_rows(p.group);
+    q.box = std::max(1, std::min(p.max_count, q.sub / p.group));
     if (p.c.D == 128) return p.c.e4m3 ? launch_form<128, true>(q, ws, s) : launch_form<128, false>(q, ws, s);
     return p.c.e4m3 ? launch_form<64, true>(q, ws, s) : launch_form<64, false>(q, ws, s);
 }
