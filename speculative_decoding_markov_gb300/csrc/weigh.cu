@@ -31,6 +31,9 @@
 // three products over the same codes, and the scales of row and key follow in
 // fp32.  Else, where a tile of keys meets many rows, its warpgroup turns the
 // codes into bf16 once.
+//
+// Unless SMALL the keys of a unit stand in tensor memory: with both operands in
+// shared memory a 128 x 128 x 128 product takes its whole bandwidth.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -43,8 +46,8 @@ namespace {
 constexpr int kTile = 128;            // keys of a tile, query rows of a tile
 constexpr int kUnit = 2 * kTile;      // keys of a unit
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 384;
-constexpr int kTmemCols = 512;        // S of warpgroup w, buffer b at 256 w + 128 b
+constexpr int kTmemCols = 512;        // S buffers of 128 columns from 0; the tiles of keys (unless SMALL) at kTmemK
+constexpr int kTmemK = 384;
 constexpr int kHeavy = 6, kBase = 2;  // costs: a unit with a product if SMALL (1 without); a unit beside its row tiles
 constexpr int kExpStages = 16;        // e4m3 exponents of tiles
 
@@ -97,27 +100,33 @@ struct Cfg {
     static constexpr int kKBytes = kTile * (kPlanes ? D : 2 * D);
     static constexpr int kPlane = kTile * D;                   // one e5m2 plane of a tile of rows
     static constexpr int kQBytes = kPlanes ? 3 * kPlane : kTile * 2 * D;
-    static constexpr int kQSlots = SMALL ? 2 : 3;
+    // warps of the weights: one per scheduler hides little of the exponentials'
+    // and the loads' latency, so many rows get two for each tile of keys
+    static constexpr int kSoft = SMALL ? 8 : 16;
+    static constexpr int kThreads = 32 * (kSoft + 4);
+    static constexpr int kQSlots = SMALL ? 2 : D == 128 ? 4 : 8;
     static constexpr int kLStages = SMALL ? 2 : 4;
     static constexpr int kRing = SMALL ? 8 : 4;                // units handed out ahead
+    static constexpr int kS = SMALL ? 4 : 3;                   // S buffers, products in turn
     static constexpr int kMiscBytes = kRing * sizeof(Blk) + kLStages * (kTile * 4 + 16) + (kPlanes ? 2 * kTile * 4 : 0) +
-                                      (kPlanes ? kExpStages * kTile : 0) + 704;
+                                      (kPlanes ? kExpStages * kTile : 0) + (SMALL ? 0 : 2 * kUnit * 4) + 704;
     static constexpr int kFit = (232448 - kMiscBytes - kQSlots * kQBytes) / kKBytes;
-    static constexpr int kKSlots = kFit < (SMALL ? 12 : 8) ? kFit : (SMALL ? 12 : 8);
-    static_assert(kFit >= 4, "shared memory");
+    static constexpr int kKSlots = !SMALL ? 2 : kFit < 12 ? kFit : 12;
+    static_assert(kFit >= (SMALL ? 4 : 2), "shared memory");
     static constexpr int kQ = kKSlots * kKBytes;
     static constexpr int kL = kQ + kQSlots * kQBytes;          // -lse log2 e of a tile's columns
     static_assert(kL >= 16384 * 8, "the plan's costs of up to 16384 requests");
     static constexpr int kCf = kL + kLStages * kTile * 4;      // planes: the columns' scales
     static constexpr int kExps = kCf + (kPlanes ? 2 * kTile * 4 : 0);
     static constexpr int kBlks = kExps + (kPlanes ? kExpStages * kTile : 0);
-    static constexpr int kBars = kBlks + kRing * static_cast<int>(sizeof(Blk));
+    static constexpr int kXch = kBlks + kRing * static_cast<int>(sizeof(Blk));   // sums of the tiles' second halves
+    static constexpr int kBars = kXch + (SMALL ? 0 : 2 * kUnit * 4);
 };
 
-template <int K, int Q, int L, int U>
+template <int K, int Q, int L, int U, int S>
 struct Bars {
     uint64_t k_full[K], k_empty[K], q_full[Q], q_empty[Q], l_full[L], l_empty[L];
-    uint64_t s_full[2][2], s_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages], x_empty[kExpStages];
+    uint64_t s_full[S], s_empty[S], kt_full[2], k_idle, j_full[2][2], j_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages], x_empty[kExpStages];
     uint64_t drain;
     uint32_t odd[L];                  // a column of the stage adds nothing
     uint32_t tmem;
@@ -241,7 +250,7 @@ __device__ __forceinline__ Start plan_few(const WeighParams& p) {
 }
 
 // cost: shared memory for R entries.  By all warps.
-template <bool SMALL>
+template <bool SMALL, int kThreads>
 __device__ __forceinline__ void plan(const WeighParams& p, unsigned long long* cost, unsigned long long* wsum,
                                      Start* start) {
     constexpr int kWarps = kThreads / 32;
@@ -402,6 +411,22 @@ __device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32
 #undef SDM_MMA4
 }
 
+// The same four bf16 products with A in tensor memory, 8 columns a step.
+__device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+        "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+        "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
 // kind::f8f6f4: e4m3 A (0 at bit 7), e5m2 B (1 at bit 10), fp32 accumulator
 __device__ __forceinline__ uint32_t idesc_f8(int M, int N) {
     return (1u << 4) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -491,12 +516,13 @@ __device__ __forceinline__ void add_weights(const uint32_t (&x)[32], float c, co
 // The kernel
 // ---------------------------------------------------------------------------
 template <int D, bool E4M3, bool SMALL>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
     weigh_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
                  const __grid_constant__ WeighParams p, const __grid_constant__ Scratch ws) {
     using C = Cfg<D, E4M3, SMALL>;
     constexpr bool kPlanes = C::kPlanes;
-    using B = Bars<C::kKSlots, C::kQSlots, C::kLStages, C::kRing>;
+    constexpr int kSoft = C::kSoft;
+    using B = Bars<C::kKSlots, C::kQSlots, C::kLStages, C::kRing, C::kS>;
     static_assert(C::kBars + sizeof(B) <= 232448, "shared memory");
     extern __shared__ __align__(1024) uint8_t smem[];
     B& bar = *reinterpret_cast<B*>(smem + C::kBars);
@@ -507,17 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned long long* wsum = reinterpret_cast<unsigned long long*>(smem + C::kL + 64);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (warp == 8) {
+    if (warp == kSoft) {
         if (lane == 0) {
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmQ);
         }
-    } else if (warp == 9) {
+    } else if (warp == kSoft + 1) {
         tmem_alloc(&bar.tmem, kTmemCols);
         tmem_relinquish();
-    } else if (warp == 10) {
+    } else if (warp == kSoft + 2) {
         for (int k = lane; k < C::kKSlots; k += 32) {
-            mbar_init(&bar.k_full[k], E4M3 && !SMALL ? 4 : 1);
+            mbar_init(&bar.k_full[k], 1);
             mbar_init(&bar.k_empty[k], 1);
         }
         if (lane < C::kQSlots) {
@@ -526,30 +552,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane < C::kLStages) {
             mbar_init(&bar.l_full[lane], 1);
-            mbar_init(&bar.l_empty[lane], 8);
+            mbar_init(&bar.l_empty[lane], kSoft);
         }
+        if (lane < C::kS) {
+            mbar_init(&bar.s_full[lane], 1);
+            mbar_init(&bar.s_empty[lane], kSoft / 2);
+        }
+        if (lane < 2) mbar_init(&bar.kt_full[lane], D == 128 ? 8 : 4);
         if (lane < 4) {
-            mbar_init(&bar.s_full[0][0] + lane, 1);
-            mbar_init(&bar.s_empty[0][0] + lane, 4);
+            mbar_init(&bar.j_full[0][0] + lane, 4);
+            mbar_init(&bar.j_empty[0][0] + lane, 4);
         }
         if (lane < C::kRing) {
             mbar_init(&bar.blk_full[lane], 1);
-            mbar_init(&bar.blk_empty[lane], 8 + 3);   // the warps that read it
+            mbar_init(&bar.blk_empty[lane], kSoft + 3);   // the warps that read it
         }
         if (lane < kExpStages) {
             mbar_init(&bar.x_full[lane], 1);
             mbar_init(&bar.x_empty[lane], 4);
         }
-        if (lane == 0) mbar_init(&bar.drain, 1);
+        if (lane == 0) {
+            mbar_init(&bar.drain, 1);
+            mbar_init(&bar.k_idle, 1);
+        }
         fence_mbar_init();
     }
     pdl_wait();
     pdl_trigger();
     const bool few = SMALL && p.R <= 32;
-    if (!few) plan<SMALL>(p, reinterpret_cast<unsigned long long*>(smem), wsum, start);
+    if (!few) plan<SMALL, C::kThreads>(p, reinterpret_cast<unsigned long long*>(smem), wsum, start);
     Start st = *start;                // read before the roles use its place
     // rows of a tile that no query row fills are zeros, so that their columns are finite
-    for (int k = tid; k < C::kQSlots * C::kQBytes / 16; k += kThreads)
+    for (int k = tid; k < C::kQSlots * C::kQBytes / 16; k += C::kThreads)
         reinterpret_cast<uint4*>(smem + C::kQ)[k] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     tc_fence_before();
@@ -572,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return b.tiles > 0;
     };
 
-    if (warp == 8) {
+    if (warp == kSoft) {
         // ------------------------------------------------------------------
         // walker: the share's units, and their keys
         // ------------------------------------------------------------------
@@ -714,15 +748,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kExpStages; ++k)
                     if (xr.turn > 0 || k < xr.at) mbar_wait(&bar.x_full[k], k < xr.at ? xr.turn & 1 : (xr.turn & 1) ^ 1);
         }
-    } else if (warp == 9) {
+    } else if (warp == kSoft + 1) {
         // ------------------------------------------------------------------
         // products
         // ------------------------------------------------------------------
         bool ok = true;
         Ring<C::kKSlots> kr;
         Ring<C::kQSlots> qr;          // SMALL: the slot in use
-        Ring<2> sr[2];
+        Ring<C::kS> sr;
         bool any_q = false;
+        uint32_t n_units = 0, n_two = 0;   // units, those of two tiles
         Blk b;
         while (take(ok, b)) {
             if (!(b.flags & U_HAS)) continue;
@@ -735,20 +770,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait_or_fail(p, &bar.q_full[qr.at], qr.full());
                 if (!ok) break;
             }
-            const int k_at[2] = {kr.at, kr.at + 1 == C::kKSlots ? 0 : kr.at + 1};
+            if constexpr (!SMALL) {
+                // the unit's keys into tensor memory, once the products of the
+                // one before have read theirs (for e4m3 the warpgroups do it)
+                if constexpr (!E4M3) {
+                    if (n_units > 0) {
+                        mma_commit_warp(&bar.k_idle);
+                        ok = wait_or_fail(p, &bar.k_idle, (n_units - 1) & 1);
+                    }
+                    for (int t = 0; t < b.tiles && ok; ++t) {
+                        ok = wait_or_fail(p, &bar.k_full[kr.at], kr.full());
+                        if (!ok) break;
+                        const uint64_t a = smem_desc_sw128(smem_u32(smem + kr.at * C::kKBytes), 16, 1024);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            tmem_cp_128x256b_warp(tmem + kTmemK + t * (D / 2) + k * 8,
+                                                  a + (k / 4) * ((kTile * 128) >> 4) + (k % 4) * 2);
+                        mma_commit_warp(&bar.k_empty[kr.at]);
+                        kr.step();
+                    }
+                } else {
+                    for (int t = 0; t < b.tiles && ok; ++t) ok = wait_or_fail(p, &bar.kt_full[t], t == 0 ? n_units & 1 : n_two & 1);
+                    n_two += b.tiles == 2;
+                }
+                ++n_units;
+                if (!ok) break;
+            }
             for (int q = b.q0; q < b.q1 && ok; ++q) {
                 if (!SMALL) ok = wait_or_fail(p, &bar.q_full[qr.at], qr.full());
                 const int N = SMALL ? (b.M + 31) & ~31 : kTile;   // what the weights read
                 for (int t = 0; t < b.tiles && ok; ++t) {
-                    if (q == b.q0) {
-                        ok = wait_or_fail(p, &bar.k_full[kr.at], kr.full());
-                        kr.step();
-                    }
-                    if (ok) ok = wait_or_fail(p, &bar.s_empty[t][sr[t].at], sr[t].empty());
+                    if (SMALL) ok = wait_or_fail(p, &bar.k_full[kr.at], kr.full());
+                    if (ok) ok = wait_or_fail(p, &bar.s_empty[sr.at], sr.empty());
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + t * 256 + sr[t].at * 128;
-                    const uint32_t ka = smem_u32(smem + k_at[t] * C::kKBytes), qa = smem_u32(smem + C::kQ + qr.at * C::kQBytes);
+                    const uint32_t d = tmem + sr.at * 128;
+                    const uint32_t ka = smem_u32(smem + kr.at * C::kKBytes), qa = smem_u32(smem + C::kQ + qr.at * C::kQBytes);
                     if constexpr (kPlanes) {
                         const uint64_t a = D == 128 ? smem_desc_sw128(ka, 16, 1024) : smem_desc_sw64(ka);
                         const uint64_t q_ = D == 128 ? smem_desc_sw128(qa, 16, 1024) : smem_desc_sw64(qa);
@@ -757,15 +814,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int pl = 0; pl < 3; ++pl)
                             issue<true, D / 32>(d, a, q_ + ((pl * C::kPlane) >> 4), id, pl > 0);
                     } else {
-                        const uint64_t a = smem_desc_sw128(ka, 16, 1024), q_ = smem_desc_sw128(qa, 16, 1024);
+                        const uint64_t q_ = smem_desc_sw128(qa, 16, 1024);
                         const uint32_t id = idesc_bf16_f32(kTile, N, false);
 #pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            issue<false, 4>(d, a + h * ((kTile * 128) >> 4), q_ + h * ((kTile * 128) >> 4), id, h > 0);
+                        for (int h = 0; h < D / 64; ++h) {
+                            const uint64_t panel = h * ((kTile * 128) >> 4);
+                            if constexpr (SMALL) issue<false, 4>(d, smem_desc_sw128(ka, 16, 1024) + panel, q_ + panel, id, h > 0);
+                            else issue_ts(d, tmem + kTmemK + t * (D / 2) + h * 32, q_ + panel, id, h > 0);
+                        }
                     }
-                    mma_commit_warp(&bar.s_full[t][sr[t].at]);
-                    sr[t].step();
-                    if (q == b.q1 - 1) mma_commit_warp(&bar.k_empty[k_at[t]]);
+                    mma_commit_warp(&bar.s_full[sr.at]);
+                    sr.step();
+                    if (SMALL) {
+                        mma_commit_warp(&bar.k_empty[kr.at]);
+                        kr.step();
+                    }
                 }
                 if (!SMALL && ok) {
                     mma_commit_warp(&bar.q_empty[qr.at]);
@@ -777,10 +840,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // products in flight end before the tensor memory goes
         mma_commit_warp(&bar.drain);
         mbar_wait(&bar.drain, 0);
-    } else if (warp == 10 || warp == 11) {
+    } else if (warp > kSoft + 1) {
         // ------------------------------------------------------------------
-        // the query rows (warp 10; split into planes: both) and their -lse (warp 11)
+        // the query rows (one warp; split into planes: both) and their -lse
         // ------------------------------------------------------------------
+        const bool rows_warp = warp == kSoft + 2;
         bool ok = true;
         Ring<C::kQSlots> qr;
         Ring<C::kLStages> lr;
@@ -857,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Counted w;
             w.row0 = b.row0;
             w.wide = b.wide;
-            for (int r0 = 4 * (warp - 10); r0 < N; r0 += 8) {
+            for (int r0 = rows_warp ? 0 : 4; r0 < N; r0 += 8) {
                 uint32_t x[4][2];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -936,21 +1000,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (SMALL) {
                 if (!(b.flags & U_NEWQ)) continue;
                 float z[4];
-                if (warp == 11) lse_of(b, 0, z);
+                if (!rows_warp) lse_of(b, 0, z);
                 ok = wait_or_fail(p, &bar.q_empty[qr.at], qr.empty());
                 if (!ok) break;
                 uint8_t* slot = smem + C::kQ + qr.at * C::kQBytes;
-                if (warp == 11) put_lse(b, 0, (b.M + 31) & ~31, z, l2 + qr.at * kTile, &bar.odd[qr.at]);
+                if (!rows_warp) put_lse(b, 0, (b.M + 31) & ~31, z, l2 + qr.at * kTile, &bar.odd[qr.at]);
                 if constexpr (kPlanes) split(b, slot, cf + qr.at * kTile);
-                else if (warp == 10 && p.path) gather(b, 0, slot);
-                if (!kPlanes && warp == 10 && !p.path) {
+                else if (rows_warp && p.path) gather(b, 0, slot);
+                if (!kPlanes && rows_warp && !p.path) {
                     fetch(b, 0, slot, &bar.q_full[qr.at]);
                 } else {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.q_full[qr.at]);
                 }
                 qr.step();
-            } else if (warp == 11) {
+            } else if (!rows_warp) {
                 // a tile's are loaded while the ones before it wait for their place
                 float z[4];
                 lse_of(b, b.q0, z);
@@ -982,20 +1046,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
         }
-        if (!ok && warp == 10 && sent > 0)   // copies in flight land before the CTA may exit
+        if (!ok && sent > 0)   // copies in flight land before the CTA may exit
             for (int k = 0; k < C::kQSlots; ++k)
                 if (qr.turn > 0 || k < qr.at) mbar_wait(&bar.q_full[k], k < qr.at ? qr.turn & 1 : (qr.turn & 1) ^ 1);
-    } else if (warp < 8) {
+    } else {
         // ------------------------------------------------------------------
         // weights: a thread per key
         // ------------------------------------------------------------------
-        const int wg = warp >> 2;
+        const int wg = (warp >> 2) & 1, half = warp >> 3;   // tile of keys; columns 64 half .. unless SMALL
         bool ok = true;
-        Ring<2> sr;
+        Ring<2> jr;
+        Ring<C::kS> sr;
         Ring<C::kQSlots> qr;
         Ring<C::kLStages> lr;
         Ring<kExpStages> xr;
-        Ring<C::kKSlots> kr;
         bool any_q = false;
         const float c0 = p.scale * kLog2e;
         Blk b;
@@ -1035,14 +1099,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if constexpr (E4M3 && !SMALL) {
-                    // the tile's codes as bf16, a key a thread
-                    const Ring<C::kKSlots> first = kr;
-                    if (wg == 1 && mine) kr.step();
-                    if (mine) {
-                        ok = wait_or_fail(p, &bar.k_empty[kr.at], kr.empty());
-                        if (!ok) break;
-                        uint8_t* slot = smem + kr.at * C::kKBytes;
-                        const int row = tid & 127;
+                    // the tile's codes as bf16 into tensor memory, a key a thread: the
+                    // products of its last tile were complete when its S was read
+                    if (mine && half < D / 64) {   // a half of the row each
+                        uint4 x[4];
+                        float s = 1.f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = make_uint4(0, 0, 0, 0);
                         if (held) {
                             int pg = page_of(p.c, b.i, key);
                             if (pg < 0) {
@@ -1050,35 +1113,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 pg = 0;
                             }
                             const size_t at = pool_row(p.c, pg, key) + (static_cast<size_t>(b.g) << p.c.page_shift);
-                            const uint4* src = reinterpret_cast<const uint4*>(p.c.k + at * D);
-                            const float s = scale_of(__ldg(p.c.k_exp + at));
-                            uint4 x[D / 16];
+                            const uint4* src = reinterpret_cast<const uint4*>(p.c.k + at * D + half * 64);
+                            s = scale_of(__ldg(p.c.k_exp + at));
 #pragma unroll
-                            for (int k = 0; k < D / 16; ++k) x[k] = __ldg(src + k);
+                            for (int k = 0; k < 4; ++k) x[k] = __ldg(src + k);
+                        }
+                        tc_fence_after();
+                        uint32_t z[32];
 #pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                                uint32_t z[8];
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(y[e >> 1] >> (16 * (e & 1)))));
-                                    z[e] = f32x2_to_bf16x2(f.x * s, f.y * s);
-                                }
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int chunk = 2 * k + e;
-                                    *reinterpret_cast<uint4*>(slot + (chunk / 8) * (kTile * 128) + row * 128 +
-                                                              (((chunk & 7) ^ (row & 7)) << 4)) =
-                                        make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
-                                }
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(y[e >> 1] >> (16 * (e & 1)))));
+                                z[8 * k + e] = f32x2_to_bf16x2(f.x * s, f.y * s);
                             }
                         }
-                        fence_proxy_async_smem();
+                        tmem_st32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemK + wg * (D / 2) + half * 32, z);
+                        tmem_st_wait();
+                        tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.k_full[kr.at]);
+                        if (lane == 0) mbar_arrive(&bar.kt_full[wg]);
                     }
-                    kr = first;
-                    for (int t = 0; t < b.tiles; ++t) kr.step();
                 }
                 for (int q = b.q0; q < b.q1 && ok; ++q) {
                     const float* lq = l2 + (SMALL ? qr.at : lr.at) * kTile;
@@ -1086,6 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = wait_or_fail(p, &bar.l_full[lr.at], lr.full());
                         if (!ok) break;
                     }
+                    if (wg == 1) sr.step();           // the other warpgroup's
                     if (mine) {
                         const int cols = SMALL ? b.M : p.sub;
                         // columns [lo, hi) see this key
@@ -1098,33 +1155,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (end * p.group < b.M) hi = min(hi, static_cast<int>(max(end, 0ll)) * p.group - first);
                         }
                         some = __any_sync(0xffffffffu, some || lo > 0 || hi < min(cols, b.M - first));
-                        ok = wait_or_fail(p, &bar.s_full[wg][sr.at], sr.full());
+                        ok = wait_or_fail(p, &bar.s_full[sr.at], sr.full());
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t s_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 256 + sr.at * 128;
-                        const int N = (cols + 31) & ~31;
+                        const uint32_t s_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + sr.at * 128;
                         float2 acc[4] = {};
                         const float4* lp = reinterpret_cast<const float4*>(lq);
                         const float4* fp = reinterpret_cast<const float4*>(cf + qr.at * kTile);
-                        // 32 columns are loaded while the 32 before them are summed
-                        uint32_t x[2][32];
-                        tmem_ld32(s_at, x[0]);
+                        auto add = [&](const uint32_t (&x)[32], int at) {   // 32 columns from `at`
+                            if (!some) add_weights<kPlanes, false>(x, c, lp + at / 4, fp + at / 4, 0, 0, acc);
+                            else add_weights<kPlanes, true>(x, c, lp + at / 4, fp + at / 4, lo - at, hi - at, acc);
+                        };
+                        if constexpr (SMALL) {
+                            // 32 columns are loaded while the 32 before them are summed
+                            const int N = (cols + 31) & ~31;
+                            uint32_t x[2][32];
+                            tmem_ld32(s_at, x[0]);
 #pragma unroll 1
-                        for (int c1 = 0; c1 < N; c1 += 64) {
-                            tmem_ld_wait();
-                            if (c1 + 32 < N) tmem_ld32(s_at + c1 + 32, x[1]);
-                            if (!some) add_weights<kPlanes, false>(x[0], c, lp + c1 / 4, fp + c1 / 4, 0, 0, acc);
-                            else add_weights<kPlanes, true>(x[0], c, lp + c1 / 4, fp + c1 / 4, lo - c1, hi - c1, acc);
-                            if (c1 + 32 >= N) break;
-                            tmem_ld_wait();
-                            if (c1 + 64 < N) tmem_ld32(s_at + c1 + 64, x[0]);
-                            if (!some) add_weights<kPlanes, false>(x[1], c, lp + c1 / 4 + 8, fp + c1 / 4 + 8, 0, 0, acc);
-                            else add_weights<kPlanes, true>(x[1], c, lp + c1 / 4 + 8, fp + c1 / 4 + 8, lo - c1 - 32, hi - c1 - 32, acc);
+                            for (int c1 = 0; c1 < N; c1 += 64) {
+                                tmem_ld_wait();
+                                if (c1 + 32 < N) tmem_ld32(s_at + c1 + 32, x[1]);
+                                add(x[0], c1);
+                                if (c1 + 32 >= N) break;
+                                tmem_ld_wait();
+                                if (c1 + 64 < N) tmem_ld32(s_at + c1 + 64, x[0]);
+                                add(x[1], c1 + 32);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int at = half * 64; at < half * 64 + 64; at += 32) {
+                                uint32_t x[32];
+                                tmem_ld32(s_at + at, x);
+                                tmem_ld_wait();
+                                add(x, at);
+                            }
                         }
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.s_empty[wg][sr.at]);
+                        if (lane == 0) mbar_arrive(&bar.s_empty[sr.at]);
                         sr.step();
+                        if (wg == 0 && b.tiles == 2) sr.step();
                         // the tiles' sums with what each addition loses: a key of a long
                         // prompt is the sum of thousands of weights
                         const float2 half = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
@@ -1141,6 +1211,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
             }
+            if constexpr (!SMALL) {
+                // the two halves of the columns
+                float* xch = reinterpret_cast<float*>(smem + C::kXch) + jr.at * kUnit + wg * kTile + (tid & 127);
+                if (half == 1) {
+                    ok = wait_or_fail(p, &bar.j_empty[wg][jr.at], jr.empty());
+                    if (!ok) break;
+                    *xch = sum;
+                } else {
+                    ok = wait_or_fail(p, &bar.j_full[wg][jr.at], jr.full());
+                    if (!ok) break;
+                    sum += *xch;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(half == 1 ? &bar.j_full[wg][jr.at] : &bar.j_empty[wg][jr.at]);
+                jr.step();
+                if (half == 1) continue;
+            }
             if (held) {
                 if ((b.flags & U_FIRST) && (b.flags & U_LAST)) p.mass_out[o] = old + sum;
                 else ws.sum[(static_cast<size_t>(blockIdx.x) * 2 + ((b.flags & U_FIRST) ? 1 : 0)) * kUnit + wg * kTile + (tid & 127)] = sum;
@@ -1150,7 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kSoft + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -1218,7 +1305,7 @@ bool encode_k(CUtensorMap* map, const CacheView& c) {
 template <int D, bool E4M3, bool SMALL>
 cudaError_t launch_one(const WeighParams& p, void* work, cudaStream_t s) {
     using C = Cfg<D, E4M3, SMALL>;
-    constexpr int kTotal = C::kBars + static_cast<int>(sizeof(Bars<C::kKSlots, C::kQSlots, C::kLStages, C::kRing>));
+    constexpr int kTotal = C::kBars + static_cast<int>(sizeof(Bars<C::kKSlots, C::kQSlots, C::kLStages, C::kRing, C::kS>));
     static const cudaError_t raised = cudaFuncSetAttribute(weigh_kernel<D, E4M3, SMALL>,
                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kTotal);
     if (raised != cudaSuccess) return raised;
@@ -1232,7 +1319,7 @@ cudaError_t launch_one(const WeighParams& p, void* work, cudaStream_t s) {
         ws.part = static_cast<Part*>(work);
         ws.sum = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + align256(sizeof(Part) * grid));
     }
-    const cudaError_t e = launch_pdl(weigh_kernel<D, E4M3, SMALL>, dim3(grid), dim3(kThreads), kTotal, s, tmK, tmQ, p, ws);
+    const cudaError_t e = launch_pdl(weigh_kernel<D, E4M3, SMALL>, dim3(grid), dim3(C::kThreads), kTotal, s, tmK, tmQ, p, ws);
     if (e != cudaSuccess || SMALL) return e;
     return launch_pdl(weigh_join_kernel, dim3(grid), dim3(kUnit), 0, s, p, ws, grid);
 }
