@@ -790,8 +790,8 @@ sdm_status sdm_token_logprobs(const void* target, sdm_dtype dtT, int row_capacit
  *      kv_heads.
  * Out: mass_out, the same shape; may be mass.
  * Scores and sums are fp32, in an order that depends on the sizes alone.  A
- * row with lse -inf saw nothing and adds nothing; one with lse +inf or NaN
- * adds what the formula gives.
+ * row whose lse is -inf or NaN adds nothing; infinite or NaN scores beside an
+ * lse of +inf, and infinities in q over an e4m3 cache, count as NaN.
  * ws:  sdm_workspace_size(SDM_OP_ATTEND_WEIGHT, R, max_count, H, head_dim, rows,
  *      kv_heads, 0) bytes.
  * Device checks as in sdm_attend; a count outside [0, max_count] or past the

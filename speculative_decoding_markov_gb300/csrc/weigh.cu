@@ -128,7 +128,7 @@ struct Bars {
     uint64_t k_full[K], k_empty[K], q_full[Q], q_empty[Q], l_full[L], l_empty[L];
     uint64_t s_full[S], s_empty[S], kt_full[2], k_idle, j_full[2][2], j_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages], x_empty[kExpStages];
     uint64_t drain;
-    uint32_t odd[L];                  // a column of the stage adds nothing
+    uint32_t live[L][5];              // columns of the stage that add something; whether some do not
     uint32_t tmem;
 };
 
@@ -475,17 +475,11 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
 }
 
 // Adds the weights of 32 columns: 2^(c f x + l), f the columns' scales (planes),
-// l their -lse log2 e.  MASKED: only columns lo .. hi - 1, and none whose l is
-// -infinity, whatever x is.
-template <bool PLANES, bool MASKED>
-__device__ __forceinline__ void add_weights(const uint32_t (&x)[32], float c, const float4* l4, const float4* f4, int lo,
-                                            int hi, float2 (&acc)[4]) {
+// l their -lse log2 e.
+template <bool PLANES>
+__device__ __forceinline__ void add_weights(const uint32_t (&x)[32], float c, const float4* l4, const float4* f4,
+                                            float2 (&acc)[4]) {
     const float2 cc = make_float2(c, c);
-    uint32_t see = 0;
-    if (MASKED) {
-        const int from = max(lo, 0);
-        see = (from >= 32 ? 0u : ~0u << from) & (hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u);
-    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const float4 l = l4[k];
@@ -499,17 +493,19 @@ __device__ __forceinline__ void add_weights(const uint32_t (&x)[32], float c, co
             a = fma2(a, cc, make_float2(l.x, l.y));
             b = fma2(b, cc, make_float2(l.z, l.w));
         }
-        a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-        b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
-        if constexpr (MASKED) {
-            if (!((see >> (4 * k)) & 1u) || l.x == -INFINITY) a.x = 0.f;
-            if (!((see >> (4 * k + 1)) & 1u) || l.y == -INFINITY) a.y = 0.f;
-            if (!((see >> (4 * k + 2)) & 1u) || l.z == -INFINITY) b.x = 0.f;
-            if (!((see >> (4 * k + 3)) & 1u) || l.w == -INFINITY) b.y = 0.f;
-        }
-        acc[2 * (k & 1)] = add2(acc[2 * (k & 1)], a);
-        acc[2 * (k & 1) + 1] = add2(acc[2 * (k & 1) + 1], b);
+        acc[2 * (k & 1)] = add2(acc[2 * (k & 1)], make_float2(fast_exp2(a.x), fast_exp2(a.y)));
+        acc[2 * (k & 1) + 1] = add2(acc[2 * (k & 1) + 1], make_float2(fast_exp2(b.x), fast_exp2(b.y)));
     }
+}
+
+// Scores of columns that a key is not seen by become -infinity (whose weight is
+// 0 whatever their l, which is no NaN and not +infinity): all but lo .. hi - 1,
+// and those whose bit is not set in `live`.
+__device__ __forceinline__ void hide(uint32_t (&x)[32], int lo, int hi, uint32_t live) {
+    const int from = max(lo, 0);
+    live &= (from >= 32 ? 0u : ~0u << from) & (hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = (live >> k) & 1u ? x[k] : 0xff800000u;
 }
 
 // ---------------------------------------------------------------------------
@@ -874,19 +870,21 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 }
             }
         };
-        // -lse log2 e, -infinity for columns that add nothing; `odd`: there are
-        // such below column N, whose scores may be anything
-        auto put_lse = [&](const Blk& b, int q, int N, const float (&z)[4], float* to, uint32_t* odd) {
-            bool none = false;
-            const int live = min(b.M - q * p.sub, p.sub);
+        // -lse log2 e, -infinity for columns that add nothing, which are noted
+        // (but for those behind a full tile's rows, where the scores are 0)
+        auto put_lse = [&](const Blk& b, int q, const float (&z)[4], float* to, uint32_t (&live)[5]) {
+            const bool full = b.M - q * p.sub >= p.sub;
+            uint32_t all = ~0u;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int col = k * 32 + lane;
-                none |= z[k] == -INFINITY && col < (live < p.sub ? N : p.sub);   // beyond a full tile's rows are zeros
-                to[col] = z[k] == -INFINITY ? -INFINITY : -z[k] * kLog2e;
+                const bool adds = z[k] > -INFINITY;             // a NaN does not
+                to[col] = adds ? -z[k] * kLog2e : -INFINITY;
+                const uint32_t bits = __ballot_sync(0xffffffffu, adds || (full && col >= p.sub));
+                if (lane == 0) live[k] = bits;
+                all &= bits;
             }
-            none = __any_sync(0xffffffffu, none);
-            if (lane == 0) *odd = none;
+            if (lane == 0) live[4] = all != ~0u;
         };
         // rows of tile q of the head into a slot, 16 bytes at a time, zeros up to N
         auto gather = [&](const Blk& b, int q, uint8_t* slot) {
@@ -1004,7 +1002,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 ok = wait_or_fail(p, &bar.q_empty[qr.at], qr.empty());
                 if (!ok) break;
                 uint8_t* slot = smem + C::kQ + qr.at * C::kQBytes;
-                if (!rows_warp) put_lse(b, 0, (b.M + 31) & ~31, z, l2 + qr.at * kTile, &bar.odd[qr.at]);
+                if (!rows_warp) put_lse(b, 0, z, l2 + qr.at * kTile, bar.live[qr.at]);
                 if constexpr (kPlanes) split(b, slot, cf + qr.at * kTile);
                 else if (rows_warp && p.path) gather(b, 0, slot);
                 if (!kPlanes && rows_warp && !p.path) {
@@ -1015,20 +1013,48 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 }
                 qr.step();
             } else if (!rows_warp) {
-                // a tile's are loaded while the ones before it wait for their place
-                float z[4];
-                lse_of(b, b.q0, z);
-                for (int q = b.q0; q < b.q1 && ok; ++q) {
-                    float next[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (q + 1 < b.q1) lse_of(b, q + 1, next);
+                // a tile's are loaded two tiles before their place is free; without
+                // a path the lane's columns only step from tile to tile (looked up
+                // anew in each, a tile took this warp 1600 clocks)
+                const float* at[4];
+                int left[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool in = col_wp[k] < tokens;
+                    left[k] = in ? b.M / p.group - b.q0 * tokens - col_wp[k] : 0;
+                    at[k] = p.lse + (b.row0 + static_cast<long long>(b.q0) * tokens + (in ? col_wp[k] : 0)) * p.H +
+                            b.g * p.group + col_h[k];
+                }
+                const int64_t step = static_cast<int64_t>(tokens) * p.H;
+                auto load = [&](int q, float (&z)[4]) {
+                    if (p.path) {
+                        lse_of(b, q, z);
+                        return;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        z[k] = -INFINITY;
+                        if (left[k] > 0) z[k] = __ldg(at[k]);
+                        at[k] += step;
+                        left[k] -= tokens;
+                    }
+                };
+                auto put = [&](int q, const float (&z)[4]) {
                     ok = wait_or_fail(p, &bar.l_empty[lr.at], lr.empty());
-                    if (!ok) break;
-                    put_lse(b, q, kTile, z, l2 + lr.at * kTile, &bar.odd[lr.at]);
+                    if (!ok) return;
+                    put_lse(b, q, z, l2 + lr.at * kTile, bar.live[lr.at]);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.l_full[lr.at]);
                     lr.step();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) z[k] = next[k];
+                };
+                float z[2][4];
+                load(b.q0, z[0]);
+                for (int q = b.q0; q < b.q1 && ok; q += 2) {
+                    if (q + 1 < b.q1) load(q + 1, z[1]);
+                    put(q, z[0]);
+                    if (!ok || q + 1 >= b.q1) break;
+                    if (q + 2 < b.q1) load(q + 2, z[0]);
+                    put(q + 1, z[1]);
                 }
             } else {
                 for (int q = b.q0; q < b.q1 && ok; ++q) {
@@ -1136,6 +1162,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         if (lane == 0) mbar_arrive(&bar.kt_full[wg]);
                     }
                 }
+                // tiles q_lo .. q_hi - 1 of the rows see all of the warp's keys
+                int q_lo = 0, q_hi = 0x7fffffff;
+                {
+                    const int key0 = b.k0 + wg * kTile + (warp & 3) * 32, key1 = key0 + 31;
+                    if (key1 > b.ctx) q_lo = ((key1 - b.ctx) * p.group + p.sub - 1) / p.sub;
+                    if (p.window > 0 && key1 >= p.sinks) {
+                        const long long end = (static_cast<long long>(key0) - b.ctx + p.window) * p.group;
+                        if (end < b.M) q_hi = end <= 0 ? 0 : static_cast<int>(end / p.sub);
+                    }
+                }
                 for (int q = b.q0; q < b.q1 && ok; ++q) {
                     const float* lq = l2 + (SMALL ? qr.at : lr.at) * kTile;
                     if (!SMALL) {
@@ -1144,17 +1180,18 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                     }
                     if (wg == 1) sr.step();           // the other warpgroup's
                     if (mine) {
-                        const int cols = SMALL ? b.M : p.sub;
+                        const int cols = SMALL ? b.M : p.sub, first = q * p.sub;
                         // columns [lo, hi) see this key
-                        const int first = q * p.sub;
                         int lo = 0, hi = min(cols, b.M - first);
-                        bool some = bar.odd[SMALL ? qr.at : lr.at];   // (junk columns, too)
-                        if (key > b.ctx) lo = (key - b.ctx) * p.group - first;
-                        if (p.window > 0 && key >= p.sinks) {
-                            const long long end = static_cast<long long>(key) - b.ctx + p.window;   // rows below it see the key
-                            if (end * p.group < b.M) hi = min(hi, static_cast<int>(max(end, 0ll)) * p.group - first);
+                        const uint32_t* live = bar.live[SMALL ? qr.at : lr.at];
+                        const bool some = q < q_lo || q >= q_hi || live[4];
+                        if (some) {
+                            if (key > b.ctx) lo = (key - b.ctx) * p.group - first;
+                            if (p.window > 0 && key >= p.sinks) {
+                                const long long end = static_cast<long long>(key) - b.ctx + p.window;   // rows below it see the key
+                                if (end * p.group < b.M) hi = min(hi, static_cast<int>(max(end, 0ll)) * p.group - first);
+                            }
                         }
-                        some = __any_sync(0xffffffffu, some || lo > 0 || hi < min(cols, b.M - first));
                         ok = wait_or_fail(p, &bar.s_full[sr.at], sr.full());
                         if (!ok) break;
                         tc_fence_after();
@@ -1162,9 +1199,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         float2 acc[4] = {};
                         const float4* lp = reinterpret_cast<const float4*>(lq);
                         const float4* fp = reinterpret_cast<const float4*>(cf + qr.at * kTile);
-                        auto add = [&](const uint32_t (&x)[32], int at) {   // 32 columns from `at`
-                            if (!some) add_weights<kPlanes, false>(x, c, lp + at / 4, fp + at / 4, 0, 0, acc);
-                            else add_weights<kPlanes, true>(x, c, lp + at / 4, fp + at / 4, lo - at, hi - at, acc);
+                        auto add = [&](uint32_t (&x)[32], int at) {   // 32 columns from `at`
+                            if (some) hide(x, lo - at, hi - at, live[at / 32]);
+                            add_weights<kPlanes>(x, c, lp + at / 4, fp + at / 4, acc);
                         };
                         if constexpr (SMALL) {
                             // 32 columns are loaded while the 32 before them are summed
@@ -1181,18 +1218,21 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                                 if (c1 + 64 < N) tmem_ld32(s_at + c1 + 64, x[0]);
                                 add(x[1], c1 + 32);
                             }
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.s_empty[sr.at]);
                         } else {
-#pragma unroll 1
-                            for (int at = half * 64; at < half * 64 + 64; at += 32) {
-                                uint32_t x[32];
-                                tmem_ld32(s_at + at, x);
-                                tmem_ld_wait();
-                                add(x, at);
-                            }
+                            uint32_t x[32];
+                            tmem_ld32(s_at + half * 64, x);
+                            tmem_ld_wait();
+                            add(x, half * 64);
+                            tmem_ld32(s_at + half * 64 + 32, x);
+                            tmem_ld_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.s_empty[sr.at]);
+                            add(x, half * 64 + 32);
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.s_empty[sr.at]);
                         sr.step();
                         if (wg == 0 && b.tiles == 2) sr.step();
                         // the tiles' sums with what each addition loses: a key of a long
