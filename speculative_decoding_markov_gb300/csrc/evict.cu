@@ -4,7 +4,8 @@
 // A cluster of CTAs per (request, kv head), each with an equal run of slots.
 //   1. Slots become 32-bit keys in order of their weight; a first or last
 //      position's is the largest.  The keep-th largest key is found by its
-//      digits (11, 11 and 10 bits): a histogram each, summed over the cluster.
+//      digits, the first of 11 bits, which tells weights of a few octaves apart:
+//      a histogram each, summed over the cluster.
 //   2. Slots above that key are kept, and of its equals the lowest, by counts
 //      in slot order.  Kept tokens that lie in front of slot `keep` stay where
 //      they are; the j-th of the others moves into the j-th slot that becomes
@@ -24,15 +25,28 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMoves = 4;          // moves of a thread in flight together
+constexpr int kList = 1024;        // keys that share the first digits
+constexpr int kFew = 16;           // slots to go that are looked for one by one
 
+// Of a run of slots: those above the keep-th largest key and equal to it, in
+// front of slot `keep` and behind.
+struct Counts {
+    int above_lo, equal_lo, above_hi, equal_hi;
+};
+
+template <int THREADS>
 struct Shared {
-    int hist[kBins];
-    int warp[kWarps][3];
-    int mine[4];           // of this CTA: equals; then holes, movers
-    int pick, before;
+    int hist[kBins];       // this CTA's
+    int all[kBins];        // the cluster's, in its first CTA
+    int sum[THREADS / 32];
+    Counts warp[THREADS / 32];
+    Counts mine;
+    int pick, before, last, listed;
+    uint32_t list[kList];
+    unsigned long long least[2][THREADS / 32];
+    int gone[kFew], src[kFew], dst[kFew];
 };
 
 struct Held {              // a request's slots
@@ -61,8 +75,10 @@ __device__ __forceinline__ Held held_of(const EvictParams& p, int i) {
     return h;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
-    __shared__ Shared sh;
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const EvictParams p) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ Shared<kThreads> sh;
     extern __shared__ uint32_t keys[];
     pdl_wait();
     pdl_trigger();
@@ -97,6 +113,15 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     // The keys stay in shared memory; a run of slots that does not fit is
     // looked up again wherever its keys are wanted.
     const bool fits = per <= p.room;
+    const bool few = cut && C == 1 && fits && h.n - keep <= kFew;
+    if (cut && !few) {
+        for (int b = tid; b < kBins; b += kThreads) {
+            sh.hist[b] = 0;
+            sh.all[b] = 0;
+        }
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+    }
     for (int b = s0; b < s1; b += 4 * kThreads) {
         int32_t at[4];
         float m[4];
@@ -112,7 +137,11 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
         for (int j = 0; j < 4; ++j) {
             const int s = b + j * kThreads + tid;
             if (s >= s1) continue;
-            if (cut && fits) keys[s - s0] = key(at[j], m[j]);
+            if (cut) {
+                const uint32_t k = key(at[j], m[j]);
+                if (fits) keys[s - s0] = k;
+                if (!few) atomicAdd(&sh.hist[k >> 21], 1);
+            }
             if (s < keep && !(same && s < h.ctx)) {   // those that stay; the others' places are overwritten below
                 mass_out[s] = m[j];
                 pos_out[s] = at[j];
@@ -121,130 +150,254 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     }
     if (!cut) return;   // the whole cluster
     auto key_of = [&](int s) { return fits ? keys[s - s0] : key(where(s), __ldcg(mass + s)); };
-    // 1. the keep-th largest key
-    uint32_t found = 0, mask = 0;
-    int need = keep;       // rank of the wanted key among those that share the digits found
-#pragma unroll 1
-    for (int d = 0; d < 3; ++d) {
-        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
-        const uint32_t digits = d == 2 ? 1023u : 2047u;
-        for (int b = tid; b < kBins; b += kThreads) sh.hist[b] = 0;
-        __syncthreads();
-        for (int s = s0 + tid; s < s1; s += kThreads) {
-            const uint32_t k = key_of(s);
-            if ((k & mask) == found) atomicAdd(&sh.hist[(k >> shift) & digits], 1);
-        }
-        if (C > 1) cluster.sync();
-        else __syncthreads();
-        // four bins a thread, from the top; their counts over the cluster
-        int n4[4], all = 0;
-        const int b0 = kBins - 4 - 4 * tid;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            n4[j] = 0;
-            for (int k = 0; k < C; ++k) n4[j] += C > 1 ? cluster.map_shared_rank(sh.hist, k)[b0 + 3 - j] : sh.hist[b0 + 3 - j];
-            all += n4[j];
-        }
-        int incl = all;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) sh.warp[warp][0] = incl;
-        __syncthreads();
-        int before = incl - all;
-        for (int w = 0; w < warp; ++w) before += sh.warp[w][0];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (before < need && need <= before + n4[j]) {
-                sh.pick = b0 + 3 - j;
-                sh.before = before;
-            }
-            before += n4[j];
-        }
-        if (C > 1) cluster.sync();
-        else __syncthreads();
-        found |= static_cast<uint32_t>(sh.pick) << shift;
-        mask |= digits << shift;
-        need -= sh.before;
-        __syncthreads();
-    }
-    // 2. which slots are kept: above `found`, and the first `need` of its equals
-    // a warp takes neighbouring groups of 32 slots
-    const int groups = (s1 - s0 + 31) / 32, each = (groups + kWarps - 1) / kWarps;
-    const int w0 = min(groups, warp * each), w1 = min(groups, w0 + each);
-    int equals = 0;
-    for (int k = w0; k < w1; ++k) {
-        const int s = s0 + k * 32 + lane;
-        equals += __popc(__ballot_sync(0xffffffffu, s < s1 && key_of(s) == found));
-    }
-    if (lane == 0) sh.warp[warp][0] = equals;
-    __syncthreads();
-    if (tid == 0) {
-        int sum = 0;
-        for (int w = 0; w < kWarps; ++w) sum += sh.warp[w][0];
-        sh.mine[0] = sum;
-    }
-    if (C > 1) cluster.sync();
-    else __syncthreads();
-    int eq = 0;
-    for (int k = 0; k < rank; ++k) eq += cluster.map_shared_rank(sh.mine, k)[0];
-    for (int w = 0; w < warp; ++w) eq += sh.warp[w][0];
-    const int eq0 = eq;
-    auto kept_of = [&](int s, int& eq) {   // by the whole warp, in order
-        const uint32_t k = s < s1 ? key_of(s) : 0u;
-        const bool even = s < s1 && k == found;
-        const unsigned who = __ballot_sync(0xffffffffu, even);
-        const bool r = s < s1 && (k > found || (even && eq + __popc(who & ((1u << lane) - 1)) < need));
-        eq += __popc(who);
-        return r;
-    };
-    int holes = 0, movers = 0;
-    for (int k = w0; k < w1; ++k) {
-        const int s = s0 + k * 32 + lane;
-        const bool kept = kept_of(s, eq);
-        holes += __popc(__ballot_sync(0xffffffffu, s < min(s1, keep) && !kept));
-        movers += __popc(__ballot_sync(0xffffffffu, s >= keep && kept));
-    }
-    if (lane == 0) {
-        sh.warp[warp][1] = holes;
-        sh.warp[warp][2] = movers;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int a = 0, b = 0;
-        for (int w = 0; w < kWarps; ++w) a += sh.warp[w][1], b += sh.warp[w][2];
-        sh.mine[1] = a;
-        sh.mine[2] = b;
-    }
-    if (C > 1) cluster.sync();
-    else __syncthreads();
-    int hole = 0, mover = 0, total = 0;
-    for (int k = 0; k < C; ++k) {
-        const int* o = C > 1 ? cluster.map_shared_rank(sh.mine, k) : sh.mine;
-        if (k < rank) hole += o[1], mover += o[2];
-        total += o[1];
-    }
-    for (int w = 0; w < warp; ++w) hole += sh.warp[w][1], mover += sh.warp[w][2];
+    int total = 0;         // moves
     int32_t* from = p.moves + 2 * static_cast<size_t>(item) * p.most;
     int32_t* to = from + p.most;
-    eq = eq0;
-    for (int k = w0; k < w1; ++k) {
-        const int s = s0 + k * 32 + lane;
-        const bool kept = kept_of(s, eq);
-        const unsigned is_hole = __ballot_sync(0xffffffffu, s < min(s1, keep) && !kept);
-        const unsigned is_mover = __ballot_sync(0xffffffffu, s >= keep && kept);
-        const unsigned lower = (1u << lane) - 1;
-        if ((is_hole >> lane) & 1u) to[hole + __popc(is_hole & lower)] = s;
-        if ((is_mover >> lane) & 1u) from[mover + __popc(is_mover & lower)] = s;
-        hole += __popc(is_hole);
-        mover += __popc(is_mover);
+    if (few) {
+        // A full cache that has grown by a few tokens (every cycle of decoding):
+        // the slots that go, one by one: the least key, among equals the last
+        // slot.  64 caches of 2048 and up to 8: 11.4 us, by digits 17.9.
+        const int e = h.n - keep;
+        auto mark = [&](int s) { return (static_cast<unsigned long long>(keys[s]) << 32) | static_cast<uint32_t>(~s); };
+        unsigned long long best = ~0ull;
+        for (int s = tid; s < h.n; s += kThreads) best = min(best, mark(s));   // of the keys this thread wrote
+        for (int r = 0; r < e; ++r) {
+            const uint32_t hi = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
+            const uint32_t low =
+                __reduce_min_sync(0xffffffffu, (best >> 32) == hi ? static_cast<uint32_t>(best) : 0xffffffffu);
+            if (lane == 0) sh.least[r & 1][warp] = (static_cast<unsigned long long>(hi) << 32) | low;
+            __syncthreads();
+            unsigned long long least = sh.least[r & 1][0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) least = min(least, sh.least[r & 1][w]);
+            const int s = static_cast<int>(~static_cast<uint32_t>(least));
+            if (tid == 0) sh.gone[r] = s;
+            if (best == least) {
+                best = ~0ull;
+                for (int t = tid; t < h.n; t += kThreads) {
+                    const unsigned long long x = mark(t);
+                    if (x > least) best = min(best, x);
+                }
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int s = lane < e ? sh.gone[lane] : 0x7fffffff;
+            int before = 0;
+            bool stays = true;      // slot keep + lane
+            for (int r = 0; r < e; ++r) {
+                const int o = __shfl_sync(0xffffffffu, s, r);
+                before += o < s;
+                stays = stays && o != keep + lane;
+            }
+            const unsigned moves = __ballot_sync(0xffffffffu, lane < e && stays);
+            if (s < keep) sh.dst[before] = s;
+            if ((moves >> lane) & 1u) sh.src[__popc(moves & ((1u << lane) - 1))] = keep + lane;
+            if (lane == 0) sh.before = __popc(moves);
+        }
+        __syncthreads();
+        total = sh.before;
+    } else {
+        // 1. the keep-th largest key, digit by digit: `need` of the keys that share
+        // the digits found are wanted
+        uint32_t found = 0, mask = 0;
+        int need = keep;
+        Shared<kThreads>* first = C > 1 ? cluster.map_shared_rank(&sh, 0) : &sh;
+        auto meet = [&]() {
+            if (C > 1) cluster.sync();
+            else __syncthreads();
+        };
+        // 11 bits, then 7 at a time by one warp, or in clusters, whose every digit
+        // costs three of their barriers, 11 and 10
+#pragma unroll 1
+        for (int d = 0, shift = 21; ; ++d) {
+            const int width = d == 0 ? 11 : C == 1 ? 7 : min(shift, 11);
+            if (d > 0) shift -= width;
+            const int bins = 1 << width;
+            if (d > 0) {   // the first digit's were counted as the keys were made
+                for (int b = tid; b < bins; b += kThreads) {
+                    sh.hist[b] = 0;
+                    if (C > 1 && rank == 0) sh.all[b] = 0;
+                }
+                if (C > 1) cluster.sync();   // the first CTA's counts are clear
+                else __syncthreads();
+                const int listed = d > 1 ? sh.listed : kList + 1;
+                if (listed <= kList) {
+                    for (int s = tid; s < listed; s += kThreads)
+                        if ((sh.list[s] & mask) == found) atomicAdd(&sh.hist[(sh.list[s] >> shift) & (bins - 1)], 1);
+                } else {
+#pragma unroll 4
+                    for (int s = s0 + tid; s < s1; s += kThreads) {
+                        const uint32_t k = key_of(s);
+                        if ((k & mask) != found) continue;
+                        atomicAdd(&sh.hist[(k >> shift) & (bins - 1)], 1);
+                        if (d == 1) {
+                            const int at = atomicAdd(&sh.listed, 1);
+                            if (at < kList) sh.list[at] = k;
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            // the bins that have any to the first CTA (each CTA reading all of the
+            // others' bins took 33000 clocks a digit in clusters of 8)
+            if (C > 1) {
+                if (d == 0) cluster.sync();   // the first CTA's counts are clear
+                for (int b = tid; b < bins; b += kThreads)
+                    if (const int n = sh.hist[b]) atomicAdd(&first->all[b], n);
+                cluster.sync();
+            }
+            // the bin of the need-th key from the top
+            const int* hist = C > 1 ? sh.all : sh.hist;
+            const bool wide = bins > 128;
+            if (rank == 0 && (wide || warp == 0)) {
+                constexpr int kPer = kBins / kThreads;   // bins a thread; 4 a lane of one warp for the short digits
+                const int per_bins = wide ? bins / kThreads : 4;
+                const int b0 = bins - per_bins - per_bins * tid;
+                int n[kPer], all = 0;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    n[j] = j < per_bins ? hist[b0 + per_bins - 1 - j] : 0;
+                    all += n[j];
+                }
+                int incl = all;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                int before = incl - all;
+                if (wide) {
+                    if (lane == 31) sh.sum[warp] = incl;
+                    __syncthreads();
+                    for (int w = 0; w < warp; ++w) before += sh.sum[w];
+                }
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    if (before < need && need <= before + n[j]) {
+                        sh.pick = b0 + per_bins - 1 - j;
+                        sh.before = before;
+                        sh.last = need == before + n[j];   // all of the bin
+                    }
+                    before += n[j];
+                }
+            }
+            meet();
+            found |= static_cast<uint32_t>(first->pick) << shift;
+            mask |= static_cast<uint32_t>(bins - 1) << shift;
+            need -= first->before;
+            if (first->last && shift > 0) {
+                // every key with these digits is wanted, so the lower ones need not
+                // be found.  (Not all are 0: fewer than all keys are wanted.)
+                found -= 1;
+                need = 0;
+                break;
+            }
+            if (shift == 0) break;
+            meet();   // before the picks are overwritten
+        }
+        // 2. which slots are kept: above `found`, and the first `need` of its equals.
+        // A warp takes neighbouring groups of 32 slots, and a lane then one group of
+        // 32 that it has looked at: few instructions a slot bound this kernel.
+        const int groups = (s1 - s0 + 31) / 32, each = (groups + kWarps - 1) / kWarps;
+        const int w0 = min(groups, warp * each), w1 = min(groups, w0 + each);
+        // lane k: which slots of group k0 + k are above and equal, and which lie in front of `keep`
+        auto look = [&](int k0, unsigned& above, unsigned& equal, unsigned& valid, unsigned& lo) {
+            above = equal = 0;
+            const int n = min(32, w1 - k0);
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const int s = s0 + (k0 + k) * 32 + lane;
+                const uint32_t x = s < s1 ? key_of(s) : 0u;
+                const unsigned a = __ballot_sync(0xffffffffu, s < s1 && x > found);
+                const unsigned e = __ballot_sync(0xffffffffu, s < s1 && x == found);
+                if (lane == k) {
+                    above = a;
+                    equal = e;
+                }
+            }
+            auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
+            const int s = s0 + (k0 + lane) * 32;
+            valid = lane < n ? below(s1 - s) : 0u;
+            lo = below(keep - s);
+        };
+        unsigned above, equal, valid, lo;
+        Counts c = {};
+        for (int k0 = w0; k0 < w1; k0 += 32) {
+            look(k0, above, equal, valid, lo);
+            c.above_lo += __popc(above & lo);
+            c.equal_lo += __popc(equal & lo);
+            c.above_hi += __popc(above & ~lo);
+            c.equal_hi += __popc(equal & ~lo);
+        }
+        c.above_lo = __reduce_add_sync(0xffffffffu, c.above_lo);
+        c.equal_lo = __reduce_add_sync(0xffffffffu, c.equal_lo);
+        c.above_hi = __reduce_add_sync(0xffffffffu, c.above_hi);
+        c.equal_hi = __reduce_add_sync(0xffffffffu, c.equal_hi);
+        if (lane == 0) sh.warp[warp] = c;
+        __syncthreads();
+        if (C > 1 && tid == 0) {
+            Counts t = {};
+            for (int w = 0; w < kWarps; ++w) {
+                t.above_lo += sh.warp[w].above_lo;
+                t.equal_lo += sh.warp[w].equal_lo;
+                t.above_hi += sh.warp[w].above_hi;
+                t.equal_hi += sh.warp[w].equal_hi;
+            }
+            sh.mine = t;
+        }
+        if (C > 1) cluster.sync();
+        // what stands before this warp's slots: equals, kept ones in front, movers.
+        // Runs are in slot order, so a run's kept equals follow from the equals before it.
+        int eq = 0, kept_lo = 0, mover = 0;
+        {
+            int all_eq = 0, all_kept = 0;
+            auto pass = [&](const Counts& t, int& eq, int& kept, int& movers) {
+                kept += t.above_lo + min(max(need - eq, 0), t.equal_lo);
+                movers += t.above_hi + min(max(need - eq - t.equal_lo, 0), t.equal_hi);
+                eq += t.equal_lo + t.equal_hi;
+            };
+            if (C > 1)
+                for (int k = 0; k < C; ++k) {
+                    const Counts t = *cluster.map_shared_rank(&sh.mine, k);
+                    if (k < rank) pass(t, eq, kept_lo, mover);
+                    pass(t, all_eq, all_kept, total);
+                }
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) pass(sh.warp[w], eq, kept_lo, mover);
+                if (C == 1) pass(sh.warp[w], all_eq, all_kept, total);
+            }
+        }
+        int hole = min(s0 + w0 * 32, keep) - kept_lo;
+        auto scan = [&](int n) {   // exclusive, over the warp
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            return incl - n;
+        };
+        for (int k0 = w0; k0 < w1; k0 += 32) {
+            if (w1 - w0 > 32) look(k0, above, equal, valid, lo);   // else as they are
+            // the group's equals that are still wanted: its lowest ones
+            const int eq_n = __popc(equal), eq_at = eq + scan(eq_n);
+            unsigned kept_eq = equal;
+            for (int k = max(need - eq_at, 0); k < __popc(kept_eq);) kept_eq &= ~(0x80000000u >> __clz(kept_eq));
+            const unsigned kept = above | kept_eq;
+            unsigned holes = valid & lo & ~kept, movers = kept & ~lo;
+            int h_at = hole + scan(__popc(holes)), m_at = mover + scan(__popc(movers));
+            eq += __reduce_add_sync(0xffffffffu, eq_n);
+            hole += __reduce_add_sync(0xffffffffu, __popc(holes));
+            mover += __reduce_add_sync(0xffffffffu, __popc(movers));
+            const int s = s0 + (k0 + lane) * 32;
+            for (; holes; holes &= holes - 1) to[h_at++] = s + __ffs(holes) - 1;
+            for (; movers; movers &= movers - 1) from[m_at++] = s + __ffs(movers) - 1;
+        }
+        meet();   // the lists are whole
     }
-    if (C > 1) cluster.sync();   // the lists are whole
-    else __syncthreads();
 
-    // 3. the moves
+    // 3. the moves, kMoves a thread together
     const int row_bytes = p.c.D * (p.c.e4m3 ? 1 : 2);
     const int pieces = row_bytes >> 4;                  // 16-byte pieces of a row: 4, 8 or 16
     const int per_move = 2 * pieces;
@@ -253,26 +406,66 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     const int piece = lane_of % pieces;
     uint8_t* pool = is_v ? p.c.v : p.c.k;
     uint8_t* exps = is_v ? p.c.v_exp : p.c.k_exp;
+    const size_t head = static_cast<size_t>(g) << p.c.page_shift;
     int bad = 0;
-    for (int j = (rank * kThreads + tid) / per_move; j < total; j += slots) {
-        const int src = __ldcg(from + j), dst = __ldcg(to + j);
-        const int pg_s = page_of(p.c, i, src), pg_d = page_of(p.c, i, dst);
-        if (lane_of == 0) {
-            mass_out[dst] = __ldcg(mass + src);
-            pos_out[dst] = where(src);
+    for (int j0 = (rank * kThreads + tid) / per_move; j0 < total; j0 += kMoves * slots) {
+        int src[kMoves], dst[kMoves];
+        int32_t at[kMoves];
+        float m[kMoves];
+        uint4 x[kMoves];
+        uint8_t e[kMoves];
+        long long rd[kMoves];
+#pragma unroll
+        for (int q = 0; q < kMoves; ++q) {
+            const int j = j0 + q * slots;
+            src[q] = j >= total ? -1 : few ? sh.src[j] : __ldcg(from + j);
+            dst[q] = j >= total ? -1 : few ? sh.dst[j] : __ldcg(to + j);
         }
-        if (pg_s < 0 || pg_d < 0) {
-            bad = SDM_DEV_BAD_PAGE;
-            continue;
+#pragma unroll
+        for (int q = 0; q < kMoves; ++q) {
+            rd[q] = -1;
+            if (src[q] < 0) continue;
+            if (lane_of == 0) {
+                m[q] = __ldcg(mass + src[q]);
+                at[q] = where(src[q]);
+            }
+            const int pg_s = page_of(p.c, i, src[q]), pg_d = page_of(p.c, i, dst[q]);
+            if (pg_s < 0 || pg_d < 0) {
+                bad = SDM_DEV_BAD_PAGE;
+                continue;
+            }
+            const size_t rs = pool_row(p.c, pg_s, src[q]) + head;
+            rd[q] = static_cast<long long>(pool_row(p.c, pg_d, dst[q]) + head);
+            x[q] = *reinterpret_cast<const uint4*>(pool + rs * row_bytes + piece * 16);
+            if (p.c.e4m3 && piece == 0) e[q] = exps[rs];
         }
-        const size_t head = static_cast<size_t>(g) << p.c.page_shift;
-        const size_t rs = pool_row(p.c, pg_s, src) + head, rd = pool_row(p.c, pg_d, dst) + head;
-        *reinterpret_cast<uint4*>(pool + rd * row_bytes + piece * 16) =
-            *reinterpret_cast<const uint4*>(pool + rs * row_bytes + piece * 16);
-        if (p.c.e4m3 && piece == 0) exps[rd] = exps[rs];
+#pragma unroll
+        for (int q = 0; q < kMoves; ++q) {
+            if (src[q] < 0) continue;
+            if (lane_of == 0) {
+                mass_out[dst[q]] = m[q];
+                pos_out[dst[q]] = at[q];
+            }
+            if (rd[q] < 0) continue;
+            *reinterpret_cast<uint4*>(pool + rd[q] * row_bytes + piece * 16) = x[q];
+            if (p.c.e4m3 && piece == 0) exps[rd[q]] = e[q];
+        }
     }
     if (bad) set_status(p.dev_status, bad);
     if (C > 1) cluster.sync();   // nobody leaves while its counts are read
+}
+
+template <int THREADS>
+cudaError_t launch_one(const EvictParams& p, int C, cudaStream_t s) {
+    constexpr int kMost = 48 * 1024;   // keys a CTA can hold
+    static const cudaError_t raised =
+        cudaFuncSetAttribute(evict_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4);
+    if (raised != cudaSuccess) return raised;
+    EvictParams q = p;
+    const long long per = ((p.stride + C - 1) / C + 31) / 32 * 32;
+    q.room = static_cast<int>(std::min<long long>(per, kMost));
+    return launch_cluster(evict_kernel<THREADS>, dim3(static_cast<unsigned>(static_cast<long long>(p.R) * p.c.heads * C)),
+                          dim3(THREADS), C, q.room * 4, s, q);
 }
 
 }  // namespace
@@ -291,13 +484,8 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
     const long long items = static_cast<long long>(p.R) * p.c.heads;
     int C = 1;
     while (C < 8 && items * C * 2 <= 2LL * num_sms() && p.stride / (2 * C) >= 2048) C *= 2;
-    const long long per = ((p.stride + C - 1) / C + 31) / 32 * 32;
-    constexpr int kMost = 48 * 1024;   // keys a CTA can hold
-    static const cudaError_t raised =
-        cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4);
-    if (raised != cudaSuccess) return raised;
-    q.room = static_cast<int>(std::min<long long>(per, kMost));
-    return launch_cluster(evict_kernel, dim3(static_cast<unsigned>(items * C)), dim3(kThreads), C, q.room * 4, s, q);
+    // short runs: smaller CTAs, more of which are on an SM together
+    return p.stride / C <= 4096 && C == 1 ? launch_one<256>(q, C, s) : launch_one<512>(q, C, s);
 }
 
 }  // namespace sdm
