@@ -30,22 +30,56 @@ struct Lane {
     bool turns;
 };
 
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
+}
+
 // One row's vectors first .. last - 1 of queries, keys or values (PLAIN): D / 8
-// lanes a vector, kBatch passes of the warp loaded while the kBatch before them
-// are worked on.
+// lanes a vector, kBatch passes of the warp loaded together.  (The next ones loaded
+// while these are worked on: 44 us for a prompt of 8192 in place of 39, for the
+// registers cost a third of the resident warps.)
 template <int D, bool INTER, bool PLAIN, int TO, int kBatch>
 __device__ __forceinline__ void section(const Lane& n, const uint16_t* src, int first, int last, const float* weight,
                                         float eps, const float (&cs)[4], const float (&sn)[4], uint8_t* dst,
                                         size_t head_bytes, uint8_t* exps, size_t head_rows, bool put) {
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;
     const int p0 = PLAIN ? 2 * n.l : n.r0, p1 = PLAIN ? 2 * n.l + 1 : n.r1;
-    float w[8];
-    if (!PLAIN && weight) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(weight) + p0);
-        const float4 b = __ldg(reinterpret_cast<const float4*>(weight) + p1);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    // weight and rotation in one: (a, b) -> (a wa cos - b wb sin, b wb cos + a wa sin),
+    // pair by pair, two pairs a register pair; 1 / norm comes after
+    float2 ac[2], bs[2], bc[2], as[2];
+    if constexpr (!PLAIN) {
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 1.f;
+        if (weight) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(weight) + p0);
+            const float4 b = __ldg(reinterpret_cast<const float4*>(weight) + p1);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float a0 = w[INTER ? 4 * j : 2 * j], a1 = w[INTER ? 4 * j + 2 : 2 * j + 1];
+            const float b0 = w[INTER ? 4 * j + 1 : 2 * j + 4], b1 = w[INTER ? 4 * j + 3 : 2 * j + 5];
+            ac[j] = make_float2(a0 * cs[2 * j], a1 * cs[2 * j + 1]);
+            as[j] = make_float2(a0 * sn[2 * j], a1 * sn[2 * j + 1]);
+            bc[j] = make_float2(b0 * cs[2 * j], b1 * cs[2 * j + 1]);
+            bs[j] = make_float2(-b0 * sn[2 * j], -b1 * sn[2 * j + 1]);
+        }
     }
-    uint2 x[2][kBatch][2];
+    uint2 x[kBatch][2];
     const uint2* s2 = reinterpret_cast<const uint2*>(src);   // not by the read-only path: the outputs may be the inputs
     auto load = [&](int v0, uint2 (&to)[kBatch][2]) {
 #pragma unroll
@@ -66,26 +100,37 @@ __device__ __forceinline__ void section(const Lane& n, const uint16_t* src, int 
             if constexpr (!PLAIN) {
                 float f[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = bf16_bits_to_float((u[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+                for (int j = 0; j < 4; ++j) {
+                    f[2 * j] = __uint_as_float(u[j] << 16);
+                    f[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+                }
+                float inv = 1.f;
                 if (weight) {
-                    float sum = 0.f;
+                    float2 sq = mul2(make_float2(f[0], f[1]), make_float2(f[0], f[1]));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+                    for (int j = 2; j < 8; j += 2) sq = fma2(make_float2(f[j], f[j + 1]), make_float2(f[j], f[j + 1]), sq);
+                    float sum = sq.x + sq.y;
 #pragma unroll
                     for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    const float inv = rsqrtf(fmaf(sum, 1.0f / D, eps));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] *= inv * w[j];
+                    inv = rsqrtf(fmaf(sum, 1.0f / D, eps));
                 }
-                if (n.turns) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float& a = f[INTER ? 2 * j : j];
-                        float& c = f[INTER ? 2 * j + 1 : j + 4];
-                        const float a0 = a, c0 = c;
-                        a = a0 * cs[j] - c0 * sn[j];
-                        c = c0 * cs[j] + a0 * sn[j];
+                for (int j = 0; j < 2; ++j) {
+                    float& a0 = f[INTER ? 4 * j : 2 * j];
+                    float& a1 = f[INTER ? 4 * j + 2 : 2 * j + 1];
+                    float& b0 = f[INTER ? 4 * j + 1 : 2 * j + 4];
+                    float& b1 = f[INTER ? 4 * j + 3 : 2 * j + 5];
+                    const float2 a = make_float2(a0, a1), b = make_float2(b0, b1);
+                    float2 x = mul2(a, ac[j]), y = mul2(b, bc[j]);
+                    if (n.turns) {   // else an infinity would meet a sine of 0
+                        x = fma2(b, bs[j], x);
+                        y = fma2(a, as[j], y);
                     }
+                    if (weight) {
+                        x = mul2(x, make_float2(inv, inv));
+                        y = mul2(y, make_float2(inv, inv));
+                    }
+                    a0 = x.x, a1 = x.y, b0 = y.x, b1 = y.y;
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) u[j] = f32x2_to_bf16x2(f[2 * j], f[2 * j + 1]);
@@ -107,21 +152,18 @@ __device__ __forceinline__ void section(const Lane& n, const uint16_t* src, int 
         }
     };
     constexpr int kStep = kPer * kBatch;
-    load(first, x[0]);
-    for (int v0 = first; v0 < last; v0 += 2 * kStep) {
-        if (v0 + kStep < last) load(v0 + kStep, x[1]);
-        work(v0, x[0]);
-        if (v0 + kStep >= last) break;
-        if (v0 + 2 * kStep < last) load(v0 + 2 * kStep, x[0]);
-        work(v0 + kStep, x[1]);
+#pragma unroll 1
+    for (int v0 = first; v0 < last; v0 += kStep) {
+        load(v0, x);
+        work(v0, x);
     }
 }
 
 // A warp takes a row, or one of `parts` equal shares of its vectors (query
 // heads, key heads and, with a cache, value heads).
 template <int D, bool INTER, int TO>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) {
-    constexpr int kLanes = D / 8, kBatch = 2;
+__global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateParams p) {
+    constexpr int kLanes = D / 8, kBatch = 4;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
@@ -152,15 +194,21 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) 
             if (held) at = pool_row(p.c, pg, w.ctx + off);
             else if (lane == 0) set_status(p.dev_status, SDM_DEV_BAD_PAGE);
         }
+        // 4 angles a lane; the lanes of the pass's vectors that have the same share the work
         float cs[4], sn[4];
+        constexpr int kPer = 32 / kLanes, kOwn = 4 / kPer;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            cs[j] = 1.f;
-            sn[j] = 0.f;
+        for (int j = 0; j < kOwn; ++j) {
+            constexpr double kInv2Pi = 0.15915494309189533577;
+            float c = 1.f, z = 0.f;
             if (n.turns) {
-                constexpr double kInv2Pi = 0.15915494309189533577;
-                const double t = pos * __ldg(p.freq + 4 * n.l + j) * kInv2Pi;
-                sincospif(2.0f * static_cast<float>(t - rint(t)), &sn[j], &cs[j]);
+                const double t = pos * __ldg(p.freq + 4 * n.l + n.sub * kOwn + j) * kInv2Pi;
+                sincospif(2.0f * static_cast<float>(t - rint(t)), &z, &c);
+            }
+#pragma unroll
+            for (int o = 0; o < kPer; ++o) {
+                cs[o * kOwn + j] = __shfl_sync(0xffffffffu, c, n.l + o * kLanes);
+                sn[o * kOwn + j] = __shfl_sync(0xffffffffu, z, n.l + o * kLanes);
             }
         }
         if (v_from < p.H)
