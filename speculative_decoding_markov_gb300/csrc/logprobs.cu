@@ -4,7 +4,8 @@
 // Mathematics, per row z of V logits, c = log2(e) / T and a reference m near
 // the row's maximum:  d_v = c z_v - m,  s = sum 2^d,  t = sum d 2^d
 //     log p(y) = ln 2 (d_y - log2 s)        H = ln 2 (log2 s - t / s)
-// (d <= a few, so H has no cancellation), in one pass over the row: every
+// (d <= a few, so H has no cancellation), in one pass over the row, which
+// streams through shared memory by bulk copies: every
 // thread keeps (m, s, t) of its own elements and moves m only when an element
 // exceeds it by more than kLazy.  The listed tokens come from the same pass:
 // a thread also keeps its largest element, and the top-th largest of (four a
@@ -25,7 +26,8 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTopMost = 32;
-constexpr int kBatch = 4;             // loads of a thread in flight together
+constexpr int kStages = 4;             // of the ring that a row streams through
+constexpr int kStageBytes = 16384;
 constexpr int kCand = 2048;           // listed elements of a CTA
 constexpr int kMaxCluster = 8;
 constexpr float kLazy = 8.0f;         // in log2 units
@@ -48,12 +50,15 @@ struct Part {                          // one CTA's share of a row
 struct Shared {
     float m[kWarps], s[kWarps], t[kWarps], top[kWarps];
     int ahead[kWarps];
-    uint32_t maxima[kWarps * 4];
+    __align__(16) uint32_t maxima[kWarps * 4];
     uint32_t bound;
-    int count, strict;
+    int count, late;
     unsigned long long round[kWarps];
     double sd[kWarps], td[kWarps];
-    Part part;
+    uint64_t full[kStages], empty[kStages];
+    Part part;                         // this CTA's
+    Part row;                          // the row's sums
+    Part parts[kMaxCluster];           // all CTAs', in the first one
     unsigned long long cand[kCand];
 };
 
@@ -87,12 +92,15 @@ struct Vec {
     uint32_t u[FP32 ? 8 : 4];
     __device__ __forceinline__ void load(const uint8_t* row, int vec) {
         const uint4* src = reinterpret_cast<const uint4*>(row) + (FP32 ? 2 * static_cast<size_t>(vec) : vec);
-        const uint4 a = __ldg(src);
+        set(__ldg(src), FP32 ? __ldg(src + 1) : make_uint4(0, 0, 0, 0));
+    }
+    __device__ __forceinline__ void load_shared(const uint8_t* stage, int vec) {
+        const uint4* src = reinterpret_cast<const uint4*>(stage) + (FP32 ? 2 * vec : vec);
+        set(src[0], FP32 ? src[1] : make_uint4(0, 0, 0, 0));
+    }
+    __device__ __forceinline__ void set(uint4 a, uint4 b) {
         u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
-        if constexpr (FP32) {
-            const uint4 b = __ldg(src + 1);
-            u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
-        }
+        if constexpr (FP32) u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
     }
     __device__ __forceinline__ float at(int j) const {
         if constexpr (FP32) return __uint_as_float(u[j]);
@@ -225,10 +233,14 @@ __device__ void pick_top(const uint8_t* row, int v0, int v1, float largest, bool
     __syncthreads();
     if (threadIdx.x < kWarps * 4) {
         const uint32_t x = sh.maxima[threadIdx.x];
+        const uint4* all = reinterpret_cast<const uint4*>(sh.maxima);
         int before = 0;
-        for (int k = 0; k < kWarps * 4; ++k) {
-            const uint32_t y = sh.maxima[k];
-            before += y > x || (y == x && k < static_cast<int>(threadIdx.x));
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const uint4 y = all[k];
+            const int at = threadIdx.x - 4 * k;   // an equal one before it counts
+            before += (y.x > x || (y.x == x && at > 0)) + (y.y > x || (y.y == x && at > 1)) +
+                      (y.z > x || (y.z == x && at > 2)) + (y.w > x || (y.w == x && at > 3));
         }
         if (before == top - 1) sh.bound = x;
     }
@@ -300,14 +312,20 @@ __device__ void pick_top(const uint8_t* row, int v0, int v1, float largest, bool
 
 // A cluster of CTAs per row; each takes an equal share of it.
 template <bool FP32>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobParams p) {
+    extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared sh;
-    __shared__ Part row_part;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x < kStages) {
+        mbar_init(&sh.full[threadIdx.x], 1);
+        mbar_init(&sh.empty[threadIdx.x], kWarps);
+    }
+    if (threadIdx.x == 0) sh.late = 0;
+    fence_mbar_init();
     pdl_wait();
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
     const int C = cluster.num_blocks(), rank = cluster.block_rank();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int item = blockIdx.x / C, i = item / p.W, pos = item % p.W;
 
     // the row, or nothing
@@ -343,52 +361,88 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
         said = FP32 ? __ldg(reinterpret_cast<const float*>(row) + tok)
                     : bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + tok));
 
-    float m = -kMaxRef, s = 0.f, t = 0.f, top = -INFINITY;
+    // The row's share streams through a ring of stages, copied by one thread.
+    constexpr int kVecBytes = FP32 ? 32 : 16, kVecs = kStageBytes / kVecBytes;
+    const uint8_t* share = row + static_cast<size_t>(v0) * kVecBytes;
+    const int vectors = v1 - v0, stages = (vectors + kVecs - 1) / kVecs;
+    auto copy = [&](int st) {   // by thread 0
+        const int bytes = min(kVecs, vectors - st * kVecs) * kVecBytes;
+        mbar_arrive_expect_tx(&sh.full[st % kStages], bytes);
+        bulk_load(ring + (st % kStages) * kStageBytes, share + static_cast<size_t>(st) * kStageBytes, bytes,
+                  &sh.full[st % kStages]);
+    };
+    __syncthreads();   // the barriers are set up
+    int sent = min(stages, kStages);   // stages copied (thread 0)
+    if (threadIdx.x == 0)
+        for (int st = 0; st < sent; ++st) copy(st);
+
+    float m = -kMaxRef, top = -INFINITY;
+    float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
     int ahead = 0;
-    bool any = false;
     const int said_in = tok >> 3;        // the vector that holds the token
-    for (int b = v0 + threadIdx.x; b < v1; b += kBatch * kThreads) {
-        Vec<FP32> xs[kBatch];
+    for (int st = 0; st < stages; ++st) {
+        if (!mbar_wait(&sh.full[st % kStages], (st / kStages) & 1)) {
+            sh.late = 1;
+            break;
+        }
+        const uint8_t* stage = ring + (st % kStages) * kStageBytes;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (b + k * kThreads < v1) xs[k].load(row, b + k * kThreads);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int v = b + k * kThreads;
+        for (int k = 0; k < kVecs / kThreads; ++k) {
+            const int at = k * kThreads + threadIdx.x, v = v0 + st * kVecs + at;
             if (v >= v1) break;
-            Vec<FP32>& x = xs[k];
+            Vec<FP32> x;
+            x.load_shared(stage, at);
             const float vm = x.largest();
             top = fmaxf(top, vm);
             if (v < said_in) ahead += x.template above<true>(said);
             else ahead += x.template above<false>(said);
             if (v == said_in)
                 for (int j = 0; j < (tok & 7); ++j) ahead += x.at(j) == said;
-            if (vm * c > m + kLazy) move_to(m, s, t, fminf(vm * c, kMaxRef));
+            if (vm * c > m + kLazy) {
+                float s = s2.x + s2.y, t = t2.x + t2.y;
+                move_to(m, s, t, fminf(vm * c, kMaxRef));
+                s2 = make_float2(s, 0.f);
+                t2 = make_float2(t, 0.f);
+            }
             x.raise();
-            float2 sum = make_float2(0.f, 0.f), tsum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 const float2 d = fma2(make_float2(x.at(j), x.at(j + 1)), make_float2(c, c), make_float2(-m, -m));
                 const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-                sum = add2(sum, e);
-                tsum = fma2(e, d, tsum);
+                s2 = add2(s2, e);
+                t2 = fma2(e, d, t2);
             }
-            s += sum.x + sum.y;
-            t += tsum.x + tsum.y;
-            any = true;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[st % kStages]);
+        // the stage before this one is free, or about to be
+        if (threadIdx.x == 0 && st > 0 && st - 1 + kStages < stages) {
+            if (mbar_wait(&sh.empty[(st - 1) % kStages], ((st - 1) / kStages) & 1)) {
+                copy(st - 1 + kStages);
+                sent = st + kStages;
+            } else {
+                sh.late = 1;
+            }
+        }
+        __syncwarp();
     }
+    const bool any = static_cast<int>(threadIdx.x) < vectors;
     const float mine = top;
 
     // the CTA's sums, in the order of lanes and warps
+    float s = s2.x + s2.y, t = t2.x + t2.y;
+    auto join_lanes = [&](int from) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        const float t2 = __shfl_xor_sync(0xffffffffu, t, o);
-        join(m, s, t, m2, s2, t2);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
-    }
+        for (int o = 16; o > 0; o >>= 1) {
+            if (o > from) continue;
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+            const float t2 = __shfl_xor_sync(0xffffffffu, t, o);
+            join(m, s, t, m2, s2, t2);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+        }
+    };
+    join_lanes(16);
     if (lane == 0) {
         sh.m[warp] = m;
         sh.s[warp] = s;
@@ -397,37 +451,41 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
         sh.ahead[warp] = ahead;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        Part& q = sh.part;
-        q.m = sh.m[0], q.s = sh.s[0], q.t = sh.t[0], q.top = sh.top[0], q.ahead = sh.ahead[0], q.n = 0;
-        for (int w = 1; w < kWarps; ++w) {
-            join(q.m, q.s, q.t, sh.m[w], sh.s[w], sh.t[w]);
-            q.top = fmaxf(q.top, sh.top[w]);
-            q.ahead += sh.ahead[w];
+    if (sh.late && threadIdx.x == 0) {   // a wait's limit: what follows is not to be trusted, and ends
+        set_status(p.dev_status, SDM_DEV_TIMEOUT);
+        for (int st = max(0, sent - kStages); st < sent; ++st) mbar_wait(&sh.full[st % kStages], (st / kStages) & 1);
+    }
+    if (warp == 0) {
+        const int w = lane & (kWarps - 1);
+        m = sh.m[w], s = sh.s[w], t = sh.t[w], top = sh.top[w], ahead = sh.ahead[w];
+        join_lanes(kWarps / 2);
+        if (lane == 0) {
+            Part& q = sh.part;
+            q.m = m, q.s = s, q.t = t, q.top = top, q.ahead = ahead, q.n = 0;
         }
     }
     __syncthreads();
     if (p.top > 0 && v1 > v0) pick_top<FP32>(row, v0, v1, mine, any, p.top, sh);
-    if (C > 1) cluster.sync();
-
-    // joined by every CTA alike
-    if (threadIdx.x == 0) {
-        Part q = sh.part;
-        if (C > 1) {
-            const Part* a = cluster.map_shared_rank(&sh.part, 0);
-            q.m = a->m, q.s = a->s, q.t = a->t, q.top = a->top, q.ahead = a->ahead;
-            for (int k = 1; k < C; ++k) {
-                const Part* b = cluster.map_shared_rank(&sh.part, k);
-                join(q.m, q.s, q.t, b->m, b->s, b->t);
-                q.top = fmaxf(q.top, b->top);
-                q.ahead += b->ahead;
-            }
-        }
-        row_part.m = q.m, row_part.s = q.s, row_part.t = q.t, row_part.top = q.top, row_part.ahead = q.ahead;
+    // the shares of a row in every CTA of its cluster, joined by all alike
+    if (C > 1) {
+        cluster.sync();
+        constexpr int kWords = sizeof(Part) / 4;
+        for (int k = threadIdx.x; k < C * kWords; k += kThreads)
+            reinterpret_cast<uint32_t*>(sh.parts)[k] =
+                reinterpret_cast<const uint32_t*>(cluster.map_shared_rank(&sh.part, k / kWords))[k % kWords];
+        __syncthreads();
+    }
+    if (warp == 0) {
+        const Part& q = C > 1 ? sh.parts[lane & (C - 1)] : sh.part;
+        m = q.m, s = q.s, t = q.t, top = q.top, ahead = q.ahead;
+        if (C > 1) join_lanes(C / 2);
+        if (lane == 0) sh.row.m = m, sh.row.s = s, sh.row.t = t, sh.row.top = top, sh.row.ahead = ahead;
     }
     __syncthreads();
+    const Part& row_part = sh.row;
     const float M = row_part.top;
-    float S = row_part.s, T = row_part.t, ref = row_part.m;
+    float S = row_part.s, T = row_part.t;
+    const float ref = row_part.m;
     // a row of logits whose products with c leave fp32: summed again in fp64,
     // relative to its largest (the type's lowest value in every place is one)
     const bool careful = fabsf(M) * c >= kHuge && fabsf(M) < INFINITY && S == S;
@@ -479,15 +537,16 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams 
         if (p.rank) p.rank[item] = known ? row_part.ahead : p.V;
     }
     if (p.top > 0) {
-        // a listed token's place: how many of all CTAs' come before it
-        const Part& own = sh.part;
-        for (int a = threadIdx.x; a < own.n; a += kThreads) {
-            const unsigned long long k = own.best[a];
-            int before = a;
+        // a listed token's place: how many of all CTAs' come before it.  The
+        // CTAs take turns by their entries.
+        for (int a = rank * kThreads + threadIdx.x; a < C * kTopMost; a += C * kThreads) {
+            const Part& own = C > 1 ? sh.parts[a / kTopMost] : sh.part;
+            if (a % kTopMost >= own.n) continue;
+            const unsigned long long k = own.best[a % kTopMost];
+            int before = 0;
             for (int b = 0; b < C; ++b) {
-                if (b == rank) continue;
-                const Part* o = cluster.map_shared_rank(&sh.part, b);
-                for (int e = 0; e < o->n && o->best[e] > k; ++e) ++before;
+                const Part& o = C > 1 ? sh.parts[b] : sh.part;
+                for (int e = 0; e < o.n; ++e) before += o.best[e] > k;
             }
             if (before < p.top) {
                 const size_t at = static_cast<size_t>(item) * p.top + before;
@@ -509,8 +568,15 @@ cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
     // few rows: several SMs a row, as long as each has some thousand elements
     int C = 1;
     while (C < kMaxCluster && items * C * 2 <= 2LL * num_sms() && p.V / (2 * C) >= 4096) C *= 2;
+    constexpr int kRing = kStages * kStageBytes;
+    static const cudaError_t raised = [] {
+        const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(logprobs_kernel<false>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+    }();
+    if (raised != cudaSuccess) return raised;
     return launch_cluster(p.fp32 ? logprobs_kernel<true> : logprobs_kernel<false>, dim3(static_cast<unsigned>(items * C)),
-                          dim3(kThreads), C, 0, s, p);
+                          dim3(kThreads), C, kRing, s, p);
 }
 
 }  // namespace sdm
