@@ -23,10 +23,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTopMost = 32;
-constexpr int kStages = 4;             // of the ring that a row streams through
+constexpr int kStages = 3;             // of the ring that a row streams through
 constexpr int kStageBytes = 16384;
 constexpr int kCand = 2048;           // listed elements of a CTA
 constexpr int kMaxCluster = 8;
@@ -52,15 +52,17 @@ struct Shared {
     int ahead[kWarps];
     __align__(16) uint32_t maxima[kWarps * 4];
     uint32_t bound;
-    int count, late;
+    int count, ones, wholes, late;
+    int one[kThreads], whole[kThreads];
     unsigned long long round[kWarps];
     double sd[kWarps], td[kWarps];
     uint64_t full[kStages], empty[kStages];
     Part part;                         // this CTA's
     Part row;                          // the row's sums
     Part parts[kMaxCluster];           // all CTAs', in the first one
-    unsigned long long cand[kCand];
+    unsigned long long* cand;          // [kCand], where the ring was
 };
+static_assert(kCand * 8 <= kStages * kStageBytes && kWarps * 4 >= kTopMost, "lists");
 
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
     float2 r;
@@ -104,7 +106,11 @@ struct Vec {
     }
     __device__ __forceinline__ float at(int j) const {
         if constexpr (FP32) return __uint_as_float(u[j]);
-        else return bf16_bits_to_float((u[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+        else return __uint_as_float(j & 1 ? u[j >> 1] & 0xffff0000u : u[j >> 1] << 16);
+    }
+    __device__ __forceinline__ void set_lowest() {
+#pragma unroll
+        for (int j = 0; j < (FP32 ? 8 : 4); ++j) u[j] = FP32 ? 0xff800000u : 0xff80ff80u;
     }
     // The largest; a NaN is left out.
     __device__ __forceinline__ float largest() const {
@@ -129,23 +135,38 @@ struct Vec {
             for (int j = 0; j < 4; ++j) u[j] = bits_of(__hmax2_nan(pair_of(u[j]), low));
         }
     }
-    // How many exceed x, or (EQUAL) reach it.
+    // Adds how many exceed x, or (EQUAL) reach it: bf16 counts in both halves of
+    // a register, exact to 256.
     template <bool EQUAL>
-    __device__ __forceinline__ int above(float x) const {
+    __device__ __forceinline__ void above(float x, int& n, __nv_bfloat162& halves) const {
         if constexpr (FP32) {
-            int n = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) n += EQUAL ? at(j) >= x : at(j) > x;
-            return n;
         } else {
             const __nv_bfloat162 y = __float2bfloat162_rn(x);   // x is one of the row's: exact
-            __nv_bfloat162 n = EQUAL ? __hge2(pair_of(u[0]), y) : __hgt2(pair_of(u[0]), y);
 #pragma unroll
-            for (int j = 1; j < 4; ++j) n = __hadd2(n, EQUAL ? __hge2(pair_of(u[j]), y) : __hgt2(pair_of(u[j]), y));
-            return static_cast<int>(__low2float(n) + __high2float(n));
+            for (int j = 0; j < 4; ++j)
+                halves = __hadd2(halves, EQUAL ? __hge2(pair_of(u[j]), y) : __hgt2(pair_of(u[j]), y));
         }
     }
 };
+
+template <int N>
+__device__ __forceinline__ float largest_of(const Vec<true> (&x)[N]) {
+    float m = x[0].largest();
+#pragma unroll
+    for (int k = 1; k < N; ++k) m = fmaxf(m, x[k].largest());
+    return m;
+}
+template <int N>
+__device__ __forceinline__ float largest_of(const Vec<false> (&x)[N]) {
+    __nv_bfloat162 m = pair_of(x[0].u[0]);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = __hmax2(m, pair_of(x[k].u[j]));
+    return fmaxf(__uint_as_float(bits_of(m) << 16), __uint_as_float(bits_of(m) & 0xffff0000u));
+}
 
 // (s, t) of a reference m, for the reference `to` >= m.  A factor of zero ends
 // what may be infinite beside it.
@@ -156,12 +177,20 @@ __device__ __forceinline__ void move_to(float& m, float& s, float& t, float to) 
     m = to;
 }
 
-__device__ __forceinline__ void join(float& m, float& s, float& t, float m2, float s2, float t2) {
-    const float to = fmaxf(m, m2);
+// The sums of a warp's lanes (or of every 2^n neighbours, n steps), in a fixed order.
+template <int LANES>
+__device__ __forceinline__ void join_lanes(float& m, float& s, float& t, float& top, int& ahead) {
+    float to = m;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
     move_to(m, s, t, to);
-    move_to(m2, s2, t2, to);
-    s += s2;
-    t += t2;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+    }
 }
 
 // The largest key below `below` of elements [v0, v1) (in vectors), by the whole CTA.
@@ -184,27 +213,46 @@ __device__ unsigned long long next_key(const uint8_t* row, int v0, int v1, unsig
     return best;
 }
 
-// Lists the elements of the threads whose largest one reaches `bound` that
-// reach it themselves (`strict`: exceed it).
+// A thread's largest element, the stage it is in, and the largest of its other
+// stages; without elements all are 0, below any key.
+struct Largest {
+    uint32_t key, next;
+    int stage;
+};
+
+// Lists the elements that reach `bound` (`strict`: exceed it), which are among
+// those of the threads whose largest one does, mostly in one stage of theirs:
+// these stages' vectors, or all of such a thread's, are looked at by all.
 template <bool FP32>
-__device__ __forceinline__ void list_candidates(const uint8_t* row, int v0, int v1, uint32_t mine, uint32_t bound,
+__device__ __forceinline__ void list_candidates(const uint8_t* row, int v0, int v1, const Largest& mine, uint32_t bound,
                                                 bool strict, Shared& sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kOwn = kStageBytes / (FP32 ? 32 : 16) / kThreads;   // a thread's vectors of a stage
     const uint32_t from = strict ? bound + 1 : bound;
-    unsigned todo = __ballot_sync(0xffffffffu, mine >= from);
-    while (todo) {
-        const int l = __ffs(todo) - 1;
-        todo &= todo - 1;
-        for (int v = v0 + warp * 32 + l + lane * kThreads; v < v1; v += 32 * kThreads) {
-            Vec<FP32> x;
-            x.load(row, v);
+    if (threadIdx.x == 0) sh.count = sh.ones = sh.wholes = 0;
+    __syncthreads();
+    if (mine.key >= from) {
+        if (mine.next >= from) sh.whole[atomicAdd(&sh.wholes, 1)] = static_cast<int>(threadIdx.x);
+        else sh.one[atomicAdd(&sh.ones, 1)] = mine.stage * kThreads * kOwn + static_cast<int>(threadIdx.x);
+    }
+    __syncthreads();
+    const int per = (v1 - v0 + kThreads - 1) / kThreads, ones = sh.ones * kOwn, all = ones + sh.wholes * per;
+    for (int k = threadIdx.x; k < all; k += kThreads) {
+        int v;
+        if (k < ones) {
+            v = v0 + sh.one[k / kOwn] + (k % kOwn) * kThreads;
+        } else {
+            const int f = (k - ones) / per;
+            v = v0 + sh.whole[f] + (k - ones - f * per) * kThreads;
+        }
+        if (v >= v1) continue;
+        Vec<FP32> x;
+        x.load(row, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float z = x.at(j);
-                if (ordered_bits(z) >= from) {
-                    const int at = atomicAdd(&sh.count, 1);
-                    if (at < kCand) sh.cand[at] = argmax_key(z, 8 * v + j);
-                }
+        for (int j = 0; j < 8; ++j) {
+            const float z = x.at(j);
+            if (ordered_bits(z) >= from) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kCand) sh.cand[at] = argmax_key(z, 8 * v + j);
             }
         }
     }
@@ -213,12 +261,11 @@ __device__ __forceinline__ void list_candidates(const uint8_t* row, int v0, int 
 
 // The `top` largest keys of the CTA's elements, in order, into sh.part.best.
 template <bool FP32>
-__device__ void pick_top(const uint8_t* row, int v0, int v1, float largest, bool any, int top, Shared& sh) {
+__device__ void pick_top(const uint8_t* row, int v0, int v1, const Largest& mine, int top, Shared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_out = min(top, 8 * (v1 - v0));
-    const uint32_t mine = any ? max(ordered_bits(largest), 1u) : 0u;
     // four largest of the warp's maxima
-    uint32_t left = mine;
+    uint32_t left = mine.key;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const uint32_t w = __reduce_max_sync(0xffffffffu, left);
@@ -226,10 +273,7 @@ __device__ void pick_top(const uint8_t* row, int v0, int v1, float largest, bool
         if (lane == __ffs(who) - 1) left = 0;
         if (lane == 0) sh.maxima[warp * 4 + r] = w;
     }
-    if (threadIdx.x == 0) {
-        sh.count = 0;
-        sh.bound = 0;
-    }
+    if (threadIdx.x == 0) sh.bound = 0;
     __syncthreads();
     if (threadIdx.x < kWarps * 4) {
         const uint32_t x = sh.maxima[threadIdx.x];
@@ -250,8 +294,6 @@ __device__ void pick_top(const uint8_t* row, int v0, int v1, float largest, bool
     int n = sh.count;
     if (n > kCand) {
         // more reach the bound than fit: those that exceed it, then its lowest ids
-        __syncthreads();
-        if (threadIdx.x == 0) sh.count = 0;
         __syncthreads();
         list_candidates<FP32>(row, v0, v1, mine, bound, true, sh);
         n = sh.count;
@@ -312,7 +354,7 @@ __device__ void pick_top(const uint8_t* row, int v0, int v1, float largest, bool
 
 // A cluster of CTAs per row; each takes an equal share of it.
 template <bool FP32>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobParams p) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -320,47 +362,45 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobPara
         mbar_init(&sh.full[threadIdx.x], 1);
         mbar_init(&sh.empty[threadIdx.x], kWarps);
     }
-    if (threadIdx.x == 0) sh.late = 0;
+    if (threadIdx.x == 0) {
+        sh.late = 0;
+        sh.cand = reinterpret_cast<unsigned long long*>(ring);
+    }
     fence_mbar_init();
     pdl_wait();
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
     const int C = cluster.num_blocks(), rank = cluster.block_rank();
-    const int item = blockIdx.x / C, i = item / p.W, pos = item % p.W;
+    const int item = blockIdx.x / C, i = item / p.W, pos = item - i * p.W;
 
-    // the row, or nothing
+    // the row, or nothing (its look-ups are independent loads)
     int n = p.n ? __ldg(p.n + i) : p.W;
+    const long long first = __ldg(p.cu + i), end = __ldg(p.cu + i + 1);
+    const int off = p.path ? __ldg(p.path + item) : pos;
+    int tok = __ldg(p.tok + item);
     int bad = 0;
     if (n < 0 || n > p.W) {
         n = min(max(n, 0), p.W);
         bad = SDM_DEV_BAD_WINDOW;
     }
-    const long long first = __ldg(p.cu + i), end = __ldg(p.cu + i + 1);
     if (!p.n) n = static_cast<int>(min(static_cast<long long>(n), max(end - first, 0ll)));
     bool live = pos < n;
-    long long r = 0;
+    const long long r = first + off;
     if (live) {
-        const int off = p.path ? __ldg(p.path + item) : pos;
-        r = first + off;
         if (first < 0 || off < 0 || r >= end) bad |= SDM_DEV_BAD_WINDOW, live = false;
         else if (r >= p.rows) bad |= SDM_DEV_CAPACITY, live = false;
     }
-    const int tok = live ? __ldg(p.tok + item) : 0;
     const bool known = static_cast<unsigned>(tok) < static_cast<unsigned>(p.V);
-    if (!known) bad |= SDM_DEV_BAD_TOKEN;
+    if (live && !known) bad |= SDM_DEV_BAD_TOKEN;
     if (bad && rank == 0 && threadIdx.x == 0) set_status(p.dev_status, bad);
     if (!live) return;   // the whole cluster
+    if (!known) tok = 0;
 
     const uint8_t* row = static_cast<const uint8_t*>(p.target) + static_cast<size_t>(r) * p.V * (FP32 ? 4 : 2);
     const int vecs = p.V / 8;
     const int v0 = static_cast<int>(static_cast<long long>(vecs) * rank / C);
     const int v1 = static_cast<int>(static_cast<long long>(vecs) * (rank + 1) / C);
     const float c = p.scale;
-    float said = 0.f;
-    if (known)
-        said = FP32 ? __ldg(reinterpret_cast<const float*>(row) + tok)
-                    : bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + tok));
-
     // The row's share streams through a ring of stages, copied by one thread.
     constexpr int kVecBytes = FP32 ? 32 : 16, kVecs = kStageBytes / kVecBytes;
     const uint8_t* share = row + static_cast<size_t>(v0) * kVecBytes;
@@ -376,9 +416,20 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobPara
     if (threadIdx.x == 0)
         for (int st = 0; st < sent; ++st) copy(st);
 
-    float m = -kMaxRef, top = -INFINITY;
+    float said = 0.f;
+    if (known)
+        said = FP32 ? __ldg(reinterpret_cast<const float*>(row) + tok)
+                    : bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + tok));
+
+    float m = -kMaxRef, top = -INFINITY, next = -INFINITY;   // the largest element; of the other stages than top_in
+    int top_in = 0;
     float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
     int ahead = 0;
+    __nv_bfloat162 halves = __float2bfloat162_rn(0.f);
+    auto flush = [&]() {
+        ahead += static_cast<int>(__low2float(halves) + __high2float(halves));
+        halves = __float2bfloat162_rn(0.f);
+    };
     const int said_in = tok >> 3;        // the vector that holds the token
     for (int st = 0; st < stages; ++st) {
         if (!mbar_wait(&sh.full[st % kStages], (st / kStages) & 1)) {
@@ -386,33 +437,51 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobPara
             break;
         }
         const uint8_t* stage = ring + (st % kStages) * kStageBytes;
+        // The thread's vectors of the stage together: one look at their largest
+        // element decides on the reference and on the comparisons with the
+        // given token (most stages have none that reaches it).
+        constexpr int kOwn = kVecs / kThreads;
+        const int at = v0 + st * kVecs + threadIdx.x;
+        Vec<FP32> x[kOwn];
 #pragma unroll
-        for (int k = 0; k < kVecs / kThreads; ++k) {
-            const int at = k * kThreads + threadIdx.x, v = v0 + st * kVecs + at;
-            if (v >= v1) break;
-            Vec<FP32> x;
-            x.load_shared(stage, at);
-            const float vm = x.largest();
-            top = fmaxf(top, vm);
-            if (v < said_in) ahead += x.template above<true>(said);
-            else ahead += x.template above<false>(said);
-            if (v == said_in)
-                for (int j = 0; j < (tok & 7); ++j) ahead += x.at(j) == said;
-            if (vm * c > m + kLazy) {
-                float s = s2.x + s2.y, t = t2.x + t2.y;
-                move_to(m, s, t, fminf(vm * c, kMaxRef));
-                s2 = make_float2(s, 0.f);
-                t2 = make_float2(t, 0.f);
+        for (int k = 0; k < kOwn; ++k) {
+            x[k].set_lowest();
+            if (at + k * kThreads < v1) x[k].load_shared(stage, k * kThreads + threadIdx.x);
+        }
+        const float sm = largest_of(x);
+        next = fmaxf(next, fminf(sm, top));
+        if (sm > top) {
+            top = sm;
+            top_in = st;
+        }
+        if (sm >= said) {
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                const int v = at + k * kThreads;
+                if (v < said_in) x[k].template above<true>(said, ahead, halves);
+                else x[k].template above<false>(said, ahead, halves);
+                if (v == said_in)
+                    for (int j = 0; j < (tok & 7); ++j) ahead += x[k].at(j) == said;
             }
-            x.raise();
+        }
+        if (sm * c > m + kLazy) {
+            float s = s2.x + s2.y, t = t2.x + t2.y;
+            move_to(m, s, t, fminf(sm * c, kMaxRef));
+            s2 = make_float2(s, 0.f);
+            t2 = make_float2(t, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            x[k].raise();
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
-                const float2 d = fma2(make_float2(x.at(j), x.at(j + 1)), make_float2(c, c), make_float2(-m, -m));
+                const float2 d = fma2(make_float2(x[k].at(j), x[k].at(j + 1)), make_float2(c, c), make_float2(-m, -m));
                 const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                 s2 = add2(s2, e);
                 t2 = fma2(e, d, t2);
             }
         }
+        if (!FP32 && st % 8 == 7) flush();   // a stage adds at most 16 to a half
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[st % kStages]);
         // the stage before this one is free, or about to be
@@ -426,23 +495,13 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobPara
         }
         __syncwarp();
     }
-    const bool any = static_cast<int>(threadIdx.x) < vectors;
-    const float mine = top;
+    flush();
+    Largest mine = {0, 0, top_in};
+    if (static_cast<int>(threadIdx.x) < vectors) mine.key = max(ordered_bits(top), 1u), mine.next = ordered_bits(next);
 
     // the CTA's sums, in the order of lanes and warps
     float s = s2.x + s2.y, t = t2.x + t2.y;
-    auto join_lanes = [&](int from) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            if (o > from) continue;
-            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-            const float t2 = __shfl_xor_sync(0xffffffffu, t, o);
-            join(m, s, t, m2, s2, t2);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
-        }
-    };
-    join_lanes(16);
+    join_lanes<32>(m, s, t, top, ahead);
     if (lane == 0) {
         sh.m[warp] = m;
         sh.s[warp] = s;
@@ -458,14 +517,14 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobPara
     if (warp == 0) {
         const int w = lane & (kWarps - 1);
         m = sh.m[w], s = sh.s[w], t = sh.t[w], top = sh.top[w], ahead = sh.ahead[w];
-        join_lanes(kWarps / 2);
+        join_lanes<kWarps>(m, s, t, top, ahead);
         if (lane == 0) {
             Part& q = sh.part;
             q.m = m, q.s = s, q.t = t, q.top = top, q.ahead = ahead, q.n = 0;
         }
     }
     __syncthreads();
-    if (p.top > 0 && v1 > v0) pick_top<FP32>(row, v0, v1, mine, any, p.top, sh);
+    if (p.top > 0 && v1 > v0) pick_top<FP32>(row, v0, v1, mine, p.top, sh);
     // the shares of a row in every CTA of its cluster, joined by all alike
     if (C > 1) {
         cluster.sync();
@@ -476,9 +535,11 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobPara
         __syncthreads();
     }
     if (warp == 0) {
+        // lanes past the cluster's CTAs add nothing
         const Part& q = C > 1 ? sh.parts[lane & (C - 1)] : sh.part;
-        m = q.m, s = q.s, t = q.t, top = q.top, ahead = q.ahead;
-        if (C > 1) join_lanes(C / 2);
+        const bool mine = lane < C;
+        m = q.m, s = mine ? q.s : 0.f, t = mine ? q.t : 0.f, top = q.top, ahead = mine ? q.ahead : 0;
+        if (C > 1) join_lanes<kMaxCluster>(m, s, t, top, ahead);
         if (lane == 0) sh.row.m = m, sh.row.s = s, sh.row.t = t, sh.row.top = top, sh.row.ahead = ahead;
     }
     __syncthreads();
@@ -552,9 +613,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobPara
                 const size_t at = static_cast<size_t>(item) * p.top + before;
                 const int id = static_cast<int>(key_token(k));
                 p.top_tok[at] = id;
-                const float z = FP32 ? __ldg(reinterpret_cast<const float*>(row) + id)
-                                     : bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + id));
-                p.top_logp[at] = logp(z);
+                p.top_logp[at] = logp(key_value(k));
             }
         }
     }
@@ -566,8 +625,11 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobPara
 cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
     const long long items = static_cast<long long>(p.R) * p.W;
     // few rows: several SMs a row, as long as each has some thousand elements
+    // and the grid stays within two rounds of four blocks an SM (64 requests of
+    // 1 to 8 in 512 places: 28.5 us with two blocks a row, 39.6 with one; up
+    // to 16 rounds 50)
     int C = 1;
-    while (C < kMaxCluster && items * C * 2 <= 2LL * num_sms() && p.V / (2 * C) >= 4096) C *= 2;
+    while (C < kMaxCluster && items * C * 2 <= 8LL * num_sms() && p.V / (2 * C) >= 4096) C *= 2;
     constexpr int kRing = kStages * kStageBytes;
     static const cudaError_t raised = [] {
         const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
