@@ -111,7 +111,7 @@ struct Cfg {
     static constexpr int kMiscBytes = kRing * sizeof(Blk) + kLStages * (kTile * 4 + 16) + (kPlanes ? 2 * kTile * 4 : 0) +
                                       (kPlanes ? kExpStages * kTile : 0) + (SMALL ? 0 : 2 * kUnit * 4) + 704;
     static constexpr int kFit = (232448 - kMiscBytes - kQSlots * kQBytes) / kKBytes;
-    static constexpr int kKSlots = !SMALL ? 2 : kFit < 12 ? kFit : 12;
+    static constexpr int kKSlots = !SMALL ? 2 : kFit < 10 ? kFit : 10;
     static_assert(kFit >= (SMALL ? 4 : 2), "shared memory");
     static constexpr int kQ = kKSlots * kKBytes;
     static constexpr int kL = kQ + kQSlots * kQBytes;          // -lse log2 e of a tile's columns
@@ -126,7 +126,7 @@ struct Cfg {
 template <int K, int Q, int L, int U, int S>
 struct Bars {
     uint64_t k_full[K], k_empty[K], q_full[Q], q_empty[Q], l_full[L], l_empty[L];
-    uint64_t s_full[S], s_empty[S], kt_full[2], k_idle, j_full[2][2], j_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages], x_empty[kExpStages];
+    uint64_t s_full[S], s_empty[S], kt_full[2], k_idle, j_full[2][2], j_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages];
     uint64_t drain;
     uint32_t live[L][5];              // columns of the stage that add something; whether some do not
     uint32_t tmem;
@@ -565,7 +565,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         }
         if (lane < kExpStages) {
             mbar_init(&bar.x_full[lane], 1);
-            mbar_init(&bar.x_empty[lane], 4);
         }
         if (lane == 0) {
             mbar_init(&bar.drain, 1);
@@ -612,9 +611,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         int i = st.i, g = st.g, u = st.u, have = -1, loaded_i = -1, loaded_g = -1;
         Req r;
         Ring<C::kRing> wr;
-        Ring<C::kKSlots> kr;
-        Ring<kExpStages> xr;
-        bool live = st.u0 < st.u1;
+        Ring<C::kKSlots> kr, k_sent;      // the next place, and the one after the last that was filled
+        Ring<kExpStages> xr, x_sent;
+        bool live_share = st.u0 < st.u1;
         Part part = {};
         // page ids of a unit's keys, a lane per page, loaded a unit ahead: the
         // table's latency would else stand before every unit's first copy
@@ -627,7 +626,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         while (ok) {
             Blk b = {};
             bool got = false;
-            while (live && us < st.u1) {
+            while (live_share && us < st.u1) {
                 if (have != i) {
                     if (i >= p.R) break;
                     r = req_of(p, i);
@@ -702,47 +701,55 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             ahead_i = b.i;
             ahead_u = this_u + 1;
             ahead = page_at(ahead_i, ahead_u);
-            for (int t = 0; t < b.tiles && ok; ++t) {
-                const int key0 = b.k0 + t * kTile;
-                const int pages_live = min(pages, (b.n - key0 + page - 1) >> p.c.page_shift);
-                int pg = __shfl_sync(0xffffffffu, ids, (t * pages + lane) & 31);
-                if (lane < pages_live && static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.n_pages)) {
-                    set_status(p.dev_status, SDM_DEV_BAD_PAGE);
-                    pg = 0;
-                }
-                const int y = (pg * p.c.heads + b.g) << p.c.page_shift;
-                ok = wait_or_fail(p, &bar.k_empty[kr.at], kr.empty());
-                if (kPlanes && ok) ok = wait_or_fail(p, &bar.x_empty[xr.at], xr.empty());
-                if (!ok) break;
-                uint8_t* slot = smem + kr.at * C::kKBytes;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&bar.k_full[kr.at], static_cast<uint32_t>(pages_live) * page * (kPlanes ? D : 2 * D));
-                    if (kPlanes) mbar_arrive_expect_tx(&bar.x_full[xr.at], static_cast<uint32_t>(pages_live) * page);
-                }
-                __syncwarp();
-                if (lane < pages_live) {
-                    if constexpr (kPlanes) {
-                        tma_load_2d(slot + lane * page * D, &tmK, &bar.k_full[kr.at], 0, y);
-                        bulk_load(smem + C::kExps + xr.at * kTile + lane * page, p.c.k_exp + y, page, &bar.x_full[xr.at]);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_2d(slot + h * (kTile * 128) + lane * page * 128, &tmK, &bar.k_full[kr.at], h * 64, y);
-                    }
-                }
-                __syncwarp();
-                kr.step();
-                if (kPlanes) xr.step();
+            // both tiles at once: lanes 0 .. 15 the first one's pages, 16 .. 31 the second's
+            const int t = lane >> 4, l = lane & 15;
+            const int live = min(pages, (b.n - b.k0 - t * kTile + page - 1) >> p.c.page_shift);   // negative: no second one
+            int pg = __shfl_sync(0xffffffffu, ids, (t * pages + l) & 31);
+            if (l < live && static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.n_pages)) {
+                set_status(p.dev_status, SDM_DEV_BAD_PAGE);
+                pg = 0;
             }
+            const int y = (pg * p.c.heads + b.g) << p.c.page_shift;
+            int slot = kr.at, stage = xr.at;
+            for (int k = 0; k < b.tiles && ok; ++k) {
+                ok = wait_or_fail(p, &bar.k_empty[kr.at], kr.empty());
+                if (!ok) break;
+                if (t == k) slot = kr.at, stage = xr.at;
+                kr.step();
+                // The exponents' stages are not waited for: a tile's keys wait for
+                // the product kKSlots before it, which waits for the weights kS
+                // before that, by when these have read theirs.
+                static_assert(!kPlanes || C::kKSlots + C::kS + 2 <= kExpStages, "stages of exponents");
+                xr.step();
+            }
+            if (!ok) break;
+            if (l < (kPlanes ? 2 : 1) && t < b.tiles)
+                mbar_arrive_expect_tx(l == 0 ? &bar.k_full[slot] : &bar.x_full[stage],
+                                      static_cast<uint32_t>(live) * page * (l == 1 ? 1 : kPlanes ? D : 2 * D));
+            __syncwarp();
+            if (l < live) {
+                uint8_t* to = smem + slot * C::kKBytes;
+                if constexpr (kPlanes) {
+                    tma_load_2d(to + l * page * D, &tmK, &bar.k_full[slot], 0, y);
+                    bulk_load(smem + C::kExps + stage * kTile + l * page, p.c.k_exp + y, page, &bar.x_full[stage]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_load_2d(to + h * (kTile * 128) + l * page * 128, &tmK, &bar.k_full[slot], h * 64, y);
+                }
+            }
+            __syncwarp();
         }
         if (!SMALL && lane == 0) ws.part[blockIdx.x] = part;
         if (!ok) {
             // copies in flight land before the CTA may exit
             for (int k = 0; k < C::kKSlots; ++k)
-                if (kr.turn > 0 || k < kr.at) mbar_wait(&bar.k_full[k], k < kr.at ? kr.turn & 1 : (kr.turn & 1) ^ 1);
+                if (k_sent.turn > 0 || k < k_sent.at)
+                    mbar_wait(&bar.k_full[k], k < k_sent.at ? k_sent.turn & 1 : (k_sent.turn & 1) ^ 1);
             if (kPlanes)
                 for (int k = 0; k < kExpStages; ++k)
-                    if (xr.turn > 0 || k < xr.at) mbar_wait(&bar.x_full[k], k < xr.at ? xr.turn & 1 : (xr.turn & 1) ^ 1);
+                    if (x_sent.turn > 0 || k < x_sent.at)
+                        mbar_wait(&bar.x_full[k], k < x_sent.at ? x_sent.turn & 1 : (x_sent.turn & 1) ^ 1);
         }
     } else if (warp == kSoft + 1) {
         // ------------------------------------------------------------------
@@ -1116,8 +1123,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         ok = wait_or_fail(p, &bar.x_full[xr.at], xr.full());
                         if (!ok) break;
                         c *= scale_of(smem[C::kExps + xr.at * kTile + (tid & 127)]);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.x_empty[xr.at]);
                         xr.step();
                         if (wg == 0 && b.tiles == 2) xr.step();
                     } else {
