@@ -474,14 +474,14 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     return r;
 }
 
-// Adds the weights of 32 columns: 2^(c f x + l), f the columns' scales (planes),
+// Adds the weights of N columns: 2^(c f x + l), f the columns' scales (planes),
 // l their -lse log2 e.
-template <bool PLANES>
-__device__ __forceinline__ void add_weights(const uint32_t (&x)[32], float c, const float4* l4, const float4* f4,
+template <bool PLANES, int N>
+__device__ __forceinline__ void add_weights(const uint32_t (&x)[N], float c, const float4* l4, const float4* f4,
                                             float2 (&acc)[4]) {
     const float2 cc = make_float2(c, c);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < N / 4; ++k) {
         const float4 l = l4[k];
         float2 a = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
         float2 b = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
@@ -501,11 +501,12 @@ __device__ __forceinline__ void add_weights(const uint32_t (&x)[32], float c, co
 // Scores of columns that a key is not seen by become -infinity (whose weight is
 // 0 whatever their l, which is no NaN and not +infinity): all but lo .. hi - 1,
 // and those whose bit is not set in `live`.
-__device__ __forceinline__ void hide(uint32_t (&x)[32], int lo, int hi, uint32_t live) {
+template <int N>
+__device__ __forceinline__ void hide(uint32_t (&x)[N], int lo, int hi, uint32_t live) {
     const int from = max(lo, 0);
     live &= (from >= 32 ? 0u : ~0u << from) & (hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) x[k] = (live >> k) & 1u ? x[k] : 0xff800000u;
+    for (int k = 0; k < N; ++k) x[k] = (live >> k) & 1u ? x[k] : 0xff800000u;
 }
 
 // ---------------------------------------------------------------------------
@@ -739,6 +740,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 }
             }
             __syncwarp();
+            k_sent = kr;
+            x_sent = xr;
         }
         if (!SMALL && lane == 0) ws.part[blockIdx.x] = part;
         if (!ok) {
@@ -801,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             }
             for (int q = b.q0; q < b.q1 && ok; ++q) {
                 if (!SMALL) ok = wait_or_fail(p, &bar.q_full[qr.at], qr.full());
-                const int N = SMALL ? (b.M + 31) & ~31 : kTile;   // what the weights read
+                const int N = !SMALL ? kTile : b.M <= 16 ? 16 : (b.M + 31) & ~31;   // what the weights read
                 for (int t = 0; t < b.tiles && ok; ++t) {
                     if (SMALL) ok = wait_or_fail(p, &bar.k_full[kr.at], kr.full());
                     if (ok) ok = wait_or_fail(p, &bar.s_empty[sr.at], sr.empty());
@@ -1204,24 +1207,33 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         float2 acc[4] = {};
                         const float4* lp = reinterpret_cast<const float4*>(lq);
                         const float4* fp = reinterpret_cast<const float4*>(cf + qr.at * kTile);
-                        auto add = [&](uint32_t (&x)[32], int at) {   // 32 columns from `at`
+                        auto add = [&](auto& x, int at) {   // columns from `at`
                             if (some) hide(x, lo - at, hi - at, live[at / 32]);
                             add_weights<kPlanes>(x, c, lp + at / 4, fp + at / 4, acc);
                         };
                         if constexpr (SMALL) {
-                            // 32 columns are loaded while the 32 before them are summed
+                            // few rows, or 32 columns loaded while the 32 before them
+                            // are summed (two contexts of 150001 to 199999 with 7 rows
+                            // a head: 48.3 us, 51.7 with 32 columns)
                             const int N = (cols + 31) & ~31;
-                            uint32_t x[2][32];
-                            tmem_ld32(s_at, x[0]);
+                            if (cols <= 16) {
+                                uint32_t x[16];
+                                tmem_ld16(s_at, x);
+                                tmem_ld_wait();
+                                add(x, 0);
+                            } else {
+                                uint32_t x[2][32];
+                                tmem_ld32(s_at, x[0]);
 #pragma unroll 1
-                            for (int c1 = 0; c1 < N; c1 += 64) {
-                                tmem_ld_wait();
-                                if (c1 + 32 < N) tmem_ld32(s_at + c1 + 32, x[1]);
-                                add(x[0], c1);
-                                if (c1 + 32 >= N) break;
-                                tmem_ld_wait();
-                                if (c1 + 64 < N) tmem_ld32(s_at + c1 + 64, x[0]);
-                                add(x[1], c1 + 32);
+                                for (int c1 = 0; c1 < N; c1 += 64) {
+                                    tmem_ld_wait();
+                                    if (c1 + 32 < N) tmem_ld32(s_at + c1 + 32, x[1]);
+                                    add(x[0], c1);
+                                    if (c1 + 32 >= N) break;
+                                    tmem_ld_wait();
+                                    if (c1 + 64 < N) tmem_ld32(s_at + c1 + 64, x[0]);
+                                    add(x[1], c1 + 32);
+                                }
                             }
                             tc_fence_before();
                             __syncwarp();

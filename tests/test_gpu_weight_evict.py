@@ -119,6 +119,39 @@ def test_many_rows_a_head(gpu_lib, e4m3, w, group):
     assert s.status.item() == 0
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_long_paths_and_parts_of_long_windows(gpu_lib, e4m3):
+    s = ref.Setup([100, 300], [260, 5], 2, 64, 16, e4m3, seed=12)
+    s.write_all()
+    check(s, 8, count=[70, 41], own_lse=False)
+    path = [sorted(np.random.default_rng(i).permutation(n)[:70].tolist()) for i, n in enumerate((100, 300))]
+    check(s, 8, count=[70, 69], path=path, own_lse=False)
+    check(s, 8, count=[70, 69], path=path, own_lse=False, window=50, sinks=7)
+    assert s.status.item() == 0
+
+
+def test_many_requests_with_many_rows(gpu_lib):
+    rng = np.random.default_rng(13)
+    w, ctx = rng.integers(0, 60, 50).tolist(), rng.integers(0, 900, 50).tolist()
+    s = ref.Setup(w, ctx, 1, 128, 32, False, seed=13)
+    s.write_all()
+    check(s, 4)
+    assert s.status.item() == 0
+
+
+@pytest.mark.parametrize("rows", [0, 3])
+def test_weights_of_no_rows(gpu_lib, rows):
+    """Without counted rows the old weights stay, and no other entry changes."""
+    s = ref.Setup([rows], [200], 2, 64, 16, False, seed=14)
+    s.write_all()
+    q, lse = torch.ones((rows, 4, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((rows, 4), device="cuda")
+    mass = torch.rand((1, 2, 220), generator=s.gen).cuda()
+    out = dict(mass=torch.full_like(mass, -7))
+    sdm.attend_weight(s.cache, q, lse, s.cu, s.ctx, 3, mass=mass, count=i32([0]), out=out, dev_status=s.status)
+    assert torch.equal(out["mass"][:, :, :200], mass[:, :, :200]) and (out["mass"][:, :, 200:] == -7).all()
+    assert s.status.item() == 0
+
+
 def test_many_requests_of_all_lengths(gpu_lib):
     rng = np.random.default_rng(5)
     w, ctx = rng.integers(0, 9, 70).tolist(), rng.integers(0, 700, 70).tolist()
@@ -255,7 +288,8 @@ def test_cuts(gpu_lib, in_place, e4m3, D, page, ctx, count, keep, sinks, recent)
         row += n[i]
 
 
-@pytest.mark.parametrize("R,n,keep", [(1, 70000, 30000), (1, 20001, 20000), (3, 9000, 100), (40, 3000, 2992)])
+@pytest.mark.parametrize("R,n,keep", [(1, 70000, 30000), (1, 20001, 20000), (3, 9000, 100), (40, 3000, 2992),
+                                      (80, 6000, 700), (40, 3000, 2983), (40, 3000, 2984), (1, 450000, 449000)])
 def test_long_caches(gpu_lib, R, n, keep):
     """Several CTAs a head, against a sort."""
     G, D, page = 2, 64, 64
