@@ -126,7 +126,9 @@ struct Cfg {
 template <int K, int Q, int L, int U, int S>
 struct Bars {
     uint64_t k_full[K], k_empty[K], q_full[Q], q_empty[Q], l_full[L], l_empty[L];
-    uint64_t s_full[S], s_empty[S], kt_full[2], k_idle, j_full[2][2], j_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages];
+    // A buffer is filled for the one warpgroup or the other, and a parity tells
+    // only the last phase from the next: each has a barrier of its own for it.
+    uint64_t s_full[S][2], s_empty[S], kt_full[2], k_idle, j_full[2][2], j_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages];
     uint64_t drain;
     uint32_t live[L][5];              // columns of the stage that add something; whether some do not
     uint32_t tmem;
@@ -552,7 +554,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             mbar_init(&bar.l_empty[lane], kSoft);
         }
         if (lane < C::kS) {
-            mbar_init(&bar.s_full[lane], 1);
+            mbar_init(&bar.s_full[lane][0], 1);
+            mbar_init(&bar.s_full[lane][1], 1);
             mbar_init(&bar.s_empty[lane], kSoft / 2);
         }
         if (lane < 2) mbar_init(&bar.kt_full[lane], D == 128 ? 8 : 4);
@@ -829,7 +832,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                             else issue_ts(d, tmem + kTmemK + t * (D / 2) + h * 32, q_ + panel, id, h > 0);
                         }
                     }
-                    mma_commit_warp(&bar.s_full[sr.at]);
+                    mma_commit_warp(&bar.s_full[sr.at][t]);
                     sr.step();
                     if (SMALL) {
                         mma_commit_warp(&bar.k_empty[kr.at]);
@@ -1091,6 +1094,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         // ------------------------------------------------------------------
         const int wg = (warp >> 2) & 1, half = warp >> 3;   // tile of keys; columns 64 half .. unless SMALL
         bool ok = true;
+        uint32_t s_phase = 0;             // of the warpgroup's barrier of each S buffer
         Ring<2> jr;
         Ring<C::kS> sr;
         Ring<C::kQSlots> qr;
@@ -1200,7 +1204,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                                 if (end * p.group < b.M) hi = min(hi, static_cast<int>(max(end, 0ll)) * p.group - first);
                             }
                         }
-                        ok = wait_or_fail(p, &bar.s_full[sr.at], sr.full());
+                        ok = wait_or_fail(p, &bar.s_full[sr.at][wg], (s_phase >> sr.at) & 1);
+                        s_phase ^= 1u << sr.at;
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t s_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + sr.at * 128;

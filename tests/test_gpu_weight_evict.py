@@ -130,6 +130,23 @@ def test_long_paths_and_parts_of_long_windows(gpu_lib, e4m3):
     assert s.status.item() == 0
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_heads_that_end_in_a_single_tile_of_keys(gpu_lib, e4m3):
+    """Units of one tile of keys, which only one half of the threads multiplies,
+    between units of two: each half waits for its own products all the same."""
+    rng = np.random.default_rng(15)
+    ctx = [int(rng.choice([3, 60, 100, 300, 250, 500, 20, 513])) for _ in range(60)]
+    s = ref.Setup([2] * 60, ctx, 4, 64, 16, e4m3, seed=15)         # a head's rows in one tile
+    s.write_all()
+    for _ in range(3):
+        check(s, 8)
+    s = ref.Setup([1300, 1100, 1420], [0, 10, 0], 8, 64, 32, e4m3, seed=16)   # many rows, few of which see a key
+    s.write_all()
+    for window, sinks in ((23, 0), (61, 1), (5, 0)):
+        check(s, 16, window=window, sinks=sinks, own_lse=False)
+    assert s.status.item() == 0
+
+
 def test_many_requests_with_many_rows(gpu_lib):
     rng = np.random.default_rng(13)
     w, ctx = rng.integers(0, 60, 50).tolist(), rng.integers(0, 900, 50).tolist()
