@@ -8,6 +8,12 @@
 // interleaved; elements from rot on pass.  Everything is fp32 and rounded to
 // bf16 once, but the angle: at positions of 10^5 a fp32 product is off by
 // 0.01 rad, so the turns position freq / 2 pi are reduced in fp64.
+//
+// What bounds it (32 query heads on 8 kv heads of 128): a prompt of 8192 tokens
+// into a bf16 cache 39 us, 5.1 TB/s, with half of the issue slots taken; 256
+// windows of 1 to 9 (28 heads on 4) into an e4m3 cache, read back, 14.7 us in a
+// graph and one token 4.0 us, both a chain of dependent loads: offsets, table,
+// rows.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -259,7 +265,8 @@ void (*kernel_of(int to))(const RotateParams) {
 cudaError_t launch_rotate(const RotateParams& p, int D, bool interleaved, cudaStream_t s) {
     RotateParams q = p;
     const int vectors = p.H + (p.cached ? 2 : 1) * p.G;
-    // few rows: a row's vectors go to several warps, down to one pass each
+    // few rows: a row's vectors go to several warps, down to one pass each (8 or
+    // 32 warps an SM wanted in place of 16: the same within 2 %)
     const long long want = 16LL * num_sms() / std::max(p.rows, 1);
     q.parts = static_cast<int>(std::max<long long>(1, std::min<long long>(want, (vectors + 3) / 4)));
     const long long items = static_cast<long long>(p.rows) * q.parts;
