@@ -118,10 +118,11 @@ struct Cfg {
     static constexpr int kThreads = 32 * (kSoft + 4);
     static constexpr int kQSlots = SMALL ? 2 : D == 128 ? 4 : 8;
     static constexpr int kLStages = SMALL ? 2 : 4;
+    static_assert(kLStages % 2 == 0, "a stage of -lse is always the same half's");
     static constexpr int kRing = SMALL ? 8 : 4;                // units handed out ahead
     static constexpr int kS = SMALL ? 4 : 3;                   // S buffers, products in turn
     static constexpr int kMiscBytes = kRing * sizeof(Blk) + kLStages * (kTile * 4 + 16) + (kPlanes ? 2 * kTile * 4 : 0) +
-                                      (kPlanes ? kExpStages * kTile : 0) + (SMALL ? 0 : 2 * kUnit * 4) + 704;
+                                      (kPlanes ? kExpStages * kTile : 0) + (SMALL ? 0 : 2 * kUnit * 4) + 832;
     static constexpr int kFit = (232448 - kMiscBytes - kQSlots * kQBytes) / kKBytes;
     static constexpr int kKSlots = !SMALL ? 2 : kFit < 10 ? kFit : 10;
     static_assert(kFit >= (SMALL ? 4 : 2), "shared memory");
@@ -131,16 +132,17 @@ struct Cfg {
     static constexpr int kCf = kL + kLStages * kTile * 4;      // planes: the columns' scales
     static constexpr int kExps = kCf + (kPlanes ? 2 * kTile * 4 : 0);
     static constexpr int kBlks = kExps + (kPlanes ? kExpStages * kTile : 0);
-    static constexpr int kXch = kBlks + kRing * static_cast<int>(sizeof(Blk));   // sums of the tiles' second halves
+    static constexpr int kXch = kBlks + kRing * static_cast<int>(sizeof(Blk));   // sums of the second half's warps
     static constexpr int kBars = kXch + (SMALL ? 0 : 2 * kUnit * 4);
 };
 
 template <int K, int Q, int L, int U, int S>
 struct Bars {
     uint64_t k_full[K], k_empty[K], q_full[Q], q_empty[Q], l_full[L], l_empty[L];
-    // A buffer is filled for the one warpgroup or the other, and a parity tells
-    // only the last phase from the next: each has a barrier of its own for it.
-    uint64_t s_full[S][2], s_empty[S], kt_full[2], k_idle, j_full[2][2], j_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages];
+    // A buffer is filled for one of two or four groups of warps (tile of keys,
+    // half), and a parity tells only the last phase from the next: each has a
+    // barrier of its own for it.
+    uint64_t s_full[S][4], s_empty[S], kt_full[2], k_idle[2], j_full[2][2], j_empty[2][2], blk_full[U], blk_empty[U], x_full[kExpStages];
     uint64_t drain;
     uint32_t live[L][5];              // columns of the stage that add something; whether some do not
     uint32_t tmem;
@@ -563,14 +565,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         }
         if (lane < C::kLStages) {
             mbar_init(&bar.l_full[lane], 1);
-            mbar_init(&bar.l_empty[lane], kSoft);
+            mbar_init(&bar.l_empty[lane], 8);
         }
         if (lane < C::kS) {
-            mbar_init(&bar.s_full[lane][0], 1);
-            mbar_init(&bar.s_full[lane][1], 1);
-            mbar_init(&bar.s_empty[lane], kSoft / 2);
+            for (int k = 0; k < 4; ++k) mbar_init(&bar.s_full[lane][k], 1);
+            mbar_init(&bar.s_empty[lane], 4);
         }
-        if (lane < 2) mbar_init(&bar.kt_full[lane], D == 128 ? 8 : 4);
+        if (lane < 2) {
+            mbar_init(&bar.kt_full[lane], D == 128 ? 8 : 4);
+            mbar_init(&bar.k_idle[lane], 1);
+        }
         if (lane < 4) {
             mbar_init(&bar.j_full[0][0] + lane, 4);
             mbar_init(&bar.j_empty[0][0] + lane, 4);
@@ -582,10 +586,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         if (lane < kExpStages) {
             mbar_init(&bar.x_full[lane], 1);
         }
-        if (lane == 0) {
-            mbar_init(&bar.drain, 1);
-            mbar_init(&bar.k_idle, 1);
-        }
+        if (lane == 0) mbar_init(&bar.drain, 1);
         fence_mbar_init();
     }
     pdl_wait();
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         Ring<C::kQSlots> qr;          // SMALL: the slot in use
         Ring<C::kS> sr;
         bool any_q = false;
-        uint32_t n_units = 0, n_two = 0;   // units, those of two tiles
+        uint32_t n_units = 0, n_two = 0, n_q = 0;   // units, those of two tiles, tiles of rows
         Blk b;
         while (take(ok, b)) {
             if (!(b.flags & U_HAS)) continue;
@@ -796,8 +797,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 // one before have read theirs (for e4m3 the warpgroups do it)
                 if constexpr (!E4M3) {
                     if (n_units > 0) {
-                        mma_commit_warp(&bar.k_idle);
-                        ok = wait_or_fail(p, &bar.k_idle, (n_units - 1) & 1);
+                        mma_commit_warp(&bar.k_idle[0]);
+                        ok = wait_or_fail(p, &bar.k_idle[0], (n_units - 1) & 1);
                     }
                     for (int t = 0; t < b.tiles && ok; ++t) {
                         ok = wait_or_fail(p, &bar.k_full[kr.at], kr.full());
@@ -844,19 +845,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                             else issue_ts(d, tmem + kTmemK + t * (D / 2) + h * 32, q_ + panel, id, h > 0);
                         }
                     }
-                    mma_commit_warp(&bar.s_full[sr.at][t]);
+                    mma_commit_warp(&bar.s_full[sr.at][SMALL ? t : t + 2 * (n_q & 1)]);
                     sr.step();
                     if (SMALL) {
                         mma_commit_warp(&bar.k_empty[kr.at]);
                         kr.step();
                     }
                 }
+                ++n_q;
                 if (!SMALL && ok) {
                     mma_commit_warp(&bar.q_empty[qr.at]);
                     qr.step();
                 }
             }
             if (!ok) break;
+            if constexpr (E4M3 && !SMALL)
+                for (int t = 0; t < b.tiles; ++t) mma_commit_warp(&bar.k_idle[t]);
         }
         // products in flight end before the tensor memory goes
         mma_commit_warp(&bar.drain);
@@ -1104,8 +1108,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         // ------------------------------------------------------------------
         // weights: a thread per key
         // ------------------------------------------------------------------
-        const int wg = (warp >> 2) & 1, half = warp >> 3;   // tile of keys; columns 64 half .. unless SMALL
+        const int wg = (warp >> 2) & 1, half = warp >> 3;   // tile of keys; which tiles of rows, unless SMALL
         bool ok = true;
+        uint32_t n_q = 0, n_mine = 0;     // tiles of rows; units with keys of this warpgroup
         uint32_t s_phase = 0;             // of the warpgroup's barrier of each S buffer
         Ring<2> jr;
         Ring<C::kS> sr;
@@ -1149,8 +1154,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                     }
                 }
                 if constexpr (E4M3 && !SMALL) {
-                    // the tile's codes as bf16 into tensor memory, a key a thread: the
-                    // products of its last tile were complete when its S was read
+                    // the tile's codes as bf16 into tensor memory, a key a thread, once
+                    // the products of its last unit are complete: those of the last tile
+                    // of rows may be the other half's. No phase of k_idle is missed: the
+                    // next one's products wait for all these warps
                     if (mine && half < D / 64) {   // a half of the row each
                         uint4 x[4];
                         float s = 1.f;
@@ -1168,6 +1175,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) x[k] = __ldg(src + k);
                         }
+                        if (n_mine > 0) ok = wait_or_fail(p, &bar.k_idle[wg], (n_mine - 1) & 1);
+                        if (!ok) break;
+                        ++n_mine;
                         tc_fence_after();
                         uint32_t z[32];
 #pragma unroll
@@ -1198,12 +1208,20 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 }
                 for (int q = b.q0; q < b.q1 && ok; ++q) {
                     const float* lq = l2 + (SMALL ? qr.at : lr.at) * kTile;
-                    if (!SMALL) {
+                    // the halves take the tiles of rows in turn: one waits and loads
+                    // while the other sums (8192 tokens, 32 / 8 heads: 222 us; 243 with
+                    // half of every tile's columns each)
+                    const bool turn = SMALL || static_cast<int>(n_q & 1) == half;
+                    ++n_q;
+                    if (!SMALL && turn) {
                         ok = wait_or_fail(p, &bar.l_full[lr.at], lr.full());
                         if (!ok) break;
                     }
                     if (wg == 1) sr.step();           // the other warpgroup's
-                    if (mine) {
+                    if (mine && !turn) {
+                        sr.step();
+                        if (wg == 0 && b.tiles == 2) sr.step();
+                    } else if (mine) {
                         const int cols = SMALL ? b.M : p.sub, first = q * p.sub;
                         // columns [lo, hi) see this key
                         int lo = 0, hi = min(cols, b.M - first);
@@ -1216,7 +1234,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                                 if (end * p.group < b.M) hi = min(hi, static_cast<int>(max(end, 0ll)) * p.group - first);
                             }
                         }
-                        ok = wait_or_fail(p, &bar.s_full[sr.at][wg], (s_phase >> sr.at) & 1);
+                        ok = wait_or_fail(p, &bar.s_full[sr.at][SMALL ? wg : wg + 2 * half], (s_phase >> sr.at) & 1);
                         s_phase ^= 1u << sr.at;
                         if (!ok) break;
                         tc_fence_after();
@@ -1257,15 +1275,21 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                             if (lane == 0) mbar_arrive(&bar.s_empty[sr.at]);
                         } else {
                             uint32_t x[32];
-                            tmem_ld32(s_at + half * 64, x);
+                            tmem_ld32(s_at, x);
                             tmem_ld_wait();
-                            add(x, half * 64);
-                            tmem_ld32(s_at + half * 64 + 32, x);
+                            add(x, 0);
+                            tmem_ld32(s_at + 32, x);
+                            tmem_ld_wait();
+                            add(x, 32);
+                            tmem_ld32(s_at + 64, x);
+                            tmem_ld_wait();
+                            add(x, 64);
+                            tmem_ld32(s_at + 96, x);
                             tmem_ld_wait();
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bar.s_empty[sr.at]);
-                            add(x, half * 64 + 32);
+                            add(x, 96);
                         }
                         sr.step();
                         if (wg == 0 && b.tiles == 2) sr.step();
@@ -1279,14 +1303,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                     }
                     if (!SMALL) {
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.l_empty[lr.at]);
+                        if (turn && lane == 0) mbar_arrive(&bar.l_empty[lr.at]);
                         lr.step();
                     }
                 }
                 if (!ok) break;
             }
             if constexpr (!SMALL) {
-                // the two halves of the columns
+                // the two halves' tiles of rows
                 float* xch = reinterpret_cast<float*>(smem + C::kXch) + jr.at * kUnit + wg * kTile + (tid & 127);
                 if (half == 1) {
                     ok = wait_or_fail(p, &bar.j_empty[wg][jr.at], jr.empty());
@@ -1380,6 +1404,7 @@ template <int D, bool E4M3, bool SMALL>
 cudaError_t launch_one(const WeighParams& p, void* work, cudaStream_t s) {
     using C = Cfg<D, E4M3, SMALL>;
     constexpr int kTotal = C::kBars + static_cast<int>(sizeof(Bars<C::kKSlots, C::kQSlots, C::kLStages, C::kRing, C::kS>));
+    static_assert(kTotal <= 232448, "shared memory");
     static const cudaError_t raised = cudaFuncSetAttribute(weigh_kernel<D, E4M3, SMALL>,
                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kTotal);
     if (raised != cudaSuccess) return raised;
