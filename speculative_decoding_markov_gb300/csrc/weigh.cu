@@ -21,8 +21,9 @@
 // leave their sums in the workspace, and weigh_join_kernel adds them in order.
 //
 // A CTA: a warp walks the share, hands units out and loads keys page by page by
-// TMA; one brings the query rows (by TMA, or gathered along a path); one their
-// -lse; one issues the products; eight turn S into weights.
+// TMA; one brings the query rows (by TMA, or gathered along a path; six split
+// those of an e4m3 cache); one their -lse; one issues the products; eight, or 16
+// unless SMALL, turn S into weights.
 //
 // An e4m3 cache: if SMALL its codes are operands as they are.  A bf16 query
 // splits exactly into three e5m2 numbers (8 significant bits as 3 + 3 + 2,
@@ -37,13 +38,15 @@
 //
 // What bounds it (32 query heads on 8 kv heads of 128, bf16, unless said):
 //   64 windows of 1 to 8 tokens over 300 to 8000: HBM, 5.7 TB/s of keys (55 us).
-//   A prompt of 8192 tokens: 243 us, 1.13 PFLOP/s.  Tensor pipe 49 %, issue 58
-//   %: the products by themselves take 164 us (without the weights), and the
-//   exponentials' unit 122 us; four warps a scheduler do not cover all of the
-//   latency of one by the other.
-//   Two rows over 150001 to 199999, e4m3 (28 heads on 4): 48 us, 3.7 TB/s.  A
-//   unit's chain through a warpgroup (unit taken, scores, 16 columns, old
-//   weight) is longer than its 33 KB take.
+//   A prompt of 8192 tokens: 222 us, 1.24 PFLOP/s.  Tensor pipe 52 %, the
+//   exponentials' unit 53 %, issue 56 %: the products by themselves take 164 us
+//   (without the weights) and the exponentials 122 us.  Tensor memory has three
+//   buffers of scores for four groups of warps.
+//   Two rows over 150001 to 199999, e4m3 (28 heads on 4): 49 us, 3.7 TB/s.  A
+//   unit of 33 KB takes each of walker, products and weights about a
+//   microsecond of waits and instructions (without its loads: 49 us; with a
+//   third of the products 46; without sums 47; two groups of weight warps in
+//   turn: 52, for want of registers).
 //   One token over 500 keys: 5.7 us in a graph, the chain of plan, loads and
 //   product.
 #include <cudaTypedefs.h>
@@ -115,7 +118,12 @@ struct Cfg {
     // warps of the weights: one per scheduler hides little of the exponentials'
     // and the loads' latency, so many rows get two for each tile of keys
     static constexpr int kSoft = SMALL ? 8 : 16;
-    static constexpr int kThreads = 32 * (kSoft + 4);
+    // warps of the query rows and their -lse: two take longer to split a head's
+    // rows into planes than its keys take (64 windows over 300 to 8000, e4m3: of
+    // 1 to 8 tokens 103 us with two, 73 with six; of 16 to 30 tokens 302 and 159);
+    // 16 warps in all leave a thread 128 registers, 18 only 96
+    static constexpr int kRows = kPlanes ? 6 : 2;
+    static constexpr int kThreads = 32 * (kSoft + 2 + kRows);
     static constexpr int kQSlots = SMALL ? 2 : D == 128 ? 4 : 8;
     static constexpr int kLStages = SMALL ? 2 : 4;
     static_assert(kLStages % 2 == 0, "a stage of -lse is always the same half's");
@@ -560,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             mbar_init(&bar.k_empty[k], 1);
         }
         if (lane < C::kQSlots) {
-            mbar_init(&bar.q_full[lane], SMALL ? 2 : 1);
+            mbar_init(&bar.q_full[lane], SMALL ? C::kRows : 1);
             mbar_init(&bar.q_empty[lane], SMALL ? 9 : 1);
         }
         if (lane < C::kLStages) {
@@ -581,7 +589,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         }
         if (lane < C::kRing) {
             mbar_init(&bar.blk_full[lane], 1);
-            mbar_init(&bar.blk_empty[lane], kSoft + 3);   // the warps that read it
+            mbar_init(&bar.blk_empty[lane], kSoft + 1 + C::kRows);   // the warps that read it
         }
         if (lane < kExpStages) {
             mbar_init(&bar.x_full[lane], 1);
@@ -867,9 +875,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         mbar_wait(&bar.drain, 0);
     } else if (warp > kSoft + 1) {
         // ------------------------------------------------------------------
-        // the query rows (one warp; split into planes: both) and their -lse
+        // the query rows (one warp; split into planes: all of them) and their -lse
         // ------------------------------------------------------------------
-        const bool rows_warp = warp == kSoft + 2;
+        const bool rows_warp = warp != kSoft + 3;
         bool ok = true;
         Ring<C::kQSlots> qr;
         Ring<C::kLStages> lr;
@@ -948,7 +956,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             Counted w;
             w.row0 = b.row0;
             w.wide = b.wide;
-            for (int r0 = rows_warp ? 0 : 4; r0 < N; r0 += 8) {
+            for (int r0 = 4 * (warp - kSoft - 2); r0 < N; r0 += 4 * C::kRows) {
                 uint32_t x[4][2];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -1209,8 +1217,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                 for (int q = b.q0; q < b.q1 && ok; ++q) {
                     const float* lq = l2 + (SMALL ? qr.at : lr.at) * kTile;
                     // the halves take the tiles of rows in turn: one waits and loads
-                    // while the other sums (8192 tokens, 32 / 8 heads: 222 us; 243 with
-                    // half of every tile's columns each)
+                    // while the other sums (8192 tokens, 32 / 8 heads: 222 us; 242 with
+                    // half of every tile's columns each; 254 with six buffers of 64
+                    // columns, whose products take as long as those of 128; 257 with
+                    // 16 columns loaded while 16 are summed)
                     const bool turn = SMALL || static_cast<int>(n_q & 1) == half;
                     ++n_q;
                     if (!SMALL && turn) {
