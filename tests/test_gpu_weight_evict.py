@@ -131,6 +131,32 @@ def test_long_paths_and_parts_of_long_windows(gpu_lib, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_number_of_rows_over_short_contexts(gpu_lib, e4m3, D):
+    """Heads of 4 to 128 rows, a unit or two of keys each: the next head's rows
+    are made ready while this one's are multiplied."""
+    w = list(range(1, 33))
+    s = ref.Setup(w, [(37 * k) % 400 for k in w], 2, D, 32, e4m3, seed=17)
+    s.write_all()
+    check(s, 8)
+    check(s, 8, window=90, sinks=2, own_lse=False)
+    assert s.status.item() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_windows_whose_units_have_one_tile_or_two(gpu_lib, e4m3, D):
+    """An odd and an even number of tiles of rows a unit, units of one tile of
+    keys between units of two, heads that follow one another."""
+    s = ref.Setup([100, 513, 65, 290], [20, 0, 300, 100], 3, D, 64, e4m3, seed=18)
+    s.write_all()
+    for _ in range(2):
+        check(s, 12)
+    check(s, 12, window=77, sinks=5, own_lse=False)
+    assert s.status.item() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_heads_that_end_in_a_single_tile_of_keys(gpu_lib, e4m3):
     """Units of one tile of keys, which only one half of the threads multiplies,
     between units of two: each half waits for its own products all the same."""
