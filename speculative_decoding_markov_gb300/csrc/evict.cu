@@ -395,9 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
             hole += __reduce_add_sync(0xffffffffu, __popc(holes));
             mover += __reduce_add_sync(0xffffffffu, __popc(movers));
             const int s = s0 + (k0 + lane) * 32;
-            for (; holes; holes &= holes - 1) to[h_at++] = s + __ffs(holes) - 1;
-            for (; movers; movers &= movers - 1) from[m_at++] = s + __ffs(movers) - 1;
+            // Keys that are looked up again are other ones if weights or positions
+            // change meanwhile (which a call does not allow): no place is taken on trust.
+            for (; holes; holes &= holes - 1, ++h_at)
+                if (static_cast<unsigned>(h_at) < p.most) to[h_at] = s + __ffs(holes) - 1;
+            for (; movers; movers &= movers - 1, ++m_at)
+                if (static_cast<unsigned>(m_at) < p.most) from[m_at] = s + __ffs(movers) - 1;
         }
+        total = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(p.most)));
         meet();   // the lists are whole
     }
 
@@ -424,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
             const int j = j0 + q * slots;
             src[q] = j >= total ? -1 : few ? sh.src[j] : __ldcg(from + j);
             dst[q] = j >= total ? -1 : few ? sh.dst[j] : __ldcg(to + j);
+            if (src[q] >= h.n || static_cast<unsigned>(dst[q]) >= static_cast<unsigned>(keep)) src[q] = -1;
         }
 #pragma unroll
         for (int q = 0; q < kMoves; ++q) {
