@@ -32,6 +32,7 @@ namespace cg = cooperative_groups;
 constexpr int kBins = 2048;
 constexpr int kMoves = 4;          // moves of a thread in flight together
 constexpr int kList = 1024;        // keys that share the first digits
+constexpr int kMost = 48 * 1024;   // keys a CTA can hold
 constexpr int kFew = 16;           // slots to go that are looked for one by one
 
 // Of a run of slots: those above the keep-th largest key and equal to it, in
@@ -467,7 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
 
 template <int THREADS>
 cudaError_t launch_one(const EvictParams& p, int C, cudaStream_t s) {
-    constexpr int kMost = 48 * 1024;   // keys a CTA can hold
     static const cudaError_t raised =
         cudaFuncSetAttribute(evict_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4);
     if (raised != cudaSuccess) return raised;
@@ -493,7 +493,9 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
     q.most = most_moves(p.stride, p.keep);
     const long long items = static_cast<long long>(p.R) * p.c.heads;
     int C = 1;
-    while (C < 8 && items * C * 2 <= 2LL * num_sms() && p.stride / (2 * C) >= 2048) C *= 2;
+    // more CTAs a head while the SMs have room, or while its keys do not fit in one
+    // (14 requests of up to 148331 tokens and 16 heads, cut to 314: 700 us alone, looked up anew)
+    while (C < 8 && p.stride / (2 * C) >= 2048 && (items * C * 2 <= 2LL * num_sms() || p.stride / C > kMost)) C *= 2;
     // short runs: smaller CTAs, more of which are on an SM together
     return p.stride / C <= 4096 && C == 1 ? launch_one<256>(q, C, s) : launch_one<512>(q, C, s);
 }
