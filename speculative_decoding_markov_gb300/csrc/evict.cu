@@ -494,7 +494,8 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
     const long long items = static_cast<long long>(p.R) * p.c.heads;
     int C = 1;
     // more CTAs a head while the SMs have room, or while its keys do not fit in one
-    // (14 requests of up to 148331 tokens and 16 heads, cut to 314: 700 us alone, looked up anew)
+    // (14 requests of up to 148331 tokens and 16 heads, cut to 314: 194 us; 700 in one CTA,
+    // which looks its keys up anew)
     while (C < 8 && p.stride / (2 * C) >= 2048 && (items * C * 2 <= 2LL * num_sms() || p.stride / C > kMost)) C *= 2;
     // short runs: smaller CTAs, more of which are on an SM together
     return p.stride / C <= 4096 && C == 1 ? launch_one<256>(q, C, s) : launch_one<512>(q, C, s);

@@ -193,3 +193,10 @@ def test_a_captured_call_and_another_stream(gpu_lib):
     graph.replay()
     check_rows(out, target, [(i, p, 4 * i + p) for i in range(2) for p in range(4)], tok.flatten().tolist(), 1.0, 5)
     assert st.item() == 0
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [256, 264, 832, 1200, 1792, 2040])
+@pytest.mark.parametrize("top,T", [(13, 1.0), (20, 0.7), (32, 1.3)])
+def test_long_lists_of_short_rows(gpu_lib, dt, V, top, T):
+    test_ragged_windows(gpu_lib, dt, V, top, T)

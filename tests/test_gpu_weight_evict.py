@@ -157,6 +157,47 @@ def test_long_windows_whose_units_have_one_tile_or_two(gpu_lib, e4m3, D):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G,window,sinks,count", [(1, 100, 3, None), (8, 700, 300, None), (2, 1, 0, [1, 0, 2, 0])])
+def test_long_contexts_of_which_little_is_seen(gpu_lib, e4m3, G, window, sinks, count):
+    """Weights that only pass through, many units at a time."""
+    s = ref.Setup([1, 4, 2, 1], [60001, 20011, 257, 40448], G, 64, 64, e4m3, seed=19)
+    s.write_all()
+    check(s, 2 * G, window=window, sinks=sinks, count=count, own_lse=False)
+    assert s.status.item() == 0
+
+
+@pytest.mark.parametrize("keep", [300, 70000])
+@pytest.mark.parametrize("G", [2, 160])
+def test_runs_of_slots_that_a_block_cannot_hold(gpu_lib, keep, G):
+    """More slots than one block's shared memory has keys for, with few heads
+    and with more than fill the SMs; weights that are often equal."""
+    n = 100003
+    gen = torch.Generator().manual_seed(G + keep)
+    table = torch.zeros((1, -(-n // 128)), dtype=torch.int32, device="cuda")
+    table[0] = torch.arange(table.shape[1], dtype=torch.int32, device="cuda")
+    cache = sdm.PagedCache.empty(table.shape[1], G, 128, 64, table)
+    cache.k.view(torch.int16).copy_(torch.arange(n // 128 + 1, device="cuda")[:, None, None, None] * 128 % 32003 +
+                                    torch.arange(128, device="cuda")[None, None, :, None])
+    before = cache.k.view(torch.int16).permute(1, 0, 2, 3).reshape(G, -1, 64)[:, :, 0].clone()
+    mass = torch.randint(0, 5000, (1, G, n), generator=gen).float().cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").expand(1, G, n).contiguous()
+    out = dict(mass=torch.zeros_like(mass), pos=torch.zeros_like(pos),
+               length=torch.zeros((1,), dtype=torch.int32, device="cuda"))
+    status = sdm.new_status()
+    sdm.cache_evict(cache, mass, pos, i32([n]), i32([n]), keep, sinks=4, recent=9, out=out, dev_status=status)
+    assert status.item() == 0 and out["length"].item() == keep
+    key = mass[0].clone()
+    key[:, :4] = key[:, n - 9:] = 1e30
+    order = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :keep]
+    want = torch.sort(order, dim=1).values
+    got = out["pos"][0, :, :keep].long()
+    assert torch.equal(torch.sort(got, dim=1).values, want)
+    assert torch.equal(out["mass"][0, :, :keep], mass[0].gather(1, got))
+    after = cache.k.view(torch.int16).permute(1, 0, 2, 3).reshape(G, -1, 64)[:, :keep]
+    assert torch.equal(after[:, :, 0], before.gather(1, got)) and torch.equal(after[:, :, 63], after[:, :, 0])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_heads_that_end_in_a_single_tile_of_keys(gpu_lib, e4m3):
     """Units of one tile of keys, which only one half of the threads multiplies,
     between units of two: each half waits for its own products all the same."""
