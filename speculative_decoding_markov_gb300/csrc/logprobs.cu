@@ -476,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
                 const int v = at + k * kThreads;
+                if (v >= v1) continue;   // filled up with -inf, which a masked token's logit equals
                 if (v < said_in) x[k].template above<true>(said, ahead, halves);
                 else x[k].template above<false>(said, ahead, halves);
                 if (v == said_in)

@@ -1,0 +1,44 @@
+"""Log probabilities where they went wrong once: masked tokens of rows that
+several blocks share."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from speculative_decoding_markov_gb300 import binding as sdm
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [40008, 151936])
+@pytest.mark.parametrize("items", [1, 13, 150, 300, 600, 700])
+def test_ranks_of_masked_tokens_in_every_share(gpu_lib, dt, V, items):
+    """Tokens of -inf, which only those of -inf in front of them and the allowed
+    ones come before, in each of the 8, 4 or 2 shares of a row, and in one."""
+    gen = torch.Generator().manual_seed(items)
+    z = torch.full((items, V), -INF)
+    z[:, 5::1013] = torch.randn((items, -(-(V - 5) // 1013)), generator=gen)
+    z[1::5] = -INF                                                 # rows without an allowed token
+    z[2::5, V - 2] = 1.0                                           # and with one of the last
+    tok = torch.randint(0, V, (1, items), generator=gen, dtype=torch.int32)
+    ends = [V - 1, V - 7, V - 9, V - V // 8, V // 8 * 3 - 1, V // 2 + 8, V // 2 - 1, 0]
+    for k in range(items):
+        if k % 3 != 2:
+            tok[0, k] = ends[k // 3 % len(ends) if items > 1 else 0]
+    z, tok = z.to(dt).cuda(), tok.cuda()
+    out = sdm.token_logprobs(z, i32([0, items]), tok, top=3)
+    assert out["dev_status"].item() == 0
+    y = tok[0].long()[:, None]
+    said, ids = z.gather(1, y), torch.arange(V, device="cuda")
+    rank = ((z > said) | ((z == said) & (ids < y))).sum(1).int()
+    assert torch.equal(out["rank"][0], rank)
+    some = (z > -INF).any(1)
+    assert (out["logp"][0][some & (said[:, 0] == -INF)] == -INF).all()
+    key = torch.where(z > -INF, z.float(), -1e30)
+    assert torch.equal(out["top_tok"][0].long(), torch.sort(key, dim=1, descending=True, stable=True)[1][:, :3])
