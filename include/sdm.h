@@ -729,7 +729,8 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
  *      < 2^31.
  * Out: q_out, and k_out without a cache (NULL with one): rows with strides of
  *      their own; each may be its input.  Rows that no window holds are left
- *      as they were.  fp32 throughout, rounded to bf16 once.
+ *      as they were; one that several hold (offsets that are not monotone) is
+ *      rotated for one of them.  fp32 throughout, rounded to bf16 once.
  * Device checks as in sdm_cache_write; a row whose page is bad still has its
  * query rotated, one past the page table is left out.
  */

@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateParams 
     n.r0 = INTER ? 2 * n.l : n.turns ? n.l : 2 * half + 2 * (n.l - half);
     n.r1 = INTER ? 2 * n.l + 1 : n.turns ? n.l + half : n.r0 + 1;
 
-    auto do_row = [&](int row, int part, int known) {
+    // `turn`: the rows' own outputs too, not only what goes into the cache
+    auto do_row = [&](int row, int part, int known, bool turn) {
         const int v_from = static_cast<int>(static_cast<long long>(vectors) * part / p.parts);
         const int v_to = static_cast<int>(static_cast<long long>(vectors) * (part + 1) / p.parts);
         const int i = known >= 0 ? known : warp_find_request(p.cu, p.R, row);
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateParams 
                 sn[o * kOwn + j] = __shfl_sync(0xffffffffu, z, n.l + o * kLanes);
             }
         }
-        if (v_from < p.H)
+        if (turn && v_from < p.H)
             section<D, INTER, false, TO_ROWS, kBatch>(n, p.q + row * p.q_stride, v_from, min(v_to, p.H), p.q_weight, p.eps,
                                                       cs, sn, reinterpret_cast<uint8_t*>(p.q_out + row * p.q_out_stride),
                                                       2 * D, nullptr, 0, true);
@@ -244,12 +245,34 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const RotateParams 
     if (static_cast<int>(blockIdx.x) < blocks) {
         const long long items = static_cast<long long>(min(p.rows, __ldg(p.cu + p.R))) * p.parts;
         for (long long t = blockIdx.x * kWarps + warp; t < items; t += blocks * kWarps)
-            do_row(static_cast<int>(t / p.parts), static_cast<int>(t % p.parts), -1);
+            do_row(static_cast<int>(t / p.parts), static_cast<int>(t % p.parts), -1, true);
     } else if (check_windows<kThreads>(p.cu, p.ctx, p.R, p.rows, tokens, p.dev_status)) {
+        // The outputs may be the inputs, so that no row may be turned twice: rows
+        // that the search finds are the other blocks', and of several windows
+        // that hold one of the rest the first turns it.  (Every window's keys
+        // and values go into its slots.)
+        const int n_rows = min(p.rows, __ldg(p.cu + p.R));
+        auto holds = [&](int i, int row) {
+            const Window w = window_of(p.cu, p.ctx, i, p.rows, 0x7fffffff, tokens);
+            return row >= w.row0 && row < w.row0 + w.n;
+        };
+        int reach = 0;   // no window before holds a row from here on
         for (int i = 0; i < p.R; ++i) {
             const Window w = window_of(p.cu, p.ctx, i, p.rows, 0x7fffffff, tokens);
-            for (int k = warp; k < w.n; k += kWarps)
-                for (int part = 0; part < p.parts; ++part) do_row(w.row0 + k, part, i);
+            for (int k = warp; k < w.n; k += kWarps) {
+                const int row = w.row0 + k;
+                bool turn = true;
+                if (row < n_rows) {
+                    const int found = warp_find_request(p.cu, p.R, row);
+                    if (found == i) continue;
+                    turn = !holds(found, row);
+                }
+                for (int j = 0; turn && row < reach && j < i; j += 32)
+                    turn = !__any_sync(0xffffffffu, j + lane < i && holds(j + lane, row));
+                if (TO == TO_ROWS && !turn) continue;
+                for (int part = 0; part < p.parts; ++part) do_row(row, part, i, turn);
+            }
+            reach = max(reach, w.row0 + w.n);
         }
     }
 }
