@@ -760,8 +760,8 @@ sdm_status sdm_qk_rotate(const sdm_cache* cache, const uint16_t* q, int64_t q_st
  *      from n[i] on are left as they were.
  * Sums are fp32 relative to a reference near the maximum.  A logit of -inf has
  * logp -inf; a row of nothing else, or with a NaN, has logp and entropy NaN (a
- * row with a NaN has some ranks and some `top` different tokens), one with
- * +inf logp -inf but for those NaN, entropy NaN.
+ * NaN has some rank, and is listed as if it were -inf), one with +inf logp
+ * -inf but for those NaN, entropy NaN.
  * Device checks: n[i] outside [0, W] (cut), a row outside its window
  * (SDM_DEV_BAD_WINDOW) or past row_capacity (SDM_DEV_CAPACITY): left out; a
  * token outside [0, V) has logp -inf and rank V (SDM_DEV_BAD_TOKEN).

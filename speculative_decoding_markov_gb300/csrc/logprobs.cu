@@ -94,6 +94,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ __nv_bfloat162 pair_of(uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); }
 __device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
+// An element's place in the list.  A NaN stands with the elements of -inf,
+// whatever its sign and payload: a thread's largest element, which leaves NaN
+// out, is then the largest of all of its places, and -inf if it has only NaN.
+__device__ __forceinline__ uint32_t place_of(float z) { return ordered_bits(z == z ? z : -INFINITY); }
+__device__ __forceinline__ unsigned long long list_key(float z, uint32_t id) {
+    return argmax_key(z == z ? z : -INFINITY, id);
+}
+
 // Eight logits of a row, from element 8 vec on.
 template <bool FP32>
 struct Vec {
@@ -207,7 +215,7 @@ __device__ unsigned long long next_key(const uint8_t* row, int v0, int v1, unsig
         Vec<FP32> x;
         x.load(row, v);
         for (int j = 0; j < 8; ++j) {
-            const unsigned long long k = argmax_key(x.at(j), 8 * v + j);
+            const unsigned long long k = list_key(x.at(j), 8 * v + j);
             if (k < below) best = umax64(best, k);
         }
     }
@@ -256,9 +264,9 @@ __device__ __forceinline__ void list_candidates(const uint8_t* row, int v0, int 
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float z = x.at(j);
-            if (ordered_bits(z) >= from) {
+            if (place_of(z) >= from) {
                 const int at = atomicAdd(&sh.count, 1);
-                if (at < kCand) sh.cand[at] = argmax_key(z, 8 * v + j);
+                if (at < kCand) sh.cand[at] = list_key(z, 8 * v + j);
             }
         }
     }
@@ -323,7 +331,7 @@ __device__ void pick_top(const uint8_t* row, int v0, int v1, const Largest& mine
                 if (v < v1) {
                     x.load(row, v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) hit |= static_cast<uint32_t>(ordered_bits(x.at(j)) == bound) << j;
+                    for (int j = 0; j < 8; ++j) hit |= static_cast<uint32_t>(place_of(x.at(j)) == bound) << j;
                 }
                 // their places, in the order of the ids
                 int incl = __popc(hit);
@@ -343,7 +351,7 @@ __device__ void pick_top(const uint8_t* row, int v0, int v1, const Largest& mine
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if ((hit >> j) & 1u) {
-                        if (at < n_out) sh.cand[at] = argmax_key(x.at(j), 8 * v + j);
+                        if (at < n_out) sh.cand[at] = list_key(x.at(j), 8 * v + j);
                         ++at;
                     }
                 n = min(n + all, n_out);

@@ -1,5 +1,5 @@
 """Log probabilities where they went wrong once: masked tokens of rows that
-several blocks share."""
+several blocks share, rows of NaN."""
 from __future__ import annotations
 
 import pytest
@@ -42,3 +42,32 @@ def test_ranks_of_masked_tokens_in_every_share(gpu_lib, dt, V, items):
     assert (out["logp"][0][some & (said[:, 0] == -INF)] == -INF).all()
     key = torch.where(z > -INF, z.float(), -1e30)
     assert torch.equal(out["top_tok"][0].long(), torch.sort(key, dim=1, descending=True, stable=True)[1][:, :3])
+
+
+@pytest.mark.parametrize("dt,bits", [(torch.bfloat16, 0x7fc0), (torch.bfloat16, 0xffc0), (torch.bfloat16, 0xffff),
+                                     (torch.float32, 0x7fffffff), (torch.float32, 0xffc00000), (torch.float32, 0xffffffff)])
+@pytest.mark.parametrize("V", [8, 64, 1000, 5000, 40008, 151936])
+def test_lists_of_rows_of_nan(gpu_lib, dt, bits, V):
+    """Different tokens of the row, NaN last of all whatever their sign and payload."""
+    whole, size = (torch.int16, 16) if dt is torch.bfloat16 else (torch.int32, 32)
+    nan = torch.tensor([bits - (1 << size if bits >> (size - 1) else 0)]).to(whole).view(dt)
+    at, gen = torch.arange(V), torch.Generator().manual_seed(V)
+    a = torch.randn((V,), generator=gen).to(dt)
+    rows = [torch.where(at < 0, a, nan), torch.where(at % 101 == 3, a, nan), torch.where(at == V - 1, a, nan),
+            torch.where(at % 2 == 0, a, nan), torch.where(at % 3 == 0, torch.tensor(-INF, dtype=dt), nan),
+            torch.where(at == V // 2, nan, a), torch.where(at < V // 2, nan, a)]
+    target = torch.stack(rows).cuda()
+    n = target.shape[0]
+    for items in (n, 700):                                         # rows of several blocks, and of one
+        z = target.repeat(-(-items // n), 1)[:items].contiguous()
+        for top in (1, 6, 32):
+            top = min(top, V)
+            out = sdm.token_logprobs(z, i32([0, items]), i32([[0] * items]), top=top)
+            assert out["dev_status"].item() == 0
+            assert out["logp"].isnan().all() and out["entropy"].isnan().all()
+            ids = out["top_tok"][0].cpu()
+            assert (ids >= 0).all() and (ids < V).all()
+            assert out["top_logp"].isnan().all()
+            key = torch.where(target.isnan(), -INF, target.float())
+            want = torch.sort(key, dim=1, descending=True, stable=True)[1][:, :top].cpu()
+            assert torch.equal(ids, want.repeat(-(-items // n), 1)[:items].int())
