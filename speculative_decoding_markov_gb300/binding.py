@@ -884,18 +884,18 @@ def attend_weight(cache, q, lse, cu_seqlens, ctx_len, max_count, mass=None, coun
         raise ValueError(f"out['mass'] must be [{R}, {G}, tokens]")
     mo = _need_out("out['mass']", out["mass"], shape, torch.float32, dev)
     mi = None if mass is None else _need_out("mass", mass, shape, torch.float32, dev)
-    stride = 0
+    stride, at = 0, None   # `path` itself lives on: a workspace could be allocated where it was
     if path is not None:
         if path.dim() != 2 or path.shape[0] != R or path.shape[1] < max_count:
             raise ValueError("path must be [requests, at least max_count]")
         stride = path.shape[1]
-        path = _need_i32("path", path, R * stride, dev)
+        at = _need_i32("path", path, R * stride, dev)
     ws = attend_weight_workspace(cache, max_count, H) if ws is None else ws
     dev_status = _new_status_in(out, q.device) if dev_status is None else dev_status
     st = lib().sdm_attend_weight(cache.ref, q.data_ptr(), qs, _need_out("lse", lse, (rows, H), torch.float32, dev),
                                  _need_i32("cu_seqlens", cu_seqlens, R + 1, dev),
                                  _need_i32("ctx_len", ctx_len, R, dev),
-                                 None if count is None else _need_i32("count", count, R, dev), path, stride, R, rows,
+                                 None if count is None else _need_i32("count", count, R, dev), at, stride, R, rows,
                                  max_count, H, D ** -0.5 if scale is None else scale, window, sinks, mi, mo, shape[2],
                                  _need_ws(ws, dev), ws.numel(), _need_status(dev_status, dev), _stream_of(cache))
     if st:

@@ -3,6 +3,8 @@ and eviction entry points and the binding's checks (no GPU: these paths return
 before any CUDA call)."""
 from __future__ import annotations
 
+import weakref
+
 import pytest
 import torch
 
@@ -211,3 +213,39 @@ def test_logprobs_binding(called, bad):
     assert not called
     binding.token_logprobs(**logprob_args())
     assert len(called) == 1
+
+
+def test_tensors_live_until_the_library_is_called(called, monkeypatch):
+    """A tensor made in the call itself is not freed before the launch: the
+    workspace would be allocated where it was."""
+    refs = []
+
+    def made(*a):
+        refs.append(weakref.ref(x := Tensor(*a)))
+        return x
+
+    def alive(*a):
+        assert all(r() is not None for r in refs)
+        return Tensor((256,), U8)
+
+    for name in ("workspace", "attend_weight_workspace", "cache_evict_workspace", "attend_workspace"):
+        monkeypatch.setattr(binding, name, lambda *a, **k: alive())
+    monkeypatch.setattr(binding, "new_status", lambda d: alive() and Tensor((1,)))
+    binding.attend_weight(paged(), made((3, 8, 128), BF16), made((3, 8), F32), made((3,)), made((2,)), 2,
+                          mass=made((2, 2, 50), F32), count=made((2,)), path=made((2, 5)),
+                          out=dict(mass=made((2, 2, 50), F32)))
+    assert len(called) == 1 and len(refs) == 8
+    refs.clear()
+    binding.cache_evict(paged(), made((2, 2, 50), F32), made((2, 2, 50)), made((2,)), made((2,)), 10, count=made((2,)),
+                        out=dict(mass=made((2, 2, 50), F32), pos=made((2, 2, 50)), length=made((2,))))
+    refs.clear()
+    binding.qk_rotate(made((3, 8, 128), BF16), made((3, 2, 128), BF16), made((3,)), made((2,)), made((64,), F64),
+                      v=made((3, 2, 128), BF16), cache=paged(), start=made((2,)), row_pos=made((3,)),
+                      q_weight=made((128,), F32), k_weight=made((128,), F32), out=dict(q=made((3, 8, 128), BF16)))
+    refs.clear()
+    binding.token_logprobs(made((5, 64), BF16), made((3,)), made((2, 4)), n=made((2,)), path=made((2, 4)),
+                           out=dict(logp=made((2, 4), F32)))
+    refs.clear()
+    binding.attend(paged(), made((3, 8, 128), BF16), made((3,)), made((2,)), 2, lse=True, tree_mask=made((2, 5, 1)),
+                   out=dict(out=made((3, 8, 128), BF16), lse=made((3, 8), F32)))
+    assert len(called) == 5
