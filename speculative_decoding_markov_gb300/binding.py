@@ -833,6 +833,8 @@ def token_logprobs(target, cu_seqlens, tok, n=None, path=None, temperature=1.0, 
         raise ValueError(f"the target is on device {dev}, not on the current one")
     if not target.is_contiguous():
         raise ValueError("target must be contiguous")
+    if path is not None and path.dim() > 1 and path.shape[-1] != W:
+        raise ValueError(f"path's rows must be of {W} entries, as tok's are")
     device = target.device
     if out is None:   # positions that hold no token keep these
         out = dict(logp=torch.zeros((R, W), dtype=torch.float32, device=device),

@@ -249,3 +249,15 @@ def test_tensors_live_until_the_library_is_called(called, monkeypatch):
     binding.attend(paged(), made((3, 8, 128), BF16), made((3,)), made((2,)), 2, lse=True, tree_mask=made((2, 5, 1)),
                    out=dict(out=made((3, 8, 128), BF16), lse=made((3, 8), F32)))
     assert len(called) == 5
+
+
+@pytest.mark.parametrize("path,fits", [((2, 4), True), ((8,), True), ((2, 5), False), ((2, 9), False), ((4, 4), True),
+                                       ((1, 8), False), ((2, 4, 1), False), ((9,), True)])
+def test_logprobs_path_has_rows_as_long_as_the_tokens(called, path, fits):
+    """Rows of another length would be read as if they had the tokens'."""
+    if fits:
+        binding.token_logprobs(**logprob_args(path=Tensor(path)))
+    else:
+        with pytest.raises(ValueError):
+            binding.token_logprobs(**logprob_args(path=Tensor(path)))
+    assert len(called) == fits
