@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
     const int per = (((h.n + C - 1) / C) + 31) & ~31;
     const int s0 = static_cast<int>(min(static_cast<long long>(per) * rank, static_cast<long long>(h.n)));
     const int s1 = static_cast<int>(min(static_cast<long long>(s0) + per, static_cast<long long>(h.n)));
+    const int run = s1 - s0;   // slots are counted from s0: near the largest length a step from one would pass 32 bits
     const bool same = mass_out == mass && pos_out == pos, cut = h.n > keep;
     auto key = [&](int32_t at, float m) {
         if (at < p.sinks || at >= h.end - p.recent) return 0xffffffffu;
@@ -127,24 +128,25 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
         if (tid == 0) sh.listed = 0;
         __syncthreads();
     }
-    for (int b = s0; b < s1; b += 4 * kThreads) {
+    for (int b = 0; b < run; b += 4 * kThreads) {
         int32_t at[4];
         float m[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int s = b + j * kThreads + tid;
-            if (s < s1) {
-                at[j] = where(s);
-                m[j] = __ldcg(mass + s);
+            const int r = b + j * kThreads + tid;
+            if (r < run) {
+                at[j] = where(s0 + r);
+                m[j] = __ldcg(mass + s0 + r);
             }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int s = b + j * kThreads + tid;
-            if (s >= s1) continue;
+            const int r = b + j * kThreads + tid;
+            if (r >= run) continue;
+            const int s = s0 + r;
             if (cut) {
                 const uint32_t k = key(at[j], m[j]);
-                if (fits) keys[s - s0] = k;
+                if (fits) keys[r] = k;
                 if (!few) atomicAdd(&sh.hist[k >> 21], 1);
             }
             if (s < keep && !(same && s < h.ctx)) {   // those that stay; the others' places are overwritten below
@@ -232,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
                         if ((sh.list[s] & mask) == found) atomicAdd(&sh.hist[(sh.list[s] >> shift) & (bins - 1)], 1);
                 } else {
 #pragma unroll 4
-                    for (int s = s0 + tid; s < s1; s += kThreads) {
-                        const uint32_t k = key_of(s);
+                    for (int r = tid; r < run; r += kThreads) {
+                        const uint32_t k = key_of(s0 + r);
                         if ((k & mask) != found) continue;
                         atomicAdd(&sh.hist[(k >> shift) & (bins - 1)], 1);
                         if (d == 1) {
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
         // 2. which slots are kept: above `found`, and the first `need` of its equals.
         // A warp takes neighbouring groups of 32 slots, and a lane then one group of
         // 32 that it has looked at: few instructions a slot bound this kernel.
-        const int groups = (s1 - s0 + 31) / 32, each = (groups + kWarps - 1) / kWarps;
+        const int groups = (run + 31) / 32, each = (groups + kWarps - 1) / kWarps;
         const int w0 = min(groups, warp * each), w1 = min(groups, w0 + each);
         // lane k: which slots of group k0 + k are above and equal, and which lie in front of `keep`
         auto look = [&](int k0, unsigned& above, unsigned& equal, unsigned& valid, unsigned& lo) {
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
                 }
             }
             auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
-            const int s = s0 + (k0 + lane) * 32;
+            const int s = s0 + min(k0 + lane, w1) * 32;
             valid = lane < n ? below(s1 - s) : 0u;
             lo = below(keep - s);
         };
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
             eq += __reduce_add_sync(0xffffffffu, eq_n);
             hole += __reduce_add_sync(0xffffffffu, __popc(holes));
             mover += __reduce_add_sync(0xffffffffu, __popc(movers));
-            const int s = s0 + (k0 + lane) * 32;
+            const int s = s0 + min(k0 + lane, w1) * 32;
             // Keys that are looked up again are other ones if weights or positions
             // change meanwhile (which a call does not allow): no place is taken on trust.
             for (; holes; holes &= holes - 1, ++h_at)

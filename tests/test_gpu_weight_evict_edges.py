@@ -1,5 +1,5 @@
-"""Attention weight at its limits: infinite keys beside columns that no row
-fills."""
+"""Attention weight and eviction at their limits: infinite keys beside columns
+that no row fills, the longest caches."""
 from __future__ import annotations
 
 import numpy as np
@@ -40,3 +40,28 @@ def test_keys_of_minus_infinity_against_every_row(gpu_lib, D, group, w):
     again = dict(mass=torch.zeros_like(mass))                      # the rows gathered along a path
     sdm.attend_weight(s.cache, q, lse, s.cu, s.ctx, w, mass=mass, path=i32([list(range(w))]), out=again, dev_status=s.status)
     assert torch.equal(again["mass"], out["mass"]) and s.status.item() == 0
+
+
+def test_eviction_from_the_longest_cache(gpu_lib):
+    """2^31 - 256 tokens, the most that a call takes: 20 of 29 unseen ones go."""
+    n, page = 2 ** 31 - 256, 128
+    keep = n - 20
+    table = torch.zeros((1, 2 ** 31 // page), dtype=torch.int32, device="cuda")    # one page of zeros for all
+    cache = sdm.PagedCache.empty(1, 1, page, 64, table)
+    mass = torch.ones((1, 1, n), device="cuda")
+    unseen = list(range(5, n, n // 23))[:24] + [n - 1, n - 3, n - 19, n - 20, n - 21, n - 22]
+    mass[0, 0, unseen] = 0.0
+    pos = torch.zeros((1, 1, n), dtype=torch.int32, device="cuda")
+    out = dict(mass=mass, pos=pos, length=i32([0]), next=i32([0]))
+    status = sdm.new_status()
+    sdm.cache_evict(cache, mass, pos, i32([0]), None, keep, count=i32([n]), out=out, dev_status=status)
+    assert status.item() == 0 and out["length"].item() == keep and out["next"].item() == n
+    gone = sorted(unseen)[-(n - keep):]                            # of equals the lowest stay
+    holes, late = [s for s in gone if s < keep], [s for s in range(keep, n) if s not in gone]
+    assert pos[0, 0, holes].tolist() == late and (mass[0, 0, holes] == 1).all()
+    assert sum(int((mass[0, 0, a:min(a + 2 ** 28, keep)] == 0).sum()) for a in range(0, keep, 2 ** 28)) == 9
+    moved = 0
+    for a in range(0, keep, 2 ** 28):
+        b = min(a + 2 ** 28, keep)
+        moved += int((pos[0, 0, a:b] != torch.arange(a, b, dtype=torch.int32, device="cuda")).sum())
+    assert moved == len(holes)
