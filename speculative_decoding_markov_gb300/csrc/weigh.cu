@@ -1134,18 +1134,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             if (SMALL && !(b.flags & U_HAS)) {
                 // nothing to add: the old weights, or zeros (88 contexts of 40140, a window
                 // of 314, 16 heads: 192 us; 896 when each unit was handed out alone)
-                const size_t row = (static_cast<size_t>(b.i) * p.c.heads + b.g) * p.stride;
-                const int end = static_cast<int>(min(static_cast<long long>(b.n), static_cast<long long>(b.k0) + b.q1 * kUnit));
-                for (int key0 = b.k0 + tid; key0 < end; key0 += 8 * kUnit) {
+                // (keys are counted from k0: a step from one near the largest length would pass 32 bits)
+                const size_t at = (static_cast<size_t>(b.i) * p.c.heads + b.g) * p.stride + b.k0;
+                const int keys = min(b.n - b.k0, b.q1 * kUnit), old_keys = b.ctx - b.k0;
+                for (int key0 = tid; key0 < keys; key0 += 8 * kUnit) {
                     float x[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const int key = key0 + k * kUnit;
-                        x[k] = p.mass && key < end && key < b.ctx ? __ldcg(p.mass + row + key) : 0.f;
+                        x[k] = p.mass && key < keys && key < old_keys ? __ldcg(p.mass + at + key) : 0.f;
                     }
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (key0 + k * kUnit < end) p.mass_out[row + key0 + k * kUnit] = x[k];
+                        if (key0 + k * kUnit < keys) p.mass_out[at + key0 + k * kUnit] = x[k];
                 }
                 continue;
             }

@@ -65,3 +65,25 @@ def test_eviction_from_the_longest_cache(gpu_lib):
         b = min(a + 2 ** 28, keep)
         moved += int((pos[0, 0, a:b] != torch.arange(a, b, dtype=torch.int32, device="cuda")).sum())
     assert moved == len(holes)
+
+
+@pytest.mark.parametrize("w", [1, 200])
+def test_weights_of_the_longest_cache(gpu_lib, w):
+    """2^31 - 256 tokens, of which a window sees the last: the others' weights
+    pass through, and nothing behind them is written."""
+    n, page, window = 2 ** 31 - 256, 128, 10
+    table = torch.zeros((1, 2 ** 31 // page), dtype=torch.int32, device="cuda")    # one page of zeros for all
+    cache = sdm.PagedCache.empty(1, 1, page, 64, table)
+    mass = torch.arange(1, 2 ** 16 + 1, dtype=torch.float32, device="cuda").repeat(2 ** 15)[:2 ** 31 - 1].view(1, 1, -1)
+    out = dict(mass=torch.full_like(mass, -7.0))
+    q, lse = torch.ones((w, 1, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((w, 1), device="cuda")
+    status = sdm.new_status()
+    sdm.attend_weight(cache, q, lse, i32([0, w]), i32([n - w]), w, mass=mass, window=window, out=out, dev_status=status)
+    assert status.item() == 0
+    got, first = out["mass"][0, 0], n - w - window + 1             # a score of 0 beside an lse of 0: a weight of 1 a row
+    assert all(torch.equal(got[a:min(a + 2 ** 28, first)], mass[0, 0, a:min(a + 2 ** 28, first)])
+               for a in range(0, first, 2 ** 28))
+    t = torch.arange(first, n, device="cuda")
+    want = sum(((t <= n - w + p) & (t > n - w + p - window)).float() for p in range(w))
+    assert torch.equal(got[first:n], want + torch.where(t < n - w, mass[0, 0, first:n], 0.0))
+    assert (got[n:] == -7).all()
