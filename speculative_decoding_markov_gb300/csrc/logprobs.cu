@@ -302,10 +302,11 @@ __device__ void pick_top(const uint8_t* row, int v0, int v1, const Largest& mine
         }
         if (before == top - 1) sh.bound = x;
     }
-    if (4 * ((v1 - v0 + 31) / 32) < top) {
-        // a short row, fewer warps of which have elements than that takes: the
-        // top-th largest of all threads' (7729 rows of 1200, 32 listed: 169 us;
-        // 2293 with all elements listed and ranked)
+    const int whole = (v1 - v0) / 32;   // warps whose threads all have elements, up to kWarps; then some of the next
+    if (whole < kWarps && 4 * whole + min(4, v1 - v0 - 32 * whole) < top) {
+        // a short row, whose warps have fewer than `top` such maxima: the top-th
+        // largest of all threads' (7729 rows of 1200, 32 listed: 169 us; 2293 with
+        // all elements listed and ranked)
         uint32_t* all = reinterpret_cast<uint32_t*>(sh.one);
         all[threadIdx.x] = mine.key;
         __syncthreads();

@@ -1,11 +1,12 @@
 """Log probabilities where they went wrong once: masked tokens of rows that
-several blocks share, rows of NaN."""
+several blocks share, rows of NaN, lists of rows just too long for a rule."""
 from __future__ import annotations
 
 import pytest
 import torch
 
 from speculative_decoding_markov_gb300 import binding as sdm
+from tests.test_gpu_logprobs import test_ragged_windows as ragged_windows
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -71,3 +72,29 @@ def test_lists_of_rows_of_nan(gpu_lib, dt, bits, V):
             key = torch.where(target.isnan(), -INF, target.float())
             want = torch.sort(key, dim=1, descending=True, stable=True)[1][:, :top].cpu()
             assert torch.equal(ids, want.repeat(-(-items // n), 1)[:items].int())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,top", [(1800, 32), (1808, 32), (1816, 32), (1800, 30), (1032, 20), (1040, 20), (1048, 20)])
+def test_lists_of_rows_whose_last_warp_has_few_elements(gpu_lib, dt, V, top):
+    """As many warps have elements as the list takes, but not as many threads of
+    them: the same tokens, and not many times as long as a few elements less."""
+    ragged_windows(gpu_lib, dt, V, top, 1.0)
+
+    def time(V):
+        gen = torch.Generator().manual_seed(V)
+        z = torch.randn((4000, V), generator=gen).to(dt).cuda()
+        args = z, i32([0, 4000]), i32([[3] * 4000])
+        out, st = sdm.token_logprobs(*args, top=top), sdm.new_status()
+        best = INF
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            sdm.token_logprobs(*args, top=top, out=out, dev_status=st)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    # a list of every element, ranked by all pairs, takes 13 times as long
+    assert time(V) < 4 * time(V // 256 * 256)
