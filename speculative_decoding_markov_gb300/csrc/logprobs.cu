@@ -459,7 +459,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
     };
     const int said_in = tok >> 3;        // the vector that holds the token
     for (int st = 0; st < stages; ++st) {
-        if (!mbar_wait(&sh.full[st % kStages], (st / kStages) & 1)) {
+        // one answer a warp: a lane that gave up by itself would leave the loop, and the others
+        // would wait for it
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[st % kStages], (st / kStages) & 1))) {
             sh.late = 1;
             break;
         }
