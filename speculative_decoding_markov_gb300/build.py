@@ -18,7 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsdm.so")
 SOURCES = ("markov_gemm.cu", "chain_pruned.cu", "stream.cu", "select.cu", "small.cu", "api.cu", "no_alloc.cu", "observe.cu", "threshold.cu", "rnn.cu", "tree_pruned.cu", "cache.cu", "attend.cu", "cache_api.cu",
            "rotate.cu", "logprobs.cu", "weigh.cu", "evict.cu")
-HEADERS = ("device.cuh", "internal.h", "verify_greedy.cuh", "tree_common.cuh", "schedule_pack.cuh", "paged.cuh")
+HEADERS = ("device.cuh", "internal.h", "verify_greedy.cuh", "tree_common.cuh", "schedule_pack.cuh", "paged.cuh",
+           "per_device.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1719,13 +1719,9 @@ bool encode(CUtensorMap* map, const CacheView& c, void* pool) {
 template <int D, bool E4M3, bool SMALL>
 cudaError_t launch_one(const AttendParams& p, void* work, cudaStream_t s) {
     using C = Cfg<D, E4M3, SMALL>;
-    static bool configured = false;
-    if (!configured) {
-        const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, E4M3, SMALL>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(attend_kernel<D, E4M3, SMALL>, C::kTotal);
+    if (raised != cudaSuccess) return raised;
     CUtensorMap tmK, tmV;
     if (!encode(&tmK, p.c, p.c.k) || !encode(&tmV, p.c, p.c.v)) return cudaErrorInvalidValue;
     CUtensorMap tmQ = tmK;

@@ -308,8 +308,8 @@ cudaError_t launch_cache_commit(const CacheCommitParams& p, cudaStream_t s) {
     // the limit is the process's, so it is raised once, to what the largest call needs
     constexpr int kMost = (2 * kCommitMost + kCommitMost + 1) * sizeof(int32_t);
     static_assert(kMost <= 224 * 1024, "shared memory");
-    static const cudaError_t raised =
-        cudaFuncSetAttribute(cache_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(cache_commit_kernel, kMost);
     if (raised != cudaSuccess) return raised;
     const size_t smem = (2 * static_cast<size_t>(p.N + 1) + p.B + 1) * sizeof(int32_t);
     return launch_pdl(cache_commit_kernel, dim3(p.R), dim3(kCommitThreads), smem, s, p);

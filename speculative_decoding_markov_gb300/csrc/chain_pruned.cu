@@ -926,19 +926,13 @@ cudaError_t launch_chain_pruned(const PrunedParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_chain_pick(const PrunedParams& p, cudaStream_t s) {
-    cudaError_t e = cudaSuccess;
     const PickLayout lay = pick_layout(p.B, p.n_chunks, p.r);
     if (lay.cap < 1) return cudaErrorInvalidValue;
-    static bool configured = false;
-    if (!configured) {
-        e = cudaFuncSetAttribute(chain_pick_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPickSmem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(chain_pick_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPickSmem);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
-    return p.l_fp32 ? launch_pdl(chain_pick_kernel<1>, dim3(p.R), dim3(kThreads), lay.total, s, p)
-                    : launch_pdl(chain_pick_kernel<0>, dim3(p.R), dim3(kThreads), lay.total, s, p);
+    static SmemLimit limits[2];
+    const auto kernel = p.l_fp32 ? chain_pick_kernel<1> : chain_pick_kernel<0>;
+    const cudaError_t raised = limits[p.l_fp32 ? 1 : 0].raise(kernel, kPickSmem);
+    if (raised != cudaSuccess) return raised;
+    return launch_pdl(kernel, dim3(p.R), dim3(kThreads), lay.total, s, p);
 }
 
 cudaError_t launch_markov_prepare(const uint16_t* U, const uint16_t* W, int V, int r, uint16_t* Wt, float* u_norm,

@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_kernel(const 
 
 template <int THREADS>
 cudaError_t launch_one(const EvictParams& p, int C, cudaStream_t s) {
-    static const cudaError_t raised =
-        cudaFuncSetAttribute(evict_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4);
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(evict_kernel<THREADS>, kMost * 4);
     if (raised != cudaSuccess) return raised;
     EvictParams q = p;
     const long long per = ((p.stride + C - 1) / C + 31) / 32 * 32;

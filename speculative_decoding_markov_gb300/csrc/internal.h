@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/sdm.h"
+#include "per_device.h"
 
 namespace sdm {
 

@@ -661,14 +661,11 @@ cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
     int C = 1;
     while (C < kMaxCluster && items * C * 2 <= 8LL * num_sms() && p.V / (2 * C) >= 4096) C *= 2;
     constexpr int kRing = kStages * kStageBytes;
-    static const cudaError_t raised = [] {
-        const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
-        return e != cudaSuccess ? e : cudaFuncSetAttribute(logprobs_kernel<false>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
-    }();
+    static SmemLimit limits[2];
+    const auto kernel = p.fp32 ? logprobs_kernel<true> : logprobs_kernel<false>;
+    const cudaError_t raised = limits[p.fp32 ? 1 : 0].raise(kernel, kRing);
     if (raised != cudaSuccess) return raised;
-    return launch_cluster(p.fp32 ? logprobs_kernel<true> : logprobs_kernel<false>, dim3(static_cast<unsigned>(items * C)),
-                          dim3(kThreads), C, kRing, s, p);
+    return launch_cluster(kernel, dim3(static_cast<unsigned>(items * C)), dim3(kThreads), C, kRing, s, p);
 }
 
 }  // namespace sdm

@@ -1156,13 +1156,9 @@ cudaError_t launch_mode(const CUtensorMap& tmW, const CUtensorMap& tmL, const Ge
     const SmemLayout lay = make_layout(p.r, p.l_rows, p.l_fp32, p.w_stages, p.l_stages, MODE, MS);
     // every sub-tile's A needs a W slot of its own, and the ring at least two
     if (lay.total > static_cast<uint32_t>(kSmemLimit) || p.w_stages < 2 * (p.r >> 6)) return cudaErrorInvalidValue;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(markov_gemm_kernel<MODE, MS, LF>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(markov_gemm_kernel<MODE, MS, LF>, kSmemLimit);
+    if (raised != cudaSuccess) return raised;
     return launch_pdl(markov_gemm_kernel<MODE, MS, LF>, dim3(gx, gy), dim3(kGemmThreads), lay.total, s, tmW, tmL, p);
 }
 

@@ -740,36 +740,32 @@ size_t stage_bytes(int stride) {
 }
 
 template <typename K>
-cudaError_t allow_smem(K kernel, bool& done) {
-    if (done) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(stage_bytes(kStageMaxRecords)));
-    done = e == cudaSuccess;
-    return e;
+cudaError_t allow_smem(K kernel, SmemLimit& limit) {
+    return limit.raise(kernel, static_cast<int>(stage_bytes(kStageMaxRecords)));
 }
 
 }  // namespace
 
 cudaError_t launch_draft_select(const DraftSelectParams& p, cudaStream_t s) {
     if (p.R <= 0) return cudaSuccess;
-    static bool configured = false;
-    cudaError_t e = allow_smem(draft_select_kernel, configured);
+    static SmemLimit limit;
+    cudaError_t e = allow_smem(draft_select_kernel, limit);
     if (e != cudaSuccess) return e;
     return launch_pdl(draft_select_kernel, dim3(p.R), dim3(kSelThreads), stage_bytes(p.nb), s, p);
 }
 
 cudaError_t launch_tree_select(const TreeSelectParams& p, cudaStream_t s) {
     if (p.rows <= 0) return cudaSuccess;
-    static bool configured = false;
-    cudaError_t e = allow_smem(tree_select_kernel, configured);
+    static SmemLimit limit;
+    cudaError_t e = allow_smem(tree_select_kernel, limit);
     if (e != cudaSuccess) return e;
     return launch_pdl(tree_select_kernel, dim3(p.rows), dim3(kSelThreads), stage_bytes(p.nb), s, p);
 }
 
 cudaError_t launch_resample(const ResampleParams& p, cudaStream_t s) {
     if (p.R <= 0) return cudaSuccess;
-    static bool configured = false;
-    cudaError_t e = allow_smem(resample_kernel, configured);
+    static SmemLimit limit;
+    cudaError_t e = allow_smem(resample_kernel, limit);
     if (e != cudaSuccess) return e;
     // the residual records, or the bonus draw's chunk of a target row (32 KB)
     const size_t smem = std::max(stage_bytes(p.nb), static_cast<size_t>(p.chunk) * (p.t_fp32 ? 4 : 2));

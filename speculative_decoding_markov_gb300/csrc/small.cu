@@ -563,12 +563,9 @@ cudaError_t launch_schedule(const float* conf, int R, int gamma, const double* c
     int n_pad = 1;
     while (n_pad < R * gamma) n_pad <<= 1;
     const size_t smem = schedule_smem_bytes(R, gamma, n_pad, kSchedThreads);
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(schedule_kernel, 200 * 1024);
+    if (raised != cudaSuccess) return raised;
     const int nt = n_pad < 64 ? 64 : (n_pad > kSchedThreads ? kSchedThreads : n_pad);
     return launch_pdl(schedule_kernel, dim3(1), dim3(nt), smem, s, conf, R, gamma, cost, survival, budget,
                       expected, total_tokens, n_pad);
@@ -581,13 +578,9 @@ cudaError_t launch_schedule_dynamic(const float* conf, const float* conf_stale, 
     while (n_pad < R * gamma) n_pad <<= 1;
     const size_t smem = static_cast<size_t>(n_pad) * 8 + kSchedThreads * 8 + static_cast<size_t>(R) * 4 +
                         static_cast<size_t>(R) * gamma * 4;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e =
-            cudaFuncSetAttribute(schedule_dynamic_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(schedule_dynamic_kernel, 200 * 1024);
+    if (raised != cudaSuccess) return raised;
     const int nt = n_pad < 64 ? 64 : (n_pad > kSchedThreads ? kSchedThreads : n_pad);
     return launch_pdl(schedule_dynamic_kernel, dim3(1), dim3(nt), smem, s, conf, conf_stale, R, gamma, cost, survival,
                       budget, expected, total_tokens, capacity, n_pad);
@@ -646,13 +639,9 @@ cudaError_t launch_tree_finalize(int R, int P, int B, int N, const int32_t* pool
                                  int32_t* n_nodes, cudaStream_t s) {
     const int pool_cap = 1 + P * B;
     const size_t smem = static_cast<size_t>(pool_cap) * 16 + static_cast<size_t>(N + 1) * 4;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(tree_finalize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             200 * 1024);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(tree_finalize_kernel, 200 * 1024);
+    if (raised != cudaSuccess) return raised;
     return launch_pdl(tree_finalize_kernel, dim3(R), dim3(256), smem, s, R, P, B, N, pool_tok, pool_parent, pool_depth,
                       pool_score, pool_n, tok, parent, depth, score, mask, n_nodes);
 }
@@ -661,26 +650,13 @@ cudaError_t launch_tree_verify_walk(const unsigned long long* row_keys, int n_ch
                                     const int32_t* n_nodes, int R, int N, int B, int V, int32_t* accept,
                                     int32_t* out_tok, int32_t* n_out, int32_t* dev_status, cudaStream_t s) {
     const size_t smem = static_cast<size_t>(N + 1) * 12;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(tree_verify_walk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             200 * 1024);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(tree_verify_walk_kernel, 200 * 1024);
+    if (raised != cudaSuccess) return raised;
     return launch_pdl(tree_verify_walk_kernel, dim3(R), dim3(32), smem, s, row_keys, n_chunks, tok, parent, n_nodes, R,
                       N, B, V, accept, out_tok, n_out, dev_status);
 }
 
-int num_sms() {
-    static int n = 0;
-    if (n == 0) {
-        int dev = 0;
-        cudaGetDevice(&dev);
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (n <= 0) n = 148;
-    }
-    return n;
-}
+int num_sms() { return sms_of_device(); }
 
 }  // namespace sdm

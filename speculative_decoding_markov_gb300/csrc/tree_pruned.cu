@@ -513,13 +513,9 @@ cudaError_t launch_tree_rows(const TreeRowsParams& p, cudaStream_t s) {
 cudaError_t launch_tree_level(const TreeLevelParams& p, cudaStream_t s) {
     if (p.P > kMaxTreeSlots || p.k > kMaxTopK || p.n_part > 32 * kMaxPartLane) return cudaErrorInvalidValue;
     const size_t smem = tree_level_smem(p.P, p.r);
-    static size_t configured = 0;   // the dynamic shared memory allowed so far
-    if (smem > configured) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(tree_level_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        configured = smem;
-    }
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(tree_level_kernel, static_cast<int>(smem));
+    if (raised != cudaSuccess) return raised;
     return launch_pdl(tree_level_kernel, dim3(p.R), dim3(kLvThreads), smem, s, p);
 }
 

@@ -1441,8 +1441,8 @@ cudaError_t launch_one(const WeighParams& p, void* work, cudaStream_t s) {
     using C = Cfg<D, E4M3, SMALL>;
     constexpr int kTotal = C::kBars + static_cast<int>(sizeof(Bars<C::kKSlots, C::kQSlots, C::kLStages, C::kRing, C::kS>));
     static_assert(kTotal <= 232448, "shared memory");
-    static const cudaError_t raised = cudaFuncSetAttribute(weigh_kernel<D, E4M3, SMALL>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kTotal);
+    static SmemLimit limit;
+    const cudaError_t raised = limit.raise(weigh_kernel<D, E4M3, SMALL>, kTotal);
     if (raised != cudaSuccess) return raised;
     CUtensorMap tmK;
     if (!encode_k(&tmK, p.c)) return cudaErrorInvalidValue;
