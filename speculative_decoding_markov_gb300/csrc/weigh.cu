@@ -61,6 +61,7 @@ namespace {
 constexpr int kTile = 128;            // keys of a tile, query rows of a tile
 constexpr int kUnit = 2 * kTile;      // keys of a unit
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMostL = 3.4028235e38f;   // of -lse log2 e, where an lse is near the type's lowest value
 constexpr int kTmemCols = 512;        // S buffers of 128 columns from 0; the tiles of keys (unless SMALL) at kTmemK
 constexpr int kTmemK = 384;
 constexpr int kHeavy = 6, kBase = 2;  // costs: a unit with a product if SMALL (1 without); a unit beside its row tiles
@@ -918,7 +919,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
             for (int k = 0; k < 4; ++k) {
                 const int col = k * 32 + lane;
                 const bool adds = z[k] > -INFINITY;             // a NaN does not
-                to[col] = adds ? -z[k] * kLog2e : -INFINITY;
+                to[col] = adds ? fminf(-z[k] * kLog2e, kMostL) : -INFINITY;   // finite: see hide()
                 const uint32_t bits = __ballot_sync(0xffffffffu, adds || (full && col >= p.sub));
                 if (lane == 0) live[k] = bits;
                 all &= bits;

@@ -87,3 +87,21 @@ def test_weights_of_the_longest_cache(gpu_lib, w):
     want = sum(((t <= n - w + p) & (t > n - w + p - window)).float() for p in range(w))
     assert torch.equal(got[first:n], want + torch.where(t < n - w, mass[0, 0, first:n], 0.0))
     assert (got[n:] == -7).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("w,window", [(3, 0), (3, 40), (200, 0), (200, 40)])
+def test_rows_of_the_lowest_lse(gpu_lib, e4m3, w, window):
+    """A row whose lse is the type's lowest value gives what it sees infinite
+    weights, and nothing to what it does not see."""
+    s = ref.Setup([w], [300], 1, 64, 16, e4m3, seed=w)
+    s.write_all()
+    q = torch.randn((w, 2, 64), generator=s.gen).to(torch.bfloat16).cuda()
+    lse = (2 + torch.rand((w, 2), generator=s.gen)).cuda()
+    lse[1], lse[2, 1] = torch.finfo(torch.float32).min, -3e38
+    out = dict(mass=torch.zeros((1, 1, 300 + w), device="cuda"))
+    sdm.attend_weight(s.cache, q, lse, s.cu, s.ctx, w, window=window, sinks=2, out=out, dev_status=s.status)
+    want, tol = weights(q, lse, s.held(0, "k"), ref.visible(w, 300, window, 2), 0.125, 2)
+    got, fine = out["mass"][0].double().cpu().numpy(), np.isfinite(want)
+    assert s.status.item() == 0 and not fine.all() and (w == 3 or fine.sum() > 150)
+    assert np.isposinf(got[~fine]).all() and (np.abs(got - want)[fine] <= tol[fine]).all()
