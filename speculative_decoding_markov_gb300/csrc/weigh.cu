@@ -501,8 +501,9 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
 }
 
 // Adds the weights of N columns: 2^(c f x + l), f the columns' scales (planes),
-// l their -lse log2 e.
-template <bool PLANES, int N>
+// l their -lse log2 e.  A scale of at most 1 comes before c, so that nothing on
+// the way is larger than the score; BIG: one above 1 after it.
+template <bool PLANES, bool BIG, int N>
 __device__ __forceinline__ void add_weights(const uint32_t (&x)[N], float c, const float4* l4, const float4* f4,
                                             float2 (&acc)[4]) {
     const float2 cc = make_float2(c, c);
@@ -513,8 +514,15 @@ __device__ __forceinline__ void add_weights(const uint32_t (&x)[N], float c, con
         float2 b = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
         if constexpr (PLANES) {
             const float4 f = f4[k];
-            a = fma2(mul2(a, cc), make_float2(f.x, f.y), make_float2(l.x, l.y));
-            b = fma2(mul2(b, cc), make_float2(f.z, f.w), make_float2(l.z, l.w));
+            if constexpr (BIG) {
+                a = mul2(mul2(a, make_float2(fminf(f.x, 1.f), fminf(f.y, 1.f))), cc);
+                b = mul2(mul2(b, make_float2(fminf(f.z, 1.f), fminf(f.w, 1.f))), cc);
+                a = fma2(a, make_float2(fmaxf(f.x, 1.f), fmaxf(f.y, 1.f)), make_float2(l.x, l.y));
+                b = fma2(b, make_float2(fmaxf(f.z, 1.f), fmaxf(f.w, 1.f)), make_float2(l.z, l.w));
+            } else {
+                a = fma2(mul2(a, make_float2(f.x, f.y)), cc, make_float2(l.x, l.y));
+                b = fma2(mul2(b, make_float2(f.z, f.w)), cc, make_float2(l.z, l.w));
+            }
         } else {
             a = fma2(a, cc, make_float2(l.x, l.y));
             b = fma2(b, cc, make_float2(l.z, l.w));
@@ -533,6 +541,24 @@ __device__ __forceinline__ void hide(uint32_t (&x)[N], int lo, int hi, uint32_t 
     live &= (from >= 32 ? 0u : ~0u << from) & (hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u);
 #pragma unroll
     for (int k = 0; k < N; ++k) x[k] = (live >> k) & 1u ? x[k] : 0xff800000u;
+}
+
+// The same of a tile's `cols` columns, from tensor memory, some of whose scales
+// are above 1.  Not inline: the registers that it takes would cost the others'
+// form a fifth of its time (two contexts of 150001 to 199999: 63.7 us, 51.2 so).
+__device__ __noinline__ float add_big(uint32_t s_at, int cols, int lo, int hi, const uint32_t* live, float c,
+                                      const float4* l4, const float4* f4) {
+    float2 acc[4] = {};
+    uint32_t x[16];
+#pragma unroll 1
+    for (int at = 0; at < cols; at += 16) {
+        tmem_ld16(s_at + at, x);
+        tmem_ld_wait();
+        hide(x, lo - at, hi - at, live[at / 32] >> (at & 31));
+        add_weights<true, true>(x, c, l4 + at / 4, f4 + at / 4, acc);
+    }
+    const float2 two = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+    return two.x + two.y;
 }
 
 // ---------------------------------------------------------------------------
@@ -990,8 +1016,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         if (u < 0x7f800000u) top = max(top, u);
                     }
                     top = __reduce_max_sync(0xffffffffu, top) >> 23;
-                    // 2^(141 - top) puts the largest into [2^14, 2^15); the factor stays normal
-                    const int shift = min(max(141 - static_cast<int>(top), -100), 100);
+                    // 2^(141 - top) puts the largest into [2^14, 2^15); it and its inverse
+                    // stay normal (-113 at least, and 126)
+                    const int shift = min(141 - static_cast<int>(top), 126);
                     const float mul = pow2f(shift);
                     uint32_t code[3] = {0, 0, 0};
 #pragma unroll
@@ -1130,6 +1157,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
         Ring<kExpStages> xr;
         bool any_q = false;
         const float c0 = p.scale * kLog2e;
+        bool big = false;                 // planes: a row's scale is above 1 (its elements from 2^15 on)
         Blk b;
         while (take(ok, b)) {
             if (SMALL && !(b.flags & U_HAS)) {
@@ -1168,6 +1196,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                     any_q = true;
                     ok = wait_or_fail(p, &bar.q_full[qr.at], qr.full());   // its -lse
                     if (!ok) break;
+                    if constexpr (kPlanes) {
+                        big = false;
+                        for (int m = lane; m < b.M; m += 32) big = big || cf[qr.at * kTile + m] > 1.f;
+                        big = __any_sync(0xffffffffu, big);
+                    }
                 }
                 float c = c0;
                 if constexpr (kPlanes) {
@@ -1281,14 +1314,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                             // of 28 heads on 4)
                             const float end = __uint_as_float(x[sizeof(x) / 4 - 1]);
                             if (some || (at >= 64 && end != end)) hide(x, lo - at, hi - at, live[at / 32]);
-                            add_weights<kPlanes>(x, c, lp + at / 4, fp + at / 4, acc);
+                            add_weights<kPlanes, false>(x, c, lp + at / 4, fp + at / 4, acc);
                         };
                         if constexpr (SMALL) {
                             // few rows, or 32 columns loaded while the 32 before them
                             // are summed (two contexts of 150001 to 199999 with 7 rows
                             // a head: 48.3 us, 51.7 with 32 columns)
                             const int N = (cols + 31) & ~31;
-                            if (cols <= 16) {
+                            if (kPlanes && big) {
+                                acc[0].x = add_big(s_at, cols, lo, hi, live, c, lp, fp);
+                            } else if (cols <= 16) {
                                 uint32_t x[16];
                                 tmem_ld16(s_at, x);
                                 tmem_ld_wait();

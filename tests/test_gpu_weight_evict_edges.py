@@ -105,3 +105,51 @@ def test_rows_of_the_lowest_lse(gpu_lib, e4m3, w, window):
     got, fine = out["mass"][0].double().cpu().numpy(), np.isfinite(want)
     assert s.status.item() == 0 and not fine.all() and (w == 3 or fine.sum() > 150)
     assert np.isposinf(got[~fine]).all() and (np.abs(got - want)[fine] <= tol[fine]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power", [-115, -60, 100, 113, 116, 118, 124])
+@pytest.mark.parametrize("w", [1, 5, 60])
+def test_queries_of_any_size_over_an_e4m3_cache(gpu_lib, D, power, w):
+    """Queries near the type's ends beside keys of the other end: scores of
+    ordinary size."""
+    s = ref.Setup([w], [300], 1, D, 16, True, seed=w)
+    s.kv[0]["k"] *= 2.0 ** (-112 if power > 0 else 40)
+    s.write_all()
+    q = (torch.randn((w, 4, D), generator=s.gen) * 2.0 ** power).to(torch.bfloat16).cuda()
+    lse = (2 + torch.rand((w, 4), generator=s.gen)).cuda()
+    scale = 2.0 ** ((112 if power > 0 else -40) - power - 3)
+    out = dict(mass=torch.zeros((1, 1, 300 + w), device="cuda"))
+    sdm.attend_weight(s.cache, q, lse, s.cu, s.ctx, w, scale=scale, out=out, dev_status=s.status)
+    want, tol = weights(q, lse, s.held(0, "k"), ref.visible(w, 300), scale, 4)
+    assert s.status.item() == 0 and np.isfinite(want).all() and want.std() > 0.02
+    assert (np.abs(out["mass"][0].double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group,w", [(7, 18), (7, 11), (1, 3), (16, 8)])
+def test_huge_and_small_queries_of_one_tile(gpu_lib, D, group, w):
+    """Rows of all sizes side by side, a window, rows that add nothing."""
+    s = ref.Setup([w, 1, w], [300, 40, 700], 2, D, 32, True, seed=group)
+    for kv in s.kv:
+        kv["k"] *= 2.0 ** -100
+    s.write_all()
+    rows, H = s.rows, 2 * group
+    size = 2.0 ** torch.randint(60, 120, (rows, H, 1), generator=s.gen).double()
+    size[rows // 2:] = 2.0 ** 96                                   # the last request has no huge row
+    q = (torch.randn((rows, H, D), generator=s.gen).double() * size).to(torch.bfloat16).cuda()
+    scale = 2.0
+    top = (q.double().abs().amax(-1) * 2.0 ** -98 * D ** 0.5).cpu()  # some way above a row's scores
+    lse = (top * scale).clamp(min=1.0).float().cuda()
+    lse[1, 0], lse[rows - 1] = -INF, INF
+    for window, sinks in ((0, 0), (50, 3)):
+        out = dict(mass=torch.zeros((3, 2, 700 + w), device="cuda"))
+        sdm.attend_weight(s.cache, q, lse, s.cu, s.ctx, w, scale=scale, window=window, sinks=sinks, out=out,
+                          dev_status=s.status)
+        assert s.status.item() == 0
+        cu = s.cu.tolist()
+        for i in range(3):
+            a, b, n = cu[i], cu[i + 1], s.ctx_list[i] + cu[i + 1] - cu[i]
+            want, tol = weights(q[a:b], lse[a:b], s.held(i, "k"), ref.visible(b - a, s.ctx_list[i], window, sinks), scale, group)
+            got = out["mass"][i, :, :n].double().cpu().numpy()
+            assert np.isfinite(want).all() and (np.abs(got - want) <= tol).all(), (window, i)
