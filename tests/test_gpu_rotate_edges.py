@@ -72,3 +72,24 @@ def test_in_place_into_a_cache_beside_unsound_windows(gpu_lib, e4m3, H):
         p, r = getattr(a.cache, n), getattr(b.cache, n)
         if p is not None:
             assert torch.equal(p.view(torch.uint8), r.view(torch.uint8)), n
+
+
+@pytest.mark.parametrize("first", [0, 100000, 2 ** 24, -3000])
+@pytest.mark.parametrize("inter", [False, True])
+def test_the_angle_keeps_what_32_bits_of_turns_lose(gpu_lib, first, inter):
+    """The turned unit vectors' sines and cosines below 1/4: the 32-bit functions'
+    last bit and a product's rounding are 2.3e-8 of them, so that whoever is 3e-8
+    from a border of bf16's rounding is on its side.  (An angle cut to 24 bits of
+    turns is off by up to 9e-8.)"""
+    n, D = 16384, 128
+    q = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    q[..., (slice(0, D, 2) if inter else slice(0, D // 2))] = 1.0
+    freq = freqs(D).cuda()
+    got = sdm.qk_rotate(q, q.clone(), i32([0, n]), None, freq, start=i32([first]), interleaved=inter)["q"][:, 0]
+    t = (first + torch.arange(n, device="cuda", dtype=torch.float64))[:, None] * freq
+    parts = [(torch.cos(t), got[:, 0::2] if inter else got[:, :D // 2]), (torch.sin(t), got[:, 1::2] if inter else got[:, D // 2:])]
+    for y, x in parts:
+        step = 2.0 ** (torch.floor(torch.log2(y.abs().clamp(min=1e-30))) - 7)
+        off = ((y.abs() / step) % 1.0 - 0.5).abs() * step
+        sure = (off > 3e-8) & (y.abs() < 0.25)
+        assert sure.sum() > 10000 and torch.equal(x[sure], y.to(torch.bfloat16)[sure])
