@@ -1370,7 +1370,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3, SMALL>::kThreads, 1)
                         const float2 half = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
                         const float one = half.x + half.y - lost;
                         const float to = sum + one;
-                        lost = (to - sum) - one;
+                        lost = to < INFINITY ? (to - sum) - one : 0.f;   // infinity loses nothing
                         sum = to;
                     }
                     if (!SMALL) {

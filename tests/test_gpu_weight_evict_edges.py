@@ -153,3 +153,19 @@ def test_huge_and_small_queries_of_one_tile(gpu_lib, D, group, w):
             want, tol = weights(q[a:b], lse[a:b], s.held(i, "k"), ref.visible(b - a, s.ctx_list[i], window, sinks), scale, group)
             got = out["mass"][i, :, :n].double().cpu().numpy()
             assert np.isfinite(want).all() and (np.abs(got - want) <= tol).all(), (window, i)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_infinite_weights_of_long_windows(gpu_lib, e4m3):
+    """An infinite weight among the sums of many tiles of rows stays infinite."""
+    s = ref.Setup([1000], [3000], 2, 64, 64, e4m3, seed=21)
+    s.write_all()
+    q = torch.randn((1000, 16, 64), generator=s.gen).to(torch.bfloat16).cuda()
+    lse = (5 + torch.rand((1000, 16), generator=s.gen)).cuda()
+    lse[3, 2], lse[400, 9] = torch.finfo(torch.float32).min, -1e30
+    out = dict(mass=torch.zeros((1, 2, 4000), device="cuda"))
+    sdm.attend_weight(s.cache, q, lse, s.cu, s.ctx, 1000, out=out, dev_status=s.status)
+    want, tol = weights(q, lse, s.held(0, "k"), ref.visible(1000, 3000), 0.125, 8)
+    got, fine = out["mass"][0].double().cpu().numpy(), np.isfinite(want)
+    assert s.status.item() == 0 and (~fine).sum() == 3004 + 3401
+    assert np.isposinf(got[~fine]).all() and (np.abs(got - want)[fine] <= tol[fine]).all()
