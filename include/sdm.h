@@ -22,7 +22,8 @@
  *   - Every pointer argument is a DEVICE pointer unless the comment says
  *     "host".  The caller owns every buffer; the library never allocates.
  *     Scratch memory is the caller's `ws` buffer of at least
- *     sdm_workspace_size(op, ...) bytes (256-byte aligned).
+ *     sdm_workspace_size(op, ...) bytes (256-byte aligned); calls, or graphs,
+ *     that may run at the same time need one each.
  *   - Work is enqueued asynchronously on `stream` (a cudaStream_t passed as
  *     void*; NULL is the legacy default stream).  The return value reports
  *     host-side validation and launch errors only.
@@ -730,7 +731,9 @@ sdm_status sdm_attend(const sdm_cache* cache, const uint16_t* q, int64_t q_strid
  * Out: q_out, and k_out without a cache (NULL with one): rows with strides of
  *      their own; each may be its input.  Rows that no window holds are left
  *      as they were; one that several hold (offsets that are not monotone) is
- *      rotated for one of them.  fp32 throughout, rounded to bf16 once.
+ *      rotated for one of them.  fp32 throughout, rounded to bf16 once (so a
+ *      vector whose sum of squares passes fp32, with elements beyond 10^18,
+ *      is normalised to zeros).
  * Device checks as in sdm_cache_write; a row whose page is bad still has its
  * query rotated, one past the page table is left out.
  */
@@ -791,7 +794,7 @@ sdm_status sdm_token_logprobs(const void* target, sdm_dtype dtT, int row_capacit
  *      kv_heads.
  * Out: mass_out, the same shape; may be mass.
  * Scores and sums are fp32, in an order that depends on the sizes alone.  A
- * row whose lse is -inf or NaN adds nothing; infinite or NaN scores beside an
+ * row whose lse is -inf or NaN adds nothing; a score of +inf or NaN beside an
  * lse of +inf, and infinities in q over an e4m3 cache, count as NaN.
  * ws:  sdm_workspace_size(SDM_OP_ATTEND_WEIGHT, R, max_count, H, head_dim, rows,
  *      kv_heads, 0) bytes.
@@ -816,10 +819,15 @@ sdm_status sdm_attend_weight(const sdm_cache* cache, const uint16_t* q, int64_t 
  * position) to the j-th slot that becomes free there.  A request with n <= keep
  * keeps all.  Keys carry their rotation, so a cache in another order attends
  * alike; sdm_attend's `window` and `sinks` go by slots, so use neither then.
- * In:  cache (its pools are written); mass, pos [R, kv_heads, stride] (pos is
- *      not read from ctx_len on), stride < 2^31; ctx_len [R]; count [R] or NULL (0); start [R]
- *      or NULL (ctx_len: nothing was evicted yet); 0 <= sinks, recent, sinks +
- *      recent <= keep, keep >= 1; R * kv_heads <= 2^24.
+ * In:  cache (its pools are written, in any page that holds one of a request's
+ *      n tokens: no other request may use that page, so a common prompt's are
+ *      copied first); mass, pos [R, kv_heads, stride] (pos is not read from
+ *      ctx_len on), stride < 2^31 (the blocks' number and shared memory follow
+ *      it: 64 full caches of 2048 and 8 heads take 13 us with a stride of 2300,
+ *      30 with 30000, 150 with 100000);
+ *      ctx_len [R]; count [R] or NULL (0); start [R] or NULL (ctx_len: nothing
+ *      was evicted yet); 0 <= sinks, recent, sinks + recent <= keep, keep >= 1;
+ *      R * kv_heads <= 2^24.
  * Out: mass_out, pos_out [R, kv_heads, stride], filled below length[i], entries
  *      from there on left as they were; may be mass and pos.  length [R] =
  *      min(n, keep), the next ctx_len; next [R] (may be NULL) = start + count,

@@ -915,8 +915,9 @@ def cache_evict(cache, mass, pos, ctx_len, start, keep, count=None, sinks=0, rec
     `sinks`, the last `recent`, then the largest mass [R, kv heads, tokens]; pos
     int32 of the same shape holds the positions of slots below ctx_len, the
     count[i] new ones are at start[i], start[i] + 1, ....  out["mass"] and
-    out["pos"] may be the inputs; out["length"] is the next ctx_len, out["next"]
-    (if there) the next start."""
+    out["pos"] may be the inputs, and without `out` are: both are written over,
+    as the cache's pools are.  out["length"] is the next ctx_len, out["next"] (if
+    there) the next start."""
     R, G, dev = cache.requests, cache.kv_heads, cache.device
     shape = mass.shape
     if len(shape) != 3 or shape[0] != R or shape[1] != G:

@@ -15,9 +15,9 @@
 // Only what has to move is moved: of a cache that runs full by 8 tokens a
 // cycle, 8 rows, not the 2048 that kept their place.
 //
-// What bounds it: 64 such caches of 8 heads x 128 (11.4 us) a chain of look-ups
+// What bounds it: 64 such caches of 8 heads x 128 (11.9 us) a chain of look-ups
 // and barriers; five prompts of up to 30000 tokens cut to 4096 (28 heads on 4,
-// e4m3, 31 to 34 us) the barriers of clusters of 8 and the moves' scattered rows.
+// e4m3, 35 us) the barriers of clusters of 8 and the moves' scattered rows.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -13,9 +13,9 @@
 // threads whose largest reaches it look at their elements again.
 //
 // What bounds it: 1000 rows of 129280 in fp32 HBM, 5.7 TB/s (90 us); 64 requests
-// of 1 to 8 tokens of 151936 in bf16 (290 rows) 28.5 us, of which the list of 20
+// of 1 to 8 tokens of 151936 in bf16 (290 rows) 29 us, of which the list of 20
 // tokens a row is 4 us, the issue of some 9 instructions an element 10 us, and
-// the rest the ends of rows that are too few to cover one another; one row 9.0
+// the rest the ends of rows that are too few to cover one another; one row 9.6
 // us in a graph, a chain of look-ups, sums and the list.
 #include <cooperative_groups.h>
 

@@ -37,12 +37,12 @@
 // shared memory a 128 x 128 x 128 product takes its whole bandwidth.
 //
 // What bounds it (32 query heads on 8 kv heads of 128, bf16, unless said):
-//   64 windows of 1 to 8 tokens over 300 to 8000: HBM, 5.7 TB/s of keys (55 us).
-//   A prompt of 8192 tokens: 222 us, 1.24 PFLOP/s.  Tensor pipe 52 %, the
+//   64 windows of 1 to 8 tokens over 300 to 8000: HBM, 5.5 TB/s of keys (56 us).
+//   A prompt of 8192 tokens: 224 us, 1.23 PFLOP/s.  Tensor pipe 52 %, the
 //   exponentials' unit 53 %, issue 56 %: the products by themselves take 164 us
 //   (without the weights) and the exponentials 122 us.  Tensor memory has three
 //   buffers of scores for four groups of warps.
-//   Two rows over 150001 to 199999, e4m3 (28 heads on 4): 49 us, 3.7 TB/s.  A
+//   Two rows over 150001 to 199999, e4m3 (28 heads on 4): 50 us, 3.6 TB/s.  A
 //   unit of 33 KB takes each of walker, products and weights about a
 //   microsecond of waits and instructions (without its loads: 49 us; with a
 //   third of the products 46; without sums 47; two groups of weight warps in
